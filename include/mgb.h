@@ -58,11 +58,14 @@ typedef enum {
   MGB_ERR_CUDA = -6,                /* a CUDA runtime call failed */
   MGB_ERR_DEVICE_TIMEOUT = -7,      /* a bounded device-side wait ran out */
   MGB_ERR_NOT_IMPLEMENTED = -8,
-  MGB_ERR_DEVICE_CHECK = -9         /* checking build (libmgb_check.so) only: a kernel's
+  MGB_ERR_DEVICE_CHECK = -9,        /* checking build (libmgb_check.so) only: a kernel's
                                        own consistency check failed (an output address
                                        outside its tensor, a misaligned TMA coordinate,
                                        a CE target outside [0, vocab)); the access it
                                        guards was skipped */
+  MGB_ERR_INDEX = -10               /* an index read from device memory (a cache page, a
+                                       sequence's length or row offset) was outside its
+                                       range; the access it guards was skipped */
 } mgb_status;
 
 typedef enum { MGB_F32 = 0, MGB_BF16 = 1 } mgb_dtype;
@@ -417,6 +420,104 @@ mgb_status mgb_attention_fwd(int32_t batch, int32_t seq, int32_t n_q_heads, int3
                              int32_t head_dim, int32_t causal, int32_t dtype,
                              const void* q, const void* k, const void* v, int64_t ld_q,
                              int64_t ld_kv, void* o, float* lse, void* stream);
+
+/* ---- serving: a paged key/value cache and the attention over it ----
+ * Three operators for running a trained layer on sequences of different
+ * lengths. The pages stop at the training step; these follow from the same
+ * attention definition [P2 section 2] with g = h / (nq / nkv).
+ *
+ * Lengths, row offsets and page numbers are device data, read by the kernels:
+ * the host never waits for them, and a captured graph replays with their new
+ * contents. The kernels check every one against its range; a value outside it
+ * records MGB_ERR_INDEX (read by mgb_device_status) and the access is skipped. */
+
+/* A paged cache. Keys and values live in two pools of n_pages pages with the
+ * same strides (elements): the vector of slot i and KV head g of page p starts
+ * at p * stride_page + i * stride_token + g * stride_head, its head_dim
+ * elements contiguous. Both [page][token][head][d] and [page][head][token][d]
+ * are such layouts. block_table [n_seqs][max_pages] int32 (row stride
+ * ld_table): entry i of row s is the page with sequence s's tokens
+ * i * page_size ... Only the entries that a sequence's length needs are read.
+ * Any page_size >= 1. */
+typedef struct {
+  void *k, *v;
+  const int32_t* block_table;
+  int64_t stride_page, stride_token, stride_head, ld_table;
+  int32_t n_pages, page_size, max_pages;
+  int32_t n_kv_heads, head_dim, dtype;
+} mgb_kv_cache;
+
+/* Appends a step's keys and values to the cache, rotating queries and keys by
+ * their positions on the way (rotary embedding). The tokens of n_seqs
+ * sequences lie packed: sequence s owns rows cu_seqlens[s] .. cu_seqlens[s+1]
+ * - 1 of q, k, v (cu_seqlens [n_seqs + 1], non-decreasing, from 0; NULL = one
+ * row per sequence, tokens == n_seqs). seq_lens [n_seqs] is each sequence's
+ * length AFTER the step, so row t of sequence s with n_s rows has position
+ *   p = seq_lens[s] - n_s + (t - cu_seqlens[s]).
+ * The first rot_dim elements of every q and k head are rotated in pairs,
+ *   (a, b) -> (a c - b s, a s + b c),  (c, s) = rope[p][j], j < rot_dim / 2,
+ * pairs (x_j, x_{j + rot_dim/2}) or, with interleaved, (x_2j, x_2j+1); rope
+ * [rope_len][rot_dim / 2][2] float32 holds cos and sin. rot_dim 0 = no
+ * rotation (rope NULL). In float32, rounded once to dtype. The rotated k and v
+ * go to slot p % page_size of page block_table[s][p / page_size].
+ *   q_out [tokens, nq*d], k_out [tokens, nkv*d]: the rotated q and k, row
+ *   strides ld_qo, ld_ko; either may be NULL (not written; q_out NULL: q is
+ *   not read and may be NULL), or the input itself with the same stride.
+ *   Other overlaps of outputs with inputs are not allowed.
+ * A sequence with seq_lens[s] == 0 is padding and a row behind the last
+ * sequence belongs to none: their rows of q_out and k_out are left as they
+ * were and nothing is cached. A position below 0, past the table's max_pages *
+ * page_size or past rope_len, and a page outside [0, n_pages), are
+ * MGB_ERR_INDEX; all of that row's stores are skipped. Two rows must not share
+ * a slot. dtype (the cache's) bf16 or float32; head_dim <= 256 a multiple of
+ * 16 (bf16) or 8 (float32), rot_dim likewise and at most head_dim. */
+typedef struct {
+  int32_t tokens, n_seqs, n_q_heads;
+  int32_t rot_dim, interleaved, rope_len;
+} mgb_kv_append_desc;
+
+mgb_status mgb_kv_append(const mgb_kv_append_desc* desc, const mgb_kv_cache* cache,
+                         const int32_t* cu_seqlens, const int32_t* seq_lens, const float* rope,
+                         const void* q, const void* k, const void* v, int64_t ld_q, int64_t ld_kv,
+                         void* q_out, int64_t ld_qo, void* k_out, int64_t ld_ko, void* stream);
+
+/* Attention of one new token per sequence over the cache. Per sequence s and
+ * query head h: o[s, h] = softmax(q[s, h] K_g^T / sqrt(d)) V_g over the first
+ * seq_lens[s] cached tokens (the new one included). Length 0 (padding): o is
+ * 0, lse is -inf.
+ *
+ * mgb_attention_decode_prepare cuts the cached tokens of a step into equal
+ * shares for the GPU's SMs and copies the lengths into `ws` (16-byte aligned,
+ * caller-owned, at least mgb_attention_decode_ws_bytes). One prepare serves
+ * every layer's mgb_attention_decode of the step with these lengths and head
+ * counts; *plan (host memory) only names the workspace, nothing is read back.
+ * seq_lens is not read again. A length below 0 is MGB_ERR_INDEX and counts
+ * as 0.
+ *
+ * mgb_attention_decode: q [n_seqs, nq*d] (row stride ld_q, e.g. the query
+ * columns of a fused qkv row), o [n_seqs, nq*d] (row stride ld_o), lse [n_seqs,
+ * nq] float32 or NULL. The cache's dtype is q's and o's; bf16 or float32,
+ * head_dim 64 or 128, any group size nq / nkv. A length past max_pages *
+ * page_size and a page outside [0, n_pages) are MGB_ERR_INDEX. Sums and softmax
+ * statistics are float32; in bf16 the weights are rounded to bf16 before
+ * they multiply V. Results repeat bit for bit with the same lengths. The
+ * calls of one plan share its workspace: each is ordered after the prepare
+ * and after the plan's previous call (same stream, or events). */
+typedef struct {
+  int32_t n_seqs, n_q_heads, n_kv_heads, head_dim;
+  void* ws;
+  size_t ws_bytes;
+} mgb_attention_decode_plan;
+
+size_t mgb_attention_decode_ws_bytes(int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                     int32_t head_dim);
+mgb_status mgb_attention_decode_prepare(int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                        int32_t head_dim, const int32_t* seq_lens, void* ws,
+                                        size_t ws_bytes, mgb_attention_decode_plan* plan,
+                                        void* stream);
+mgb_status mgb_attention_decode(const mgb_attention_decode_plan* plan, const mgb_kv_cache* cache,
+                                const void* q, int64_t ld_q, void* o, int64_t ld_o, float* lse,
+                                void* stream);
 
 /* Vocab-parallel embedding lookup [P2 section 3]: the table's rows [v0, v1)
  * are held as emb_shard [(v1 - v0), hidden] (row-major, the vocab shard of a

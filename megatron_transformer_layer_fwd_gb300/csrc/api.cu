@@ -330,6 +330,7 @@ const char* mgb_status_string(mgb_status s) {
     case MGB_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait ran out";
     case MGB_ERR_NOT_IMPLEMENTED: return "not implemented";
     case MGB_ERR_DEVICE_CHECK: return "a device-side consistency check failed (checking build)";
+    case MGB_ERR_INDEX: return "an index in device memory was out of range; the access was skipped";
   }
   return "unknown status";
 }
@@ -343,7 +344,8 @@ mgb_status mgb_device_status(void* stream) {
     if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof(int)) != cudaSuccess) return MGB_ERR_CUDA;
   }
   if (w & kErrTimeout) return MGB_ERR_DEVICE_TIMEOUT;
-  return (w & kErrCheck) ? MGB_ERR_DEVICE_CHECK : MGB_OK;
+  if (w & kErrCheck) return MGB_ERR_DEVICE_CHECK;
+  return (w & kErrIndex) ? MGB_ERR_INDEX : MGB_OK;
 }
 
 mgb_status mgb_memcpy_async(void* dst, const void* src, size_t bytes, void* stream) {

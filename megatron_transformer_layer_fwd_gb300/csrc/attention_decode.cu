@@ -1,0 +1,792 @@
+// Attention of one new token per sequence over a paged key/value cache.
+//
+// Per sequence s and query head h: o = softmax(q_h K_g^T / sqrt(d)) V_g over
+// the first len[s] cached tokens, g = h / (nq / nkv). Bound: HBM (each cached
+// key and value is used once per query head of its group).
+//
+// Work is cut into units: 64 consecutive cached tokens of one (sequence, KV
+// head, group of at most 16 query heads). Units are numbered sequence by
+// sequence, head by head, in token order, and dealt out as one contiguous
+// range of `chunk` units per CTA, so every CTA gets the same number whatever the
+// lengths are. An item (all units of one sequence and head group) that lies in
+// one range is finished there. An item that spans CTAs is split: each CTA
+// leaves its unnormalised sums, maximum and row sum in the workspace, and the
+// last one to arrive (a counter per first CTA of a split item) joins the parts
+// in CTA order, so results do not depend on who was last.
+//
+// The prepare kernel derives the ranges from the lengths (they are the same
+// for every layer of a model's step) and zeroes the counters; each split item
+// leaves its counter at zero again.
+//
+// Within a CTA (four warps) warp w takes tokens 16 w .. 16 w + 15 of each unit
+// and keeps its own running maximum, row sums and output sums; the warps'
+// sums are joined at the end of an item. Each warp streams its tokens through
+// a private ring in shared memory by 16-byte asynchronous copies, so the main
+// loop has no CTA-wide barrier, any page size and any page layout works, and
+// tokens past the length are never read (zero fill).
+//   bf16: products on mma.sync m16n8k16 with the group's query heads as the 16
+//   rows. One query token per sequence gives at most 16 rows, so the products
+//   are a small share of the time and operands come straight from registers.
+//   float32: FFMA with a lane per (token, quarter of d) for the scores and a
+//   lane per 4 (2) columns for the output.
+#include "common.cuh"
+#include "internal.h"
+
+namespace mgb {
+
+namespace {
+
+constexpr int WARPS = 4;
+constexpr int NT = WARPS * 32;
+constexpr int TK = 64;                 // tokens per unit
+constexpr int MAXR = 16;               // query heads per item
+constexpr int NCTA = 304;              // two per SM of a GB300
+constexpr int MIN_CHUNK = 2;           // units per CTA at least
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float TAU = 8.0f;            // the reference maximum moves in steps above this (log2 units)
+
+struct Header {
+  int64_t units;
+  int32_t chunk, pad;
+};
+struct Start {
+  int32_t s, h, t, pad;  // first unit of a CTA: sequence, head group, token tile
+};
+
+struct Layout {
+  size_t header, start, counter, len, prefix, ml, part, total;
+  int rows, groups;  // query heads per item at most; items per sequence
+};
+
+Layout make_layout(int n, int nq, int nkv, int d) {
+  Layout l;
+  size_t o = 0;
+  auto take = [&](size_t b) { const size_t at = o; o += (b + 255) & ~(size_t)255; return at; };
+  const int G = nq / nkv, per = (G + MAXR - 1) / MAXR;
+  l.rows = (G + per - 1) / per;
+  l.groups = nkv * ((G + l.rows - 1) / l.rows);
+  l.header = take(sizeof(Header));
+  l.start = take(sizeof(Start) * NCTA);
+  l.counter = take(4 * NCTA);
+  l.len = take(4 * (size_t)n);
+  l.prefix = take(8 * ((size_t)n + 1));
+  l.ml = take(8 * (size_t)2 * NCTA * l.rows);
+  l.part = take(4 * (size_t)2 * NCTA * l.rows * d);
+  l.total = o;
+  return l;
+}
+
+__host__ __device__ inline int tiles_of(int len) { return len > TK ? (int)(((int64_t)len + TK - 1) / TK) : 1; }
+
+// ---------------------------------------------------------------- prepare
+// One block: lengths copied (negative ones count as 0 and are an error), units
+// summed up, the ranges' first units found, counters zeroed.
+__global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups, const int32_t* lens,
+                                                              Header* hdr, Start* start,
+                                                              uint32_t* counter, int32_t* len_out,
+                                                              int64_t* prefix, int* err) {
+  __shared__ int64_t warp_sum[32];
+  __shared__ int64_t carry_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t carry = 0;
+  for (int i = tid; i < NCTA; i += 1024) counter[i] = 0;
+  for (int base = 0; base < n; base += 1024) {
+    const int i = base + tid;
+    int64_t v = 0;
+    if (i < n) {
+      int len = lens[i];
+      if (len < 0) {
+        record_error(err, kErrIndex);
+        len = 0;
+      }
+      len_out[i] = len;
+      v = tiles_of(len);
+    }
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      int64_t w = warp_sum[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+      }
+      warp_sum[lane] = w;
+      if (lane == 31) carry_s = w;
+    }
+    __syncthreads();
+    if (i < n) prefix[i] = carry + x - v + (warp > 0 ? warp_sum[warp - 1] : 0);
+    carry += carry_s;
+    __syncthreads();
+  }
+  if (tid == 0) prefix[n] = carry;
+  __syncthreads();
+  const int64_t units = carry * groups;
+  int64_t chunk = (units + NCTA - 1) / NCTA;
+  if (chunk < MIN_CHUNK) chunk = MIN_CHUNK;
+  if (tid == 0) *hdr = Header{units, (int32_t)chunk, 0};
+  for (int c = tid; c < NCTA; c += 1024) {
+    const int64_t u = c * chunk;
+    Start st{0, 0, 0, 0};
+    if (u < units) {
+      int lo = 0, hi = n - 1;  // the largest s with prefix[s] * groups <= u
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (prefix[mid] * groups <= u) lo = mid;
+        else hi = mid - 1;
+      }
+      const int64_t nt = prefix[lo + 1] - prefix[lo], r = u - prefix[lo] * groups;
+      st.s = lo;
+      st.h = (int)(r / nt);
+      st.t = (int)(r % nt);
+    }
+    start[c] = st;
+  }
+}
+
+// ---------------------------------------------------------------- main kernel
+struct Params {
+  int n, nkv, groups, per_kv, rows, G;  // head groups per sequence / per KV head, rows per group
+  const Header* hdr;
+  const Start* start;
+  uint32_t* counter;
+  const int32_t* len;
+  float2* ml;    // [2 NCTA][rows] (maximum, row sum) of a part
+  float* part;   // [2 NCTA][rows][d]
+  const void *k, *v;
+  const int32_t* table;
+  int64_t s_page, s_tok, s_head, ld_table;
+  int n_pages, page_size, max_pages;
+  const void* q;
+  int64_t ld_q;
+  void* o;
+  int64_t ld_o;
+  float* lse;
+  int nq;
+  float sl2;     // log2(e) / sqrt(d)
+  int* err;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  const int n = on ? 16 : 0;  // 0: the 16 bytes are zeroed and src is not read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Position in a CTA's range of units.
+struct Cursor {
+  int s, h, t, nt, len, next_len;
+  __device__ void init(const Params& p, const Start& st) {
+    s = st.s; h = st.h; t = st.t;
+    len = p.len[s];
+    next_len = s + 1 < p.n ? p.len[s + 1] : 0;
+    nt = tiles_of(len);
+  }
+  // to the next unit; the next sequence's length was requested one sequence ago
+  __device__ void next(const Params& p) {
+    if (++t < nt) return;
+    t = 0;
+    if (++h < p.groups) return;
+    h = 0;
+    ++s;
+    len = next_len;
+    nt = tiles_of(len);
+    next_len = s + 1 < p.n ? p.len[s + 1] : 0;
+  }
+};
+
+template <typename T, int D>
+struct Cfg {
+  static constexpr int ES = sizeof(T);
+  static constexpr int SK = ES == 2 ? 16 : 8;        // tokens per warp and stage
+  static constexpr int SUB = TK / (WARPS * SK);      // stages per unit
+  static constexpr int ROW = D * ES;                 // bytes of a token's vector
+  static constexpr int CH = ROW / 16;                // 16-byte chunks of it
+  static constexpr int KV = SK * ROW;                // bytes of a stage's keys (or values)
+  static constexpr int STAGES = D == 128 ? 3 : 6;
+  static constexpr int RING = STAGES * 2 * KV;       // per warp
+  static constexpr int MR = ES == 2 ? 8 : 4;         // rows joined at a time
+  static constexpr int OFF_JOIN = WARPS * RING;      // [WARPS][MR][D] float
+  static constexpr int OFF_Q = OFF_JOIN + WARPS * MR * D * 4;  // float32: [MAXR][D]
+  static constexpr int OFF_ML = OFF_Q + (ES == 4 ? MAXR * D * 4 : 0);  // [WARPS][MAXR] float2
+  static constexpr int SMEM = OFF_ML + WARPS * MAXR * 8 + 16;
+  static_assert(SMEM <= 114 * 1024, "two CTAs per SM");
+};
+
+// Shared-memory offset of chunk c of a stage's token row (rotated by the row
+// so that eight rows' same chunk fall into different banks).
+template <int CH>
+__device__ __forceinline__ uint32_t chunk_at(int row, int c) {
+  return (uint32_t)(row * CH + (c ^ (row & 7))) * 16u;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
+  using C = Cfg<T, D>;
+  constexpr bool BF = sizeof(T) == 2;
+  constexpr int ST = C::STAGES;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c = blockIdx.x;
+  const Header hd = *p.hdr;
+  const Start st0 = p.start[c];
+  const int64_t u0 = (int64_t)c * hd.chunk;
+  if (u0 >= hd.units) return;
+  const int64_t u1 = u0 + hd.chunk < hd.units ? u0 + hd.chunk : hd.units;
+  const uint32_t ring = smem_u32(smem) + warp * C::RING;
+  float* join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
+  float* sq = reinterpret_cast<float*>(smem + C::OFF_Q);
+  float2* sml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+  int* flag = reinterpret_cast<int*>(smem + C::OFF_ML + WARPS * MAXR * 8);
+
+  // ---------------- loader: a cursor one stage ahead of the copies, whose
+  // page number is in flight while the previous stage's copies are issued
+  Cursor ld;
+  ld.init(p, st0);
+  int64_t ld_u = u0;
+  int ld_sub = 0, ld_n = 0;
+  int pg = 0, slot = 0, hkv = 0;
+  bool on = false, look = false;
+  auto peek = [&]() {  // request the page of this lane's token of the next stage
+    on = false;
+    look = ld_u < u1;
+    if (!look) return;
+    const int key = ld.t * TK + ld_sub * (WARPS * C::SK) + warp * C::SK + (lane % C::SK);
+    hkv = ld.h / p.per_kv;
+    if (key < ld.len) {
+      const int i = key / p.page_size;
+      slot = key - i * p.page_size;
+      on = i < p.max_pages;
+      if (on) pg = p.table[ld.s * p.ld_table + i];
+      else record_error(p.err, kErrIndex);
+    }
+    if (++ld_sub == C::SUB) {
+      ld_sub = 0;
+      ++ld_u;
+      ld.next(p);
+    }
+  };
+  auto fetch = [&]() {  // copy the stage the last peek looked at, then peek
+    if (look) {
+      bool ok = on && pg >= 0 && pg < p.n_pages;
+      if (on && !ok) record_error(p.err, kErrIndex);
+      const int64_t off = ok ? pg * p.s_page + slot * p.s_tok + hkv * p.s_head : -1;
+      const uint32_t dst = ring + (ld_n % ST) * 2 * C::KV;
+      constexpr int RPI = 32 / C::CH;  // rows per pass of the warp (0: half a row)
+      if (__any_sync(0xffffffffu, ok)) {
+#pragma unroll
+        for (int i = 0; i < C::SK * C::CH / 32; ++i) {
+          const int row = (i * 32 + lane) / C::CH, ch = (i * 32 + lane) % C::CH;
+          const int64_t ro = __shfl_sync(0xffffffffu, off, row);
+          const T* ks = static_cast<const T*>(p.k) + (ro >= 0 ? ro : 0) + ch * (16 / C::ES);
+          const T* vs = static_cast<const T*>(p.v) + (ro >= 0 ? ro : 0) + ch * (16 / C::ES);
+          const uint32_t at = dst + chunk_at<C::CH>(row, ch);
+          cp_async16(at, ks, ro >= 0);
+          cp_async16(at + C::KV, vs, ro >= 0);
+        }
+      }
+      (void)RPI;
+    }
+    cp_async_commit();
+    ++ld_n;
+    peek();
+  };
+  peek();
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i) fetch();
+
+  // ---------------- queries: the next item's are requested one item ahead
+  Cursor cu;
+  cu.init(p, st0);
+  auto q_row = [&](int s, int h, int r) {  // first query head of the group + r, or -1
+    const int first = (h % p.per_kv) * p.rows + r;
+    return r < p.rows && first < p.G ? (h / p.per_kv) * p.G + first : -1;
+  };
+  constexpr int NQ = BF ? D / 16 * 4 : MAXR * D / 4 / NT * 4;
+  uint32_t qn[NQ];
+  auto request_q = [&](int s, int h) {
+    const T* qs = static_cast<const T*>(p.q) + s * p.ld_q;
+    if constexpr (BF) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int head = q_row(s, h, (lane >> 2) + 8 * half);
+        const T* x = qs + (int64_t)(head < 0 ? 0 : head) * D + (lane & 3) * 2;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          qn[kk * 4 + half] = head < 0 ? 0u : *reinterpret_cast<const uint32_t*>(x + kk * 16);
+          qn[kk * 4 + 2 + half] = head < 0 ? 0u : *reinterpret_cast<const uint32_t*>(x + kk * 16 + 8);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NQ / 4; ++i) {
+        const int e = (i * NT + tid) * 4, head = q_row(s, h, e / D);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (head >= 0) x = *reinterpret_cast<const float4*>(qs + (int64_t)head * D + e % D);
+        qn[4 * i] = __float_as_uint(x.x);
+        qn[4 * i + 1] = __float_as_uint(x.y);
+        qn[4 * i + 2] = __float_as_uint(x.z);
+        qn[4 * i + 3] = __float_as_uint(x.w);
+      }
+    }
+  };
+  request_q(cu.s, cu.h);
+
+  int64_t u = u0;
+  int n_use = 0;  // stages consumed
+  while (u < u1) {
+    const int s = cu.s, h = cu.h, len = cu.len, nt = cu.nt, t0 = cu.t;
+    const int64_t item0 = u - t0;                       // the item's first unit
+    const int64_t end = item0 + nt < u1 ? item0 + nt : u1;
+    const int rows = min(p.rows, p.G - (h % p.per_kv) * p.rows);
+    uint32_t qa[BF ? NQ : 1];
+    if constexpr (BF) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) qa[i] = qn[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < NQ / 4; ++i)
+        *reinterpret_cast<float4*>(sq + (i * NT + tid) * 4) =
+            make_float4(__uint_as_float(qn[4 * i]), __uint_as_float(qn[4 * i + 1]),
+                        __uint_as_float(qn[4 * i + 2]), __uint_as_float(qn[4 * i + 3]));
+      __syncthreads();
+    }
+    {  // the next item's queries
+      Cursor nx = cu;
+      nx.t = nx.nt - 1;
+      nx.next(p);
+      if (item0 + nt < u1) request_q(nx.s, nx.h);
+    }
+
+    // bf16: rows lane / 4 and + 8, columns 8 n + 2 (lane % 4) + {0, 1}
+    // float32: all rows, columns lane * (D / 32) ..
+    constexpr int CPL = D / 32;
+    constexpr int NO = BF ? D / 8 : MAXR;
+    constexpr int NI = BF ? 4 : CPL;
+    constexpr int NM = BF ? 2 : MAXR;
+    float acc[NO][NI], m[NM], l[NM];
+#pragma unroll
+    for (int i = 0; i < NO; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) acc[i][j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NM; ++i) m[i] = -INFINITY, l[i] = 0.0f;
+
+    for (; u < end; ++u) {
+#pragma unroll
+      for (int sub = 0; sub < C::SUB; ++sub) {
+        cp_async_wait<ST - 2>();
+        __syncwarp();  // the stage is complete and the one before it no longer read
+        fetch();
+        const uint32_t sk = ring + (n_use % ST) * 2 * C::KV, sv = sk + C::KV;
+        ++n_use;
+        const int key0 = cu.t * TK + sub * (WARPS * C::SK) + warp * C::SK;
+        const int left = len - key0;  // visible tokens of the slice
+        if (left <= 0) continue;
+        if constexpr (BF) {
+          float sc[2][4] = {};
+          const int mi = lane >> 3, r8 = lane & 7;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t b[4];
+            ldsm4(sk + chunk_at<C::CH>((mi >> 1) * 8 + r8, 2 * kk + (mi & 1)), b);
+            const uint32_t a[4] = {qa[kk * 4], qa[kk * 4 + 1], qa[kk * 4 + 2], qa[kk * 4 + 3]};
+            mma_bf16(sc[0], a, b[0], b[1]);
+            mma_bf16(sc[1], a, b[2], b[3]);
+          }
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = 8 * n + 2 * (lane & 3) + (e & 1);
+              sc[n][e] = key < left ? sc[n][e] * p.sl2 : -INFINITY;
+              mx[e >> 1] = fmaxf(mx[e >> 1], sc[n][e]);
+            }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+          }
+          // the reference moves only when it must: P stays below 2^TAU
+          const bool up0 = mx[0] > m[0] + TAU, up1 = mx[1] > m[1] + TAU;
+          if (__any_sync(0xffffffffu, up0 || up1)) {
+            const float a0 = up0 ? exp2f(m[0] - mx[0]) : 1.0f;
+            const float a1 = up1 ? exp2f(m[1] - mx[1]) : 1.0f;
+            if (up0) m[0] = mx[0];
+            if (up1) m[1] = mx[1];
+            l[0] *= a0;
+            l[1] *= a1;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+              acc[n][0] *= a0;
+              acc[n][1] *= a0;
+              acc[n][2] *= a1;
+              acc[n][3] *= a1;
+            }
+          }
+          const float r0 = m[0] == -INFINITY ? 0.0f : m[0], r1 = m[1] == -INFINITY ? 0.0f : m[1];
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              sc[n][e] = ex2_ftz(sc[n][e] - (e < 2 ? r0 : r1));
+              l[e >> 1] += sc[n][e];
+            }
+          // P as bf16 (the row sums take it unrounded): relative error 2^-9 per
+          // weight, below the output's own rounding after averaging
+          const uint32_t pa[4] = {pack_bf16x2(sc[0][0], sc[0][1]), pack_bf16x2(sc[0][2], sc[0][3]),
+                                  pack_bf16x2(sc[1][0], sc[1][1]), pack_bf16x2(sc[1][2], sc[1][3])};
+#pragma unroll
+          for (int nn = 0; nn < D / 16; ++nn) {
+            uint32_t b[4];
+            ldsm4_t(sv + chunk_at<C::CH>((mi & 1) * 8 + r8, 2 * nn + (mi >> 1)), b);
+            mma_bf16(acc[2 * nn], pa, b[0], b[1]);
+            mma_bf16(acc[2 * nn + 1], pa, b[2], b[3]);
+          }
+        } else {
+          const int key = lane & 7, part = lane >> 3;  // token, quarter of d
+          float4 kx[D / 16];
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+            asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(kx[i].x), "=f"(kx[i].y), "=f"(kx[i].z), "=f"(kx[i].w)
+                         : "r"(sk + chunk_at<C::CH>(key, i * 4 + part)));
+          float pr[MAXR];
+#pragma unroll
+          for (int r = 0; r < MAXR; ++r) {
+            pr[r] = 0.0f;
+            if (r >= rows) continue;
+            float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const float4 qx = *reinterpret_cast<const float4*>(sq + r * D + (i * 4 + part) * 4);
+              d0 = fmaf(qx.x, kx[i].x, d0);
+              d1 = fmaf(qx.y, kx[i].y, d1);
+              d0 = fmaf(qx.z, kx[i].z, d0);
+              d1 = fmaf(qx.w, kx[i].w, d1);
+            }
+            float sc = d0 + d1;
+            sc += __shfl_xor_sync(0xffffffffu, sc, 8);
+            sc += __shfl_xor_sync(0xffffffffu, sc, 16);
+            sc = key < left ? sc * p.sl2 : -INFINITY;
+            float mx = sc;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (mx > m[r] + TAU) {  // the same in every lane
+              const float a = exp2f(m[r] - mx);
+              m[r] = mx;
+              l[r] *= a;
+#pragma unroll
+              for (int j = 0; j < CPL; ++j) acc[r][j] *= a;
+            }
+            pr[r] = exp2f(sc - (m[r] == -INFINITY ? 0.0f : m[r]));
+            l[r] += pr[r];  // the lane's token; the four quarters hold copies
+          }
+#pragma unroll
+          for (int kx2 = 0; kx2 < C::SK; ++kx2) {
+            float vx[CPL];
+            const uint32_t va = sv + chunk_at<C::CH>(kx2, lane * CPL / 4) + (lane * CPL % 4) * 4;
+            if constexpr (CPL == 4)
+              asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                           : "=f"(vx[0]), "=f"(vx[1]), "=f"(vx[2]), "=f"(vx[3])
+                           : "r"(va));
+            else
+              asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(vx[0]), "=f"(vx[1]) : "r"(va));
+#pragma unroll
+            for (int r = 0; r < MAXR; ++r) {
+              if (r >= rows) continue;
+              const float w = __shfl_sync(0xffffffffu, pr[r], kx2);
+#pragma unroll
+              for (int j = 0; j < CPL; ++j) acc[r][j] = fmaf(w, vx[j], acc[r][j]);
+            }
+          }
+        }
+      }
+      cu.next(p);
+    }
+
+    // ---------------- the item's units in this CTA are done: join the warps
+    if constexpr (BF) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        if ((lane & 3) == 0) sml[warp * MAXR + (lane >> 2) + 8 * i] = make_float2(m[i], l[i]);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < MAXR; ++r) {
+        if (r >= rows) continue;
+        float x = l[r];
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0) sml[warp * MAXR + r] = make_float2(m[r], x);
+      }
+    }
+    __syncthreads();
+    auto joined = [&](int r, float& M, float& L) {
+      M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sml[w * MAXR + r].x);
+      L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float2 x = sml[w * MAXR + r];
+        if (x.x > -INFINITY) L += x.y * exp2f(x.x - M);
+      }
+    };
+    const bool whole = item0 >= u0 && item0 + nt <= u1;
+    const int cf = (int)(item0 / hd.chunk), cl = (int)((item0 + nt - 1) / hd.chunk);
+    // a CTA's first piece goes to part 2 c, a later one to 2 c + 1
+    auto part_of = [&](int cc) { return 2 * cc + ((int64_t)cc * hd.chunk < item0 ? 1 : 0); };
+    const int my = part_of(c);
+    const int head0 = (h / p.per_kv) * p.G + (h % p.per_kv) * p.rows;
+    auto store_o = [&](int r, int col, float4 x) {
+      T* o = static_cast<T*>(p.o) + s * p.ld_o + (int64_t)(head0 + r) * D + col;
+      if constexpr (BF)
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+      else
+        *reinterpret_cast<float4*>(o) = x;
+    };
+#pragma unroll
+    for (int r0 = 0; r0 < MAXR; r0 += C::MR) {
+      if (r0 >= rows) break;
+      if (r0 > 0) __syncthreads();
+      if constexpr (BF) {
+        const int r = lane >> 2, i = r0 / 8;
+        float M, L;
+        joined(r0 + r, M, L);
+        const float a = m[i] > -INFINITY ? exp2f(m[i] - M) : 0.0f;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+          *reinterpret_cast<float2*>(join + (warp * C::MR + r) * D + n * 8 + 2 * (lane & 3)) =
+              make_float2(acc[n][2 * i] * a, acc[n][2 * i + 1] * a);
+      } else {
+#pragma unroll
+        for (int rr = 0; rr < C::MR; ++rr) {
+          const int r = r0 + rr;
+          if (r >= rows) continue;
+          float M, L;
+          joined(r, M, L);
+          const float a = m[r] > -INFINITY ? exp2f(m[r] - M) : 0.0f;
+#pragma unroll
+          for (int j = 0; j < CPL; ++j)
+            join[(warp * C::MR + rr) * D + lane * CPL + j] = acc[r][j] * a;
+        }
+      }
+      __syncthreads();
+      for (int e = tid * 4; e < C::MR * D; e += NT * 4) {
+        const int r = r0 + e / D, col = e % D;
+        if (r >= rows) break;
+        float4 x = *reinterpret_cast<const float4*>(join + e);
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(join + w * C::MR * D + e);
+          x.x += y.x;
+          x.y += y.y;
+          x.z += y.z;
+          x.w += y.w;
+        }
+        float M, L;
+        joined(r, M, L);
+        if (whole) {
+          const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+          store_o(r, col, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+          if (p.lse != nullptr && col == 0)
+            p.lse[(int64_t)s * p.nq + head0 + r] = (M + log2f(L)) * LN2;
+        } else {
+          *reinterpret_cast<float4*>(p.part + ((int64_t)my * p.rows + r) * D + col) = x;
+          if (col == 0) p.ml[(int64_t)my * p.rows + r] = make_float2(M, L);
+        }
+      }
+    }
+    if (!whole) {
+      // ---- split item: the last CTA to arrive joins the parts in CTA order
+      __threadfence();
+      __syncthreads();
+      if (tid == 0)
+        *flag = atomicInc(p.counter + cf, (uint32_t)(cl - cf)) == (uint32_t)(cl - cf);
+      __syncthreads();
+      if (*flag) {
+        __threadfence();
+        for (int r = warp; r < rows; r += WARPS) {
+          float M = -INFINITY;
+          for (int cc = cf + lane; cc <= cl; cc += 32)
+            M = fmaxf(M, __ldcg(&p.ml[(int64_t)part_of(cc) * p.rows + r]).x);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+          float L = 0.0f, x[CPL] = {};
+          for (int cc0 = cf; cc0 <= cl; cc0 += 32) {
+            float a = 0.0f, lp = 0.0f;
+            if (cc0 + lane <= cl) {
+              const float2 y = __ldcg(&p.ml[(int64_t)part_of(cc0 + lane) * p.rows + r]);
+              a = y.x > -INFINITY ? exp2f(y.x - M) : 0.0f;
+              lp = y.y * a;
+            }
+            const int np = min(32, cl - cc0 + 1);
+#pragma unroll 8
+            for (int i = 0; i < np; ++i) {
+              const float w = __shfl_sync(0xffffffffu, a, i);
+              const float* y = p.part + ((int64_t)part_of(cc0 + i) * p.rows + r) * D + lane * CPL;
+              float z[CPL];
+              if constexpr (CPL == 4) {
+                const float4 zz = __ldcg(reinterpret_cast<const float4*>(y));
+                z[0] = zz.x; z[1] = zz.y; z[2] = zz.z; z[3] = zz.w;
+              } else {
+                const float2 zz = __ldcg(reinterpret_cast<const float2*>(y));
+                z[0] = zz.x; z[1] = zz.y;
+              }
+#pragma unroll
+              for (int j = 0; j < CPL; ++j) x[j] = fmaf(w, z[j], x[j]);
+              L += __shfl_sync(0xffffffffu, lp, i);
+            }
+          }
+          const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+          T* o = static_cast<T*>(p.o) + s * p.ld_o + (int64_t)(head0 + r) * D + lane * CPL;
+#pragma unroll
+          for (int j = 0; j < CPL; ++j) o[j] = from_f<T>(x[j] * inv);
+          if (p.lse != nullptr && lane == 0)
+            p.lse[(int64_t)s * p.nq + head0 + r] = (M + log2f(L)) * LN2;
+        }
+      }
+    }
+    __syncthreads();  // the join buffer, sml and sq are free for the next item
+  }
+  cp_async_wait<0>();
+}
+
+template <typename T, int D>
+mgb_status launch(const Params& p, cudaStream_t st) {
+  using C = Cfg<T, D>;
+  auto k = decode_kernel<T, D>;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return MGB_ERR_CUDA;
+  LaunchScope scope(PROF_ATTN_DECODE, st);
+  k<<<NCTA, NT, C::SMEM, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? MGB_OK : MGB_ERR_CUDA;
+}
+
+mgb_status check_shape(int n, int nq, int nkv, int d) {
+  if (n < 0 || nq < 1 || nkv < 1 || nq % nkv || nq > (1 << 20)) return MGB_ERR_INVALID_ARG;
+  return d == 64 || d == 128 ? MGB_OK : MGB_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+}  // namespace mgb
+
+using namespace mgb;
+
+extern "C" {
+
+size_t mgb_attention_decode_ws_bytes(int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                     int32_t head_dim) {
+  if (check_shape(n_seqs, n_q_heads, n_kv_heads, head_dim) != MGB_OK) return 0;
+  return make_layout(n_seqs, n_q_heads, n_kv_heads, head_dim).total;
+}
+
+mgb_status mgb_attention_decode_prepare(int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                        int32_t head_dim, const int32_t* seq_lens, void* ws,
+                                        size_t ws_bytes, mgb_attention_decode_plan* plan,
+                                        void* stream) {
+  if (fault_injected() || plan == nullptr) return MGB_ERR_INVALID_ARG;
+  mgb_status s = check_shape(n_seqs, n_q_heads, n_kv_heads, head_dim);
+  if (s != MGB_OK) return s;
+  if (ws == nullptr || (n_seqs > 0 && seq_lens == nullptr)) return MGB_ERR_INVALID_ARG;
+  if (!is_aligned16(ws) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u)) return MGB_ERR_MISALIGNED;
+  const Layout l = make_layout(n_seqs, n_q_heads, n_kv_heads, head_dim);
+  if (ws_bytes < l.total) return MGB_ERR_WORKSPACE_TOO_SMALL;
+  s = check_arch();
+  if (s != MGB_OK) return s;
+  int* err = device_error_word();
+  if (err == nullptr) return MGB_ERR_CUDA;
+  char* b = static_cast<char*>(ws);
+  if (n_seqs > 0) {
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    LaunchScope scope(PROF_ATTN_DECODE, st);
+    decode_prepare_kernel<<<1, 1024, 0, st>>>(
+        n_seqs, l.groups, seq_lens, reinterpret_cast<Header*>(b + l.header),
+        reinterpret_cast<Start*>(b + l.start), reinterpret_cast<uint32_t*>(b + l.counter),
+        reinterpret_cast<int32_t*>(b + l.len), reinterpret_cast<int64_t*>(b + l.prefix), err);
+    if (cudaGetLastError() != cudaSuccess) return MGB_ERR_CUDA;
+  }
+  *plan = mgb_attention_decode_plan{n_seqs, n_q_heads, n_kv_heads, head_dim, ws, ws_bytes};
+  return MGB_OK;
+}
+
+mgb_status mgb_attention_decode(const mgb_attention_decode_plan* plan, const mgb_kv_cache* c,
+                                const void* q, int64_t ld_q, void* o, int64_t ld_o, float* lse,
+                                void* stream) {
+  if (fault_injected() || plan == nullptr || plan->ws == nullptr) return MGB_ERR_INVALID_ARG;
+  const int n = plan->n_seqs, nq = plan->n_q_heads, nkv = plan->n_kv_heads, d = plan->head_dim;
+  mgb_status s = check_shape(n, nq, nkv, d);
+  if (s != MGB_OK) return s;
+  s = check_kv_cache(c, n);
+  if (s != MGB_OK) return s;
+  if (c->n_kv_heads != nkv || c->head_dim != d || (n > 0 && (!q || !o))) return MGB_ERR_INVALID_ARG;
+  if (n > 1 && (ld_q < (int64_t)nq * d || ld_o < (int64_t)nq * d)) return MGB_ERR_INVALID_ARG;
+  const int vn = c->dtype == MGB_BF16 ? 8 : 4;
+  if (!is_aligned16(q) || !is_aligned16(o) || ld_q % vn || ld_o % vn || !is_aligned16(plan->ws) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return MGB_ERR_MISALIGNED;
+  const Layout l = make_layout(n, nq, nkv, d);
+  if (plan->ws_bytes < l.total) return MGB_ERR_WORKSPACE_TOO_SMALL;
+  s = check_arch();
+  if (s != MGB_OK) return s;
+  if (n == 0) return MGB_OK;
+  char* b = static_cast<char*>(plan->ws);
+  Params p{};
+  p.n = n; p.nkv = nkv; p.groups = l.groups; p.per_kv = l.groups / nkv; p.rows = l.rows;
+  p.G = nq / nkv; p.nq = nq;
+  p.hdr = reinterpret_cast<const Header*>(b + l.header);
+  p.start = reinterpret_cast<const Start*>(b + l.start);
+  p.counter = reinterpret_cast<uint32_t*>(b + l.counter);
+  p.len = reinterpret_cast<const int32_t*>(b + l.len);
+  p.ml = reinterpret_cast<float2*>(b + l.ml);
+  p.part = reinterpret_cast<float*>(b + l.part);
+  p.k = c->k; p.v = c->v; p.table = c->block_table;
+  p.s_page = c->stride_page; p.s_tok = c->stride_token; p.s_head = c->stride_head;
+  p.ld_table = c->ld_table;
+  p.n_pages = c->n_pages; p.page_size = c->page_size; p.max_pages = c->max_pages;
+  p.q = q; p.ld_q = ld_q; p.o = o; p.ld_o = ld_o; p.lse = lse;
+  p.sl2 = LOG2E / sqrtf((float)d);
+  p.err = device_error_word();
+  if (p.err == nullptr) return MGB_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (c->dtype == MGB_BF16) return d == 64 ? launch<bf16, 64>(p, st) : launch<bf16, 128>(p, st);
+  return d == 64 ? launch<float, 64>(p, st) : launch<float, 128>(p, st);
+}
+
+}  // extern "C"

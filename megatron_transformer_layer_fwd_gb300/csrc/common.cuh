@@ -17,7 +17,7 @@ typedef __nv_bfloat16 bf16;
 // Kernels that wait on barriers get a pointer to the per-device error word
 // (owned by the C-ABI translation unit) and OR-in MGB error bits;
 // mgb_device_status() reads and clears it.
-enum : int { kErrTimeout = 1, kErrCheck = 2 };
+enum : int { kErrTimeout = 1, kErrCheck = 2, kErrIndex = 4 };
 // Upper bound of any single device-side wait, in nanoseconds.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 

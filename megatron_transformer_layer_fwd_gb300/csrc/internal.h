@@ -291,6 +291,11 @@ mgb_status embedding_bwd_launch(int T, int H, int dtype, int v0, int v1, const i
                                 const void* dout, void* d_emb, int accumulate, void* ws,
                                 cudaStream_t st);
 
+// Checks of the serving entry points: the cache descriptor's geometry
+// (MGB_OK or the documented error), and the 16-byte rule.
+mgb_status check_kv_cache(const mgb_kv_cache* c, int n_seqs);
+inline bool is_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 // Streaming multiprocessors of the current device (cached per device).
 int device_sm_count();
 
@@ -315,6 +320,8 @@ enum ProfKind : int {
   PROF_CE_GRAD, PROF_GEMM_CE_LOGITS, PROF_EMBEDDING, PROF_DROPOUT,
   // the CE's input-gradient (G E) and weight-gradient (G^T hidden) products
   PROF_GEMM_CE_DGRAD, PROF_GEMM_CE_WGRAD, PROF_SPLITK_REDUCE,
+  // serving: the cache append, packed prompt attention, paged decode attention
+  PROF_KV_APPEND, PROF_ATTN_PACKED, PROF_ATTN_DECODE,
   // stages of the layer (CUDA events around groups of launches, not kernels):
   // attention sublayer forward (LN1, QKV, attention, output projection +
   // residual), MLP sublayer forward (LN2, fc1 + activation, fc2 + residual),

@@ -1,0 +1,331 @@
+// Appending a step's keys and values to a paged cache, with the rotary
+// rotation of queries and keys on the way.
+//
+// Row t of sequence s (rows cu[s] .. cu[s+1] - 1, length len[s] after the
+// step) has position p = len[s] - (cu[s+1] - cu[s]) + t - cu[s]. The first
+// rot elements of each q and k head rotate in pairs, a' = a c - b s,
+// b' = a s + b c with (c, s) = rope[p][j]; k' and v go to slot p % page_size of
+// page table[s][p / page_size].
+//
+// Bound: HBM (each element read once; q' once, k' twice, v once written; the
+// table's row is 4 bytes per rotated element and stays in L2 for the heads of
+// one token). A thread owns a unit: the two 16-byte vectors of one head whose
+// elements pair up (half split: vectors u and u + rot / (2 VN), so the pair
+// partners sit at the same place of the two vectors; interleaved: vectors 2u
+// and 2u + 1). Both read the same 2 VN floats of the table row, VN u onwards.
+// The owner both reads and writes its unit, so the output may be the input.
+//
+// A block's groups of threads each take TB tokens at a time. A thread requests
+// its unit of all TB tokens before it needs to know where they go; meanwhile
+// the group's first warp finds each token's sequence, position and page (a
+// 32-way search over cu, then two dependent loads).
+#include "common.cuh"
+#include "internal.h"
+
+namespace mgb {
+
+namespace {
+
+constexpr int MAX_TOKENS_PER_BLOCK = 16;
+
+struct AppendParams {
+  int tokens, n_seqs, nq, nkv, rot, rope_len;
+  int units_head;              // units per head
+  int units;                   // per token: (nq + 2 nkv) heads (0 q heads without q_out)
+  int page_size, max_pages, n_pages, d;
+  const int32_t *cu, *lens, *table;
+  int64_t ld_table, s_page, s_tok, s_head;
+  const float* rope;
+  const char *q, *k, *v;
+  char *q_out, *k_out, *k_pool, *v_pool;
+  int64_t ld_q, ld_kv, ld_qo, ld_ko;
+  int* err;
+};
+
+// The largest s in [0, n] with s == 0 or cu[s] <= t (whole warp, same result in
+// every lane). Reads cu[1 .. n] only, whatever they hold.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int n, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;  // the answer lies in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const int i = lo + (lane + 1) * step;
+    const bool le = i <= hi && cu[i] <= t;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));
+    lo += c * step;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
+template <typename T>
+struct Vec {
+  static constexpr int VN = 16 / sizeof(T);
+  __device__ static void unpack(const uint4& w, float (&f)[VN]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        const float2 p = unpack_bf16x2(u[i]);
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
+      } else {
+        f[i] = __uint_as_float(u[i]);
+      }
+    }
+  }
+  __device__ static uint4 pack(const float (&f)[VN]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) u[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+      else u[i] = __float_as_uint(f[i]);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+
+// Rotates the unit's VN pairs; cs = the unit's 2 VN table floats.
+template <typename T, bool INTER>
+__device__ __forceinline__ void rotate(uint4& w0, uint4& w1, const float4* cs) {
+  constexpr int VN = Vec<T>::VN;
+  float x[VN], y[VN];
+  Vec<T>::unpack(w0, x);
+  Vec<T>::unpack(w1, y);
+#pragma unroll
+  for (int i = 0; i < VN / 2; ++i) {
+    const float4 t = cs[i];  // (c, s) of pairs 2i and 2i + 1
+    const float c[2] = {t.x, t.z}, s[2] = {t.y, t.w};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int j = 2 * i + e;
+      // the pair's two elements: (x[j], y[j]), or neighbours of one vector
+      float* v = j < VN / 2 ? x : y;
+      float& a = INTER ? v[(2 * j) % VN] : x[j];
+      float& b = INTER ? v[(2 * j + 1) % VN] : y[j];
+      const float a0 = a, b0 = b;
+      a = fmaf(a0, c[e], -(b0 * s[e]));
+      b = fmaf(a0, s[e], b0 * c[e]);
+    }
+  }
+  w0 = Vec<T>::pack(x);
+  w1 = Vec<T>::pack(y);
+}
+
+template <typename T, int TB, bool INTER>
+__global__ void kv_append_kernel(const AppendParams p) {
+  constexpr int VN = Vec<T>::VN;
+  __shared__ int s_pos[MAX_TOKENS_PER_BLOCK];       // -1: nothing to do for the token
+  __shared__ int64_t s_slot[MAX_TOKENS_PER_BLOCK];  // element offset in the pools, head 0
+  const int g = threadIdx.y;
+  const int t0 = (blockIdx.x * blockDim.y + g) * TB;
+  const int rot_units = p.rot / (2 * VN);
+
+  // the unit's two vectors in its row, for q / k / v of token t
+  auto locate = [&](int u, int& head, int& e0, int& e1, int& ju) {
+    head = u / p.units_head;
+    const int w = u - head * p.units_head;
+    ju = w < rot_units ? w * VN : -1;  // first table pair of the unit
+    if (INTER || ju < 0) {
+      e0 = 2 * w * VN;
+      e1 = e0 + VN;
+    } else {
+      e0 = w * VN;
+      e1 = e0 + p.rot / 2;
+    }
+  };
+  const int q_heads = p.q_out != nullptr ? p.nq : 0;
+  auto src = [&](int head, int64_t t) -> const T* {
+    if (head < q_heads) return reinterpret_cast<const T*>(p.q) + t * p.ld_q + (int64_t)head * p.d;
+    head -= q_heads;
+    if (head < p.nkv) return reinterpret_cast<const T*>(p.k) + t * p.ld_kv + (int64_t)head * p.d;
+    return reinterpret_cast<const T*>(p.v) + t * p.ld_kv + (int64_t)(head - p.nkv) * p.d;
+  };
+  uint4 a[TB], b[TB];
+  auto load = [&](int u) {
+    int head, e0, e1, ju;
+    locate(u, head, e0, e1, ju);
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+      if (t0 + i < p.tokens) {
+        const T* x = src(head, t0 + i);
+        a[i] = *reinterpret_cast<const uint4*>(x + e0);
+        b[i] = *reinterpret_cast<const uint4*>(x + e1);
+      }
+  };
+  if (threadIdx.x < p.units) load(threadIdx.x);
+
+  if (threadIdx.x < 32) {
+#pragma unroll
+    for (int i = 0; i < TB; ++i) {
+      const int t = t0 + i;
+      if (t >= p.tokens) break;
+      int s = t, first = t, rows = 1;
+      if (p.cu != nullptr) {
+        s = find_seq(p.cu, p.n_seqs, t);
+        if (s < p.n_seqs) {
+          first = p.cu[s];
+          rows = p.cu[s + 1] - first;
+        }
+      }
+      int pos = -1;
+      int64_t slot = 0;
+      const int len = s < p.n_seqs ? p.lens[s] : 0;
+      if (len != 0) {  // else padding, or behind the last sequence
+        const int64_t at = (int64_t)len - rows + (t - first);
+        bool ok = at >= 0 && at < (int64_t)p.max_pages * p.page_size && at < INT32_MAX &&
+                  (p.rot == 0 || at < p.rope_len);
+        if (ok) {
+          const int pg = (int)at / p.page_size;
+          const int page = p.table[s * p.ld_table + pg];
+          ok = page >= 0 && page < p.n_pages;
+          slot = page * p.s_page + ((int)at - pg * p.page_size) * p.s_tok;
+        }
+        if (ok) pos = (int)at;
+        else if (threadIdx.x == 0) record_error(p.err, kErrIndex);
+      }
+      if (threadIdx.x == 0) {
+        s_pos[g * TB + i] = pos;
+        s_slot[g * TB + i] = slot;
+      }
+    }
+  }
+  __syncthreads();
+
+  for (int u = threadIdx.x; u < p.units; u += blockDim.x) {
+    if (u != threadIdx.x) load(u);
+    int head, e0, e1, ju;
+    locate(u, head, e0, e1, ju);
+    const bool is_q = head < q_heads;
+    const int kh = head - q_heads;            // k heads, then v heads
+    const bool is_k = !is_q && kh < p.nkv;
+#pragma unroll
+    for (int i = 0; i < TB; ++i) {
+      const int t = t0 + i;
+      if (t >= p.tokens) break;
+      const int pos = s_pos[g * TB + i];
+      if (pos < 0) continue;
+      if (ju >= 0 && (is_q || is_k))
+        rotate<T, INTER>(a[i], b[i],
+                         reinterpret_cast<const float4*>(p.rope + (int64_t)pos * p.rot + 2 * ju));
+      if (is_q || (is_k && p.k_out != nullptr)) {
+        T* o = is_q ? reinterpret_cast<T*>(p.q_out) + (int64_t)t * p.ld_qo + (int64_t)head * p.d
+                    : reinterpret_cast<T*>(p.k_out) + (int64_t)t * p.ld_ko + (int64_t)kh * p.d;
+        *reinterpret_cast<uint4*>(o + e0) = a[i];
+        *reinterpret_cast<uint4*>(o + e1) = b[i];
+      }
+      if (!is_q) {
+        T* o = is_k ? reinterpret_cast<T*>(p.k_pool) + kh * p.s_head
+                    : reinterpret_cast<T*>(p.v_pool) + (kh - p.nkv) * p.s_head;
+        o += s_slot[g * TB + i];
+        *reinterpret_cast<uint4*>(o + e0) = a[i];
+        *reinterpret_cast<uint4*>(o + e1) = b[i];
+      }
+    }
+  }
+}
+
+template <typename T, int TB>
+mgb_status launch(const AppendParams& p, bool inter, cudaStream_t st) {
+  // threads along a token's units (up to 512, whole warps), and groups of them
+  // until a block has about 256
+  const int x = p.units >= 512 ? 512 : (p.units + 31) / 32 * 32;
+  int y = x >= 256 ? 1 : 256 / x;
+  if (y * TB > MAX_TOKENS_PER_BLOCK) y = MAX_TOKENS_PER_BLOCK / TB;
+  if ((int64_t)y * TB > p.tokens) y = (p.tokens + TB - 1) / TB;
+  const int per = y * TB;
+  const int grid = (int)(((int64_t)p.tokens + per - 1) / per);
+  LaunchScope scope(PROF_KV_APPEND, st);
+  if (inter) kv_append_kernel<T, TB, true><<<grid, dim3(x, y), 0, st>>>(p);
+  else kv_append_kernel<T, TB, false><<<grid, dim3(x, y), 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? MGB_OK : MGB_ERR_CUDA;
+}
+
+template <typename T>
+mgb_status launch_t(const AppendParams& p, bool inter, cudaStream_t st) {
+  return launch<T, 1>(p, inter, st);
+}
+
+}  // namespace
+
+mgb_status check_kv_cache(const mgb_kv_cache* c, int n_seqs) {
+  if (c == nullptr) return MGB_ERR_INVALID_ARG;
+  if (c->dtype != MGB_BF16 && c->dtype != MGB_F32) return MGB_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->page_size < 1 || c->max_pages < 1 || c->n_kv_heads < 1 ||
+      c->head_dim < 1 || c->stride_page < 0 || c->stride_token < 0 || c->stride_head < 0 ||
+      (n_seqs > 1 && c->ld_table < c->max_pages))
+    return MGB_ERR_INVALID_ARG;
+  if (!c->k || !c->v || (n_seqs > 0 && !c->block_table)) return MGB_ERR_INVALID_ARG;
+  const int vn = c->dtype == MGB_BF16 ? 8 : 4;
+  if (!is_aligned16(c->k) || !is_aligned16(c->v) || c->stride_page % vn || c->stride_token % vn ||
+      c->stride_head % vn || (reinterpret_cast<uintptr_t>(c->block_table) & 3u))
+    return MGB_ERR_MISALIGNED;
+  // slots and heads of a page do not overlap
+  if ((c->page_size > 1 && c->stride_token < c->head_dim) ||
+      (c->n_kv_heads > 1 && c->stride_head < c->head_dim) ||
+      (c->n_pages > 1 && c->stride_page < c->head_dim))
+    return MGB_ERR_INVALID_ARG;
+  return MGB_OK;
+}
+
+}  // namespace mgb
+
+using namespace mgb;
+
+extern "C" mgb_status mgb_kv_append(const mgb_kv_append_desc* d, const mgb_kv_cache* c,
+                                    const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                    const float* rope, const void* q, const void* k, const void* v,
+                                    int64_t ld_q, int64_t ld_kv, void* q_out, int64_t ld_qo,
+                                    void* k_out, int64_t ld_ko, void* stream) {
+  if (fault_injected()) return MGB_ERR_INVALID_ARG;
+  if (d == nullptr || d->tokens < 0 || d->n_seqs < 0 || d->rot_dim < 0 || d->rope_len < 0 ||
+      (d->interleaved & ~1))
+    return MGB_ERR_INVALID_ARG;
+  mgb_status s = check_kv_cache(c, d->n_seqs);
+  if (s != MGB_OK) return s;
+  const int vn = c->dtype == MGB_BF16 ? 8 : 4;
+  if (c->head_dim > 256 || c->head_dim % (2 * vn) || d->rot_dim % (2 * vn))
+    return MGB_ERR_UNSUPPORTED;
+  if (d->rot_dim > c->head_dim || (d->rot_dim > 0 && (d->rope_len < 1 || rope == nullptr)))
+    return MGB_ERR_INVALID_ARG;
+  if (cu_seqlens == nullptr && d->tokens != d->n_seqs) return MGB_ERR_INVALID_ARG;
+  if (q_out != nullptr && (d->n_q_heads < 1 || q == nullptr)) return MGB_ERR_INVALID_ARG;
+  if (d->tokens > 0 && (!k || !v || (d->n_seqs > 0 && !seq_lens))) return MGB_ERR_INVALID_ARG;
+  const int64_t wq = (int64_t)d->n_q_heads * c->head_dim, wk = (int64_t)c->n_kv_heads * c->head_dim;
+  if (wk >= ((int64_t)1 << 28) || (q_out != nullptr && wq >= ((int64_t)1 << 28)))
+    return MGB_ERR_INVALID_ARG;
+  if (ld_kv < wk || (k_out != nullptr && ld_ko < wk) ||
+      (q_out != nullptr && (ld_q < wq || ld_qo < wq)))
+    return MGB_ERR_INVALID_ARG;
+  if ((q_out != nullptr && q_out == q && ld_qo != ld_q) ||
+      (k_out != nullptr && k_out == k && ld_ko != ld_kv))
+    return MGB_ERR_INVALID_ARG;
+  const void* ps[] = {k, v, k_out, q_out, rope, q_out ? q : nullptr};
+  for (const void* x : ps)
+    if (!is_aligned16(x)) return MGB_ERR_MISALIGNED;
+  if (ld_kv % vn || (k_out && ld_ko % vn) || (q_out && (ld_q % vn || ld_qo % vn)) ||
+      (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u))
+    return MGB_ERR_MISALIGNED;
+  s = check_arch();
+  if (s != MGB_OK) return s;
+  if (d->tokens == 0 || d->n_seqs == 0) return MGB_OK;
+  AppendParams p{};
+  p.tokens = d->tokens; p.n_seqs = d->n_seqs; p.nq = d->n_q_heads; p.nkv = c->n_kv_heads;
+  p.rot = d->rot_dim; p.rope_len = d->rope_len; p.d = c->head_dim;
+  p.units_head = c->head_dim / (2 * vn);
+  p.units = ((q_out ? p.nq : 0) + 2 * p.nkv) * p.units_head;
+  p.page_size = c->page_size; p.max_pages = c->max_pages; p.n_pages = c->n_pages;
+  p.cu = cu_seqlens; p.lens = seq_lens; p.table = c->block_table; p.ld_table = c->ld_table;
+  p.s_page = c->stride_page; p.s_tok = c->stride_token; p.s_head = c->stride_head;
+  p.rope = rope;
+  p.q = static_cast<const char*>(q); p.k = static_cast<const char*>(k);
+  p.v = static_cast<const char*>(v);
+  p.q_out = static_cast<char*>(q_out); p.k_out = static_cast<char*>(k_out);
+  p.k_pool = static_cast<char*>(c->k); p.v_pool = static_cast<char*>(c->v);
+  p.ld_q = ld_q; p.ld_kv = ld_kv; p.ld_qo = ld_qo; p.ld_ko = ld_ko;
+  p.err = device_error_word();
+  if (p.err == nullptr) return MGB_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return c->dtype == MGB_BF16 ? launch_t<bf16>(p, d->interleaved != 0, st)
+                              : launch_t<float>(p, d->interleaved != 0, st);
+}

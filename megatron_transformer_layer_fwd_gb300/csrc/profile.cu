@@ -60,7 +60,7 @@ const char* kKindNames[PROF_KINDS] = {
     "gemm_tc_fwd",  "gemm_tc_dgrad", "gemm_tc_wgrad", "gemm_f32",  "attn_fwd",   "attn_bwd",
     "layernorm_fwd", "layernorm_bwd", "colsum",       "ce_stats", "ce_combine", "ce_grad",
     "gemm_tc_ce_logits", "embedding", "dropout", "gemm_tc_ce_dgrad", "gemm_tc_ce_wgrad",
-    "splitk_reduce",
+    "splitk_reduce", "kv_append", "attn_packed", "attn_decode",
     "stage_attention", "stage_ffn", "stage_backward", "stage_ce_products"};
 
 }  // namespace

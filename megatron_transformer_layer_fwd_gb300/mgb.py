@@ -29,6 +29,7 @@ MGB_ERR_CUDA = -6
 MGB_ERR_DEVICE_TIMEOUT = -7
 MGB_ERR_NOT_IMPLEMENTED = -8
 MGB_ERR_DEVICE_CHECK = -9
+MGB_ERR_INDEX = -10
 
 MGB_F32, MGB_BF16 = 0, 1
 MGB_CE_STREAM, MGB_CE_FUSED, MGB_CE_RESIDENT, MGB_CE_BLOCKED = 0, 1, 2, 3
@@ -89,6 +90,25 @@ class EmbeddingBwdPlan(ctypes.Structure):
                 ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
 
 
+class KVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("stride_page", ctypes.c_int64), ("stride_token", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("ld_table", ctypes.c_int64),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class KVAppendDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "tokens", "n_seqs", "n_q_heads", "rot_dim", "interleaved", "rope_len")]
+
+
+class AttentionDecodePlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_q_heads", "n_kv_heads", "head_dim")] + [
+        ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+
+
 class GemmDesc(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("a_major", ctypes.c_int32), ("b_major", ctypes.c_int32),
@@ -146,6 +166,12 @@ def load() -> ctypes.CDLL:
             "mgb_embedding_bwd_prepare": [I32, I32, I32, P, P, SZ,
                                           ctypes.POINTER(EmbeddingBwdPlan), P],
             "mgb_embedding_bwd_apply": [ctypes.POINTER(EmbeddingBwdPlan), I32, I32, P, P, I32, P],
+            "mgb_kv_append": [ctypes.POINTER(KVAppendDesc), ctypes.POINTER(KVCache), P, P, P, P, P, P,
+                              I64, I64, P, I64, P, I64, P],
+            "mgb_attention_decode_prepare": [I32, I32, I32, I32, P, P, SZ,
+                                             ctypes.POINTER(AttentionDecodePlan), P],
+            "mgb_attention_decode": [ctypes.POINTER(AttentionDecodePlan), ctypes.POINTER(KVCache), P,
+                                     I64, P, I64, P, P],
             "mgb_device_status": [P],
             "mgb_selftest_wait_timeout": [U64, P],
         }
@@ -167,6 +193,8 @@ def load() -> ctypes.CDLL:
         lib.mgb_gemm_f32_tc_ws_bytes.restype = SZ
         lib.mgb_embedding_bwd_ws_bytes.argtypes = [I32, I32, I32]
         lib.mgb_embedding_bwd_ws_bytes.restype = SZ
+        lib.mgb_attention_decode_ws_bytes.argtypes = [I32, I32, I32, I32]
+        lib.mgb_attention_decode_ws_bytes.restype = SZ
         lib.mgb_launch_count.argtypes = []
         lib.mgb_launch_count.restype = ctypes.c_uint64
         lib.mgb_profile_enable.argtypes = [I32]
@@ -417,6 +445,69 @@ def mgb_attention_bwd(batch, seq, n_q_heads, n_kv_heads, head_dim, causal, dtype
                                     _ptr(dout), ld_do, _ptr(dq), _ptr(dk), _ptr(dv), ld_dq, ld_dkv,
                                     _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
            "mgb_attention_bwd")
+
+
+def kv_cache(k_pool, v_pool, block_table) -> KVCache:
+    """A paged cache from its pools, [n_pages, page_size, n_kv_heads, head_dim]
+    tensors (for pages stored head by head, the transposed view of a [n_pages,
+    n_kv_heads, page_size, head_dim] tensor), and its block table [n_seqs,
+    max_pages] int32. The returned struct keeps the three tensors alive."""
+    import torch
+    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape or k_pool.stride() != v_pool.stride() \
+            or k_pool.dtype != v_pool.dtype:
+        raise ValueError("k_pool and v_pool must be 4-D with the same shape, strides and dtype")
+    if k_pool.shape[3] > 1 and k_pool.stride(3) != 1:
+        raise ValueError("the head dimension of the pools must be contiguous")
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [n_seqs, max_pages] int32 with contiguous rows")
+    dtypes = {torch.bfloat16: MGB_BF16, torch.float32: MGB_F32}
+    if k_pool.dtype not in dtypes:
+        raise ValueError("the pools must be bfloat16 or float32")
+    n_pages, page_size, n_kv_heads, head_dim = k_pool.shape
+    sp, st, sh, _ = k_pool.stride()
+    cache = KVCache(k=k_pool.data_ptr(), v=v_pool.data_ptr(), block_table=block_table.data_ptr(),
+                    stride_page=sp, stride_token=st, stride_head=sh, ld_table=block_table.stride(0),
+                    n_pages=n_pages, page_size=page_size, max_pages=block_table.shape[1],
+                    n_kv_heads=n_kv_heads, head_dim=head_dim, dtype=dtypes[k_pool.dtype])
+    cache.tensors = (k_pool, v_pool, block_table)
+    return cache
+
+
+def kv_append_desc(tokens: int, n_seqs: int, n_q_heads: int, rot_dim: int, interleaved: bool,
+                   rope_len: int) -> KVAppendDesc:
+    return KVAppendDesc(tokens, n_seqs, n_q_heads, rot_dim, int(interleaved), rope_len)
+
+
+def mgb_kv_append(desc: KVAppendDesc, cache: KVCache, cu_seqlens, seq_lens, rope, q, k, v, ld_q,
+                  ld_kv, q_out, ld_qo, k_out, ld_ko, stream=None) -> None:
+    _check(load().mgb_kv_append(ctypes.byref(desc), ctypes.byref(cache), _ptr(cu_seqlens),
+                                _ptr(seq_lens), _ptr(rope), _ptr(q), _ptr(k), _ptr(v), ld_q, ld_kv,
+                                _ptr(q_out), ld_qo, _ptr(k_out), ld_ko, _stream(stream)),
+           "mgb_kv_append")
+
+
+def mgb_attention_decode_ws_bytes(n_seqs: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return load().mgb_attention_decode_ws_bytes(n_seqs, n_q_heads, n_kv_heads, head_dim)
+
+
+def mgb_attention_decode_prepare(n_seqs, n_q_heads, n_kv_heads, head_dim, seq_lens, ws,
+                                 stream=None) -> AttentionDecodePlan:
+    """The step's plan (host struct, keeps `ws` alive) for mgb_attention_decode."""
+    plan = AttentionDecodePlan()
+    plan.tensors = (ws,)
+    _check(load().mgb_attention_decode_prepare(n_seqs, n_q_heads, n_kv_heads, head_dim,
+                                               _ptr(seq_lens), _ptr(ws),
+                                               ws.numel() * ws.element_size(), ctypes.byref(plan),
+                                               _stream(stream)), "mgb_attention_decode_prepare")
+    return plan
+
+
+def mgb_attention_decode(plan: AttentionDecodePlan, cache: KVCache, q, ld_q, o, ld_o, lse=None,
+                         stream=None) -> None:
+    _check(load().mgb_attention_decode(ctypes.byref(plan), ctypes.byref(cache), _ptr(q), ld_q,
+                                       _ptr(o), ld_o, _ptr(lse), _stream(stream)),
+           "mgb_attention_decode")
 
 
 def mgb_memcpy_async(dst, src, nbytes: int, stream=None) -> None:

@@ -81,3 +81,12 @@ class CERunner:
     def run(self, stream=None):
         mgb.mgb_vocab_ce_fwd_bwd(self.desc, self.hidden, self.emb, self.targets, self.loss,
                                  self.loss_mean, self.lse, self.d_hidden, self.d_emb, self.ws, stream)
+
+
+def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The rotary table mgb_kv_append reads, [positions, rot_dim / 2, 2] float32:
+    cos and sin of p * base^(-2 j / rot_dim), from float64 angles (a float32
+    product p * frequency is off by up to 2^-24 p radians)."""
+    j = torch.arange(rot_dim // 2, dtype=torch.float64)
+    a = torch.arange(positions, dtype=torch.float64)[:, None] * base ** (-2.0 * j / rot_dim)[None, :]
+    return torch.stack((torch.cos(a), torch.sin(a)), dim=-1).to(device, torch.float32).contiguous()
