@@ -481,6 +481,43 @@ mgb_status mgb_kv_append(const mgb_kv_append_desc* desc, const mgb_kv_cache* cac
                          const void* q, const void* k, const void* v, int64_t ld_q, int64_t ld_kv,
                          void* q_out, int64_t ld_qo, void* k_out, int64_t ld_ko, void* stream);
 
+/* Attention over a batch of sequences of different lengths laid one behind
+ * the other: sequence s owns rows cu_seqlens[s] .. cu_seqlens[s+1] - 1
+ * (cu_seqlens [n_seqs + 1] int32, non-decreasing, from 0 to at most tokens).
+ * Within each sequence, per query head h: softmax(Q_h K_g^T / sqrt(d)) V_g,
+ * with causal key j visible to query i iff j <= i. Rows that belong to no
+ * sequence are not read, and their rows of o and lse are left as they were.
+ *
+ * mgb_attention_packed_prepare derives the work list of a batch from the row
+ * offsets into `ws` (16-byte aligned, caller-owned, at least
+ * mgb_attention_packed_ws_bytes). One prepare serves every layer's
+ * mgb_attention_packed_fwd of the batch, whatever its heads and dtype, also on
+ * several streams at once (they only read it), each ordered after the prepare;
+ * *plan (host memory) only names the workspace, nothing is read back.
+ * cu_seqlens is not read again. A sequence whose offsets decrease or leave
+ * [0, tokens] is MGB_ERR_INDEX and counts as empty.
+ *
+ * mgb_attention_packed_fwd: q [tokens, nq*d], k, v [tokens, nkv*d], row strides
+ * ld_q, ld_kv (e.g. the columns of one fused qkv buffer), o [tokens, nq*d] (row
+ * stride ld_o; not overlapping the inputs), lse [nq, tokens] float32 or NULL.
+ * dtype bf16 or float32, head_dim 64 or 128. Sums and softmax statistics are
+ * float32; in bf16 the weights are rounded to bf16 before they multiply V.
+ * Results repeat bit for bit. */
+typedef struct {
+  int32_t n_seqs, tokens, causal;
+  void* ws;
+  size_t ws_bytes;
+} mgb_attention_packed_plan;
+
+size_t mgb_attention_packed_ws_bytes(int32_t n_seqs, int32_t tokens);
+mgb_status mgb_attention_packed_prepare(int32_t n_seqs, int32_t tokens, int32_t causal,
+                                        const int32_t* cu_seqlens, void* ws, size_t ws_bytes,
+                                        mgb_attention_packed_plan* plan, void* stream);
+mgb_status mgb_attention_packed_fwd(const mgb_attention_packed_plan* plan, int32_t n_q_heads,
+                                    int32_t n_kv_heads, int32_t head_dim, int32_t dtype,
+                                    const void* q, const void* k, const void* v, int64_t ld_q,
+                                    int64_t ld_kv, void* o, int64_t ld_o, float* lse, void* stream);
+
 /* Attention of one new token per sequence over the cache. Per sequence s and
  * query head h: o[s, h] = softmax(q[s, h] K_g^T / sqrt(d)) V_g over the first
  * seq_lens[s] cached tokens (the new one included). Length 0 (padding): o is

@@ -109,6 +109,11 @@ class AttentionDecodePlan(ctypes.Structure):
         ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
 
 
+class AttentionPackedPlan(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("tokens", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+
+
 class GemmDesc(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("a_major", ctypes.c_int32), ("b_major", ctypes.c_int32),
@@ -172,6 +177,10 @@ def load() -> ctypes.CDLL:
                                              ctypes.POINTER(AttentionDecodePlan), P],
             "mgb_attention_decode": [ctypes.POINTER(AttentionDecodePlan), ctypes.POINTER(KVCache), P,
                                      I64, P, I64, P, P],
+            "mgb_attention_packed_prepare": [I32, I32, I32, P, P, SZ,
+                                             ctypes.POINTER(AttentionPackedPlan), P],
+            "mgb_attention_packed_fwd": [ctypes.POINTER(AttentionPackedPlan), I32, I32, I32, I32, P, P,
+                                         P, I64, I64, P, I64, P, P],
             "mgb_device_status": [P],
             "mgb_selftest_wait_timeout": [U64, P],
         }
@@ -195,6 +204,8 @@ def load() -> ctypes.CDLL:
         lib.mgb_embedding_bwd_ws_bytes.restype = SZ
         lib.mgb_attention_decode_ws_bytes.argtypes = [I32, I32, I32, I32]
         lib.mgb_attention_decode_ws_bytes.restype = SZ
+        lib.mgb_attention_packed_ws_bytes.argtypes = [I32, I32]
+        lib.mgb_attention_packed_ws_bytes.restype = SZ
         lib.mgb_launch_count.argtypes = []
         lib.mgb_launch_count.restype = ctypes.c_uint64
         lib.mgb_profile_enable.argtypes = [I32]
@@ -508,6 +519,28 @@ def mgb_attention_decode(plan: AttentionDecodePlan, cache: KVCache, q, ld_q, o, 
     _check(load().mgb_attention_decode(ctypes.byref(plan), ctypes.byref(cache), _ptr(q), ld_q,
                                        _ptr(o), ld_o, _ptr(lse), _stream(stream)),
            "mgb_attention_decode")
+
+
+def mgb_attention_packed_ws_bytes(n_seqs: int, tokens: int) -> int:
+    return load().mgb_attention_packed_ws_bytes(n_seqs, tokens)
+
+
+def mgb_attention_packed_prepare(n_seqs, tokens, causal, cu_seqlens, ws,
+                                 stream=None) -> AttentionPackedPlan:
+    """The batch's plan (host struct, keeps `ws` alive) for mgb_attention_packed_fwd."""
+    plan = AttentionPackedPlan()
+    plan.tensors = (ws,)
+    _check(load().mgb_attention_packed_prepare(n_seqs, tokens, int(causal), _ptr(cu_seqlens), _ptr(ws),
+                                               ws.numel() * ws.element_size(), ctypes.byref(plan),
+                                               _stream(stream)), "mgb_attention_packed_prepare")
+    return plan
+
+
+def mgb_attention_packed_fwd(plan: AttentionPackedPlan, n_q_heads, n_kv_heads, head_dim, dtype, q, k,
+                             v, ld_q, ld_kv, o, ld_o, lse=None, stream=None) -> None:
+    _check(load().mgb_attention_packed_fwd(ctypes.byref(plan), n_q_heads, n_kv_heads, head_dim, dtype,
+                                           _ptr(q), _ptr(k), _ptr(v), ld_q, ld_kv, _ptr(o), ld_o,
+                                           _ptr(lse), _stream(stream)), "mgb_attention_packed_fwd")
 
 
 def mgb_memcpy_async(dst, src, nbytes: int, stream=None) -> None:

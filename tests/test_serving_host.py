@@ -154,11 +154,71 @@ def test_decode_rejects_bad_arguments(lib, kw, status):
     assert _decode(lib, **kw) == status
 
 
+def test_packed_workspace(lib):
+    assert lib.mgb_attention_packed_ws_bytes(-1, 5) == 0 and lib.mgb_attention_packed_ws_bytes(2, -1) == 0
+    # an entry per 128 (256) rows and sequence, bounded by the rows
+    assert lib.mgb_attention_packed_ws_bytes(1 << 20, 10) < 20 << 20
+    assert lib.mgb_attention_packed_ws_bytes(8, 1 << 20) >= 16 * ((1 << 13) + (1 << 12))
+
+
+@pytest.mark.parametrize("a,status", [
+    ((-1, 9, 1, P, P), mgb.MGB_ERR_INVALID_ARG), ((2, -9, 1, P, P), mgb.MGB_ERR_INVALID_ARG),
+    ((2, 9, 2, P, P), mgb.MGB_ERR_INVALID_ARG), ((2, 9, 1, None, P), mgb.MGB_ERR_INVALID_ARG),
+    ((2, 9, 1, P, None), mgb.MGB_ERR_INVALID_ARG), ((2, 9, 1, P + 2, P), mgb.MGB_ERR_MISALIGNED),
+    ((2, 9, 1, P, P + 4), mgb.MGB_ERR_MISALIGNED),
+])
+def test_packed_prepare_rejects(lib, a, status):
+    plan = mgb.AttentionPackedPlan()
+    n, tokens, causal, cu, ws = a
+    assert lib.mgb_attention_packed_prepare(n, tokens, causal, cu, ws, 1 << 30, ctypes.byref(plan),
+                                            None) == status
+    assert plan.ws is None
+
+
+def test_packed_prepare_small_workspace_and_no_plan(lib):
+    plan = mgb.AttentionPackedPlan()
+    size = lib.mgb_attention_packed_ws_bytes(2, 900)
+    assert lib.mgb_attention_packed_prepare(2, 900, 1, P, P, size - 1, ctypes.byref(plan),
+                                            None) == mgb.MGB_ERR_WORKSPACE_TOO_SMALL
+    assert lib.mgb_attention_packed_prepare(2, 9, 1, P, P, 1 << 30, None, None) == mgb.MGB_ERR_INVALID_ARG
+
+
+def _packed(lib, plan=None, nq=4, nkv=2, d=64, dtype=mgb.MGB_BF16, **kw):
+    p = dict(n_seqs=3, tokens=50, causal=1, ws=P, ws_bytes=1 << 30)
+    p.update(plan or {})
+    a = dict(q=P, k=P, v=P, ld_q=512, ld_kv=512, o=2 * P, ld_o=256, lse=P)
+    a.update(kw)
+    return lib.mgb_attention_packed_fwd(ctypes.byref(mgb.AttentionPackedPlan(**p)), nq, nkv, d, dtype,
+                                        a["q"], a["k"], a["v"], a["ld_q"], a["ld_kv"], a["o"], a["ld_o"],
+                                        a["lse"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(plan=dict(ws=None)), mgb.MGB_ERR_INVALID_ARG), (dict(plan=dict(tokens=-1)), mgb.MGB_ERR_INVALID_ARG),
+    (dict(plan=dict(causal=3)), mgb.MGB_ERR_INVALID_ARG),
+    (dict(plan=dict(ws_bytes=100)), mgb.MGB_ERR_WORKSPACE_TOO_SMALL),
+    (dict(plan=dict(ws=P + 8)), mgb.MGB_ERR_MISALIGNED),
+    (dict(nq=0), mgb.MGB_ERR_INVALID_ARG), (dict(nkv=3), mgb.MGB_ERR_INVALID_ARG),
+    (dict(nkv=0), mgb.MGB_ERR_INVALID_ARG), (dict(dtype=2), mgb.MGB_ERR_INVALID_ARG),
+    (dict(d=96), mgb.MGB_ERR_UNSUPPORTED), (dict(d=32, dtype=mgb.MGB_F32), mgb.MGB_ERR_UNSUPPORTED),
+    (dict(plan=dict(tokens=1 << 30), nq=1 << 20, nkv=1, ld_q=1 << 27, ld_o=1 << 27), mgb.MGB_ERR_UNSUPPORTED),
+    (dict(ld_q=248), mgb.MGB_ERR_INVALID_ARG), (dict(ld_kv=120), mgb.MGB_ERR_INVALID_ARG),
+    (dict(ld_o=248), mgb.MGB_ERR_INVALID_ARG), (dict(q=None), mgb.MGB_ERR_INVALID_ARG),
+    (dict(k=None), mgb.MGB_ERR_INVALID_ARG), (dict(v=None), mgb.MGB_ERR_INVALID_ARG),
+    (dict(o=None), mgb.MGB_ERR_INVALID_ARG), (dict(ld_q=516), mgb.MGB_ERR_MISALIGNED),
+    (dict(ld_kv=516), mgb.MGB_ERR_MISALIGNED), (dict(ld_o=260), mgb.MGB_ERR_MISALIGNED),
+    (dict(v=P + 8), mgb.MGB_ERR_MISALIGNED), (dict(lse=P + 2), mgb.MGB_ERR_MISALIGNED),
+])
+def test_packed_rejects_bad_arguments(lib, kw, status):
+    assert _packed(lib, **kw) == status
+
+
 def test_fault_injection_and_status_text(lib, monkeypatch):
     assert mgb.status_string(mgb.MGB_ERR_INDEX) not in ("", "unknown status")
     monkeypatch.setenv("MGB_FAULT", "validate")
     assert _append(lib) == mgb.MGB_ERR_INVALID_ARG
     assert _decode(lib) == mgb.MGB_ERR_INVALID_ARG
+    assert _packed(lib) == mgb.MGB_ERR_INVALID_ARG
 
 
 def test_kv_cache_helper_checks_its_tensors():
