@@ -5,14 +5,16 @@
 // key and value is used once per query head of its group).
 //
 // Work is cut into units: 64 consecutive cached tokens of one (sequence, KV
-// head, group of at most 16 query heads). Units are numbered sequence by
-// sequence, head by head, in token order, and dealt out as one contiguous
-// range of `chunk` units per CTA, so every CTA gets the same number whatever the
-// lengths are. An item (all units of one sequence and head group) that lies in
-// one range is finished there. An item that spans CTAs is split: each CTA
-// leaves its unnormalised sums, maximum and row sum in the workspace, and the
-// last one to arrive (a counter per first CTA of a split item) joins the parts
-// in CTA order, so results do not depend on who was last.
+// head, group of at most 16 query heads). An item is all units of one
+// sequence and head group. Items stand one behind the other on a cost axis,
+// sequence by sequence, head by head: an item with n units takes n UNIT + ITEM,
+// its unit t beginning at t UNIT (ITEM is the fixed cost of an item: its
+// queries, the join of the warps, the store). CTA c takes the units that begin
+// in [c chunk, (c + 1) chunk): the same cost for every CTA whatever the lengths
+// are. An item that lies in one range is finished there. An item that spans
+// CTAs is split: each CTA leaves its unnormalised sums, maximum and row sum in
+// the workspace, and the last one to arrive (a counter per first CTA of a split
+// item) joins the parts in CTA order, so results do not depend on who was last.
 //
 // The prepare kernel derives the ranges from the lengths (they are the same
 // for every layer of a model's step) and zeroes the counters; each split item
@@ -24,9 +26,12 @@
 // a private ring in shared memory by 16-byte asynchronous copies, so the main
 // loop has no CTA-wide barrier, any page size and any page layout works, and
 // tokens past the length are never read (zero fill).
-//   bf16: products on mma.sync m16n8k16 with the group's query heads as the 16
-//   rows. One query token per sequence gives at most 16 rows, so the products
-//   are a small share of the time and operands come straight from registers.
+//   bf16: products on mma.sync m16n8k16, transposed: S^T = K Q^T with 16 tokens
+//   as the rows and the query heads as the 8 (2 x 8) columns, and O^T = V^T P^T
+//   with d as the rows. One query token per sequence leaves at most 16 query
+//   heads per item, so the products are a small share of the time; with the
+//   heads on the narrow side, none of them is spent on rows that do not exist
+//   for groups of 8 or fewer that are a multiple of 8.
 //   float32: FFMA with a lane per (token, quarter of d) for the scores and a
 //   lane per 4 (2) columns for the output.
 #include "common.cuh"
@@ -40,23 +45,32 @@ constexpr int WARPS = 4;
 constexpr int NT = WARPS * 32;
 constexpr int TK = 64;                 // tokens per unit
 constexpr int MAXR = 16;               // query heads per item
-constexpr int NCTA = 304;              // two per SM of a GB300
-constexpr int MIN_CHUNK = 2;           // units per CTA at least
+constexpr int SMS = 152;               // of a GB300 (fewer: the same ranges, in more waves)
+__host__ __device__ constexpr int ctas_per_sm(int d) { return d == 64 ? 3 : 2; }
+constexpr int UNIT = 4;                // cost of a unit
+#ifndef ITEMC
+#define ITEMC 8
+#endif
+constexpr int ITEM = ITEMC;                // fixed cost of an item
+constexpr int MIN_CHUNK = 2 * UNIT;    // of a CTA (at least UNIT: no CTA between two others is empty)
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float TAU = 8.0f;            // the reference maximum moves in steps above this (log2 units)
 
 struct Header {
-  int64_t units;
-  int32_t chunk, pad;
+  int64_t cost;  // of all items
+  int64_t chunk;
 };
 struct Start {
-  int32_t s, h, t, pad;  // first unit of a CTA: sequence, head group, token tile
+  int64_t at;       // where the item of the CTA's first unit begins on the cost axis
+  int32_t s, h, t;  // the unit: sequence, head group, token tile
+  int32_t pad;
 };
 
 struct Layout {
   size_t header, start, counter, len, prefix, ml, part, total;
   int rows, groups;  // query heads per item at most; items per sequence
+  int ctas;
 };
 
 Layout make_layout(int n, int nq, int nkv, int d) {
@@ -67,22 +81,24 @@ Layout make_layout(int n, int nq, int nkv, int d) {
   l.rows = (G + per - 1) / per;
   l.groups = nkv * ((G + l.rows - 1) / l.rows);
   l.header = take(sizeof(Header));
-  l.start = take(sizeof(Start) * NCTA);
-  l.counter = take(4 * NCTA);
+  l.ctas = SMS * ctas_per_sm(d);
+  l.start = take(sizeof(Start) * l.ctas);
+  l.counter = take(4 * (size_t)l.ctas);
   l.len = take(4 * (size_t)n);
   l.prefix = take(8 * ((size_t)n + 1));
-  l.ml = take(8 * (size_t)2 * NCTA * l.rows);
-  l.part = take(4 * (size_t)2 * NCTA * l.rows * d);
+  l.ml = take(8 * (size_t)2 * l.ctas * l.rows);
+  l.part = take(4 * (size_t)2 * l.ctas * l.rows * d);
   l.total = o;
   return l;
 }
 
+__host__ __device__ inline int64_t cost_of(int tiles) { return (int64_t)tiles * UNIT + ITEM; }
 __host__ __device__ inline int tiles_of(int len) { return len > TK ? (int)(((int64_t)len + TK - 1) / TK) : 1; }
 
 // ---------------------------------------------------------------- prepare
-// One block: lengths copied (negative ones count as 0 and are an error), units
-// summed up, the ranges' first units found, counters zeroed.
-__global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups, const int32_t* lens,
+// One block: lengths copied (negative ones count as 0 and are an error), costs
+// (per head group) summed up, the ranges' first units found, counters zeroed.
+__global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups, int ctas, const int32_t* lens,
                                                               Header* hdr, Start* start,
                                                               uint32_t* counter, int32_t* len_out,
                                                               int64_t* prefix, int* err) {
@@ -90,7 +106,7 @@ __global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups,
   __shared__ int64_t carry_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t carry = 0;
-  for (int i = tid; i < NCTA; i += 1024) counter[i] = 0;
+  for (int i = tid; i < ctas; i += 1024) counter[i] = 0;
   for (int base = 0; base < n; base += 1024) {
     const int i = base + tid;
     int64_t v = 0;
@@ -101,7 +117,7 @@ __global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups,
         len = 0;
       }
       len_out[i] = len;
-      v = tiles_of(len);
+      v = cost_of(tiles_of(len));
     }
     int64_t x = v;
 #pragma unroll
@@ -128,24 +144,34 @@ __global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups,
   }
   if (tid == 0) prefix[n] = carry;
   __syncthreads();
-  const int64_t units = carry * groups;
-  int64_t chunk = (units + NCTA - 1) / NCTA;
+  const int64_t cost = carry * groups;
+  int64_t chunk = (cost + ctas - 1) / ctas;
   if (chunk < MIN_CHUNK) chunk = MIN_CHUNK;
-  if (tid == 0) *hdr = Header{units, (int32_t)chunk, 0};
-  for (int c = tid; c < NCTA; c += 1024) {
+  if (tid == 0) *hdr = Header{cost, chunk};
+  for (int c = tid; c < ctas; c += 1024) {
     const int64_t u = c * chunk;
-    Start st{0, 0, 0, 0};
-    if (u < units) {
+    Start st{cost, n, 0, 0, 0};
+    if (u < cost) {
       int lo = 0, hi = n - 1;  // the largest s with prefix[s] * groups <= u
       while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
         if (prefix[mid] * groups <= u) lo = mid;
         else hi = mid - 1;
       }
-      const int64_t nt = prefix[lo + 1] - prefix[lo], r = u - prefix[lo] * groups;
+      const int64_t per = prefix[lo + 1] - prefix[lo], r = u - prefix[lo] * groups;
+      const int64_t h = r / per, t = (r - h * per + UNIT - 1) / UNIT;
+      st.at = prefix[lo] * groups + h * per;
       st.s = lo;
-      st.h = (int)(r / nt);
-      st.t = (int)(r % nt);
+      st.h = (int)h;
+      if (t < (per - ITEM) / UNIT) {
+        st.t = (int)t;
+      } else {  // the item's last unit begins before: the next item
+        st.at += per;
+        if (++st.h == groups) {
+          st.h = 0;
+          ++st.s;
+        }
+      }
     }
     start[c] = st;
   }
@@ -158,8 +184,8 @@ struct Params {
   const Start* start;
   uint32_t* counter;
   const int32_t* len;
-  float2* ml;    // [2 NCTA][rows] (maximum, row sum) of a part
-  float* part;   // [2 NCTA][rows][d]
+  float2* ml;    // [2 CTAs][rows] (maximum, row sum) of a part
+  float* part;   // [2 CTAs][rows][d]
   const void *k, *v;
   const int32_t* table;
   int64_t s_page, s_tok, s_head, ld_table;
@@ -205,11 +231,19 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// 8 x 8 matrix of 16-bit values, row lane / 4, columns 2 (lane % 4) + {0, 1} -> its transpose
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+
 // Position in a CTA's range of units.
 struct Cursor {
+  int64_t at;  // the item on the cost axis
   int s, h, t, nt, len, next_len;
   __device__ void init(const Params& p, const Start& st) {
-    s = st.s; h = st.h; t = st.t;
+    at = st.at; s = st.s; h = st.h; t = st.t;
     len = p.len[s];
     next_len = s + 1 < p.n ? p.len[s + 1] : 0;
     nt = tiles_of(len);
@@ -218,6 +252,7 @@ struct Cursor {
   __device__ void next(const Params& p) {
     if (++t < nt) return;
     t = 0;
+    at += cost_of(nt);
     if (++h < p.groups) return;
     h = 0;
     ++s;
@@ -225,9 +260,10 @@ struct Cursor {
     nt = tiles_of(len);
     next_len = s + 1 < p.n ? p.len[s + 1] : 0;
   }
+  __device__ bool before(int64_t end) const { return at + (int64_t)t * UNIT < end; }
 };
 
-template <typename T, int D>
+template <typename T, int D, int NR>
 struct Cfg {
   static constexpr int ES = sizeof(T);
   static constexpr int SK = ES == 2 ? 16 : 8;        // tokens per warp and stage
@@ -235,14 +271,15 @@ struct Cfg {
   static constexpr int ROW = D * ES;                 // bytes of a token's vector
   static constexpr int CH = ROW / 16;                // 16-byte chunks of it
   static constexpr int KV = SK * ROW;                // bytes of a stage's keys (or values)
-  static constexpr int STAGES = D == 128 ? 3 : 6;
+  static constexpr int STAGES = D == 128 ? 3 : 4;
   static constexpr int RING = STAGES * 2 * KV;       // per warp
   static constexpr int MR = ES == 2 ? 8 : 4;         // rows joined at a time
-  static constexpr int OFF_JOIN = WARPS * RING;      // [WARPS][MR][D] float
-  static constexpr int OFF_Q = OFF_JOIN + WARPS * MR * D * 4;  // float32: [MAXR][D]
-  static constexpr int OFF_ML = OFF_Q + (ES == 4 ? MAXR * D * 4 : 0);  // [WARPS][MAXR] float2
-  static constexpr int SMEM = OFF_ML + WARPS * MAXR * 8 + 16;
-  static_assert(SMEM <= 114 * 1024, "two CTAs per SM");
+  static constexpr int JS = D + 4;                   // row stride of the join buffer (floats)
+  static constexpr int OFF_JOIN = WARPS * RING;      // [WARPS][MR][JS] float
+  static constexpr int OFF_Q = OFF_JOIN + WARPS * MR * JS * 4;  // float32: [NR][D]
+  static constexpr int OFF_ML = OFF_Q + (ES == 4 ? NR * D * 4 : 0);  // [WARPS][MAXR] float2
+  static constexpr int SMEM = OFF_ML + WARPS * MAXR * 8;
+  static_assert((SMEM + 1024) * ctas_per_sm(D) <= 228 * 1024, "CTAs per SM");
 };
 
 // Shared-memory offset of chunk c of a stage's token row (rotated by the row
@@ -252,9 +289,10 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
   return (uint32_t)(row * CH + (c ^ (row & 7))) * 16u;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
-  using C = Cfg<T, D>;
+// NR: query heads per item at most
+template <typename T, int D, int NR>
+__global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params p) {
+  using C = Cfg<T, D, NR>;
   constexpr bool BF = sizeof(T) == 2;
   constexpr int ST = C::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -262,26 +300,24 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
   const int c = blockIdx.x;
   const Header hd = *p.hdr;
   const Start st0 = p.start[c];
-  const int64_t u0 = (int64_t)c * hd.chunk;
-  if (u0 >= hd.units) return;
-  const int64_t u1 = u0 + hd.chunk < hd.units ? u0 + hd.chunk : hd.units;
+  const int64_t end = min((int64_t)(c + 1) * hd.chunk, hd.cost);
+  if (st0.s >= p.n || st0.at + (int64_t)st0.t * UNIT >= end) return;  // no unit begins in the range
   const uint32_t ring = smem_u32(smem) + warp * C::RING;
   float* join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
   float* sq = reinterpret_cast<float*>(smem + C::OFF_Q);
   float2* sml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-  int* flag = reinterpret_cast<int*>(smem + C::OFF_ML + WARPS * MAXR * 8);
+  int* flag = reinterpret_cast<int*>(sml);  // once sml is read
 
   // ---------------- loader: a cursor one stage ahead of the copies, whose
   // page number is in flight while the previous stage's copies are issued
   Cursor ld;
   ld.init(p, st0);
-  int64_t ld_u = u0;
   int ld_sub = 0, ld_n = 0;
   int pg = 0, slot = 0, hkv = 0;
   bool on = false, look = false;
   auto peek = [&]() {  // request the page of this lane's token of the next stage
     on = false;
-    look = ld_u < u1;
+    look = ld.before(end);
     if (!look) return;
     const int key = ld.t * TK + ld_sub * (WARPS * C::SK) + warp * C::SK + (lane % C::SK);
     hkv = ld.h / p.per_kv;
@@ -294,7 +330,6 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
     }
     if (++ld_sub == C::SUB) {
       ld_sub = 0;
-      ++ld_u;
       ld.next(p);
     }
   };
@@ -304,7 +339,6 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
       if (on && !ok) record_error(p.err, kErrIndex);
       const int64_t off = ok ? pg * p.s_page + slot * p.s_tok + hkv * p.s_head : -1;
       const uint32_t dst = ring + (ld_n % ST) * 2 * C::KV;
-      constexpr int RPI = 32 / C::CH;  // rows per pass of the warp (0: half a row)
       if (__any_sync(0xffffffffu, ok)) {
 #pragma unroll
         for (int i = 0; i < C::SK * C::CH / 32; ++i) {
@@ -317,7 +351,6 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
           cp_async16(at + C::KV, vs, ro >= 0);
         }
       }
-      (void)RPI;
     }
     cp_async_commit();
     ++ld_n;
@@ -334,25 +367,27 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
     const int first = (h % p.per_kv) * p.rows + r;
     return r < p.rows && first < p.G ? (h / p.per_kv) * p.G + first : -1;
   };
-  constexpr int NQ = BF ? D / 16 * 4 : MAXR * D / 4 / NT * 4;
+  constexpr int HT = BF ? NR / 8 : 1;  // bf16: tiles of 8 query heads
+  constexpr int NQ = BF ? D / 16 * 2 * HT : (NR * D / 4 + NT - 1) / NT * 4;
   uint32_t qn[NQ];
   auto request_q = [&](int s, int h) {
     const T* qs = static_cast<const T*>(p.q) + s * p.ld_q;
     if constexpr (BF) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int head = q_row(s, h, (lane >> 2) + 8 * half);
+      for (int ht = 0; ht < HT; ++ht) {
+        const int head = q_row(s, h, (lane >> 2) + 8 * ht);
         const T* x = qs + (int64_t)(head < 0 ? 0 : head) * D + (lane & 3) * 2;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          qn[kk * 4 + half] = head < 0 ? 0u : *reinterpret_cast<const uint32_t*>(x + kk * 16);
-          qn[kk * 4 + 2 + half] = head < 0 ? 0u : *reinterpret_cast<const uint32_t*>(x + kk * 16 + 8);
+          qn[(kk * HT + ht) * 2] = head < 0 ? 0u : *reinterpret_cast<const uint32_t*>(x + kk * 16);
+          qn[(kk * HT + ht) * 2 + 1] =
+              head < 0 ? 0u : *reinterpret_cast<const uint32_t*>(x + kk * 16 + 8);
         }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < NQ / 4; ++i) {
-        const int e = (i * NT + tid) * 4, head = q_row(s, h, e / D);
+        const int e = (i * NT + tid) * 4, head = e < NR * D ? q_row(s, h, e / D) : -1;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (head >= 0) x = *reinterpret_cast<const float4*>(qs + (int64_t)head * D + e % D);
         qn[4 * i] = __float_as_uint(x.x);
@@ -364,12 +399,10 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
   };
   request_q(cu.s, cu.h);
 
-  int64_t u = u0;
   int n_use = 0;  // stages consumed
-  while (u < u1) {
-    const int s = cu.s, h = cu.h, len = cu.len, nt = cu.nt, t0 = cu.t;
-    const int64_t item0 = u - t0;                       // the item's first unit
-    const int64_t end = item0 + nt < u1 ? item0 + nt : u1;
+  while (cu.before(end)) {
+    const int s = cu.s, h = cu.h, len = cu.len, nt = cu.nt;
+    const int64_t at = cu.at;
     const int rows = min(p.rows, p.G - (h % p.per_kv) * p.rows);
     uint32_t qa[BF ? NQ : 1];
     if constexpr (BF) {
@@ -378,7 +411,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
     } else {
 #pragma unroll
       for (int i = 0; i < NQ / 4; ++i)
-        *reinterpret_cast<float4*>(sq + (i * NT + tid) * 4) =
+        if ((i * NT + tid) * 4 < NR * D) *reinterpret_cast<float4*>(sq + (i * NT + tid) * 4) =
             make_float4(__uint_as_float(qn[4 * i]), __uint_as_float(qn[4 * i + 1]),
                         __uint_as_float(qn[4 * i + 2]), __uint_as_float(qn[4 * i + 3]));
       __syncthreads();
@@ -387,15 +420,16 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
       Cursor nx = cu;
       nx.t = nx.nt - 1;
       nx.next(p);
-      if (item0 + nt < u1) request_q(nx.s, nx.h);
+      if (nx.before(end)) request_q(nx.s, nx.h);
     }
 
-    // bf16: rows lane / 4 and + 8, columns 8 n + 2 (lane % 4) + {0, 1}
-    // float32: all rows, columns lane * (D / 32) ..
+    // bf16: acc[i] holds d = 16 (i / HT) + lane / 4 (+ 8 in the upper two) of
+    // heads 8 (i % HT) + 2 (lane % 4) + {0, 1}; m, l those heads' (l of the
+    // lane's tokens only). float32: all rows, columns lane * (D / 32) ..
     constexpr int CPL = D / 32;
-    constexpr int NO = BF ? D / 8 : MAXR;
+    constexpr int NO = BF ? D / 16 * HT : NR;
     constexpr int NI = BF ? 4 : CPL;
-    constexpr int NM = BF ? 2 : MAXR;
+    constexpr int NM = BF ? 2 * HT : NR;
     float acc[NO][NI], m[NM], l[NM];
 #pragma unroll
     for (int i = 0; i < NO; ++i)
@@ -404,7 +438,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
 #pragma unroll
     for (int i = 0; i < NM; ++i) m[i] = -INFINITY, l[i] = 0.0f;
 
-    for (; u < end; ++u) {
+    for (bool more = true; more;) {
 #pragma unroll
       for (int sub = 0; sub < C::SUB; ++sub) {
         cp_async_wait<ST - 2>();
@@ -416,65 +450,68 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
         const int left = len - key0;  // visible tokens of the slice
         if (left <= 0) continue;
         if constexpr (BF) {
-          float sc[2][4] = {};
+          float sc[HT][4] = {};  // token lane / 4 (+ 8 in the upper two), heads 2 (lane % 4) + {0, 1}
           const int mi = lane >> 3, r8 = lane & 7;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t b[4];
-            ldsm4(sk + chunk_at<C::CH>((mi >> 1) * 8 + r8, 2 * kk + (mi & 1)), b);
-            const uint32_t a[4] = {qa[kk * 4], qa[kk * 4 + 1], qa[kk * 4 + 2], qa[kk * 4 + 3]};
-            mma_bf16(sc[0], a, b[0], b[1]);
-            mma_bf16(sc[1], a, b[2], b[3]);
+            uint32_t a[4];
+            ldsm4(sk + chunk_at<C::CH>((mi & 1) * 8 + r8, 2 * kk + (mi >> 1)), a);
+#pragma unroll
+            for (int ht = 0; ht < HT; ++ht)
+              mma_bf16(sc[ht], a, qa[(kk * HT + ht) * 2], qa[(kk * HT + ht) * 2 + 1]);
           }
-          float mx[2] = {-INFINITY, -INFINITY};
+          uint32_t pb[HT][2];
+          bool up[NM];
+          float mx[NM];
+          bool any = false;
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int ht = 0; ht < HT; ++ht) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = 8 * n + 2 * (lane & 3) + (e & 1);
-              sc[n][e] = key < left ? sc[n][e] * p.sl2 : -INFINITY;
-              mx[e >> 1] = fmaxf(mx[e >> 1], sc[n][e]);
+            for (int e = 0; e < 4; ++e)
+              sc[ht][e] = (lane >> 2) + (e >> 1) * 8 < left ? sc[ht][e] * p.sl2 : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float x = fmaxf(sc[ht][i], sc[ht][i + 2]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+              mx[2 * ht + i] = x;
+              up[2 * ht + i] = x > m[2 * ht + i] + TAU;
+              any |= up[2 * ht + i];
             }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
           }
           // the reference moves only when it must: P stays below 2^TAU
-          const bool up0 = mx[0] > m[0] + TAU, up1 = mx[1] > m[1] + TAU;
-          if (__any_sync(0xffffffffu, up0 || up1)) {
-            const float a0 = up0 ? exp2f(m[0] - mx[0]) : 1.0f;
-            const float a1 = up1 ? exp2f(m[1] - mx[1]) : 1.0f;
-            if (up0) m[0] = mx[0];
-            if (up1) m[1] = mx[1];
-            l[0] *= a0;
-            l[1] *= a1;
+          if (__any_sync(0xffffffffu, any)) {
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              acc[n][0] *= a0;
-              acc[n][1] *= a0;
-              acc[n][2] *= a1;
-              acc[n][3] *= a1;
+            for (int i = 0; i < NM; ++i) {
+              const float a = up[i] ? exp2f(m[i] - mx[i]) : 1.0f;
+              if (up[i]) m[i] = mx[i];
+              l[i] *= a;
+#pragma unroll
+              for (int nn = 0; nn < D / 16; ++nn) {
+                acc[nn * HT + i / 2][i & 1] *= a;
+                acc[nn * HT + i / 2][2 + (i & 1)] *= a;
+              }
             }
           }
-          const float r0 = m[0] == -INFINITY ? 0.0f : m[0], r1 = m[1] == -INFINITY ? 0.0f : m[1];
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int ht = 0; ht < HT; ++ht) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              sc[n][e] = ex2_ftz(sc[n][e] - (e < 2 ? r0 : r1));
-              l[e >> 1] += sc[n][e];
+              const int i = 2 * ht + (e & 1);
+              sc[ht][e] = ex2_ftz(sc[ht][e] - (m[i] == -INFINITY ? 0.0f : m[i]));
+              l[i] += sc[ht][e];
             }
-          // P as bf16 (the row sums take it unrounded): relative error 2^-9 per
-          // weight, below the output's own rounding after averaging
-          const uint32_t pa[4] = {pack_bf16x2(sc[0][0], sc[0][1]), pack_bf16x2(sc[0][2], sc[0][3]),
-                                  pack_bf16x2(sc[1][0], sc[1][1]), pack_bf16x2(sc[1][2], sc[1][3])};
+            // P as bf16 (the row sums take it unrounded): relative error 2^-8 at
+            // most per weight, below the output's own rounding after averaging
+            pb[ht][0] = transpose8x8(pack_bf16x2(sc[ht][0], sc[ht][1]));
+            pb[ht][1] = transpose8x8(pack_bf16x2(sc[ht][2], sc[ht][3]));
+          }
 #pragma unroll
           for (int nn = 0; nn < D / 16; ++nn) {
-            uint32_t b[4];
-            ldsm4_t(sv + chunk_at<C::CH>((mi & 1) * 8 + r8, 2 * nn + (mi >> 1)), b);
-            mma_bf16(acc[2 * nn], pa, b[0], b[1]);
-            mma_bf16(acc[2 * nn + 1], pa, b[2], b[3]);
+            uint32_t a[4];
+            ldsm4_t(sv + chunk_at<C::CH>((mi >> 1) * 8 + r8, 2 * nn + (mi & 1)), a);
+#pragma unroll
+            for (int ht = 0; ht < HT; ++ht) mma_bf16(acc[nn * HT + ht], a, pb[ht][0], pb[ht][1]);
           }
         } else {
           const int key = lane & 7, part = lane >> 3;  // token, quarter of d
@@ -484,9 +521,9 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
             asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
                          : "=f"(kx[i].x), "=f"(kx[i].y), "=f"(kx[i].z), "=f"(kx[i].w)
                          : "r"(sk + chunk_at<C::CH>(key, i * 4 + part)));
-          float pr[MAXR];
+          float pr[NR];
 #pragma unroll
-          for (int r = 0; r < MAXR; ++r) {
+          for (int r = 0; r < NR; ++r) {
             pr[r] = 0.0f;
             if (r >= rows) continue;
             float d0 = 0.0f, d1 = 0.0f;
@@ -526,7 +563,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
             else
               asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(vx[0]), "=f"(vx[1]) : "r"(va));
 #pragma unroll
-            for (int r = 0; r < MAXR; ++r) {
+            for (int r = 0; r < NR; ++r) {
               if (r >= rows) continue;
               const float w = __shfl_sync(0xffffffffu, pr[r], kx2);
 #pragma unroll
@@ -536,19 +573,20 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
         }
       }
       cu.next(p);
+      more = cu.at == at && cu.before(end);
     }
 
     // ---------------- the item's units in this CTA are done: join the warps
     if constexpr (BF) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        if ((lane & 3) == 0) sml[warp * MAXR + (lane >> 2) + 8 * i] = make_float2(m[i], l[i]);
+      for (int i = 0; i < NM; ++i) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+        if (lane < 4) sml[warp * MAXR + 8 * (i / 2) + 2 * lane + (i & 1)] = make_float2(m[i], l[i]);
       }
     } else {
 #pragma unroll
-      for (int r = 0; r < MAXR; ++r) {
+      for (int r = 0; r < NR; ++r) {
         if (r >= rows) continue;
         float x = l[r];
 #pragma unroll
@@ -568,10 +606,12 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
         if (x.x > -INFINITY) L += x.y * exp2f(x.x - M);
       }
     };
-    const bool whole = item0 >= u0 && item0 + nt <= u1;
-    const int cf = (int)(item0 / hd.chunk), cl = (int)((item0 + nt - 1) / hd.chunk);
-    // a CTA's first piece goes to part 2 c, a later one to 2 c + 1
-    auto part_of = [&](int cc) { return 2 * cc + ((int64_t)cc * hd.chunk < item0 ? 1 : 0); };
+    // first and last CTA of the item
+    const int64_t last = at + (int64_t)(nt - 1) * UNIT;
+    const bool whole = at >= (int64_t)c * hd.chunk && last < end;
+    const int cf = whole ? c : (int)(at / hd.chunk), cl = whole ? c : (int)(last / hd.chunk);
+    // part 2 c: the CTA's range begins at or inside the item; 2 c + 1: before it
+    auto part_of = [&](int cc) { return 2 * cc + ((int64_t)cc * hd.chunk < at ? 1 : 0); };
     const int my = part_of(c);
     const int head0 = (h / p.per_kv) * p.G + (h % p.per_kv) * p.rows;
     auto store_o = [&](int r, int col, float4 x) {
@@ -582,18 +622,25 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
         *reinterpret_cast<float4*>(o) = x;
     };
 #pragma unroll
-    for (int r0 = 0; r0 < MAXR; r0 += C::MR) {
+    for (int r0 = 0; r0 < NR; r0 += C::MR) {
       if (r0 >= rows) break;
       if (r0 > 0) __syncthreads();
       if constexpr (BF) {
-        const int r = lane >> 2, i = r0 / 8;
-        float M, L;
-        joined(r0 + r, M, L);
-        const float a = m[i] > -INFINITY ? exp2f(m[i] - M) : 0.0f;
+        const int ht = r0 / 8;
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-          *reinterpret_cast<float2*>(join + (warp * C::MR + r) * D + n * 8 + 2 * (lane & 3)) =
-              make_float2(acc[n][2 * i] * a, acc[n][2 * i + 1] * a);
+        for (int i = 0; i < 2; ++i) {
+          const int r = 2 * (lane & 3) + i;
+          if (r0 + r >= rows) continue;
+          float M, L;
+          joined(r0 + r, M, L);
+          const float mm = m[2 * ht + i], a = mm > -INFINITY ? exp2f(mm - M) : 0.0f;
+          float* x = join + (warp * C::MR + r) * C::JS + (lane >> 2);
+#pragma unroll
+          for (int nn = 0; nn < D / 16; ++nn) {
+            x[16 * nn] = acc[nn * HT + ht][i] * a;
+            x[16 * nn + 8] = acc[nn * HT + ht][2 + i] * a;
+          }
+        }
       } else {
 #pragma unroll
         for (int rr = 0; rr < C::MR; ++rr) {
@@ -604,17 +651,18 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
           const float a = m[r] > -INFINITY ? exp2f(m[r] - M) : 0.0f;
 #pragma unroll
           for (int j = 0; j < CPL; ++j)
-            join[(warp * C::MR + rr) * D + lane * CPL + j] = acc[r][j] * a;
+            join[(warp * C::MR + rr) * C::JS + lane * CPL + j] = acc[r][j] * a;
         }
       }
       __syncthreads();
       for (int e = tid * 4; e < C::MR * D; e += NT * 4) {
         const int r = r0 + e / D, col = e % D;
         if (r >= rows) break;
-        float4 x = *reinterpret_cast<const float4*>(join + e);
+        const float* jr = join + (r - r0) * C::JS + col;
+        float4 x = *reinterpret_cast<const float4*>(jr);
 #pragma unroll
         for (int w = 1; w < WARPS; ++w) {
-          const float4 y = *reinterpret_cast<const float4*>(join + w * C::MR * D + e);
+          const float4 y = *reinterpret_cast<const float4*>(jr + w * C::MR * C::JS);
           x.x += y.x;
           x.y += y.y;
           x.z += y.z;
@@ -688,15 +736,24 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const Params p) {
   cp_async_wait<0>();
 }
 
-template <typename T, int D>
+template <typename T, int D, int NR>
 mgb_status launch(const Params& p, cudaStream_t st) {
-  using C = Cfg<T, D>;
-  auto k = decode_kernel<T, D>;
+  using C = Cfg<T, D, NR>;
+  auto k = decode_kernel<T, D, NR>;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return MGB_ERR_CUDA;
   LaunchScope scope(PROF_ATTN_DECODE, st);
-  k<<<NCTA, NT, C::SMEM, st>>>(p);
+  k<<<SMS * ctas_per_sm(D), NT, C::SMEM, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? MGB_OK : MGB_ERR_CUDA;
+}
+
+// The smallest form that holds the item's query heads: fewer products, and
+// (float32, unrolled over the heads) code that stays in the instruction cache.
+template <typename T, int D>
+mgb_status launch_rows(const Params& p, cudaStream_t st) {
+  if constexpr (sizeof(T) == 4)
+    if (p.rows <= 4) return launch<T, D, 4>(p, st);
+  return p.rows <= 8 ? launch<T, D, 8>(p, st) : launch<T, D, 16>(p, st);
 }
 
 mgb_status check_shape(int n, int nq, int nkv, int d) {
@@ -737,7 +794,7 @@ mgb_status mgb_attention_decode_prepare(int32_t n_seqs, int32_t n_q_heads, int32
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     LaunchScope scope(PROF_ATTN_DECODE, st);
     decode_prepare_kernel<<<1, 1024, 0, st>>>(
-        n_seqs, l.groups, seq_lens, reinterpret_cast<Header*>(b + l.header),
+        n_seqs, l.groups, l.ctas, seq_lens, reinterpret_cast<Header*>(b + l.header),
         reinterpret_cast<Start*>(b + l.start), reinterpret_cast<uint32_t*>(b + l.counter),
         reinterpret_cast<int32_t*>(b + l.len), reinterpret_cast<int64_t*>(b + l.prefix), err);
     if (cudaGetLastError() != cudaSuccess) return MGB_ERR_CUDA;
@@ -785,8 +842,9 @@ mgb_status mgb_attention_decode(const mgb_attention_decode_plan* plan, const mgb
   p.err = device_error_word();
   if (p.err == nullptr) return MGB_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (c->dtype == MGB_BF16) return d == 64 ? launch<bf16, 64>(p, st) : launch<bf16, 128>(p, st);
-  return d == 64 ? launch<float, 64>(p, st) : launch<float, 128>(p, st);
+  if (c->dtype == MGB_BF16)
+    return d == 64 ? launch_rows<bf16, 64>(p, st) : launch_rows<bf16, 128>(p, st);
+  return d == 64 ? launch_rows<float, 64>(p, st) : launch_rows<float, 128>(p, st);
 }
 
 }  // extern "C"
