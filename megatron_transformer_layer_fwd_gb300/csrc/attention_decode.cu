@@ -11,7 +11,8 @@
 // its unit t beginning at t UNIT (ITEM is the fixed cost of an item: its
 // queries, the join of the warps, the store). CTA c takes the units that begin
 // in [c chunk, (c + 1) chunk): the same cost for every CTA whatever the lengths
-// are. An item that lies in one range is finished there. An item that spans
+// are. (All units of an item of at most WHOLE units count as beginning at its
+// start: splitting it would cost more than it evens out.) An item that lies in one range is finished there. An item that spans
 // CTAs is split: each CTA leaves its unnormalised sums, maximum and row sum in
 // the workspace, and the last one to arrive (a counter per first CTA of a split
 // item) joins the parts in CTA order, so results do not depend on who was last.
@@ -43,15 +44,13 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int NT = WARPS * 32;
-constexpr int TK = 64;                 // tokens per unit
 constexpr int MAXR = 16;               // query heads per item
 constexpr int SMS = 152;               // of a GB300 (fewer: the same ranges, in more waves)
 __host__ __device__ constexpr int ctas_per_sm(int d) { return d == 64 ? 3 : 2; }
+__host__ __device__ constexpr int unit_tokens(int d) { return d == 64 ? 128 : 64; }
 constexpr int UNIT = 4;                // cost of a unit
-#ifndef ITEMC
-#define ITEMC 8
-#endif
-constexpr int ITEM = ITEMC;                // fixed cost of an item
+constexpr int ITEM = 8;                // fixed cost of an item
+constexpr int WHOLE = 4;               // units of an item that is never split
 constexpr int MIN_CHUNK = 2 * UNIT;    // of a CTA (at least UNIT: no CTA between two others is empty)
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -64,7 +63,7 @@ struct Header {
 struct Start {
   int64_t at;       // where the item of the CTA's first unit begins on the cost axis
   int32_t s, h, t;  // the unit: sequence, head group, token tile
-  int32_t pad;
+  int32_t len, next_len, pad;  // lengths of sequences s and s + 1
 };
 
 struct Layout {
@@ -92,19 +91,26 @@ Layout make_layout(int n, int nq, int nkv, int d) {
   return l;
 }
 
+// where unit t of an item with n units begins on its part of the cost axis
+__host__ __device__ inline int64_t begin_of(int t, int n) { return n > WHOLE ? (int64_t)t * UNIT : 0; }
 __host__ __device__ inline int64_t cost_of(int tiles) { return (int64_t)tiles * UNIT + ITEM; }
-__host__ __device__ inline int tiles_of(int len) { return len > TK ? (int)(((int64_t)len + TK - 1) / TK) : 1; }
+// units of a sequence: at least one, so that an empty one gets its zeros
+__host__ __device__ inline int tiles_of(int len, int tk) {
+  return len > tk ? (int)(((int64_t)len + tk - 1) / tk) : 1;
+}
 
 // ---------------------------------------------------------------- prepare
 // One block: lengths copied (negative ones count as 0 and are an error), costs
 // (per head group) summed up, the ranges' first units found, counters zeroed.
-__global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups, int ctas, const int32_t* lens,
+__global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups, int ctas, int tk,
+                                                              const int32_t* lens,
                                                               Header* hdr, Start* start,
                                                               uint32_t* counter, int32_t* len_out,
                                                               int64_t* prefix, int* err) {
   __shared__ int64_t warp_sum[32];
   __shared__ int64_t carry_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();  // the attention kernel may start up; it waits for this one's end
   int64_t carry = 0;
   for (int i = tid; i < ctas; i += 1024) counter[i] = 0;
   for (int base = 0; base < n; base += 1024) {
@@ -117,7 +123,7 @@ __global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups,
         len = 0;
       }
       len_out[i] = len;
-      v = cost_of(tiles_of(len));
+      v = cost_of(tiles_of(len, tk));
     }
     int64_t x = v;
 #pragma unroll
@@ -150,7 +156,7 @@ __global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups,
   if (tid == 0) *hdr = Header{cost, chunk};
   for (int c = tid; c < ctas; c += 1024) {
     const int64_t u = c * chunk;
-    Start st{cost, n, 0, 0, 0};
+    Start st{cost, n, 0, 0, 0, 0, 0};
     if (u < cost) {
       int lo = 0, hi = n - 1;  // the largest s with prefix[s] * groups <= u
       while (lo < hi) {
@@ -159,11 +165,12 @@ __global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups,
         else hi = mid - 1;
       }
       const int64_t per = prefix[lo + 1] - prefix[lo], r = u - prefix[lo] * groups;
-      const int64_t h = r / per, t = (r - h * per + UNIT - 1) / UNIT;
+      const int64_t h = r / per, into = r - h * per, t = (into + UNIT - 1) / UNIT;
+      const int64_t nt = (per - ITEM) / UNIT;
       st.at = prefix[lo] * groups + h * per;
       st.s = lo;
       st.h = (int)h;
-      if (t < (per - ITEM) / UNIT) {
+      if (into == 0 || (nt > WHOLE && t < nt)) {
         st.t = (int)t;
       } else {  // the item's last unit begins before: the next item
         st.at += per;
@@ -172,6 +179,8 @@ __global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups,
           ++st.s;
         }
       }
+      if (st.s < n) st.len = len_out[st.s];
+      if (st.s + 1 < n) st.next_len = len_out[st.s + 1];
     }
     start[c] = st;
   }
@@ -238,15 +247,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return r;
 }
 
-// Position in a CTA's range of units.
+// Position in a CTA's range of units of TK tokens.
+template <int TK>
 struct Cursor {
   int64_t at;  // the item on the cost axis
   int s, h, t, nt, len, next_len;
-  __device__ void init(const Params& p, const Start& st) {
-    at = st.at; s = st.s; h = st.h; t = st.t;
-    len = p.len[s];
-    next_len = s + 1 < p.n ? p.len[s + 1] : 0;
-    nt = tiles_of(len);
+  __device__ void init(const Start& st) {
+    at = st.at; s = st.s; h = st.h; t = st.t; len = st.len; next_len = st.next_len;
+    nt = tiles_of(len, TK);
   }
   // to the next unit; the next sequence's length was requested one sequence ago
   __device__ void next(const Params& p) {
@@ -257,21 +265,22 @@ struct Cursor {
     h = 0;
     ++s;
     len = next_len;
-    nt = tiles_of(len);
+    nt = tiles_of(len, TK);
     next_len = s + 1 < p.n ? p.len[s + 1] : 0;
   }
-  __device__ bool before(int64_t end) const { return at + (int64_t)t * UNIT < end; }
+  __device__ bool before(int64_t end) const { return at + begin_of(t, nt) < end; }
 };
 
 template <typename T, int D, int NR>
 struct Cfg {
   static constexpr int ES = sizeof(T);
-  static constexpr int SK = ES == 2 ? 16 : 8;        // tokens per warp and stage
+  static constexpr int TK = unit_tokens(D);
+  static constexpr int SK = 4096 / (D * ES);         // tokens per warp and stage: 4 KB of keys
   static constexpr int SUB = TK / (WARPS * SK);      // stages per unit
   static constexpr int ROW = D * ES;                 // bytes of a token's vector
   static constexpr int CH = ROW / 16;                // 16-byte chunks of it
   static constexpr int KV = SK * ROW;                // bytes of a stage's keys (or values)
-  static constexpr int STAGES = D == 128 ? 3 : 4;
+  static constexpr int STAGES = D == 128 ? 3 : 2;
   static constexpr int RING = STAGES * 2 * KV;       // per warp
   static constexpr int MR = ES == 2 ? 8 : 4;         // rows joined at a time
   static constexpr int JS = D + 4;                   // row stride of the join buffer (floats)
@@ -294,10 +303,11 @@ template <typename T, int D, int NR>
 __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params p) {
   using C = Cfg<T, D, NR>;
   constexpr bool BF = sizeof(T) == 2;
-  constexpr int ST = C::STAGES;
+  constexpr int ST = C::STAGES, TK = C::TK;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x;
+  pdl_wait();  // everything the call reads may come from the kernel before
   const Header hd = *p.hdr;
   const Start st0 = p.start[c];
   const int64_t end = min((int64_t)(c + 1) * hd.chunk, hd.cost);
@@ -310,8 +320,8 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
 
   // ---------------- loader: a cursor one stage ahead of the copies, whose
   // page number is in flight while the previous stage's copies are issued
-  Cursor ld;
-  ld.init(p, st0);
+  Cursor<TK> ld;
+  ld.init(st0);
   int ld_sub = 0, ld_n = 0;
   int pg = 0, slot = 0, hkv = 0;
   bool on = false, look = false;
@@ -361,8 +371,8 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
   for (int i = 0; i < ST - 1; ++i) fetch();
 
   // ---------------- queries: the next item's are requested one item ahead
-  Cursor cu;
-  cu.init(p, st0);
+  Cursor<TK> cu;
+  cu.init(st0);
   auto q_row = [&](int s, int h, int r) {  // first query head of the group + r, or -1
     const int first = (h % p.per_kv) * p.rows + r;
     return r < p.rows && first < p.G ? (h / p.per_kv) * p.G + first : -1;
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
       __syncthreads();
     }
     {  // the next item's queries
-      Cursor nx = cu;
+      Cursor<TK> nx = cu;
       nx.t = nx.nt - 1;
       nx.next(p);
       if (nx.before(end)) request_q(nx.s, nx.h);
@@ -450,34 +460,43 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
         const int left = len - key0;  // visible tokens of the slice
         if (left <= 0) continue;
         if constexpr (BF) {
-          float sc[HT][4] = {};  // token lane / 4 (+ 8 in the upper two), heads 2 (lane % 4) + {0, 1}
+          // sc[mt][ht]: token 16 mt + lane / 4 (+ 8 in the upper two), heads 8 ht +
+          // 2 (lane % 4) + {0, 1}
+          constexpr int MT = C::SK / 16;
+          float sc[MT][HT][4] = {};
           const int mi = lane >> 3, r8 = lane & 7;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t a[4];
-            ldsm4(sk + chunk_at<C::CH>((mi & 1) * 8 + r8, 2 * kk + (mi >> 1)), a);
+          for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-            for (int ht = 0; ht < HT; ++ht)
-              mma_bf16(sc[ht], a, qa[(kk * HT + ht) * 2], qa[(kk * HT + ht) * 2 + 1]);
-          }
-          uint32_t pb[HT][2];
-          bool up[NM];
-          float mx[NM];
-          bool any = false;
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t a[4];
+              ldsm4(sk + chunk_at<C::CH>(16 * mt + (mi & 1) * 8 + r8, 2 * kk + (mi >> 1)), a);
 #pragma unroll
-          for (int ht = 0; ht < HT; ++ht) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              sc[ht][e] = (lane >> 2) + (e >> 1) * 8 < left ? sc[ht][e] * p.sl2 : -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float x = fmaxf(sc[ht][i], sc[ht][i + 2]);
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-              mx[2 * ht + i] = x;
-              up[2 * ht + i] = x > m[2 * ht + i] + TAU;
-              any |= up[2 * ht + i];
+              for (int ht = 0; ht < HT; ++ht)
+                mma_bf16(sc[mt][ht], a, qa[(kk * HT + ht) * 2], qa[(kk * HT + ht) * 2 + 1]);
             }
+          if (left < C::SK) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (16 * mt + (lane >> 2) + (e >> 1) * 8 >= left) sc[mt][ht][e] = -INFINITY;
+          }
+          bool up[NM], any = false;
+          float mx[NM];
+#pragma unroll
+          for (int i = 0; i < NM; ++i) {
+            float x = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              x = fmax3(x, sc[mt][i / 2][i & 1], sc[mt][i / 2][2 + (i & 1)]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+            mx[i] = x * p.sl2;
+            up[i] = mx[i] > m[i] + TAU;
+            any |= up[i];
           }
           // the reference moves only when it must: P stays below 2^TAU
           if (__any_sync(0xffffffffu, any)) {
@@ -493,81 +512,103 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
               }
             }
           }
+          // P as bf16 (the row sums take it unrounded): relative error 2^-8 at
+          // most per weight, below the output's own rounding after averaging
+          uint32_t pb[MT][HT][2];
 #pragma unroll
           for (int ht = 0; ht < HT; ++ht) {
+            const float r0 = m[2 * ht] == -INFINITY ? 0.0f : m[2 * ht];
+            const float r1 = m[2 * ht + 1] == -INFINITY ? 0.0f : m[2 * ht + 1];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = 2 * ht + (e & 1);
-              sc[ht][e] = ex2_ftz(sc[ht][e] - (m[i] == -INFINITY ? 0.0f : m[i]));
-              l[i] += sc[ht][e];
+            for (int mt = 0; mt < MT; ++mt) {
+              float(&x)[4] = sc[mt][ht];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = ex2_ftz(fmaf(x[e], p.sl2, (e & 1) ? -r1 : -r0));
+              l[2 * ht] += x[0] + x[2];
+              l[2 * ht + 1] += x[1] + x[3];
+              pb[mt][ht][0] = transpose8x8(pack_bf16x2(x[0], x[1]));
+              pb[mt][ht][1] = transpose8x8(pack_bf16x2(x[2], x[3]));
             }
-            // P as bf16 (the row sums take it unrounded): relative error 2^-8 at
-            // most per weight, below the output's own rounding after averaging
-            pb[ht][0] = transpose8x8(pack_bf16x2(sc[ht][0], sc[ht][1]));
-            pb[ht][1] = transpose8x8(pack_bf16x2(sc[ht][2], sc[ht][3]));
           }
 #pragma unroll
-          for (int nn = 0; nn < D / 16; ++nn) {
-            uint32_t a[4];
-            ldsm4_t(sv + chunk_at<C::CH>((mi >> 1) * 8 + r8, 2 * nn + (mi & 1)), a);
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int ht = 0; ht < HT; ++ht) mma_bf16(acc[nn * HT + ht], a, pb[ht][0], pb[ht][1]);
-          }
+            for (int nn = 0; nn < D / 16; ++nn) {
+              uint32_t a[4];
+              ldsm4_t(sv + chunk_at<C::CH>(16 * mt + (mi >> 1) * 8 + r8, 2 * nn + (mi & 1)), a);
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht)
+                mma_bf16(acc[nn * HT + ht], a, pb[mt][ht][0], pb[mt][ht][1]);
+            }
         } else {
           const int key = lane & 7, part = lane >> 3;  // token, quarter of d
-          float4 kx[D / 16];
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-            asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                         : "=f"(kx[i].x), "=f"(kx[i].y), "=f"(kx[i].z), "=f"(kx[i].w)
-                         : "r"(sk + chunk_at<C::CH>(key, i * 4 + part)));
-          float pr[NR];
+          for (int kt = 0; kt < C::SK / 8; ++kt) {  // eight tokens at a time
+            if (left <= 8 * kt) break;
+            float4 kx[D / 16];
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            pr[r] = 0.0f;
-            if (r >= rows) continue;
-            float d0 = 0.0f, d1 = 0.0f;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              const float4 qx = *reinterpret_cast<const float4*>(sq + r * D + (i * 4 + part) * 4);
-              d0 = fmaf(qx.x, kx[i].x, d0);
-              d1 = fmaf(qx.y, kx[i].y, d1);
-              d0 = fmaf(qx.z, kx[i].z, d0);
-              d1 = fmaf(qx.w, kx[i].w, d1);
-            }
-            float sc = d0 + d1;
-            sc += __shfl_xor_sync(0xffffffffu, sc, 8);
-            sc += __shfl_xor_sync(0xffffffffu, sc, 16);
-            sc = key < left ? sc * p.sl2 : -INFINITY;
-            float mx = sc;
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if (mx > m[r] + TAU) {  // the same in every lane
-              const float a = exp2f(m[r] - mx);
-              m[r] = mx;
-              l[r] *= a;
-#pragma unroll
-              for (int j = 0; j < CPL; ++j) acc[r][j] *= a;
-            }
-            pr[r] = exp2f(sc - (m[r] == -INFINITY ? 0.0f : m[r]));
-            l[r] += pr[r];  // the lane's token; the four quarters hold copies
-          }
-#pragma unroll
-          for (int kx2 = 0; kx2 < C::SK; ++kx2) {
-            float vx[CPL];
-            const uint32_t va = sv + chunk_at<C::CH>(kx2, lane * CPL / 4) + (lane * CPL % 4) * 4;
-            if constexpr (CPL == 4)
+            for (int i = 0; i < D / 16; ++i)
               asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                           : "=f"(vx[0]), "=f"(vx[1]), "=f"(vx[2]), "=f"(vx[3])
-                           : "r"(va));
-            else
-              asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(vx[0]), "=f"(vx[1]) : "r"(va));
+                           : "=f"(kx[i].x), "=f"(kx[i].y), "=f"(kx[i].z), "=f"(kx[i].w)
+                           : "r"(sk + chunk_at<C::CH>(8 * kt + key, i * 4 + part)));
+            float pr[NR], mx[NR];
+            bool any = false;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              pr[r] = mx[r] = -INFINITY;
+              if (r >= rows) continue;
+              float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const float4 qx = *reinterpret_cast<const float4*>(sq + r * D + (i * 4 + part) * 4);
+                fma2(d0, d1, qx.x, qx.y, kx[i].x, kx[i].y, d0, d1);
+                fma2(d0, d1, qx.z, qx.w, kx[i].z, kx[i].w, d0, d1);
+              }
+              float sc = d0 + d1;
+              sc += __shfl_xor_sync(0xffffffffu, sc, 8);
+              sc += __shfl_xor_sync(0xffffffffu, sc, 16);
+              pr[r] = 8 * kt + key < left ? sc * p.sl2 : -INFINITY;
+              mx[r] = pr[r];
+#pragma unroll
+              for (int o = 1; o < 8; o <<= 1)
+                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], o));
+              any |= mx[r] > m[r] + TAU;  // the same in every lane
+            }
+            if (any) {
+#pragma unroll
+              for (int r = 0; r < NR; ++r) {
+                const bool up = mx[r] > m[r] + TAU;
+                const float a = up ? exp2f(m[r] - mx[r]) : 1.0f;
+                if (up) m[r] = mx[r];
+                l[r] *= a;
+#pragma unroll
+                for (int j = 0; j < CPL; ++j) acc[r][j] *= a;
+              }
+            }
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
               if (r >= rows) continue;
-              const float w = __shfl_sync(0xffffffffu, pr[r], kx2);
+              pr[r] = exp2f(pr[r] - (m[r] == -INFINITY ? 0.0f : m[r]));
+              l[r] += pr[r];  // the lane's token; the four quarters hold copies
+            }
 #pragma unroll
-              for (int j = 0; j < CPL; ++j) acc[r][j] = fmaf(w, vx[j], acc[r][j]);
+            for (int kx2 = 0; kx2 < 8; ++kx2) {
+              float vx[CPL];
+              const uint32_t va = sv + chunk_at<C::CH>(8 * kt + kx2, lane * CPL / 4) + (lane * CPL % 4) * 4;
+              if constexpr (CPL == 4)
+                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                             : "=f"(vx[0]), "=f"(vx[1]), "=f"(vx[2]), "=f"(vx[3])
+                             : "r"(va));
+              else
+                asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(vx[0]), "=f"(vx[1]) : "r"(va));
+#pragma unroll
+              for (int r = 0; r < NR; ++r) {
+                if (r >= rows) continue;
+                const float w = __shfl_sync(0xffffffffu, pr[r], kx2);
+#pragma unroll
+                for (int j = 0; j < CPL; j += 2)
+                  fma2(acc[r][j], acc[r][j + 1], w, w, vx[j], vx[j + 1], acc[r][j], acc[r][j + 1]);
+              }
             }
           }
         }
@@ -607,7 +648,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
       }
     };
     // first and last CTA of the item
-    const int64_t last = at + (int64_t)(nt - 1) * UNIT;
+    const int64_t last = at + begin_of(nt - 1, nt);
     const bool whole = at >= (int64_t)c * hd.chunk && last < end;
     const int cf = whole ? c : (int)(at / hd.chunk), cl = whole ? c : (int)(last / hd.chunk);
     // part 2 c: the CTA's range begins at or inside the item; 2 c + 1: before it
@@ -683,13 +724,14 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
     }
     if (!whole) {
       // ---- split item: the last CTA to arrive joins the parts in CTA order
-      __threadfence();
-      __syncthreads();
-      if (tid == 0)
+      __syncthreads();  // the part is written; thread 0's fence covers all of it
+      if (tid == 0) {
+        __threadfence();
         *flag = atomicInc(p.counter + cf, (uint32_t)(cl - cf)) == (uint32_t)(cl - cf);
+        __threadfence();
+      }
       __syncthreads();
       if (*flag) {
-        __threadfence();
         for (int r = warp; r < rows; r += WARPS) {
           float M = -INFINITY;
           for (int cc = cf + lane; cc <= cl; cc += 32)
@@ -705,21 +747,27 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
               lp = y.y * a;
             }
             const int np = min(32, cl - cc0 + 1);
-#pragma unroll 8
-            for (int i = 0; i < np; ++i) {
-              const float w = __shfl_sync(0xffffffffu, a, i);
-              const float* y = p.part + ((int64_t)part_of(cc0 + i) * p.rows + r) * D + lane * CPL;
-              float z[CPL];
-              if constexpr (CPL == 4) {
-                const float4 zz = __ldcg(reinterpret_cast<const float4*>(y));
-                z[0] = zz.x; z[1] = zz.y; z[2] = zz.z; z[3] = zz.w;
-              } else {
-                const float2 zz = __ldcg(reinterpret_cast<const float2*>(y));
-                z[0] = zz.x; z[1] = zz.y;
+            for (int i0 = 0; i0 < np; i0 += 16) {  // 16 parts requested together
+              float z[16][CPL];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int cc = min(cc0 + i0 + i, cl);  // (behind the last: weight 0)
+                const float* y = p.part + ((int64_t)part_of(cc) * p.rows + r) * D + lane * CPL;
+                if constexpr (CPL == 4) {
+                  const float4 zz = __ldcg(reinterpret_cast<const float4*>(y));
+                  z[i][0] = zz.x; z[i][1] = zz.y; z[i][2] = zz.z; z[i][3] = zz.w;
+                } else {
+                  const float2 zz = __ldcg(reinterpret_cast<const float2*>(y));
+                  z[i][0] = zz.x; z[i][1] = zz.y;
+                }
               }
 #pragma unroll
-              for (int j = 0; j < CPL; ++j) x[j] = fmaf(w, z[j], x[j]);
-              L += __shfl_sync(0xffffffffu, lp, i);
+              for (int i = 0; i < 16; ++i) {
+                const float w = __shfl_sync(0xffffffffu, a, i0 + i);
+                L += __shfl_sync(0xffffffffu, lp, i0 + i);
+#pragma unroll
+                for (int j = 0; j < CPL; ++j) x[j] = fmaf(w, z[i][j], x[j]);
+              }
             }
           }
           const float inv = L > 0.0f ? 1.0f / L : 0.0f;
@@ -743,8 +791,7 @@ mgb_status launch(const Params& p, cudaStream_t st) {
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return MGB_ERR_CUDA;
   LaunchScope scope(PROF_ATTN_DECODE, st);
-  k<<<SMS * ctas_per_sm(D), NT, C::SMEM, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MGB_OK : MGB_ERR_CUDA;
+  return launch_pdl(k, SMS * ctas_per_sm(D), NT, C::SMEM, st, p);
 }
 
 // The smallest form that holds the item's query heads: fewer products, and
@@ -794,7 +841,7 @@ mgb_status mgb_attention_decode_prepare(int32_t n_seqs, int32_t n_q_heads, int32
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     LaunchScope scope(PROF_ATTN_DECODE, st);
     decode_prepare_kernel<<<1, 1024, 0, st>>>(
-        n_seqs, l.groups, l.ctas, seq_lens, reinterpret_cast<Header*>(b + l.header),
+        n_seqs, l.groups, l.ctas, unit_tokens(head_dim), seq_lens, reinterpret_cast<Header*>(b + l.header),
         reinterpret_cast<Start*>(b + l.start), reinterpret_cast<uint32_t*>(b + l.counter),
         reinterpret_cast<int32_t*>(b + l.len), reinterpret_cast<int64_t*>(b + l.prefix), err);
     if (cudaGetLastError() != cudaSuccess) return MGB_ERR_CUDA;

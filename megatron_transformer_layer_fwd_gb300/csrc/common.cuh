@@ -425,6 +425,31 @@ __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- launch overlap
+// A kernel launched by launch_pdl may start its blocks while the kernel before
+// it in the stream is still running its last ones (or once every block of that
+// kernel has called pdl_trigger); pdl_wait returns when that kernel has
+// finished and its writes are visible. Every thread calls pdl_wait before it
+// touches memory, so the order of the stream is kept.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename K, typename... A>
+mgb_status launch_pdl(K kernel, int grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? MGB_OK : MGB_ERR_CUDA;
+}
+
 // ---------------------------------------------------------------- warp roles
 // One lane of a converged warp is elected (the same lane on every call).
 __device__ __forceinline__ bool elect_one() {
