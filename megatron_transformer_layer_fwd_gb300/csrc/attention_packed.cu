@@ -2,10 +2,32 @@
 // cores (tcgen05): O_h = softmax(Q_h K_g^T / sqrt(d)) V_g within each sequence,
 // optionally causal, and its log-sum-exp.
 //
-// The products, the softmax and their overlap are those of the dense forward
-// (attention_tc2.cu): a work item is 256 query rows of one (sequence, head) in
-// two tiles of 128 that take turns on the tensor core, S and P of a tile share
-// TMEM columns, a lazy reference maximum. What differs:
+// A work item is 256 query rows of one (sequence, head), in two tiles A and B
+// of 128 that take turns on the tensor core. Per 128 keys the MMA warp issues
+// PV_A(j), S_A(j+1), PV_B(j), S_B(j+1); while tile A's scores are turned into
+// weights, tile B's two products run. TMEM (512 columns) holds S_A, S_B, O_A, O_B; a
+// tile's weights P (bf16 pairs) overwrite scores already read and are read from
+// there by PV.
+//
+// Each tile goes round a chain: scores complete - softmax - weights ready -
+// PV and the next scores (16 products of 64 cycles) - scores complete. Two
+// tiles cover the tensor core only as far as that chain is short (measured at
+// D = 128, in cycles: softmax 1020, to the MMA warp 220, products 1270; the
+// tensor core is busy for 2048 of the 2515). What shortens it:
+//   - the row maximum is not on it: weights are formed in log2 units with the
+//     reference maximum so far, and only if a row's then sum to more than
+//     SUM_LIMIT (each is at most the sum) does its warp take the maximum, move the
+//     reference, rescale the sums and the O rows, and form the weights again;
+//   - one thread issues all products: the waits and votes of a whole warp
+//     between two tiles' products took 900 cycles in which the tensor core ran
+//     dry; and a ring stage holds V_j and K_{j+1}, which the same round needs, so
+//     a round has one wait and one release for both;
+//   - the exponentials are spread between the other steps in a fixed order
+//     (weights() below: 1340 -> 1020 cycles), as only one warp per scheduler is
+//     at work on a tile. (Two threads per row, 16 softmax warps, took 1070 and a
+//     barrier.)
+// 8177 tokens in two sequences, 32 / 8 heads, D = 128, causal: 184 us, 1490
+// TFLOP/s.
 //
 // Items come from a list that the prepare kernel derives from the row offsets
 // (longest first, so that the snake order of item_index evens the CTAs out);
@@ -16,8 +38,8 @@
 // softmax (by selection, so NaN scores vanish too) and a query row's products
 // stay in its own TMEM lane, which is not stored; but a weight of zero times a
 // NaN value is NaN. So the PV product of the last tile takes only the K steps
-// (16 keys) that hold keys of the sequence, and the MMA warp clears the up to 15
-// value rows behind the end of the last step in shared memory first.
+// (16 keys) that hold keys of the sequence, and the softmax warps clear the up
+// to 15 value rows behind the end of the last step in shared memory first.
 #include "common.cuh"
 #include "internal.h"
 #include "packed.cuh"
@@ -31,13 +53,12 @@ namespace {
 
 constexpr int TQ = 128;         // query rows per tile (TMEM lanes)
 constexpr int TK = 128;         // keys per KV tile
-constexpr int NSK = 2;          // K ring stages
-constexpr int NSV = 2;          // V ring stages
-constexpr int NSOFT = 128;      // softmax threads per tile
+constexpr int NST = 2;          // ring stages, each a K tile and the V tile before it
+constexpr int NSOFTW = 4;       // softmax warps per tile
 constexpr int NTHREADS = 320;   // MMA warp, producer warp, 2 x 4 softmax warps
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr float TAU = 8.0f;
+constexpr float SUM_LIMIT = 8192.0f;  // of a row's weights in a tile
 
 template <int D>
 struct Cfg2 {
@@ -48,8 +69,8 @@ struct Cfg2 {
   static constexpr int OFF_QA = 0;
   static constexpr int OFF_QB = Q_BYTES;
   static constexpr int OFF_K = 2 * Q_BYTES;
-  static constexpr int OFF_V = OFF_K + NSK * KV_BYTES;
-  static constexpr int OFF_BAR = OFF_V + NSV * KV_BYTES;
+  static constexpr int OFF_V = OFF_K + NST * KV_BYTES;
+  static constexpr int OFF_BAR = OFF_V + NST * KV_BYTES;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;     // barriers, alignment slack
   static constexpr int COL_S = 0;                       // S_A at 0, S_B at TK
   static constexpr int COL_O = 2 * TK;                  // O_A, then O_B at + D
@@ -99,6 +120,62 @@ __device__ __forceinline__ int item_index(int k) {
   return k * g + ((k & 1) ? g - 1 - c : c);
 }
 
+// The steps of the weights in an order that the compiler keeps (volatile): see
+// the softmax warps.
+__device__ __forceinline__ void v_fma2(float& r0, float& r1, uint32_t a0, uint32_t a1, float b, float c) {
+  asm volatile(
+      "{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n"
+      " mov.b64 c, {%5, %5};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r0), "=f"(r1)
+      : "r"(a0), "r"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void v_ex2(float& x) {
+  asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
+}
+__device__ __forceinline__ void v_add2(float& r0, float& r1, float a0, float a1) {
+  asm volatile(
+      "{\n .reg .b64 a, b, d;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "+f"(r0), "+f"(r1)
+      : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ uint32_t v_pack(float lo, float hi) {
+  uint32_t r;
+  asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Whole warp: waits for the phase, for a bounded time and only while no role has
+// given up; the same result in every lane. The usual case, a phase already
+// complete, is one try and one vote.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, int* err,
+                                           volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    const bool ok = mbar_try_wait_suspend(bar, parity, 50000u);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    const bool late = global_ns() - t0 > kWaitLimitNs;
+    if (late) record_error(err, kErrTimeout);
+    if (__any_sync(0xffffffffu, late || *abort != 0)) return false;
+  }
+}
+
+// The same for one thread.
+__device__ __forceinline__ bool wait_phase_1(uint32_t bar, uint32_t parity, int* err,
+                                             volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort != 0) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      record_error(err, kErrTimeout);
+      return false;
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(NTHREADS, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -114,10 +191,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const uint32_t bar = sb + C::OFF_BAR;
   const uint32_t q_full = bar;         // both Q tiles loaded                   (tx)
   const uint32_t q_empty = bar + 8;    // the item's last S product done        (commit)
-  const uint32_t k_full0 = bar + 16;   // [2] K stage loaded                    (tx)
-  const uint32_t k_empty0 = bar + 32;  // [2] S products with it done           (commit)
-  const uint32_t v_full0 = bar + 48;   // [2] V stage loaded                    (tx)
-  const uint32_t v_empty0 = bar + 64;  // [2] PV products with it done          (commit)
+  const uint32_t l_full0 = bar + 16;   // [2] stage loaded                      (tx)
+  const uint32_t l_empty0 = bar + 32;  // [2] products with it done             (commit)
   const uint32_t s_full0 = bar + 80;   // [tile] S_X(j) complete                (commit)
   const uint32_t p_full0 = bar + 96;   // [tile] P_X(j) written, O_X rescaled   (4: one per warp)
   const uint32_t o_full0 = bar + 112;  // [tile] the item's last PV_X done      (commit)
@@ -136,14 +211,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full0 + 8 * i, 1);
-      mbar_init(k_empty0 + 8 * i, 1);
-      mbar_init(v_full0 + 8 * i, 1);
-      mbar_init(v_empty0 + 8 * i, 1);
+      mbar_init(l_full0 + 8 * i, 1);
+      mbar_init(l_empty0 + 8 * i, 1);
       mbar_init(s_full0 + 8 * i, 1);
-      mbar_init(p_full0 + 8 * i, NSOFT / 32);
+      mbar_init(p_full0 + 8 * i, NSOFTW);
       mbar_init(o_full0 + 8 * i, 1);
-      mbar_init(o_empty0 + 8 * i, NSOFT / 32);
+      mbar_init(o_empty0 + 8 * i, NSOFTW);
     }
     fence_mbar_init();
     *abort = 0;
@@ -154,10 +227,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  if (warp < 2) {
   if (warp == 1) {
-    // ---------------- producer: per item Q_A, Q_B, then K_0, V_0, K_1, V_1, ...
+    // ---------------- producer: per item Q_A, Q_B, then the stages (K_0),
+    // (V_0, K_1), (V_1, K_2), .., (V_last)
     if (lane == 0) {
-      int nk = 0, nv = 0;  // K / V tiles loaded so far (ring positions)
+      int nl = 0;  // stages loaded so far
       for (int k = 0, i = item_index(0); i < n_items && !*abort; ++k, i = item_index(k)) {
         const Item w = item_of(i, p);
         const int xcol = (w.h / p.group) * D;
@@ -183,35 +258,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         const int nt = max(w.n[0], w.n[1]);
         bool good = true;
-        for (int j = 0; j < nt && good; ++j) {
-          // K_j
-          {
-            const int s = nk % NSK;
-            if (nk >= NSK && !mbar_wait(k_empty0 + 8 * s, ((nk - NSK) / NSK) & 1, p.err)) {
-              good = false;
-              break;
-            }
-            mbar_arrive_expect_tx(k_full0 + 8 * s, C::KV_BYTES);
-#pragma unroll
-            for (int kb = 0; kb < C::KB; ++kb)
-              tma_load_2d(sK + s * C::KV_BYTES + kb * C::BOX, &tmK, xcol + kb * 64,
-                          w.a + j * TK, k_full0 + 8 * s);
-            ++nk;
+        for (int j = 0; j <= nt; ++j, ++nl) {
+          const int s = nl % NST;
+          if (nl >= NST && !mbar_wait(l_empty0 + 8 * s, ((nl - NST) / NST) & 1, p.err)) {
+            good = false;
+            break;
           }
-          // V_j
-          {
-            const int s = nv % NSV;
-            if (nv >= NSV && !mbar_wait(v_empty0 + 8 * s, ((nv - NSV) / NSV) & 1, p.err)) {
-              good = false;
-              break;
-            }
-            mbar_arrive_expect_tx(v_full0 + 8 * s, C::KV_BYTES);
+          mbar_arrive_expect_tx(l_full0 + 8 * s, (j > 0 && j < nt ? 2 : 1) * C::KV_BYTES);
+          if (j > 0)
 #pragma unroll
             for (int kb = 0; kb < C::KB; ++kb)
               tma_load_2d(sV + s * C::KV_BYTES + kb * C::BOX, &tmV, xcol + kb * 64,
-                          w.a + j * TK, v_full0 + 8 * s);
-            ++nv;
-          }
+                          w.a + (j - 1) * TK, l_full0 + 8 * s);
+          if (j < nt)
+#pragma unroll
+            for (int kb = 0; kb < C::KB; ++kb)
+              tma_load_2d(sK + s * C::KV_BYTES + kb * C::BOX, &tmK, xcol + kb * 64, w.a + j * TK,
+                          l_full0 + 8 * s);
         }
         if (!good) {
           *abort = 1;
@@ -220,287 +283,285 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     }
   } else if (warp == 0) {
-    // ---------------- MMA issuer
-    constexpr uint32_t idesc_s = idesc_bf16_f32(TQ, TK, 0, 0);
-    constexpr uint32_t idesc_pv = idesc_bf16_f32(TQ, D, 0, 1);
-    const uint64_t dq0[2] = {smem_desc_sw128(sQ[0], 16, 1024), smem_desc_sw128(sQ[1], 16, 1024)};
-    const uint64_t dk0 = smem_desc_sw128(sK, 16, 1024);
-    const uint64_t dv0 = smem_desc_sw128(sV, C::BOX, 1024);
-    int nk = 0, nv = 0;     // K / V tiles consumed so far
-    int np[2] = {0, 0};     // PV products of each tile so far (p_full phases)
-    int no[2] = {0, 0};     // items with a non-empty tile X so far (o_full / o_empty phases)
-    bool good = true;
-    // S_X = Q_X K^T into tile X's score columns (K stage sk)
-    auto issue_s = [&](int x, int sk) {
-      const uint64_t db = dk0 + (uint64_t)((sk * C::KV_BYTES) >> 4);
-      const uint32_t td = tmem + C::COL_S + x * TK;
-      if (elect_one()) {
+    // ---------------- MMA issuer: one thread
+    if (elect_one()) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(TQ, TK, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(TQ, D, 0, 1);
+      const uint64_t dq0[2] = {smem_desc_sw128(sQ[0], 16, 1024), smem_desc_sw128(sQ[1], 16, 1024)};
+      const uint64_t dk0 = smem_desc_sw128(sK, 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(sV, C::BOX, 1024);
+      int nl = 0;             // stages consumed so far
+      int np[2] = {0, 0};     // PV products of each tile so far (p_full phases)
+      int no[2] = {0, 0};     // items with a non-empty tile X so far (o_full / o_empty phases)
+      bool good = true;
+      // S_X = Q_X K^T into tile X's score columns (K stage sk)
+      auto issue_s = [&](int x, int sk) {
+        const uint64_t db = dk0 + (uint64_t)((sk * C::KV_BYTES) >> 4);
+        const uint32_t td = tmem + C::COL_S + x * TK;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * C::BOX + (kk & 3) * 32;
           tc_mma_f16(td, dq0[x] + (uint64_t)(off >> 4), db + (uint64_t)(off >> 4), idesc_s, kk > 0);
         }
         tc_commit(s_full0 + 8 * x);
-      }
-      __syncwarp();
-    };
-    // O_X += P_X V (P from tile X's score columns, V stage sv), `steps` steps of 16 keys
-    auto issue_pv = [&](int x, int sv, bool acc, int steps) {
-      const uint64_t db = dv0 + (uint64_t)((sv * C::KV_BYTES) >> 4);
-      const uint32_t ta = tmem + C::COL_S + x * TK;
-      const uint32_t to = tmem + C::COL_O + x * D;
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < TK / 16; ++kk)
-          if (kk < steps)
-            tc_mma_f16_ts(to, ta + kk * 8, db + (uint64_t)((kk * 2048) >> 4), idesc_pv,
-                          (acc || kk > 0) ? 1u : 0u);
-      }
-      __syncwarp();
-      ++np[x];
-    };
-    for (int k = 0, i = item_index(0); i < n_items && good; ++k, i = item_index(k)) {
-      const Item w = item_of(i, p);
-      const int nt = max(w.n[0], w.n[1]);
-      if (warp_aborted(abort) || !warp_wait(q_full, k & 1, p.err)) {
-        good = false;
-        break;
-      }
-      // K_0 for both tiles' first scores
-      {
-        const int s = nk % NSK;
-        if (!warp_wait(k_full0 + 8 * s, (nk / NSK) & 1, p.err)) {
+      };
+      for (int k = 0, i = item_index(0); i < n_items && good; ++k, i = item_index(k)) {
+        const Item w = item_of(i, p);
+        const int nt = max(w.n[0], w.n[1]);
+        const int s0 = nl % NST;
+        if (!wait_phase_1(q_full, k & 1, p.err, abort) ||
+            !wait_phase_1(l_full0 + 8 * s0, (nl / NST) & 1, p.err, abort)) {
           good = false;
           break;
         }
         tc_fence_after();
+#pragma unroll
         for (int x = 0; x < 2; ++x)
-          if (w.n[x] > 0) issue_s(x, s);
-        if (elect_one()) {
-          tc_commit(k_empty0 + 8 * s);
-          if (nt == 1) tc_commit(q_empty);
-        }
-        __syncwarp();
-        ++nk;
-      }
-      for (int j = 0; j < nt && good; ++j) {
-        const int sv = nv % NSV;
-        if (warp_aborted(abort) || !warp_wait(v_full0 + 8 * sv, (nv / NSV) & 1, p.err)) {
-          good = false;
-          break;
-        }
-        const bool next = j + 1 < nt;
-        const int sk = nk % NSK;
-        if (next && !warp_wait(k_full0 + 8 * sk, (nk / NSK) & 1, p.err)) {
-          good = false;
-          break;
-        }
-        const int left = w.len - j * TK;  // keys of the sequence from this tile on
-        const int steps = left >= TK ? TK / 16 : (left + 15) / 16;
-        if (left < TK && (left & 15)) {
-          // the value rows behind the end, up to the step's last: 8 chunks per
-          // 64-column box
-          const int rows = 16 * steps - left;
-          for (int c = lane; c < rows * 8 * C::KB; c += 32) {
-            const int kb = c / (rows * 8), rc = c - kb * (rows * 8);
-            st_shared_v4u(sV + sv * C::KV_BYTES + kb * C::BOX + (left + rc / 8) * 128 + (rc % 8) * 16,
-                          0, 0, 0, 0);
-          }
-          fence_proxy_async();  // before the tensor core reads them
-          __syncwarp();
-        }
-        for (int x = 0; x < 2 && good; ++x) {
-          if (j >= w.n[x]) continue;
-          // O_X of the previous item read out before this item's first PV_X
-          if (j == 0 && no[x] >= 1 && !warp_wait(o_empty0 + 8 * x, (no[x] - 1) & 1, p.err)) {
+          if (w.n[x] > 0) issue_s(x, s0);
+        tc_commit(l_empty0 + 8 * s0);
+        if (nt == 1) tc_commit(q_empty);
+        ++nl;
+        for (int j = 0; j < nt && good; ++j) {
+          const int s = nl % NST;  // V_j, K_{j+1}
+          if (!wait_phase_1(l_full0 + 8 * s, (nl / NST) & 1, p.err, abort)) {
             good = false;
             break;
           }
-          if (!warp_wait(p_full0 + 8 * x, np[x] & 1, p.err)) {
-            good = false;
-            break;
+          const int left = w.len - j * TK;  // keys of the sequence from this tile on
+          const int steps = left >= TK ? TK / 16 : (left + 15) / 16;
+          const uint64_t db = dv0 + (uint64_t)((s * C::KV_BYTES) >> 4);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!good || j >= w.n[x]) continue;
+            // O_X of the previous item read out before this item's first PV_X
+            if ((j == 0 && no[x] >= 1 &&
+                 !wait_phase_1(o_empty0 + 8 * x, (no[x] - 1) & 1, p.err, abort)) ||
+                !wait_phase_1(p_full0 + 8 * x, np[x] & 1, p.err, abort)) {
+              good = false;
+              continue;
+            }
+            tc_fence_after();
+            const uint32_t ta = tmem + C::COL_S + x * TK, to = tmem + C::COL_O + x * D;
+            if (steps == TK / 16) {
+#pragma unroll
+              for (int kk = 0; kk < TK / 16; ++kk)
+                tc_mma_f16_ts(to, ta + kk * 8, db + (uint64_t)((kk * 2048) >> 4),
+                              idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+            } else {
+#pragma unroll 1
+              for (int kk = 0; kk < steps; ++kk)
+                tc_mma_f16_ts(to, ta + kk * 8, db + (uint64_t)((kk * 2048) >> 4),
+                              idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+            }
+            ++np[x];
+            if (j == w.n[x] - 1) {
+              tc_commit(o_full0 + 8 * x);
+              ++no[x];
+            } else {
+              issue_s(x, s);
+            }
           }
-          tc_fence_after();
-          issue_pv(x, sv, j > 0, steps);
-          if (j == w.n[x] - 1) {
-            if (elect_one()) tc_commit(o_full0 + 8 * x);
-            __syncwarp();
-            ++no[x];
-          } else {
-            issue_s(x, sk);
-          }
-        }
-        if (!good) break;
-        if (elect_one()) {
-          tc_commit(v_empty0 + 8 * sv);
-          if (next) tc_commit(k_empty0 + 8 * sk);
-        }
-        __syncwarp();
-        ++nv;
-        if (next) ++nk;
-        // the item's last score product has been issued once j + 1 == nt - 1
-        if (next && j + 2 == nt) {
-          if (elect_one()) tc_commit(q_empty);
-          __syncwarp();
+          if (!good) break;
+          tc_commit(l_empty0 + 8 * s);
+          ++nl;
+          // the item's last score product has been issued once j + 1 == nt - 1
+          if (j + 2 == nt) tc_commit(q_empty);
         }
       }
+      if (!good) *abort = 1;
     }
-    if (!good) *abort = 1;
+    __syncwarp();
+  }
   } else {
-    // ---------------- softmax: warps 2-5 tile A, 6-9 tile B
+    // ---------------- softmax: warps 2-5 tile A, 6-9 tile B, a thread per row
     const int x = (warp - 2) >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;                // row of the tile
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t ts = tmem + C::COL_S + x * TK + lane_base;
+    const uint32_t t_s = tmem + C::COL_S + x * TK + lane_base;  // scores, then P
     const uint32_t t_o = tmem + C::COL_O + x * D + lane_base;
     const uint32_t sfull = s_full0 + 8 * x, pfull = p_full0 + 8 * x;
     const uint32_t ofull = o_full0 + 8 * x, oempty = o_empty0 + 8 * x;
     bool good = true;
     int n = 0;   // S_X products consumed so far
     int ko = 0;  // items with a non-empty tile X so far
+    int nl = 0;  // ring stages of the items before
     for (int k = 0, i = item_index(0); i < n_items && good; ++k, i = item_index(k)) {
       const Item w = item_of(i, p);
+      const int nt = max(w.n[0], w.n[1]), nl0 = nl;
+      nl += nt + 1;
       if (w.n[x] == 0) continue;  // tile past the sequence end: nothing to do
-      const int row = w.q0 + x * TQ + r;
       const int row0 = w.q0 + x * TQ;  // first row of the tile
+      const int row = row0 + r;
       float m_ref = -INFINITY, l = 0.0f;
       for (int j = 0; j < w.n[x]; ++j, ++n) {
         const int kv0 = j * TK;
-        if (warp_aborted(abort) || !warp_wait(sfull, n & 1, p.err)) {
+        if (!wait_phase(sfull, n & 1, p.err, abort)) {
           good = false;
           break;
         }
         tc_fence_after();
-        const bool interior = kv0 + TK <= w.len && (!p.causal || kv0 + TK - 1 <= row0);
-        // The scores are read in chunks of CW keys. From the second key tile on
-        // (m_ref is then finite: key 0 is visible to every row) one pass: each
-        // chunk's maximum is checked against the reference as it is read, and
-        // only a chunk that exceeds it by more than TAU moves it, by a whole
-        // number k of log2 units, so that the P already written for this tile
-        // and the O row scale by 2^-k exactly. The first tile takes the row
-        // maximum in a pass of its own.
-        constexpr int CW = 64;
-        auto load_chunk = [&](int c, float (&sc)[CW]) {
-          uint32_t qa[32];
-          tmem_ld32(ts + c * CW, qa);
-          uint32_t qb[32];
-          tmem_ld32(ts + c * CW + 32, qb);
-          tmem_ld_wait();
-          tmem_regs_ready(qb);
+        // visible keys of the tile: kv0 .. kv0 + see - 1
+        const bool edge = kv0 + TK > w.len || (p.causal && kv0 + TK - 1 > row0);
+        const int see = min(w.len, p.causal ? row + 1 : w.len) - kv0;
+        auto mask = [&](int c, float (&sc)[32]) {
+          if (edge) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sc[32 + e] = __uint_as_float(qb[e]);
-          tmem_regs_ready(qa);
+            for (int e = 0; e < 32; ++e)
+              if (c * 32 + e >= see) sc[e] = -INFINITY;
+          }
+        };
+        // P = 2^(s log2e / sqrt(d) - m_ref) as bf16 pairs (the row sum takes them
+        // unrounded): a relative error of at most 2^-8 per weight, below the
+        // output's own rounding after averaging
+        uint32_t pk[64];
+        float sum = 0.0f;
+        auto weights = [&]() {
+          const float nref = m_ref == -INFINITY ? 0.0f : -m_ref;
+          float r0 = 0.0f, r1 = 0.0f, r2 = 0.0f, r3 = 0.0f;
+          if (edge) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sc[e] = __uint_as_float(qa[e]);
-          if (!interior) {
+            for (int c = 0; c < 4; ++c) {
+              uint32_t q[32];
+              tmem_ld32(t_s + c * 32, q);
+              tmem_ld_wait();
+              tmem_regs_ready(q);
+              float sc[32];
 #pragma unroll
-            for (int e = 0; e < CW; ++e) {
-              const int key = kv0 + c * CW + e;
-              if (key >= w.len || (p.causal && key > row)) sc[e] = -INFINITY;
+              for (int e = 0; e < 32; ++e) sc[e] = __uint_as_float(q[e]);
+              mask(c, sc);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                fma2(sc[e], sc[e + 1], sc[e], sc[e + 1], p.sl2, p.sl2, nref, nref);
+                fma2(sc[e + 2], sc[e + 3], sc[e + 2], sc[e + 3], p.sl2, p.sl2, nref, nref);
+                sc[e] = ex2_ftz(sc[e]);
+                sc[e + 1] = ex2_ftz(sc[e + 1]);
+                sc[e + 2] = ex2_ftz(sc[e + 2]);
+                sc[e + 3] = ex2_ftz(sc[e + 3]);
+                add2(r0, r1, r0, r1, sc[e], sc[e + 1]);
+                add2(r2, r3, r2, r3, sc[e + 2], sc[e + 3]);
+                pk[c * 16 + e / 2] = pack_bf16x2(sc[e], sc[e + 1]);
+                pk[c * 16 + e / 2 + 1] = pack_bf16x2(sc[e + 2], sc[e + 3]);
+              }
+            }
+          } else {
+            // One warp per scheduler has to keep the exponential unit (4 cycles
+            // per instruction) busy by itself: groups of four keys, the exponentials of
+            // one between the sums and packing of the one before and the scaling
+            // of the second next, scores of the next 32 keys on their way.
+            uint32_t q[2][32];
+            float t[4][4];
+            auto scale = [&](int g) {
+              const uint32_t* z = q[(g >> 3) & 1] + (g & 7) * 4;
+              v_fma2(t[g & 3][0], t[g & 3][1], z[0], z[1], p.sl2, nref);
+              v_fma2(t[g & 3][2], t[g & 3][3], z[2], z[3], p.sl2, nref);
+            };
+            tmem_ld32(t_s, q[0]);
+            tmem_ld_wait();
+            tmem_regs_ready(q[0]);
+            tmem_ld32(t_s + 32, q[1]);
+            scale(0);
+            scale(1);
+#pragma unroll
+            for (int g = 0; g < 32; ++g) {
+              float* y = t[g & 3];
+              const float* u = t[(g + 3) & 3];  // group g - 1
+              v_ex2(y[0]);
+              if (g > 0) v_add2(r0, r1, u[0], u[1]);
+              v_ex2(y[1]);
+              if (g > 0) pk[2 * g - 2] = v_pack(u[0], u[1]);
+              v_ex2(y[2]);
+              if (g > 0) v_add2(r2, r3, u[2], u[3]);
+              v_ex2(y[3]);
+              if (g > 0) pk[2 * g - 1] = v_pack(u[2], u[3]);
+              if (g + 2 < 32) {
+                if (((g + 2) & 7) == 0) {
+                  const int c = (g + 2) >> 3;
+                  tmem_ld_wait();
+                  tmem_regs_ready(q[c & 1]);
+                  if (c < 3) tmem_ld32(t_s + (c + 1) * 32, q[(c + 1) & 1]);
+                }
+                scale(g + 2);
+              }
+            }
+            v_add2(r0, r1, t[3][0], t[3][1]);
+            v_add2(r2, r3, t[3][2], t[3][3]);
+            pk[62] = v_pack(t[3][0], t[3][1]);
+            pk[63] = v_pack(t[3][2], t[3][3]);
+          }
+          sum = (r0 + r1) + (r2 + r3);
+        };
+        bool again = true;
+        if (j > 0) {
+          weights();
+          // (NaN too; no reference yet: every score so far was -infinity)
+          again = __any_sync(0xffffffffu, !(sum <= SUM_LIMIT) || m_ref == -INFINITY);
+        }
+        if (again) {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t q[32];
+            tmem_ld32(t_s + c * 32, q);
+            tmem_ld_wait();
+            tmem_regs_ready(q);
+            float sc[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sc[e] = __uint_as_float(q[e]);
+            mask(c, sc);
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              m4[0] = fmax3(m4[0], sc[e], sc[e + 1]);
+              m4[1] = fmax3(m4[1], sc[e + 2], sc[e + 3]);
+              m4[2] = fmax3(m4[2], sc[e + 4], sc[e + 5]);
+              m4[3] = fmax3(m4[3], sc[e + 6], sc[e + 7]);
             }
           }
-        };
-        auto chunk_max = [&](const float (&sc)[CW], float m0) {
-          float m4[4] = {m0, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < CW; e += 8) {
-            m4[0] = fmax3(m4[0], sc[e], sc[e + 1]);
-            m4[1] = fmax3(m4[1], sc[e + 2], sc[e + 3]);
-            m4[2] = fmax3(m4[2], sc[e + 4], sc[e + 5]);
-            m4[3] = fmax3(m4[3], sc[e + 6], sc[e + 7]);
-          }
-          return fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
-        };
-        const bool one_pass = j > 0 && __all_sync(0xffffffffu, m_ref > -INFINITY);
-        bool need = false;
-        float alpha = 1.0f;
-        if (!one_pass) {
-          // pass 1: the row maximum over the 128 scores
-          float mx = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < TK / CW; ++c) {
-            float sc[CW];
-            load_chunk(c, sc);
-            mx = chunk_max(sc, mx);
-          }
-          mx *= p.sl2;
-          need = mx > m_ref + TAU;
-          if (need) {
+          const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * p.sl2;
+          float alpha = 1.0f;
+          if (mx > m_ref) {
             alpha = exp2f(m_ref - mx);
             m_ref = mx;
             l *= alpha;
           }
-        }
-        float nref = m_ref == -INFINITY ? 0.0f : -m_ref;
-        // pass 2: P = 2^(s log2e / sqrt(d) - m_ref) as bf16 pairs over the
-        // tile's first 64 score columns (chunk c's keys -> columns c CW / 2 ..),
-        // which only ever cover scores already read in this pass
-        float r0 = 0.0f, r1 = 0.0f, r2 = 0.0f, r3 = 0.0f;
+          if (j > 0) {
+            // rescale the O_X row (PV_X(j - 1) completed before S_X(j) did)
 #pragma unroll
-        for (int c = 0; c < TK / CW; ++c) {
-          float sc[CW];
-          load_chunk(c, sc);
-          if (one_pass) {
-            const float cm = chunk_max(sc, -INFINITY) * p.sl2;
-            const bool up = cm > m_ref + TAU;
-            if (__any_sync(0xffffffffu, up)) {
-              // this row's reference moves up by k: l, the P chunks already
-              // written for this tile and (after the pass) O scale by 2^-k
-              float a = 1.0f;
-              if (up) {
-                const float k = ceilf(cm - m_ref);
-                a = k < 126.0f ? __int_as_float((127 - (int)k) << 23) : 0.0f;
-                m_ref += k;
-                l *= a;
-                r0 *= a; r1 *= a; r2 *= a; r3 *= a;
-                alpha *= a;
-                need = true;
-              }
-              tmem_st_wait();  // the chunks' P stores have landed
-              for (int g = 0; g < c * CW / 32; ++g) {
-                uint32_t pw[16];
-                tmem_ld16(ts + g * 16, pw);
-                tmem_ld_wait();
-                tmem_regs_ready(pw);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t ro[32];
+              tmem_ld32(t_o + c * 32, ro);
+              tmem_ld_wait();
+              tmem_regs_ready(ro);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const float2 f = unpack_bf16x2(pw[e]);
-                  pw[e] = pack_bf16x2(f.x * a, f.y * a);
-                }
-                tmem_st16(ts + g * 16, pw);
-              }
-              nref = -m_ref;
+              for (int e = 0; e < 32; ++e) ro[e] = __float_as_uint(__uint_as_float(ro[e]) * alpha);
+              tmem_st32(t_o + c * 32, ro);
             }
           }
-#pragma unroll
-          for (int e = 0; e < CW; e += 4) {
-            fma2(sc[e], sc[e + 1], sc[e], sc[e + 1], p.sl2, p.sl2, nref, nref);
-            fma2(sc[e + 2], sc[e + 3], sc[e + 2], sc[e + 3], p.sl2, p.sl2, nref, nref);
-            sc[e] = ex2_ftz(sc[e]);
-            sc[e + 1] = ex2_ftz(sc[e + 1]);
-            sc[e + 2] = ex2_ftz(sc[e + 2]);
-            sc[e + 3] = ex2_ftz(sc[e + 3]);
-            add2(r0, r1, r0, r1, sc[e], sc[e + 1]);
-            add2(r2, r3, r2, r3, sc[e + 2], sc[e + 3]);
-          }
-          uint32_t pk[CW / 2];
-#pragma unroll
-          for (int e = 0; e < CW / 2; ++e) pk[e] = pack_bf16x2(sc[2 * e], sc[2 * e + 1]);
-          tmem_st32(ts + c * 32, pk);
+          weights();
         }
-        l += (r0 + r1) + (r2 + r3);
-        if (j > 0 && __any_sync(0xffffffffu, need)) {
-          // rescale this O_X row (PV_X(j - 1) completed before S_X(j) did)
+        l += sum;
+        {
+          uint32_t h[32];
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t ro[32];
-            tmem_ld32(t_o + c * 32, ro);
-            tmem_ld_wait();
+          for (int c = 0; c < 2; ++c) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ro[e] = __float_as_uint(__uint_as_float(ro[e]) * alpha);
-            tmem_st32(t_o + c * 32, ro);
+            for (int e = 0; e < 32; ++e) h[e] = pk[c * 32 + e];
+            tmem_st32(t_s + c * 32, h);
           }
+        }
+        const int left = w.len - j * TK;  // keys of the sequence from this tile on
+        if (left < TK && (left & 15) && (x == 0 || j >= w.n[0])) {
+          // clear the value rows behind the end, up to the K step's last (8
+          // chunks per 64-column box); j is the item's last tile
+          const int v = nl0 + j + 1, rows = 16 - (left & 15);
+          if (!wait_phase(l_full0 + 8 * (v % NST), (v / NST) & 1, p.err, abort)) *abort = 1;
+          for (int c = r; c < rows * 8 * C::KB; c += TQ) {
+            const int kb = c / (rows * 8), rc = c - kb * (rows * 8);
+            st_shared_v4u(sV + (v % NST) * C::KV_BYTES + kb * C::BOX + (left + rc / 8) * 128 +
+                              (rc % 8) * 16,
+                          0, 0, 0, 0);
+          }
+          fence_proxy_async();  // before the tensor core reads them
         }
         tmem_st_wait();
         tc_fence_before();
@@ -509,7 +570,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       if (!good) break;
       // ---- tile done: O / l and LSE
-      if (!warp_wait(ofull, ko & 1, p.err)) {
+      if (!wait_phase(ofull, ko & 1, p.err, abort)) {
         good = false;
         break;
       }
