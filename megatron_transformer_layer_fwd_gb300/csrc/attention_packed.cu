@@ -23,7 +23,7 @@
 //     dry; and a ring stage holds V_j and K_{j+1}, which the same round needs, so
 //     a round has one wait and one release for both;
 //   - the exponentials are spread between the other steps in a fixed order
-//     (weights() below: 1340 -> 1020 cycles), as only one warp per scheduler is
+//     (form() below: 1340 -> 1020 cycles), as only one warp per scheduler is
 //     at work on a tile. (Two threads per row, 16 softmax warps, took 1070 and a
 //     barrier.)
 // 8177 tokens in two sequences, 32 / 8 heads, D = 128, causal: 184 us, 1490
@@ -40,6 +40,8 @@
 // NaN value is NaN. So the PV product of the last tile takes only the K steps
 // (16 keys) that hold keys of the sequence, and the softmax warps clear the up
 // to 15 value rows behind the end of the last step in shared memory first.
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "packed.cuh"
@@ -85,6 +87,7 @@ struct Params {
   const int4* list;  // entries of 256 rows
   bf16* o;
   int64_t ld_o;
+  int wide;  // o's rows are 32-byte aligned
   float* lse;
   int* err;
   float sl2;  // log2(e) / sqrt(d)
@@ -143,6 +146,13 @@ __device__ __forceinline__ uint32_t v_pack(float lo, float hi) {
   uint32_t r;
   asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// 32 bytes to a 32-byte aligned address: a whole sector by one store.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // Whole warp: waits for the phase, for a bounded time and only while no role has
@@ -404,120 +414,92 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // visible keys of the tile: kv0 .. kv0 + see - 1
         const bool edge = kv0 + TK > w.len || (p.causal && kv0 + TK - 1 > row0);
         const int see = min(w.len, p.causal ? row + 1 : w.len) - kv0;
-        auto mask = [&](int c, float (&sc)[32]) {
-          if (edge) {
+        // the maximum of the 32 scores of chunk c, or m0 if it is larger
+        auto chunk_max = [&](int c, float m0) {
+          uint32_t q[32];
+          tmem_ld32(t_s + c * 32, q);
+          tmem_ld_wait();
+          tmem_regs_ready(q);
+          float m4[4] = {m0, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c * 32 + e >= see) sc[e] = -INFINITY;
+          for (int e = 0; e < 32; e += 2) {
+            const float a = edge && c * 32 + e >= see ? -INFINITY : __uint_as_float(q[e]);
+            const float b = edge && c * 32 + e + 1 >= see ? -INFINITY : __uint_as_float(q[e + 1]);
+            m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], a, b);
           }
+          return fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
         };
         // P = 2^(s log2e / sqrt(d) - m_ref) as bf16 pairs (the row sum takes them
         // unrounded): a relative error of at most 2^-8 per weight, below the
         // output's own rounding after averaging
         uint32_t pk[64];
         float sum = 0.0f;
-        auto weights = [&]() {
+        auto form = [&](auto masked) {
+          // One warp per scheduler has to keep the exponential unit (4 cycles
+          // per instruction) busy by itself: groups of four keys, the exponentials of
+          // one between the sums and packing of the one before and the scaling
+          // of the second next, scores of the next 16 keys on their way.
           const float nref = m_ref == -INFINITY ? 0.0f : -m_ref;
           float r0 = 0.0f, r1 = 0.0f, r2 = 0.0f, r3 = 0.0f;
-          if (edge) {
+          uint32_t q[2][16];
+          float t[4][4];
+          auto scale = [&](int g) {
+            uint32_t z[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t q[32];
-              tmem_ld32(t_s + c * 32, q);
-              tmem_ld_wait();
-              tmem_regs_ready(q);
-              float sc[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) sc[e] = __uint_as_float(q[e]);
-              mask(c, sc);
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                fma2(sc[e], sc[e + 1], sc[e], sc[e + 1], p.sl2, p.sl2, nref, nref);
-                fma2(sc[e + 2], sc[e + 3], sc[e + 2], sc[e + 3], p.sl2, p.sl2, nref, nref);
-                sc[e] = ex2_ftz(sc[e]);
-                sc[e + 1] = ex2_ftz(sc[e + 1]);
-                sc[e + 2] = ex2_ftz(sc[e + 2]);
-                sc[e + 3] = ex2_ftz(sc[e + 3]);
-                add2(r0, r1, r0, r1, sc[e], sc[e + 1]);
-                add2(r2, r3, r2, r3, sc[e + 2], sc[e + 3]);
-                pk[c * 16 + e / 2] = pack_bf16x2(sc[e], sc[e + 1]);
-                pk[c * 16 + e / 2 + 1] = pack_bf16x2(sc[e + 2], sc[e + 3]);
-              }
+            for (int e = 0; e < 4; ++e) {
+              z[e] = q[(g >> 2) & 1][(g & 3) * 4 + e];
+              if constexpr (decltype(masked)::value)
+                if (4 * g + e >= see) z[e] = 0xff800000u;  // -infinity
             }
-          } else {
-            // One warp per scheduler has to keep the exponential unit (4 cycles
-            // per instruction) busy by itself: groups of four keys, the exponentials of
-            // one between the sums and packing of the one before and the scaling
-            // of the second next, scores of the next 32 keys on their way.
-            uint32_t q[2][32];
-            float t[4][4];
-            auto scale = [&](int g) {
-              const uint32_t* z = q[(g >> 3) & 1] + (g & 7) * 4;
-              v_fma2(t[g & 3][0], t[g & 3][1], z[0], z[1], p.sl2, nref);
-              v_fma2(t[g & 3][2], t[g & 3][3], z[2], z[3], p.sl2, nref);
-            };
-            tmem_ld32(t_s, q[0]);
-            tmem_ld_wait();
-            tmem_regs_ready(q[0]);
-            tmem_ld32(t_s + 32, q[1]);
-            scale(0);
-            scale(1);
+            v_fma2(t[g & 3][0], t[g & 3][1], z[0], z[1], p.sl2, nref);
+            v_fma2(t[g & 3][2], t[g & 3][3], z[2], z[3], p.sl2, nref);
+          };
+          tmem_ld16(t_s, q[0]);
+          tmem_ld_wait();
+          tmem_regs_ready(q[0]);
+          tmem_ld16(t_s + 16, q[1]);
+          scale(0);
+          scale(1);
 #pragma unroll
-            for (int g = 0; g < 32; ++g) {
-              float* y = t[g & 3];
-              const float* u = t[(g + 3) & 3];  // group g - 1
-              v_ex2(y[0]);
-              if (g > 0) v_add2(r0, r1, u[0], u[1]);
-              v_ex2(y[1]);
-              if (g > 0) pk[2 * g - 2] = v_pack(u[0], u[1]);
-              v_ex2(y[2]);
-              if (g > 0) v_add2(r2, r3, u[2], u[3]);
-              v_ex2(y[3]);
-              if (g > 0) pk[2 * g - 1] = v_pack(u[2], u[3]);
-              if (g + 2 < 32) {
-                if (((g + 2) & 7) == 0) {
-                  const int c = (g + 2) >> 3;
-                  tmem_ld_wait();
-                  tmem_regs_ready(q[c & 1]);
-                  if (c < 3) tmem_ld32(t_s + (c + 1) * 32, q[(c + 1) & 1]);
-                }
-                scale(g + 2);
+          for (int g = 0; g < 32; ++g) {
+            float* y = t[g & 3];
+            const float* u = t[(g + 3) & 3];  // group g - 1
+            v_ex2(y[0]);
+            if (g > 0) v_add2(r0, r1, u[0], u[1]);
+            v_ex2(y[1]);
+            if (g > 0) pk[2 * g - 2] = v_pack(u[0], u[1]);
+            v_ex2(y[2]);
+            if (g > 0) v_add2(r2, r3, u[2], u[3]);
+            v_ex2(y[3]);
+            if (g > 0) pk[2 * g - 1] = v_pack(u[2], u[3]);
+            if (g + 2 < 32) {
+              if (((g + 2) & 3) == 0) {
+                const int c = (g + 2) >> 2;
+                tmem_ld_wait();
+                tmem_regs_ready(q[c & 1]);
+                if (c < 7) tmem_ld16(t_s + (c + 1) * 16, q[(c + 1) & 1]);
               }
+              scale(g + 2);
             }
-            v_add2(r0, r1, t[3][0], t[3][1]);
-            v_add2(r2, r3, t[3][2], t[3][3]);
-            pk[62] = v_pack(t[3][0], t[3][1]);
-            pk[63] = v_pack(t[3][2], t[3][3]);
           }
+          v_add2(r0, r1, t[3][0], t[3][1]);
+          v_add2(r2, r3, t[3][2], t[3][3]);
+          pk[62] = v_pack(t[3][0], t[3][1]);
+          pk[63] = v_pack(t[3][2], t[3][3]);
           sum = (r0 + r1) + (r2 + r3);
         };
-        bool again = true;
-        if (j > 0) {
-          weights();
-          // (NaN too; no reference yet: every score so far was -infinity)
-          again = __any_sync(0xffffffffu, !(sum <= SUM_LIMIT) || m_ref == -INFINITY);
-        }
-        if (again) {
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // The first reference is the maximum of the first 32 keys (key 0 is
+        // visible to every row): at most the row's, so the sum is at least 1, and
+        // far below it only if the sum shows it.
+        if (j == 0) m_ref = chunk_max(0, -INFINITY) * p.sl2;
+        if (edge) form(std::true_type{});
+        else form(std::false_type{});
+        // (NaN too; no reference: all first scores were -infinity)
+        if (__any_sync(0xffffffffu, !(sum <= SUM_LIMIT) || m_ref == -INFINITY)) {
+          float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t q[32];
-            tmem_ld32(t_s + c * 32, q);
-            tmem_ld_wait();
-            tmem_regs_ready(q);
-            float sc[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) sc[e] = __uint_as_float(q[e]);
-            mask(c, sc);
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              m4[0] = fmax3(m4[0], sc[e], sc[e + 1]);
-              m4[1] = fmax3(m4[1], sc[e + 2], sc[e + 3]);
-              m4[2] = fmax3(m4[2], sc[e + 4], sc[e + 5]);
-              m4[3] = fmax3(m4[3], sc[e + 6], sc[e + 7]);
-            }
-          }
-          const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * p.sl2;
+          for (int c = 0; c < 4; ++c) mx = chunk_max(c, mx);
+          mx *= p.sl2;
           float alpha = 1.0f;
           if (mx > m_ref) {
             alpha = exp2f(m_ref - mx);
@@ -537,7 +519,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               tmem_st32(t_o + c * 32, ro);
             }
           }
-          weights();
+          form(std::true_type{});  // (masks nothing inside)
         }
         l += sum;
         {
@@ -579,7 +561,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
       const bool row_ok = row < w.len;
       bf16* out = p.o + (int64_t)(w.a + row) * p.ld_o + w.h * D;
-      store_tmem_row<D>(t_o, inv, row_ok ? out : nullptr);
+      if (p.wide) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t q[32], h[16];
+          tmem_ld32(t_o + c * 32, q);
+          tmem_ld_wait();
+          tmem_regs_ready(q);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            h[e] = pack_bf16x2(__uint_as_float(q[2 * e]) * inv, __uint_as_float(q[2 * e + 1]) * inv);
+          if (row_ok) {
+            st_global_32(out + c * 32, h);
+            st_global_32(out + c * 32 + 16, h + 8);
+          }
+        }
+      } else {
+        store_tmem_row<D>(t_o, inv, row_ok ? out : nullptr);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(oempty);
@@ -611,6 +610,7 @@ mgb_status fwd_d(const PackedArgs& a, cudaStream_t st) {
   p.nq = a.nq; p.group = a.nq / a.nkv; p.causal = a.causal; p.tokens = a.tokens;
   p.hdr = a.hdr256; p.list = a.list256;
   p.o = static_cast<bf16*>(a.o); p.ld_o = a.ld_o; p.lse = a.lse;
+  p.wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0 && a.ld_o % 16 == 0;
   p.err = device_error_word();
   if (p.err == nullptr) return MGB_ERR_CUDA;
   p.sl2 = LOG2E / sqrtf((float)D);
