@@ -2,13 +2,15 @@
 // softmax(Q_h K_g^T / sqrt(d)) V_g within each sequence, optionally causal, and
 // its log-sum-exp. Exact float32 products (no TF32), online softmax.
 //
-// A block of 256 threads takes 128 query rows of one (sequence, head) and walks
-// key tiles of 64. Thread (ty, tx) of a 16 x 16 grid holds rows 8 ty .. + 7 and
+// A block of 128 threads takes 64 query rows of one (sequence, head) and walks
+// key tiles of BN. Thread (ty, tx) of an 8 x 16 grid holds rows 8 ty .. + 7 and
 // keys tx + 16 c of the score tile, then the same rows and columns 4 tx + 64 c ..
-// + 3 of the output: per 4 (inner) steps the scores take 12 16-byte
-// shared-memory reads for 128 FMAs, the output product 8 + 8 for 256 (D = 128),
-// so the FMA pipe is the bound. K of the next tile is copied while the softmax
-// and the second product run, V of this one while the scores are formed.
+// + 3 of the output: per 4 (inner) steps the scores take 8 + BN / 16 16-byte
+// shared-memory reads for 2 BN FMAs (two per instruction), the output product
+// 8 + 4 D / 64 for 2 D, so the FMA pipe is the bound (8 x 1000 tokens, 16 heads:
+// 35 TFLOP/s at either head dim). K of the next tile is copied while the softmax and
+// the second product run, V of this one while the scores are formed. Three
+// (D = 64) or two blocks per SM fill each other's barriers and softmax.
 // Rows behind the sequence are zeros in shared memory (never read).
 #include "common.cuh"
 #include "internal.h"
@@ -18,18 +20,22 @@ namespace mgb {
 
 namespace {
 
-constexpr int BM = 128, BN = 64, NT = 256;
-constexpr int PS = BN + 4;  // row stride of P (floats)
+constexpr int NT = 128;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
-template <int D>
+template <int D, int RPT>
 struct Cfg {
+  static constexpr int BM = 8 * RPT;              // query rows per block
+  static constexpr int BN = D == 64 ? 64 : 32;    // keys per tile
+  static constexpr int BLOCKS = D == 64 ? 3 : 2;  // per SM
+  static constexpr int PS = BN + 4;               // row stride of P (floats)
   static constexpr int RS = D + 4;  // row stride of Q, K, V (floats): 16 rows' float4 hit all banks
   static constexpr int OFF_K = BM * RS;
   static constexpr int OFF_V = OFF_K + BN * RS;
   static constexpr int OFF_P = OFF_V + BN * RS;
   static constexpr int SMEM = (OFF_P + BM * PS) * 4;
+  static_assert((SMEM + 1024) * BLOCKS <= 228 * 1024, "blocks per SM");
 };
 
 struct Params {
@@ -55,19 +61,27 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int D>
-__global__ void __launch_bounds__(NT, D == 64 ? 2 : 1) packed_f32_kernel(const Params p) {
-  using C = Cfg<D>;
-  constexpr int RS = C::RS, OC = D / 64;  // 4-column groups per thread
+// RPT: query rows per thread
+template <int D, int RPT>
+__global__ void __launch_bounds__(NT, Cfg<D, RPT>::BLOCKS) packed_f32_kernel(const Params p) {
+  using C = Cfg<D, RPT>;
+  constexpr int RS = C::RS, PS = C::PS, BN = C::BN, BM = C::BM, PARTS = 128 / BM;
+  constexpr int OC = D / 64, KC = BN / 16;  // 4-column groups, keys per thread
   extern __shared__ __align__(16) float sh[];
   float *sq = sh, *sk = sh + C::OFF_K, *sv = sh + C::OFF_V, *sp = sh + C::OFF_P;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int n_items = p.hdr->entries * p.nq;
+  const int n_items = p.hdr->entries * PARTS * p.nq;  // an entry is 128 rows
   const uint32_t bq = smem_u32(sq), bk = smem_u32(sk), bv = smem_u32(sv);
 
-  for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
-    const int4 e = p.list[i / p.nq];
-    const int h = i % p.nq, len = e.y, q0 = e.z;
+  // snake order over the list (longest first), as in the bf16 kernel
+  auto item_index = [&](int turn) {
+    const int g = (int)gridDim.x, c = (int)blockIdx.x;
+    return turn * g + ((turn & 1) ? g - 1 - c : c);
+  };
+  for (int turn = 0, i = item_index(0); i < n_items; ++turn, i = item_index(turn)) {
+    const int4 e = p.list[i / (PARTS * p.nq)];
+    const int h = i % p.nq, len = e.y, q0 = e.z + (i / p.nq % PARTS) * BM;
+    if (q0 >= len) continue;
     const float* Q = p.q + (int64_t)(e.x + q0) * p.ld_q + (int64_t)h * D;
     const float* K = p.k + (int64_t)e.x * p.ld_kv + (int64_t)(h / p.group) * D;
     const float* V = p.v + (int64_t)e.x * p.ld_kv + (int64_t)(h / p.group) * D;
@@ -85,9 +99,9 @@ __global__ void __launch_bounds__(NT, D == 64 ? 2 : 1) packed_f32_kernel(const P
     copy(bq, Q, p.ld_q, BM, rows);
     copy(bk, K, p.ld_kv, BN, len);
     cp_async_commit();
-    float acc[8][4 * OC], m[8], l[8];
+    float acc[RPT][4 * OC], m[RPT], l[RPT];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
+    for (int r = 0; r < RPT; ++r) {
       m[r] = -INFINITY;
       l[r] = 0.0f;
 #pragma unroll
@@ -100,33 +114,31 @@ __global__ void __launch_bounds__(NT, D == 64 ? 2 : 1) packed_f32_kernel(const P
       cp_async_commit();
       cp_async_wait<1>();  // Q and this tile's K
       __syncthreads();
-      float s[8][4] = {};
+      float s[RPT][KC] = {}, s2[RPT][KC] = {};  // sums over even and odd inner indices
 #pragma unroll 4
       for (int f = 0; f < D; f += 4) {
-        float4 kk[4];
+        float4 kk[KC];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) kk[c] = *reinterpret_cast<const float4*>(sk + (tx + 16 * c) * RS + f);
+        for (int c = 0; c < KC; ++c) kk[c] = *reinterpret_cast<const float4*>(sk + (tx + 16 * c) * RS + f);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float4 qq = *reinterpret_cast<const float4*>(sq + (8 * ty + r) * RS + f);
+        for (int r = 0; r < RPT; ++r) {
+          const float4 qq = *reinterpret_cast<const float4*>(sq + (RPT * ty + r) * RS + f);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            s[r][c] = fmaf(qq.x, kk[c].x, s[r][c]);
-            s[r][c] = fmaf(qq.y, kk[c].y, s[r][c]);
-            s[r][c] = fmaf(qq.z, kk[c].z, s[r][c]);
-            s[r][c] = fmaf(qq.w, kk[c].w, s[r][c]);
+          for (int c = 0; c < KC; ++c) {
+            fma2(s[r][c], s2[r][c], qq.x, qq.y, kk[c].x, kk[c].y, s[r][c], s2[r][c]);
+            fma2(s[r][c], s2[r][c], qq.z, qq.w, kk[c].z, kk[c].w, s[r][c], s2[r][c]);
           }
         }
       }
       const bool edge = k0 + BN > len || (p.causal && k0 + BN - 1 > q0);
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
+      for (int r = 0; r < RPT; ++r) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < KC; ++c) {
           const int key = k0 + tx + 16 * c;
-          s[r][c] *= p.sl2;
-          if (edge && (key >= len || (p.causal && key > q0 + 8 * ty + r))) s[r][c] = -INFINITY;
+          s[r][c] = (s[r][c] + s2[r][c]) * p.sl2;
+          if (edge && (key >= len || (p.causal && key > q0 + RPT * ty + r))) s[r][c] = -INFINITY;
           mx = fmaxf(mx, s[r][c]);
         }
 #pragma unroll
@@ -140,10 +152,10 @@ __global__ void __launch_bounds__(NT, D == 64 ? 2 : 1) packed_f32_kernel(const P
         }
         const float mr = m[r] == -INFINITY ? 0.0f : m[r];  // -infinity: every score so far is
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < KC; ++c) {
           s[r][c] = exp2f(s[r][c] - mr);
           l[r] += s[r][c];
-          sp[(8 * ty + r) * PS + tx + 16 * c] = s[r][c];
+          sp[(RPT * ty + r) * PS + tx + 16 * c] = s[r][c];
         }
       }
       __syncthreads();  // K is read, P written
@@ -160,26 +172,25 @@ __global__ void __launch_bounds__(NT, D == 64 ? 2 : 1) packed_f32_kernel(const P
           for (int c = 0; c < OC; ++c)
             vv[g][c] = *reinterpret_cast<const float4*>(sv + (f + g) * RS + 4 * tx + 64 * c);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float4 w = *reinterpret_cast<const float4*>(sp + (8 * ty + r) * PS + f);
+        for (int r = 0; r < RPT; ++r) {
+          const float4 w = *reinterpret_cast<const float4*>(sp + (RPT * ty + r) * PS + f);
           const float ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int g = 0; g < 4; ++g)
 #pragma unroll
             for (int c = 0; c < OC; ++c) {
-              acc[r][4 * c] = fmaf(ww[g], vv[g][c].x, acc[r][4 * c]);
-              acc[r][4 * c + 1] = fmaf(ww[g], vv[g][c].y, acc[r][4 * c + 1]);
-              acc[r][4 * c + 2] = fmaf(ww[g], vv[g][c].z, acc[r][4 * c + 2]);
-              acc[r][4 * c + 3] = fmaf(ww[g], vv[g][c].w, acc[r][4 * c + 3]);
+              float* o = acc[r] + 4 * c;
+              fma2(o[0], o[1], ww[g], ww[g], vv[g][c].x, vv[g][c].y, o[0], o[1]);
+              fma2(o[2], o[3], ww[g], ww[g], vv[g][c].z, vv[g][c].w, o[2], o[3]);
             }
         }
       }
     }
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
+    for (int r = 0; r < RPT; ++r) {
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-      const int row = 8 * ty + r;
+      const int row = RPT * ty + r;
       if (row >= rows) continue;
       const float inv = l[r] > 0.0f ? 1.0f / l[r] : 0.0f;
       float* o = p.o + (int64_t)(e.x + q0 + row) * p.ld_o + (int64_t)h * D;
@@ -195,14 +206,24 @@ __global__ void __launch_bounds__(NT, D == 64 ? 2 : 1) packed_f32_kernel(const P
   cp_async_wait<0>();
 }
 
-template <int D>
+template <int D, int RPT>
 mgb_status launch(const Params& p, int64_t most, cudaStream_t st) {
-  auto k = packed_f32_kernel<D>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM) != cudaSuccess)
+  using C = Cfg<D, RPT>;
+  auto k = packed_f32_kernel<D, RPT>;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return MGB_ERR_CUDA;
-  const int64_t slots = (int64_t)device_sm_count() * (D == 64 ? 2 : 1);
-  k<<<(int)(most < slots ? most : slots), NT, Cfg<D>::SMEM, st>>>(p);
+  const int64_t items = most * (128 / C::BM), slots = (int64_t)device_sm_count() * C::BLOCKS;
+  k<<<(int)(items < slots ? items : slots), NT, C::SMEM, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? MGB_OK : MGB_ERR_CUDA;
+}
+
+// 64 query rows per block, or 32 while 64 would leave less than three blocks per
+// slot (`most`: 128-row entries x heads at most): D = 64, 32 heads, 3 x 900
+// tokens (3.2 per slot) 358 us against 369, 2 x 600 (1.4) 211 against 198.
+template <int D>
+mgb_status launch_d(const Params& p, int64_t most, cudaStream_t st) {
+  return 2 * most < 3 * (int64_t)device_sm_count() * Cfg<D, 8>::BLOCKS ? launch<D, 4>(p, most, st)
+                                                                     : launch<D, 8>(p, most, st);
 }
 
 }  // namespace
@@ -216,7 +237,7 @@ mgb_status attention_packed_f32(const PackedArgs& a, cudaStream_t st) {
   p.ld_q = a.ld_q; p.ld_kv = a.ld_kv;
   p.o = static_cast<float*>(a.o); p.ld_o = a.ld_o; p.lse = a.lse;
   p.sl2 = LOG2E / sqrtf((float)a.d);
-  return a.d == 64 ? launch<64>(p, a.max128 * a.nq, st) : launch<128>(p, a.max128 * a.nq, st);
+  return a.d == 64 ? launch_d<64>(p, a.max128 * a.nq, st) : launch_d<128>(p, a.max128 * a.nq, st);
 }
 
 }  // namespace mgb

@@ -205,8 +205,8 @@ mgb_status mgb_attention_packed_fwd(const mgb_attention_packed_plan* plan, int32
     return MGB_ERR_MISALIGNED;
   const Layout l = make_layout(plan->n_seqs, plan->tokens);
   if (plan->ws_bytes < l.total) return MGB_ERR_WORKSPACE_TOO_SMALL;
-  // item numbers (entries x heads) are 32-bit
-  if (l.max128 * n_q_heads >= (int64_t)1 << 31) return MGB_ERR_UNSUPPORTED;
+  // item numbers (entries x heads, up to four per entry) are 32-bit
+  if (4 * l.max128 * n_q_heads >= (int64_t)1 << 30) return MGB_ERR_UNSUPPORTED;
   const mgb_status s = check_arch();
   if (s != MGB_OK) return s;
   if (plan->n_seqs == 0 || plan->tokens == 0) return MGB_OK;
