@@ -3,17 +3,17 @@
 // optionally causal, and its log-sum-exp.
 //
 // A work item is 256 query rows of one (sequence, head), in two tiles A and B
-// of 128 that take turns on the tensor core. Per 128 keys the MMA warp issues
+// of 128 that take turns on the tensor core. Per 128 keys the MMA thread issues
 // PV_A(j), S_A(j+1), PV_B(j), S_B(j+1); while tile A's scores are turned into
-// weights, tile B's two products run. TMEM (512 columns) holds S_A, S_B, O_A, O_B; a
-// tile's weights P (bf16 pairs) overwrite scores already read and are read from
-// there by PV.
+// weights, tile B's two products run. TMEM (512 columns) holds the scores and O_A,
+// O_B; a tile's weights P (bf16 pairs) overwrite scores already read and are
+// read from there by PV.
 //
 // Each tile goes round a chain: scores complete - softmax - weights ready -
 // PV and the next scores (16 products of 64 cycles) - scores complete. Two
 // tiles cover the tensor core only as far as that chain is short (measured at
-// D = 128, in cycles: softmax 1020, to the MMA warp 220, products 1270; the
-// tensor core is busy for 2048 of the 2515). What shortens it:
+// D = 128, in cycles: softmax 1040, to the MMA thread 170, products 1270; the
+// tensor core is busy for 2048 of the 2500). What shortens it:
 //   - the row maximum is not on it: weights are formed in log2 units with the
 //     reference maximum so far, and only if a row's then sum to more than
 //     SUM_LIMIT (each is at most the sum) does its warp take the maximum, move the
@@ -26,8 +26,14 @@
 //     (form() below: 1340 -> 1020 cycles), as only one warp per scheduler is
 //     at work on a tile. (Two threads per row, 16 softmax warps, took 1070 and a
 //     barrier.)
-// 8177 tokens in two sequences, 32 / 8 heads, D = 128, causal: 184 us, 1490
-// TFLOP/s.
+// Where TMEM has room the next scores are formed before the weights are done,
+// which takes the products off the chain: at D = 64 in three score buffers that
+// the tasks of both tiles take in turn, and for an item whose tile B is empty
+// in the two buffers by turns.
+//
+// Measured (causal but the last): two sequences of 4012 and 4165 tokens, 32 / 8
+// heads: D = 128 179 us, 1530 TFLOP/s; 2 x 4096, D = 64 119 us, 1160 TFLOP/s;
+// 8 x 1024, D = 128, no mask 96 us, 1430 TFLOP/s.
 //
 // Items come from a list that the prepare kernel derives from the row offsets
 // (longest first, so that the snake order of item_index evens the CTAs out);
@@ -55,7 +61,6 @@ namespace {
 
 constexpr int TQ = 128;         // query rows per tile (TMEM lanes)
 constexpr int TK = 128;         // keys per KV tile
-constexpr int NST = 2;          // ring stages, each a K tile and the V tile before it
 constexpr int NSOFTW = 4;       // softmax warps per tile
 constexpr int NTHREADS = 320;   // MMA warp, producer warp, 2 x 4 softmax warps
 constexpr float LOG2E = 1.4426950408889634f;
@@ -64,25 +69,40 @@ constexpr float SUM_LIMIT = 8192.0f;  // of a row's weights in a tile
 
 template <int D>
 struct Cfg2 {
+  static constexpr int NB = D == 64 ? 3 : 2;            // score buffers in TMEM
+  static constexpr int NST = D == 64 ? 4 : 2;           // ring stages: V_j and K_{j+1}
   static constexpr int KB = D / 64;                     // 64-wide d boxes
   static constexpr int BOX = 128 * 128;                 // bytes of one [128][64] box
   static constexpr int Q_BYTES = TQ * D * 2;
   static constexpr int KV_BYTES = TK * D * 2;
-  static constexpr int OFF_QA = 0;
-  static constexpr int OFF_QB = Q_BYTES;
-  static constexpr int OFF_K = 2 * Q_BYTES;
-  static constexpr int OFF_V = OFF_K + NST * KV_BYTES;
+  static constexpr int OFF_Q = 0;                       // [tile]
+  static constexpr int OFF_K = 2 * Q_BYTES;             // [stage]
+  static constexpr int OFF_V = OFF_K + NST * KV_BYTES;  // [stage]
   static constexpr int OFF_BAR = OFF_V + NST * KV_BYTES;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;     // barriers, alignment slack
-  static constexpr int COL_S = 0;                       // S_A at 0, S_B at TK
-  static constexpr int COL_O = 2 * TK;                  // O_A, then O_B at + D
+  static constexpr int COL_S = 0;                       // score buffers
+  static constexpr int COL_O = NB * TK;                 // O_A, then O_B at + D
   static constexpr int TMEM_COLS = 512;
   static_assert(COL_O + 2 * D <= TMEM_COLS, "TMEM budget");
   static_assert(SMEM <= 232448, "shared memory budget");
+  // Barriers (8 bytes each). A waiter sees every phase of a barrier or knows that
+  // at most one is outstanding (parity). Up to two tasks of a tile are under way,
+  // so the barriers of scores and weights take turns by the tile's task count.
+  static constexpr int Q_FULL = 0;              // the item's Q tiles loaded          (tx)
+  static constexpr int Q_EMPTY = 1;             // the item's last S product done     (commit)
+  static constexpr int L_FULL = 2;              // [stage] loaded                    (tx)
+  static constexpr int L_EMPTY = L_FULL + NST;  // [stage] products with it done     (commit)
+  static constexpr int S_FULL = L_EMPTY + NST;  // [tile][task & 1] scores complete  (commit)
+  static constexpr int P_FULL = S_FULL + 4;     // [tile][task & 1] weights written  (4: one per warp)
+  static constexpr int O_FULL = P_FULL + 4;     // [tile] the item's last PV done     (commit)
+  static constexpr int O_EMPTY = O_FULL + 2;    // [tile] O read out                 (4: one per warp)
+  static constexpr int N_BAR = O_EMPTY + 2;
+  static_assert(N_BAR * 8 <= 232, "barriers");
 };
 
 struct Params {
-  int nq, group, causal, tokens;
+  int nq, causal, tokens;
+  uint64_t m_nq, m_group;  // div_by of nq and of the group size nq / nkv
   const PackedHeader* hdr;
   const int4* list;  // entries of 256 rows
   bf16* o;
@@ -93,27 +113,24 @@ struct Params {
   float sl2;  // log2(e) / sqrt(d)
 };
 
-struct Item {
-  int a, len, q0, h, n[2];  // sequence's first row and length; first query row in it; head;
-                            // key tiles of tile A and B
+// A number for each of the tiles A (0) and B (1); selected, not indexed, so that
+// it stays in registers.
+struct PerTile {
+  int a, b;
+  __device__ int operator[](int x) const { return x ? b : a; }
+  __device__ void inc(int x) { (x ? b : a) += 1; }
 };
 
-// Item i: entry i / nq, head i % nq (the heads of a group next to each other
-// share their keys and values in L2).
-__device__ __forceinline__ Item item_of(int i, const Params& p) {
-  const int4 e = p.list[i / p.nq];
-  Item it;
-  it.a = e.x;
-  it.len = e.y;
-  it.q0 = e.z;
-  it.h = i % p.nq;
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int r0 = it.q0 + x * TQ;
-    const int end = p.causal ? min(it.len, r0 + TQ) : it.len;
-    it.n[x] = r0 < it.len ? (end + TK - 1) / TK : 0;
-  }
-  return it;
+// An item: 256 query rows of one (sequence, head).
+struct Job {
+  int a, len;    // the sequence's first row and length
+  int q, h;      // first query row in it (tile B: + 128), head
+  PerTile n;     // key tiles (B 0, or at least A's)
+};
+
+// i / d for i < 2^31 by one high product; `m` = 2^64 / d rounded up, 0 for d = 1.
+__device__ __forceinline__ int div_by(int i, uint64_t m) {
+  return m == 0 ? i : (int)__umul64hi((uint64_t)(uint32_t)i, m);
 }
 
 // The item a CTA takes in its k-th round: snake order over the list, as in the
@@ -122,6 +139,45 @@ __device__ __forceinline__ int item_index(int k) {
   const int g = (int)gridDim.x, c = (int)blockIdx.x;
   return k * g + ((k & 1) ? g - 1 - c : c);
 }
+
+// A CTA's items in order, the same for every role: item i is entry i / nq of the
+// list and head i % nq (the heads of a group next to each other share their keys
+// and values in L2). The next item's entry is requested one item ahead.
+struct Jobs {
+  int k, n_items;
+  int i, h;  // next item, its head
+  int4 e;    // its entry
+  Job w;
+  __device__ void fetch(const Params& p) {
+    i = item_index(k++);
+    if (i < n_items) {
+      const int u = div_by(i, p.m_nq);
+      h = i - u * p.nq;
+      e = p.list[u];
+    }
+  }
+  __device__ bool begin(int items, const Params& p) {
+    n_items = items;
+    k = 0;
+    fetch(p);
+    return next(p);
+  }
+  // false: no more items
+  __device__ bool next(const Params& p) {
+    if (i >= n_items) return false;
+    w.a = e.x;
+    w.len = e.y;
+    w.q = e.z;
+    w.h = h;
+    auto tiles = [&](int q0) {
+      const int end = p.causal ? min(w.len, q0 + TQ) : w.len;
+      return q0 < w.len ? (end + TK - 1) / TK : 0;
+    };
+    w.n = {tiles(w.q), tiles(w.q + TQ)};
+    fetch(p);
+    return true;
+  }
+};
 
 // The steps of the weights in an order that the compiler keeps (volatile): see
 // the softmax warps.
@@ -196,21 +252,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_u32(smem);
-  const uint32_t sQ[2] = {sb + C::OFF_QA, sb + C::OFF_QB};
-  const uint32_t sK = sb + C::OFF_K, sV = sb + C::OFF_V;
-  const uint32_t bar = sb + C::OFF_BAR;
-  const uint32_t q_full = bar;         // both Q tiles loaded                   (tx)
-  const uint32_t q_empty = bar + 8;    // the item's last S product done        (commit)
-  const uint32_t l_full0 = bar + 16;   // [2] stage loaded                      (tx)
-  const uint32_t l_empty0 = bar + 32;  // [2] products with it done             (commit)
-  const uint32_t s_full0 = bar + 80;   // [tile] S_X(j) complete                (commit)
-  const uint32_t p_full0 = bar + 96;   // [tile] P_X(j) written, O_X rescaled   (4: one per warp)
-  const uint32_t o_full0 = bar + 112;  // [tile] the item's last PV_X done      (commit)
-  const uint32_t o_empty0 = bar + 128; // [tile] O_X read out                   (4: one per warp)
+  const uint32_t sQ = sb + C::OFF_Q, sK = sb + C::OFF_K, sV = sb + C::OFF_V;
+  constexpr int NB = C::NB, NST = C::NST;
+  auto bar = [&](int which) { return sb + C::OFF_BAR + 8 * which; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 240);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 244);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();  // the list and the inputs may come from the kernel before
   const int n_items = p.hdr->entries * p.nq;
   if ((int)blockIdx.x >= n_items) return;
 
@@ -218,16 +267,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(l_full0 + 8 * i, 1);
-      mbar_init(l_empty0 + 8 * i, 1);
-      mbar_init(s_full0 + 8 * i, 1);
-      mbar_init(p_full0 + 8 * i, NSOFTW);
-      mbar_init(o_full0 + 8 * i, 1);
-      mbar_init(o_empty0 + 8 * i, NSOFTW);
-    }
+    for (int i = 0; i < C::N_BAR; ++i)
+      mbar_init(bar(i), (i >= C::P_FULL && i < C::O_FULL) || i >= C::O_EMPTY ? NSOFTW : 1);
     fence_mbar_init();
     *abort = 0;
   }
@@ -237,176 +278,243 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp < 2) {
   if (warp == 1) {
-    // ---------------- producer: per item Q_A, Q_B, then the stages (K_0),
-    // (V_0, K_1), (V_1, K_2), .., (V_last)
-    if (lane == 0) {
-      int nl = 0;  // stages loaded so far
-      for (int k = 0, i = item_index(0); i < n_items && !*abort; ++k, i = item_index(k)) {
-        const Item w = item_of(i, p);
-        const int xcol = (w.h / p.group) * D;
-        // the item lies in the tensors and the TMA x coordinates are 16-byte
-        // multiples (head columns: multiples of 64)
-        if (!dcheck(w.a >= 0 && w.q0 >= 0 && w.q0 < w.len && w.len <= p.tokens - w.a &&
-                        w.h < p.nq && (xcol & 7) == 0 && ((w.h * D) & 7) == 0,
-                    p.err)) {
-          *abort = 1;
-          break;
-        }
-        if (k >= 1 && !mbar_wait(q_empty, (k - 1) & 1, p.err)) {
-          *abort = 1;
-          break;
-        }
-        mbar_arrive_expect_tx(q_full, (w.n[1] > 0 ? 2 : 1) * C::Q_BYTES);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (w.n[x] == 0) continue;
-#pragma unroll
-          for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_2d(sQ[x] + kb * C::BOX, &tmQ, w.h * D + kb * 64, w.a + w.q0 + x * TQ, q_full);
-        }
-        const int nt = max(w.n[0], w.n[1]);
-        bool good = true;
-        for (int j = 0; j <= nt; ++j, ++nl) {
-          const int s = nl % NST;
-          if (nl >= NST && !mbar_wait(l_empty0 + 8 * s, ((nl - NST) / NST) & 1, p.err)) {
-            good = false;
-            break;
-          }
-          mbar_arrive_expect_tx(l_full0 + 8 * s, (j > 0 && j < nt ? 2 : 1) * C::KV_BYTES);
-          if (j > 0)
-#pragma unroll
-            for (int kb = 0; kb < C::KB; ++kb)
-              tma_load_2d(sV + s * C::KV_BYTES + kb * C::BOX, &tmV, xcol + kb * 64,
-                          w.a + (j - 1) * TK, l_full0 + 8 * s);
-          if (j < nt)
-#pragma unroll
-            for (int kb = 0; kb < C::KB; ++kb)
-              tma_load_2d(sK + s * C::KV_BYTES + kb * C::BOX, &tmK, xcol + kb * 64, w.a + j * TK,
-                          l_full0 + 8 * s);
-        }
-        if (!good) {
-          *abort = 1;
-          break;
-        }
-      }
-    }
-  } else if (warp == 0) {
-    // ---------------- MMA issuer: one thread
+    // ---------------- producer (one thread): per item the Q tiles, then the
+    // stages (K_0), (V_0, K_1), .., (V_last)
     if (elect_one()) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(TQ, TK, 0, 0);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(TQ, D, 0, 1);
-      const uint64_t dq0[2] = {smem_desc_sw128(sQ[0], 16, 1024), smem_desc_sw128(sQ[1], 16, 1024)};
-      const uint64_t dk0 = smem_desc_sw128(sK, 16, 1024);
-      const uint64_t dv0 = smem_desc_sw128(sV, C::BOX, 1024);
-      int nl = 0;             // stages consumed so far
-      int np[2] = {0, 0};     // PV products of each tile so far (p_full phases)
-      int no[2] = {0, 0};     // items with a non-empty tile X so far (o_full / o_empty phases)
+      int nl = 0;  // stages loaded so far
+      int k = 0;   // items so far
       bool good = true;
-      // S_X = Q_X K^T into tile X's score columns (K stage sk)
-      auto issue_s = [&](int x, int sk) {
-        const uint64_t db = dk0 + (uint64_t)((sk * C::KV_BYTES) >> 4);
-        const uint32_t td = tmem + C::COL_S + x * TK;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::BOX + (kk & 3) * 32;
-          tc_mma_f16(td, dq0[x] + (uint64_t)(off >> 4), db + (uint64_t)(off >> 4), idesc_s, kk > 0);
-        }
-        tc_commit(s_full0 + 8 * x);
-      };
-      for (int k = 0, i = item_index(0); i < n_items && good; ++k, i = item_index(k)) {
-        const Item w = item_of(i, p);
-        const int nt = max(w.n[0], w.n[1]);
-        const int s0 = nl % NST;
-        if (!wait_phase_1(q_full, k & 1, p.err, abort) ||
-            !wait_phase_1(l_full0 + 8 * s0, (nl / NST) & 1, p.err, abort)) {
+      Jobs js;
+      for (bool more = js.begin(n_items, p); more && good; more = js.next(p), ++k) {
+        const Job& w = js.w;
+        const int xkv = div_by(w.h, p.m_group) * D;
+        // the item lies in the tensors (TMA x coordinates are multiples of 64)
+        if (!dcheck(w.a >= 0 && w.q >= 0 && w.q < w.len && w.len <= p.tokens - w.a && w.h < p.nq,
+                    p.err) ||
+            (k >= 1 && !wait_phase_1(bar(C::Q_EMPTY), (k - 1) & 1, p.err, abort))) {
           good = false;
           break;
         }
-        tc_fence_after();
+        mbar_arrive_expect_tx(bar(C::Q_FULL), (w.n[1] > 0 ? 2 : 1) * C::Q_BYTES);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          if (w.n[x] > 0) issue_s(x, s0);
-        tc_commit(l_empty0 + 8 * s0);
-        if (nt == 1) tc_commit(q_empty);
-        ++nl;
-        for (int j = 0; j < nt && good; ++j) {
-          const int s = nl % NST;  // V_j, K_{j+1}
-          if (!wait_phase_1(l_full0 + 8 * s, (nl / NST) & 1, p.err, abort)) {
+          if (w.n[x] > 0)
+#pragma unroll
+            for (int kb = 0; kb < C::KB; ++kb)
+              tma_load_2d(sQ + x * C::Q_BYTES + kb * C::BOX, &tmQ, w.h * D + kb * 64, w.a + w.q + x * TQ,
+                          bar(C::Q_FULL));
+        const int nt = max(w.n[0], w.n[1]);
+        for (int j = 0; j <= nt && good; ++j, ++nl) {
+          const int s = nl % NST;
+          if (nl >= NST && !wait_phase_1(bar(C::L_EMPTY + s), ((nl - NST) / NST) & 1, p.err, abort)) {
             good = false;
             break;
           }
-          const int left = w.len - j * TK;  // keys of the sequence from this tile on
-          const int steps = left >= TK ? TK / 16 : (left + 15) / 16;
-          const uint64_t db = dv0 + (uint64_t)((s * C::KV_BYTES) >> 4);
+          const uint32_t full = bar(C::L_FULL + s), dk = sK + s * C::KV_BYTES,
+                         dv = sV + s * C::KV_BYTES;
+          mbar_arrive_expect_tx(full, (j > 0 && j < nt ? 2 : 1) * C::KV_BYTES);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!good || j >= w.n[x]) continue;
-            // O_X of the previous item read out before this item's first PV_X
-            if ((j == 0 && no[x] >= 1 &&
-                 !wait_phase_1(o_empty0 + 8 * x, (no[x] - 1) & 1, p.err, abort)) ||
-                !wait_phase_1(p_full0 + 8 * x, np[x] & 1, p.err, abort)) {
-              good = false;
-              continue;
-            }
-            tc_fence_after();
-            const uint32_t ta = tmem + C::COL_S + x * TK, to = tmem + C::COL_O + x * D;
-            if (steps == TK / 16) {
-#pragma unroll
-              for (int kk = 0; kk < TK / 16; ++kk)
-                tc_mma_f16_ts(to, ta + kk * 8, db + (uint64_t)((kk * 2048) >> 4),
-                              idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-            } else {
-#pragma unroll 1
-              for (int kk = 0; kk < steps; ++kk)
-                tc_mma_f16_ts(to, ta + kk * 8, db + (uint64_t)((kk * 2048) >> 4),
-                              idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-            }
-            ++np[x];
-            if (j == w.n[x] - 1) {
-              tc_commit(o_full0 + 8 * x);
-              ++no[x];
-            } else {
-              issue_s(x, s);
-            }
+          for (int kb = 0; kb < C::KB; ++kb) {
+            if (j > 0) tma_load_2d(dv + kb * C::BOX, &tmV, xkv + kb * 64, w.a + (j - 1) * TK, full);
+            if (j < nt) tma_load_2d(dk + kb * C::BOX, &tmK, xkv + kb * 64, w.a + j * TK, full);
           }
-          if (!good) break;
-          tc_commit(l_empty0 + 8 * s);
-          ++nl;
-          // the item's last score product has been issued once j + 1 == nt - 1
-          if (j + 2 == nt) tc_commit(q_empty);
         }
       }
       if (!good) *abort = 1;
     }
     __syncwarp();
-  }
+  } else if (warp == 0) {
+    // ---------------- MMA issuer: one thread
+    if (elect_one()) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(TQ, TK, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(TQ, D, 0, 1);
+      const uint64_t dq0 = smem_desc_sw128(sQ, 16, 1024);
+      const uint64_t dk0 = smem_desc_sw128(sK, 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(sV, C::BOX, 1024);
+      int nl = 0;             // stages consumed so far
+      PerTile nt_ = {0, 0};   // tasks of each tile whose PV products are issued
+      PerTile ns = {0, 0};    // .. whose S products are issued
+      PerTile no = {0, 0};    // items of each tile so far
+      bool good = true;
+      Jobs js;
+      int k = 0;
+      for (bool more = js.begin(n_items, p); more && good; more = js.next(p), ++k) {
+        const Job& w = js.w;
+        const int n0 = w.n[0], n1 = w.n[1], nt = max(n0, n1), st0 = nl;
+        // S_X(j) = Q_X K_j^T into score buffer buf (stage st)
+        auto issue_s = [&](int x, int st, int buf) {
+          const uint64_t da = dq0 + (x ? (uint64_t)(C::Q_BYTES >> 4) : 0);
+          const uint64_t db = dk0 + (uint64_t)((st % NST * C::KV_BYTES) >> 4);
+          const uint32_t td = tmem + C::COL_S + buf * TK;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * C::BOX + (kk & 3) * 32;
+            tc_mma_f16(td, da + (uint64_t)(off >> 4), db + (uint64_t)(off >> 4), idesc_s, kk > 0);
+          }
+          tc_commit(bar(C::S_FULL + 2 * x + (ns[x] & 1)));
+          ns.inc(x);
+        };
+        // O_X += P_X V_j, the K steps (16 keys) that hold keys of the sequence
+        auto issue_pv = [&](int x, int j, int st, int buf) {
+          // O_X of the item before read out before this item's first PV_X
+          if ((j == 0 && no[x] >= 1 &&
+               !wait_phase_1(bar(C::O_EMPTY + x), (no[x] - 1) & 1, p.err, abort)) ||
+              !wait_phase_1(bar(C::P_FULL + 2 * x + (nt_[x] & 1)), (nt_[x] >> 1) & 1, p.err, abort))
+            return false;
+          nt_.inc(x);
+          tc_fence_after();
+          const int left = w.len - j * TK;
+          const int ks = left >= TK ? TK / 16 : (left + 15) / 16;
+          const uint64_t db = dv0 + (uint64_t)((st % NST * C::KV_BYTES) >> 4);
+          const uint32_t ta = tmem + C::COL_S + buf * TK, to = tmem + C::COL_O + x * D;
+          if (ks == TK / 16) {
+#pragma unroll
+            for (int kk = 0; kk < TK / 16; ++kk)
+              tc_mma_f16_ts(to, ta + kk * 8, db + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                            (j > 0 || kk > 0) ? 1u : 0u);
+          } else {
+#pragma unroll 1
+            for (int kk = 0; kk < ks; ++kk)
+              tc_mma_f16_ts(to, ta + kk * 8, db + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                            (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          if (j == w.n[x] - 1) {
+            tc_commit(bar(C::O_FULL + x));
+            no.inc(x);
+          }
+          return true;
+        };
+        // stage of K_j and V_{j-1}, once loaded
+        auto ready = [&](int j) {
+          return wait_phase_1(bar(C::L_FULL + (st0 + j) % NST), ((st0 + j) / NST) & 1, p.err, abort);
+        };
+        auto release = [&](int j) { tc_commit(bar(C::L_EMPTY + (st0 + j) % NST)); };
+        nl += nt + 1;
+        if (!wait_phase_1(bar(C::Q_FULL), k & 1, p.err, abort) || !ready(0)) {
+          good = false;
+          break;
+        }
+        tc_fence_after();
+        if (n1 == 0) {
+          // tile A alone: its scores take turns in buffers 0 and 1, one task ahead
+          issue_s(0, st0, 0);
+          release(0);
+          if (nt == 1) tc_commit(bar(C::Q_EMPTY));
+          for (int j = 0; j < nt; ++j) {
+            if (!ready(j + 1)) {
+              good = false;
+              break;
+            }
+            if (j + 1 < nt) {
+              tc_fence_after();
+              issue_s(0, st0 + j + 1, (j + 1) & 1);
+              if (j + 2 == nt) tc_commit(bar(C::Q_EMPTY));
+            }
+            if (!issue_pv(0, j, st0 + j + 1, j & 1)) {
+              good = false;
+              break;
+            }
+            release(j + 1);
+          }
+        } else if (NB == 2) {
+          issue_s(0, st0, 0);
+          issue_s(1, st0, 1);
+          release(0);
+          if (nt == 1) tc_commit(bar(C::Q_EMPTY));
+          for (int j = 0; j < nt; ++j) {
+            if (!ready(j + 1)) {
+              good = false;
+              break;
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (!good || j >= w.n[x]) continue;
+              good = issue_pv(x, j, st0 + j + 1, x);
+              if (good && j + 1 < w.n[x]) issue_s(x, st0 + j + 1, x);
+            }
+            if (!good) break;
+            release(j + 1);
+            if (j + 2 == nt) tc_commit(bar(C::Q_EMPTY));
+          }
+        } else {
+          // Three buffers in turn: the scores of task t + 3 follow task t's PV, so
+          // a tile's next scores are there when its weights are written. After
+          // PV_A(j) that is S_B(j + 1), after PV_B(j) S_A(j + 2), or, if A ends
+          // one step before B, the last S_B.
+          issue_s(0, st0, 0);
+          issue_s(1, st0, 1);
+          release(0);
+          if (nt == 1) tc_commit(bar(C::Q_EMPTY));
+          if (nt > 1) {
+            good = ready(1);
+            tc_fence_after();
+            if (good) issue_s(n0 > 1 ? 0 : 1, st0 + 1, 2);
+            if (n0 == 1) tc_commit(bar(C::Q_EMPTY));
+          }
+          int b0 = 0, b1 = 1, b2 = 2;  // buffers of tasks t, t + 1, t + 2
+          for (int j = 0; j < nt && good; ++j) {
+            if (j + 1 == nt && !ready(nt)) {  // (earlier stages: before their S products)
+              good = false;
+              break;
+            }
+            if (j < n0) {
+              good = issue_pv(0, j, st0 + j + 1, b0);
+              if (!good) break;
+              if (j + 1 < n0) {
+                issue_s(1, st0 + j + 1, b0);
+                if (j + 1 == n1 - 1) tc_commit(bar(C::Q_EMPTY));
+              }
+              const int b = b0;
+              b0 = b1; b1 = b2; b2 = b;
+            }
+            good = issue_pv(1, j, st0 + j + 1, b0);
+            if (!good) break;
+            release(j + 1);
+            if (j + 2 < n0 || (j + 2 == n0 && n1 > n0)) {
+              good = ready(j + 2);
+              if (!good) break;
+              tc_fence_after();
+              if (j + 2 < n0) {
+                issue_s(0, st0 + j + 2, b0);
+              } else {
+                issue_s(1, st0 + j + 2, b0);
+                tc_commit(bar(C::Q_EMPTY));
+              }
+            }
+            const int b = b0;
+            b0 = b1; b1 = b2; b2 = b;
+          }
+        }
+      }
+      if (!good) *abort = 1;
+    }
+    __syncwarp();
   } else {
     // ---------------- softmax: warps 2-5 tile A, 6-9 tile B, a thread per row
     const int x = (warp - 2) >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;                // row of the tile
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t t_s = tmem + C::COL_S + x * TK + lane_base;  // scores, then P
     const uint32_t t_o = tmem + C::COL_O + x * D + lane_base;
-    const uint32_t sfull = s_full0 + 8 * x, pfull = p_full0 + 8 * x;
-    const uint32_t ofull = o_full0 + 8 * x, oempty = o_empty0 + 8 * x;
     bool good = true;
-    int n = 0;   // S_X products consumed so far
-    int ko = 0;  // items with a non-empty tile X so far
-    int nl = 0;  // ring stages of the items before
-    for (int k = 0, i = item_index(0); i < n_items && good; ++k, i = item_index(k)) {
-      const Item w = item_of(i, p);
-      const int nt = max(w.n[0], w.n[1]), nl0 = nl;
-      nl += nt + 1;
-      if (w.n[x] == 0) continue;  // tile past the sequence end: nothing to do
-      const int row0 = w.q0 + x * TQ;  // first row of the tile
+    int nx = 0;     // tasks of this tile so far
+    int ko = 0;     // items of this tile so far
+    int stage = 0;  // ring stages of the items before
+    Jobs js;
+    for (bool more = js.begin(n_items, p); more && good; more = js.next(p)) {
+      const Job& w = js.w;
+      const int stage_job = stage, both = min(w.n[0], w.n[1]);
+      stage += max(w.n[0], w.n[1]) + 1;
+      if (w.n[x] == 0) continue;
+      const int row0 = w.q + x * TQ;  // first row of the tile
       const int row = row0 + r;
       float m_ref = -INFINITY, l = 0.0f;
-      for (int j = 0; j < w.n[x]; ++j, ++n) {
+      for (int j = 0; j < w.n[x]; ++j, ++nx) {
         const int kv0 = j * TK;
-        if (!wait_phase(sfull, n & 1, p.err, abort)) {
+        const int buf = w.n[1] == 0 ? j & 1 : NB == 2 ? x : (j < both ? 2 * j + x : both + j) % 3;
+        const uint32_t t_s = tmem + C::COL_S + buf * TK + lane_base;  // scores, then P
+        if (!wait_phase(bar(C::S_FULL + 2 * x + (nx & 1)), (nx >> 1) & 1, p.err, abort)) {
           good = false;
           break;
         }
@@ -507,7 +615,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             l *= alpha;
           }
           if (j > 0) {
-            // rescale the O_X row (PV_X(j - 1) completed before S_X(j) did)
+            // rescale the O_X row once PV_X(j - 1) is complete: the stage of
+            // V_{j-1} has been released (and not been filled and released again,
+            // which takes this task's weights)
+            const int st = stage_job + j;
+            if (!wait_phase(bar(C::L_EMPTY + st % NST), (st / NST) & 1, p.err, abort)) *abort = 1;
+            tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t ro[32];
@@ -534,25 +647,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int left = w.len - j * TK;  // keys of the sequence from this tile on
         if (left < TK && (left & 15) && (x == 0 || j >= w.n[0])) {
           // clear the value rows behind the end, up to the K step's last (8
-          // chunks per 64-column box); j is the item's last tile
-          const int v = nl0 + j + 1, rows = 16 - (left & 15);
-          if (!wait_phase(l_full0 + 8 * (v % NST), (v / NST) & 1, p.err, abort)) *abort = 1;
+          // chunks per 64-column box); j is the item's last step
+          const int st = stage_job + j + 1, rows = 16 - (left & 15);
+          if (!wait_phase(bar(C::L_FULL + st % NST), (st / NST) & 1, p.err, abort)) *abort = 1;
+          const uint32_t dv = sV + (st % NST) * C::KV_BYTES;
           for (int c = r; c < rows * 8 * C::KB; c += TQ) {
             const int kb = c / (rows * 8), rc = c - kb * (rows * 8);
-            st_shared_v4u(sV + (v % NST) * C::KV_BYTES + kb * C::BOX + (left + rc / 8) * 128 +
-                              (rc % 8) * 16,
-                          0, 0, 0, 0);
+            st_shared_v4u(dv + kb * C::BOX + (left + rc / 8) * 128 + (rc % 8) * 16, 0, 0, 0, 0);
           }
           fence_proxy_async();  // before the tensor core reads them
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();  // the warp's P stores are done: one arrival for the warp
-        if (lane == 0) mbar_arrive(pfull);
+        if (lane == 0) mbar_arrive(bar(C::P_FULL + 2 * x + (nx & 1)));
       }
       if (!good) break;
       // ---- tile done: O / l and LSE
-      if (!wait_phase(ofull, ko & 1, p.err, abort)) {
+      if (!wait_phase(bar(C::O_FULL + x), ko & 1, p.err, abort)) {
         good = false;
         break;
       }
@@ -581,7 +693,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(oempty);
+      if (lane == 0) mbar_arrive(bar(C::O_EMPTY + x));
       if (row_ok && p.lse != nullptr)
         p.lse[(int64_t)w.h * p.tokens + w.a + row] = (m_ref + log2f(l)) * LN2;
     }
@@ -607,7 +719,8 @@ mgb_status fwd_d(const PackedArgs& a, cudaStream_t st) {
       tmap_encode_bf16_2d(&tv, a.v, (uint64_t)a.nkv * D, T, a.ld_kv, 64, TK) != CUDA_SUCCESS)
     return MGB_ERR_CUDA;
   Params p{};
-  p.nq = a.nq; p.group = a.nq / a.nkv; p.causal = a.causal; p.tokens = a.tokens;
+  auto magic = [](int d) { return d == 1 ? 0 : ~(uint64_t)0 / (uint64_t)d + 1; };
+  p.nq = a.nq; p.m_nq = magic(a.nq); p.m_group = magic(a.nq / a.nkv); p.causal = a.causal; p.tokens = a.tokens;
   p.hdr = a.hdr256; p.list = a.list256;
   p.o = static_cast<bf16*>(a.o); p.ld_o = a.ld_o; p.lse = a.lse;
   p.wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0 && a.ld_o % 16 == 0;
@@ -619,8 +732,7 @@ mgb_status fwd_d(const PackedArgs& a, cudaStream_t st) {
     return MGB_ERR_CUDA;
   const int64_t most = a.max256 * a.nq;
   const int grid = most < device_sm_count() ? (int)most : device_sm_count();
-  k<<<grid, NTHREADS, C::SMEM, st>>>(tq, tk, tv, p);
-  return cudaGetLastError() == cudaSuccess ? MGB_OK : MGB_ERR_CUDA;
+  return launch_pdl(k, grid, NTHREADS, C::SMEM, st, tq, tk, tv, p);
 }
 
 }  // namespace

@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(NTH) packed_prepare_kernel(int n, int tokens, 
   __shared__ int carry_s, top_s;
   __shared__ int bin[BINS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();  // the attention kernel may start up; it waits for this one's end
   const int R = blockIdx.x == 0 ? 256 : 128;
   int32_t* pre = prefix + (int64_t)blockIdx.x * (n + 1);
   int4* list = blockIdx.x == 0 ? list256 : list128;
