@@ -90,3 +90,92 @@ def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda
     j = torch.arange(rot_dim // 2, dtype=torch.float64)
     a = torch.arange(positions, dtype=torch.float64)[:, None] * base ** (-2.0 * j / rot_dim)[None, :]
     return torch.stack((torch.cos(a), torch.sin(a)), dim=-1).to(device, torch.float32).contiguous()
+
+
+class ServingBatch:
+    """What all layers share in one step of running sequences: the lengths, the
+    block table and the attention plan. Without `cu_seqlens` the step has one
+    new token per sequence (decode); with it, the rows of whole prompts packed
+    one behind the other (`tokens` rows, possibly more than they fill)."""
+
+    def __init__(self, shape, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                 cu_seqlens: torch.Tensor | None = None, tokens: int | None = None, stream=None):
+        self.block_table, self.seq_lens, self.cu_seqlens = block_table, seq_lens, cu_seqlens
+        n, dev = seq_lens.numel(), seq_lens.device
+        self.tokens = n if cu_seqlens is None else tokens
+        if cu_seqlens is None:
+            self.ws = torch.empty(mgb.mgb_attention_decode_ws_bytes(
+                n, shape.n_q_heads, shape.n_kv_heads, shape.head_dim), dtype=torch.uint8, device=dev)
+            self.plan = mgb.mgb_attention_decode_prepare(
+                n, shape.n_q_heads, shape.n_kv_heads, shape.head_dim, seq_lens, self.ws, stream)
+        else:
+            self.ws = torch.empty(mgb.mgb_attention_packed_ws_bytes(n, tokens), dtype=torch.uint8,
+                                  device=dev)
+            self.plan = mgb.mgb_attention_packed_prepare(n, tokens, shape.causal, cu_seqlens, self.ws,
+                                                         stream)
+
+
+class ServingLayer:
+    """One layer for running sequences: its weights and its paged key/value
+    pools ([n_pages, page_size, n_kv_heads, head_dim]; every layer has its own,
+    the block table is shared). `rope`: the table of rope_table, or None."""
+
+    def __init__(self, shape, arrays: dict, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                 rope: torch.Tensor | None = None, rope_interleaved: bool = False):
+        self.shape, self.k_pool, self.v_pool = shape, k_pool, v_pool
+        self.rope, self.rope_interleaved = rope, rope_interleaved
+        self.dtype = torch_dtype(shape.dtype)
+        self.mgb_dtype = mgb.MGB_BF16 if shape.dtype == "bf16" else mgb.MGB_F32
+        self.w = {k: (to_device(arrays[k], self.dtype, k_pool.device) if arrays.get(k) is not None
+                      else None) for k in WEIGHT_KEYS}
+
+    def _gemm(self, epilogue, a, w, bias, c, c2=None, resid=None, stream=None):
+        m, k, n = a.shape[0], a.shape[1], w.shape[0]
+        d = mgb.GemmExDesc(
+            g=mgb.GemmDesc(m=m, n=n, k=k, a_major=mgb.MGB_K_MAJOR, b_major=mgb.MGB_K_MAJOR, lda=k, ldb=k,
+                           ldc=n, dtype=self.mgb_dtype, c_f32=0, accumulate=0, alpha=1.0),
+            epilogue=epilogue, glu_block=self.shape.glu_block, ldc2=c2.shape[1] if c2 is not None else 0,
+            ldr=n, ldaux=0)
+        mgb.mgb_gemm_ex(d, a, w, bias, c, c2=c2, resid=resid, stream=stream)
+        return c
+
+    def _norm(self, x, which, stream):
+        y = torch.empty_like(x)
+        mgb.mgb_layernorm_fwd(x.shape[0], x.shape[1], self.mgb_dtype, self.shape.ln_eps, x,
+                              self.w[f"ln{which}_g"], self.w[f"ln{which}_b"], y, None, None, stream)
+        return y
+
+    def step(self, x: torch.Tensor, batch: ServingBatch, stream=None) -> torch.Tensor:
+        """The layer's output [tokens, hidden] for the batch's new rows x, whose
+        keys and values enter the cache. Rows of no sequence come out as the
+        layer of a zero attention output."""
+        s, w, d = self.shape, self.w, self.shape.head_dim
+        T, nq, nkv = x.shape[0], self.shape.n_q_heads, self.shape.n_kv_heads
+        pre = s.norm_pos == "pre"
+        width = (nq + 2 * nkv) * d
+        new = lambda cols: torch.empty((T, cols), dtype=self.dtype, device=x.device)
+        qkv = self._gemm(mgb.MGB_EPI_STORE, self._norm(x, 1, stream) if pre else x, w["w_qkv"],
+                         w["b_qkv"], new(width), stream=stream)
+        q, k, v = qkv, qkv[:, nq * d:], qkv[:, (nq + nkv) * d:]
+        cache = mgb.kv_cache(self.k_pool, self.v_pool, batch.block_table)
+        rot = 2 * self.rope.shape[1] if self.rope is not None else 0
+        desc = mgb.kv_append_desc(T, batch.seq_lens.numel(), nq, rot, self.rope_interleaved,
+                                  self.rope.shape[0] if rot else 0)
+        # queries and keys are rotated where they lie
+        mgb.mgb_kv_append(desc, cache, batch.cu_seqlens, batch.seq_lens, self.rope, q, k, v, width, width,
+                          q, width, k, width, stream)
+        o = torch.zeros((T, nq * d), dtype=self.dtype, device=x.device)
+        if batch.cu_seqlens is None:
+            mgb.mgb_attention_decode(batch.plan, cache, q, width, o, nq * d, None, stream)
+        else:
+            mgb.mgb_attention_packed_fwd(batch.plan, nq, nkv, d, self.mgb_dtype, q, k, v, width, width, o,
+                                         nq * d, None, stream)
+        h = self._gemm(mgb.MGB_EPI_BIAS_RESID, o, w["w_o"], w["b_o"], new(s.hidden), resid=x, stream=stream)
+        if not pre:
+            h = self._norm(h, 1, stream)
+        epi = mgb.MGB_EPI_BIAS_SWIGLU if s.act == "swiglu" else mgb.MGB_EPI_BIAS_GELU
+        a = new(s.ffn)
+        self._gemm(epi, self._norm(h, 2, stream) if pre else h, w["w_1"], w["b_1"], new(w["w_1"].shape[0]),
+                   c2=a, stream=stream)
+        y = self._gemm(mgb.MGB_EPI_BIAS_RESID, a, w["w_2"], w["b_2"], new(s.hidden), resid=h, stream=stream)
+        return y if pre else self._norm(y, 2, stream)

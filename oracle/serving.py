@@ -17,6 +17,8 @@ Test infrastructure only.
 import numpy as np
 
 from .attention import attention_fwd
+from .layer import _act, _lin
+from .layernorm import ln_fwd
 
 
 def rope_rotate(x, rows, interleaved=False):
@@ -102,3 +104,23 @@ def decode_attention(q, k_pool, v_pool, table, lens):
             o[s, h] = (e / e.sum()) @ v[:, g]
             lse[s, h] = m + np.log(e.sum())
     return o, lse
+
+
+def layer_fwd(cfg, w, x, rope=None, interleaved=False):
+    """The layer (layer.block_fwd) on one whole sequence x [L, H] at positions
+    0 .. L - 1, queries and keys rotated (rope [L or more, rot/2, 2])."""
+    x = np.asarray(x, dtype=np.float64)
+    L, nq, nkv, d, eps = x.shape[0], cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim, cfg.ln_eps
+    pre = cfg.norm_pos == "pre"
+    a = ln_fwd(x, w["ln1_g"], w["ln1_b"], eps)[0] if pre else x
+    qkv = _lin(a, w["w_qkv"], w["b_qkv"]).reshape(L, nq + 2 * nkv, d)
+    q, k, v = qkv[:, :nq], qkv[:, nq:nq + nkv], qkv[:, nq + nkv:]
+    if rope is not None:
+        q, k = (rope_rotate(z, rope[:L], interleaved) for z in (q, k))
+    o, _ = packed_attention(q, k, v, [0, L], cfg.causal)
+    h = x + _lin(o.reshape(L, nq * d), w["w_o"], w["b_o"])
+    if not pre:
+        h = ln_fwd(h, w["ln1_g"], w["ln1_b"], eps)[0]
+    f = ln_fwd(h, w["ln2_g"], w["ln2_b"], eps)[0] if pre else h
+    y = h + _lin(_act(_lin(f, w["w_1"], w["b_1"]), cfg), w["w_2"], w["b_2"])
+    return y if pre else ln_fwd(y, w["ln2_g"], w["ln2_b"], eps)[0]

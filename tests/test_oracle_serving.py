@@ -88,3 +88,18 @@ def test_decode_is_the_last_row_of_causal_attention():
     np.testing.assert_allclose(dl[0], lse[:, -1], atol=1e-13)
     assert (do[1] == 0).all() and np.isneginf(dl[1]).all()
     assert abs(oracle.serving.decode_attention(q[-1:], kp, vp, table, [n - 1])[0] - o[-1]).max() > 1e-3
+
+
+@pytest.mark.parametrize("norm_pos,act", [("pre", "gelu"), ("post", "swiglu")])
+def test_layer_without_rotation_is_the_block(norm_pos, act):
+    from megatron_transformer_layer_fwd_gb300.inputs import LayerShape, layer_inputs
+    shape = LayerShape(1, 6, 16, 4, 2, 4, 32, norm_pos=norm_pos, act=act, causal=True, glu_block=16)
+    arr = layer_inputs(shape, seed=1, random_affine=True)
+    y, _ = oracle.block_fwd(shape, arr, arr["x"])
+    np.testing.assert_allclose(serving.layer_fwd(shape, arr, arr["x"]), y, atol=1e-12)
+    # rotation by position: the first row of a sequence is at position 0, and a
+    # causal row does not depend on the rows after it
+    r = serving.layer_fwd(shape, arr, arr["x"], _rope(6, 4))
+    np.testing.assert_allclose(r[0], y[0], atol=1e-12)
+    assert np.abs(r[1:] - y[1:]).max() > 1e-9
+    np.testing.assert_allclose(serving.layer_fwd(shape, arr, arr["x"][:4], _rope(6, 4)), r[:4], atol=1e-12)
