@@ -48,8 +48,10 @@ constexpr int MAXR = 16;               // query heads per item
 constexpr int SMS = 152;               // of a GB300 (fewer: the same ranges, in more waves)
 __host__ __device__ constexpr int ctas_per_sm(int d) { return d == 64 ? 3 : 2; }
 __host__ __device__ constexpr int unit_tokens(int d) { return d == 64 ? 128 : 64; }
+// fixed cost of an item (ITEM); 16 heads, 200 sequences of 20 to 600 tokens: 55.3 us
+// with 4 at D = 128, 59.7 with 8, 64 with 12; D = 64, to 1200 tokens, 45 with 2, 47 with 6
+__host__ __device__ constexpr int item_cost(int d) { return d == 64 ? 2 : 4; }
 constexpr int UNIT = 4;                // cost of a unit
-constexpr int ITEM = 8;                // fixed cost of an item
 constexpr int WHOLE = 4;               // units of an item that is never split
 constexpr int MIN_CHUNK = 2 * UNIT;    // of a CTA (at least UNIT: no CTA between two others is empty)
 constexpr float LOG2E = 1.4426950408889634f;
@@ -93,7 +95,7 @@ Layout make_layout(int n, int nq, int nkv, int d) {
 
 // where unit t of an item with n units begins on its part of the cost axis
 __host__ __device__ inline int64_t begin_of(int t, int n) { return n > WHOLE ? (int64_t)t * UNIT : 0; }
-__host__ __device__ inline int64_t cost_of(int tiles) { return (int64_t)tiles * UNIT + ITEM; }
+__host__ __device__ inline int64_t cost_of(int tiles, int item) { return (int64_t)tiles * UNIT + item; }
 // units of a sequence: at least one, so that an empty one gets its zeros
 __host__ __device__ inline int tiles_of(int len, int tk) {
   return len > tk ? (int)(((int64_t)len + tk - 1) / tk) : 1;
@@ -102,7 +104,7 @@ __host__ __device__ inline int tiles_of(int len, int tk) {
 // ---------------------------------------------------------------- prepare
 // One block: lengths copied (negative ones count as 0 and are an error), costs
 // (per head group) summed up, the ranges' first units found, counters zeroed.
-__global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups, int ctas, int tk,
+__global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups, int ctas, int tk, int item,
                                                               const int32_t* lens,
                                                               Header* hdr, Start* start,
                                                               uint32_t* counter, int32_t* len_out,
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups,
         len = 0;
       }
       len_out[i] = len;
-      v = cost_of(tiles_of(len, tk));
+      v = cost_of(tiles_of(len, tk), item);
     }
     int64_t x = v;
 #pragma unroll
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(1024) decode_prepare_kernel(int n, int groups,
       }
       const int64_t per = prefix[lo + 1] - prefix[lo], r = u - prefix[lo] * groups;
       const int64_t h = r / per, into = r - h * per, t = (into + UNIT - 1) / UNIT;
-      const int64_t nt = (per - ITEM) / UNIT;
+      const int64_t nt = (per - item) / UNIT;
       st.at = prefix[lo] * groups + h * per;
       st.s = lo;
       st.h = (int)h;
@@ -248,8 +250,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 }
 
 // Position in a CTA's range of units of TK tokens.
-template <int TK>
+template <int D>
 struct Cursor {
+  static constexpr int TK = unit_tokens(D);
   int64_t at;  // the item on the cost axis
   int s, h, t, nt, len, next_len;
   __device__ void init(const Start& st) {
@@ -260,7 +263,7 @@ struct Cursor {
   __device__ void next(const Params& p) {
     if (++t < nt) return;
     t = 0;
-    at += cost_of(nt);
+    at += cost_of(nt, item_cost(D));
     if (++h < p.groups) return;
     h = 0;
     ++s;
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
 
   // ---------------- loader: a cursor one stage ahead of the copies, whose
   // page number is in flight while the previous stage's copies are issued
-  Cursor<TK> ld;
+  Cursor<D> ld;
   ld.init(st0);
   int ld_sub = 0, ld_n = 0;
   int pg = 0, slot = 0, hkv = 0;
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
   for (int i = 0; i < ST - 1; ++i) fetch();
 
   // ---------------- queries: the next item's are requested one item ahead
-  Cursor<TK> cu;
+  Cursor<D> cu;
   cu.init(st0);
   auto q_row = [&](int s, int h, int r) {  // first query head of the group + r, or -1
     const int first = (h % p.per_kv) * p.rows + r;
@@ -427,7 +430,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
       __syncthreads();
     }
     {  // the next item's queries
-      Cursor<TK> nx = cu;
+      Cursor<D> nx = cu;
       nx.t = nx.nt - 1;
       nx.next(p);
       if (nx.before(end)) request_q(nx.s, nx.h);
@@ -588,7 +591,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
               if (r >= rows) continue;
-              pr[r] = exp2f(pr[r] - (m[r] == -INFINITY ? 0.0f : m[r]));
+              pr[r] = ex2_ftz(pr[r] - (m[r] == -INFINITY ? 0.0f : m[r]));
               l[r] += pr[r];  // the lane's token; the four quarters hold copies
             }
 #pragma unroll
@@ -841,7 +844,7 @@ mgb_status mgb_attention_decode_prepare(int32_t n_seqs, int32_t n_q_heads, int32
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     LaunchScope scope(PROF_ATTN_DECODE, st);
     decode_prepare_kernel<<<1, 1024, 0, st>>>(
-        n_seqs, l.groups, l.ctas, unit_tokens(head_dim), seq_lens, reinterpret_cast<Header*>(b + l.header),
+        n_seqs, l.groups, l.ctas, unit_tokens(head_dim), item_cost(head_dim), seq_lens, reinterpret_cast<Header*>(b + l.header),
         reinterpret_cast<Start*>(b + l.start), reinterpret_cast<uint32_t*>(b + l.counter),
         reinterpret_cast<int32_t*>(b + l.len), reinterpret_cast<int64_t*>(b + l.prefix), err);
     if (cudaGetLastError() != cudaSuccess) return MGB_ERR_CUDA;

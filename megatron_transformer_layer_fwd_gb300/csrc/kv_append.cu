@@ -31,6 +31,7 @@ constexpr int MAX_GROUPS = 8;  // tokens per block
 struct AppendParams {
   int tokens, n_seqs, nq, nkv, rot, rope_len;
   int units_head;              // units per head
+  uint32_t m_head;             // 2^32 / units_head, rounded up; 0 for one unit
   int units;                   // per token: (nq + 2 nkv) heads (0 q heads without q_out)
   int page_size, max_pages, n_pages, d;
   const int32_t *cu, *lens, *table;
@@ -124,7 +125,7 @@ __global__ void kv_append_kernel(const AppendParams p) {
 
   // the unit's two vectors in its row, for q / k / v of token t
   auto locate = [&](int u, int& head, int& e0, int& e1, int& ju) {
-    head = u / p.units_head;
+    head = p.m_head == 0 ? u : (int)__umulhi((uint32_t)u, p.m_head);  // u / units_head
     const int w = u - head * p.units_head;
     ju = w < rot_units ? w * VN : -1;  // first table pair of the unit
     if (INTER || ju < 0) {
@@ -305,6 +306,7 @@ extern "C" mgb_status mgb_kv_append(const mgb_kv_append_desc* d, const mgb_kv_ca
   if (q_out != nullptr && (d->n_q_heads < 1 || q == nullptr)) return MGB_ERR_INVALID_ARG;
   if (d->tokens > 0 && (!k || !v || (d->n_seqs > 0 && !seq_lens))) return MGB_ERR_INVALID_ARG;
   const int64_t wq = (int64_t)d->n_q_heads * c->head_dim, wk = (int64_t)c->n_kv_heads * c->head_dim;
+  // (units x units per head stays below 2^32, for the division by multiplication)
   if (wk >= ((int64_t)1 << 28) || (q_out != nullptr && wq >= ((int64_t)1 << 28)))
     return MGB_ERR_INVALID_ARG;
   if (ld_kv < wk || (k_out != nullptr && ld_ko < wk) ||
@@ -326,6 +328,7 @@ extern "C" mgb_status mgb_kv_append(const mgb_kv_append_desc* d, const mgb_kv_ca
   p.tokens = d->tokens; p.n_seqs = d->n_seqs; p.nq = d->n_q_heads; p.nkv = c->n_kv_heads;
   p.rot = d->rot_dim; p.rope_len = d->rope_len; p.d = c->head_dim;
   p.units_head = c->head_dim / (2 * vn);
+  p.m_head = p.units_head == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + p.units_head - 1) / p.units_head);
   p.units = ((q_out ? p.nq : 0) + 2 * p.nkv) * p.units_head;
   p.page_size = c->page_size; p.max_pages = c->max_pages; p.n_pages = c->n_pages;
   p.cu = cu_seqlens; p.lens = seq_lens; p.table = c->block_table; p.ld_table = c->ld_table;
