@@ -157,6 +157,7 @@ __global__ void kv_append_kernel(const AppendParams p) {
       }
     }
   };
+  pdl_wait();  // everything the call reads may come from the kernel before
   load(threadIdx.x);
 
   if (threadIdx.x < 32 && t < p.tokens) {
@@ -246,9 +247,8 @@ mgb_status launch(const AppendParams& p, bool inter, int most, cudaStream_t st) 
   if (y > p.tokens) y = p.tokens;
   const int grid = (int)(((int64_t)p.tokens + y - 1) / y);
   LaunchScope scope(PROF_KV_APPEND, st);
-  if (inter) kv_append_kernel<T, UB, true><<<grid, dim3(x, y), 0, st>>>(p);
-  else kv_append_kernel<T, UB, false><<<grid, dim3(x, y), 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MGB_OK : MGB_ERR_CUDA;
+  return launch_pdl(inter ? kv_append_kernel<T, UB, true> : kv_append_kernel<T, UB, false>, grid,
+                    dim3(x, y), 0, st, p);
 }
 
 template <typename T>
