@@ -4,37 +4,47 @@
 // the first len[s] cached tokens, g = h / (nq / nkv). Bound: HBM (each cached
 // key and value is used once per query head of its group).
 //
-// Work is cut into units: 64 consecutive cached tokens of one (sequence, KV
-// head, group of at most 16 query heads). An item is all units of one
+// Work is cut into units: 64 (d = 64: 128) consecutive cached tokens of one
+// (sequence, KV head, group of at most 16 query heads). An item is all units of one
 // sequence and head group. Items stand one behind the other on a cost axis,
 // sequence by sequence, head by head: an item with n units takes n UNIT + ITEM,
 // its unit t beginning at t UNIT (ITEM is the fixed cost of an item: its
 // queries, the join of the warps, the store). CTA c takes the units that begin
 // in [c chunk, (c + 1) chunk): the same cost for every CTA whatever the lengths
 // are. (All units of an item of at most WHOLE units count as beginning at its
-// start: splitting it would cost more than it evens out.) An item that lies in one range is finished there. An item that spans
-// CTAs is split: each CTA leaves its unnormalised sums, maximum and row sum in
-// the workspace, and the last one to arrive (a counter per first CTA of a split
-// item) joins the parts in CTA order, so results do not depend on who was last.
+// start: splitting it would cost more than it evens out.) An item that lies in
+// one range is finished there. An item that spans CTAs is split: each CTA leaves
+// its unnormalised sums, maximum and row sum in the workspace, and the last one
+// to arrive (a counter per first CTA of a split item) joins the parts in CTA
+// order, so results do not depend on who was last.
 //
 // The prepare kernel derives the ranges from the lengths (they are the same
 // for every layer of a model's step) and zeroes the counters; each split item
 // leaves its counter at zero again.
 //
-// Within a CTA (four warps) warp w takes tokens 16 w .. 16 w + 15 of each unit
-// and keeps its own running maximum, row sums and output sums; the warps'
-// sums are joined at the end of an item. Each warp streams its tokens through
-// a private ring in shared memory by 16-byte asynchronous copies, so the main
-// loop has no CTA-wide barrier, any page size and any page layout works, and
-// tokens past the length are never read (zero fill).
+// Within a CTA (four warps) a unit is dealt out to the warps in stages of 4 KB of
+// keys and as much of values, and each warp keeps its own running maximum, row
+// sums and output sums; the warps' sums are joined at the end of an item. Each
+// warp streams its tokens through a private ring in shared memory by 16-byte
+// asynchronous copies, so the main loop has no CTA-wide barrier, any page size
+// and any page layout works, and tokens past the length are never read (zero
+// fill). 2 (d = 64: 3) CTAs per SM keep 128 (96) KB in flight per SM.
 //   bf16: products on mma.sync m16n8k16, transposed: S^T = K Q^T with 16 tokens
-//   as the rows and the query heads as the 8 (2 x 8) columns, and O^T = V^T P^T
-//   with d as the rows. One query token per sequence leaves at most 16 query
-//   heads per item, so the products are a small share of the time; with the
-//   heads on the narrow side, none of them is spent on rows that do not exist
-//   for groups of 8 or fewer that are a multiple of 8.
+//   as the rows and the query heads as the columns, and O^T = V^T P^T with d as
+//   the rows. There is one query token per sequence, so an item has at most 16
+//   query rows and the 128 rows of a tcgen05 tile would stand empty; on the
+//   narrow side the heads come in eights, and the products stay a small share of
+//   the time.
 //   float32: FFMA with a lane per (token, quarter of d) for the scores and a
-//   lane per 4 (2) columns for the output.
+//   lane per D / 32 columns for the output; the quarters' sums are dealt out so
+//   that each lane keeps the softmax of a quarter of the heads.
+//
+// Measured: bf16, d = 128, 32 query and 8 KV heads: one sequence of 131001 cached
+// tokens 90 us, 5.96 TB/s; 64 sequences of 33 to 16000 tokens 108 us, 6.3 TB/s (a
+// copy reaches 6.79). d = 64, 16 query and KV heads, 200 sequences of 20 to 1200
+// tokens: 45 us with the prepare kernel. float32, d = 128, 16 and 4 heads, 12
+// sequences to 5000 tokens: 14.6 us for 49 MB; the start of the loads (2 us), the
+// last CTAs' second item and the join (3 us) are as long as the copies.
 #include "common.cuh"
 #include "internal.h"
 
@@ -52,6 +62,7 @@ __host__ __device__ constexpr int unit_tokens(int d) { return d == 64 ? 128 : 64
 // with 4 at D = 128, 59.7 with 8, 64 with 12; D = 64, to 1200 tokens, 45 with 2, 47 with 6
 __host__ __device__ constexpr int item_cost(int d) { return d == 64 ? 2 : 4; }
 constexpr int UNIT = 4;                // cost of a unit
+constexpr int PARTS = 16;              // of a split item, joined at a time (at most 32)
 constexpr int WHOLE = 4;               // units of an item that is never split
 constexpr int MIN_CHUNK = 2 * UNIT;    // of a CTA (at least UNIT: no CTA between two others is empty)
 constexpr float LOG2E = 1.4426950408889634f;
@@ -438,11 +449,12 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
 
     // bf16: acc[i] holds d = 16 (i / HT) + lane / 4 (+ 8 in the upper two) of
     // heads 8 (i % HT) + 2 (lane % 4) + {0, 1}; m, l those heads' (l of the
-    // lane's tokens only). float32: all rows, columns lane * (D / 32) ..
+    // lane's tokens only). float32: acc all rows, columns lane * (D / 32) ..; m, l
+    // rows 4 i + lane / 8 (l of the lane's tokens only)
     constexpr int CPL = D / 32;
     constexpr int NO = BF ? D / 16 * HT : NR;
     constexpr int NI = BF ? 4 : CPL;
-    constexpr int NM = BF ? 2 * HT : NR;
+    constexpr int NM = BF ? 2 * HT : NR / 4;
     float acc[NO][NI], m[NM], l[NM];
 #pragma unroll
     for (int i = 0; i < NO; ++i)
@@ -544,56 +556,75 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
                 mma_bf16(acc[nn * HT + ht], a, pb[mt][ht][0], pb[mt][ht][1]);
             }
         } else {
+          // no branch on `rows`: heads that do not exist have zero queries, and
+          // NR independent chains hide what four dependent ones did not
           const int key = lane & 7, part = lane >> 3;  // token, quarter of d
+          float* sp = join + warp * 8 * NR;  // [token][head] (join is free until the item's end)
 #pragma unroll
           for (int kt = 0; kt < C::SK / 8; ++kt) {  // eight tokens at a time
             if (left <= 8 * kt) break;
-            float4 kx[D / 16];
+            float d0[NR] = {}, d1[NR] = {};
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
+            for (int i = 0; i < D / 16; ++i) {
+              float4 kx;
               asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                           : "=f"(kx[i].x), "=f"(kx[i].y), "=f"(kx[i].z), "=f"(kx[i].w)
+                           : "=f"(kx.x), "=f"(kx.y), "=f"(kx.z), "=f"(kx.w)
                            : "r"(sk + chunk_at<C::CH>(8 * kt + key, i * 4 + part)));
-            float pr[NR], mx[NR];
-            bool any = false;
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              pr[r] = mx[r] = -INFINITY;
-              if (r >= rows) continue;
-              float d0 = 0.0f, d1 = 0.0f;
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                const float4 qx = *reinterpret_cast<const float4*>(sq + r * D + (i * 4 + part) * 4);
-                fma2(d0, d1, qx.x, qx.y, kx[i].x, kx[i].y, d0, d1);
-                fma2(d0, d1, qx.z, qx.w, kx[i].z, kx[i].w, d0, d1);
-              }
-              float sc = d0 + d1;
-              sc += __shfl_xor_sync(0xffffffffu, sc, 8);
-              sc += __shfl_xor_sync(0xffffffffu, sc, 16);
-              pr[r] = 8 * kt + key < left ? sc * p.sl2 : -INFINITY;
-              mx[r] = pr[r];
-#pragma unroll
-              for (int o = 1; o < 8; o <<= 1)
-                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], o));
-              any |= mx[r] > m[r] + TAU;  // the same in every lane
-            }
-            if (any) {
 #pragma unroll
               for (int r = 0; r < NR; ++r) {
-                const bool up = mx[r] > m[r] + TAU;
-                const float a = up ? exp2f(m[r] - mx[r]) : 1.0f;
-                if (up) m[r] = mx[r];
-                l[r] *= a;
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) acc[r][j] *= a;
+                const float4 qx = *reinterpret_cast<const float4*>(sq + r * D + (i * 4 + part) * 4);
+                fma2(d0[r], d1[r], qx.x, qx.y, kx.x, kx.y, d0[r], d1[r]);
+                fma2(d0[r], d1[r], qx.z, qx.w, kx.z, kx.w, d0[r], d1[r]);
               }
             }
+            // sums over the quarters, dealt out: this lane gets heads 4 i + part
+            float pr[NM], mx[NM];
+            bool up[NM], any = false;
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              if (r >= rows) continue;
-              pr[r] = ex2_ftz(pr[r] - (m[r] == -INFINITY ? 0.0f : m[r]));
-              l[r] += pr[r];  // the lane's token; the four quarters hold copies
+            for (int i = 0; i < NM; ++i) {
+              float x[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) x[r] = d0[4 * i + r] + d1[4 * i + r];
+              const bool hi = part & 2, odd = part & 1;
+              const float y0 = (hi ? x[2] : x[0]) + __shfl_xor_sync(0xffffffffu, hi ? x[0] : x[2], 16);
+              const float y1 = (hi ? x[3] : x[1]) + __shfl_xor_sync(0xffffffffu, hi ? x[1] : x[3], 16);
+              const float sc = (odd ? y1 : y0) + __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 8);
+              pr[i] = 8 * kt + key < left ? sc * p.sl2 : -INFINITY;
+              mx[i] = pr[i];
             }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+              for (int i = 0; i < NM; ++i)
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+              up[i] = mx[i] > m[i] + TAU;
+              any |= up[i];
+            }
+            if (__any_sync(0xffffffffu, any)) {
+              float a[NM];
+#pragma unroll
+              for (int i = 0; i < NM; ++i) {
+                a[i] = up[i] ? exp2f(m[i] - mx[i]) : 1.0f;
+                if (up[i]) m[i] = mx[i];
+                l[i] *= a[i];
+              }
+#pragma unroll
+              for (int r = 0; r < NR; ++r) {
+                const float f = __shfl_sync(0xffffffffu, a[r / 4], (r % 4) * 8);
+#pragma unroll
+                for (int j = 0; j < CPL; ++j) acc[r][j] *= f;
+              }
+            }
+            __syncwarp();  // the weights before are read
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+              pr[i] = ex2_ftz(pr[i] - (m[i] == -INFINITY ? 0.0f : m[i]));
+              l[i] += pr[i];
+              sp[key * NR + 4 * i + part] = pr[i];
+            }
+            __syncwarp();
 #pragma unroll
             for (int kx2 = 0; kx2 < 8; ++kx2) {
               float vx[CPL];
@@ -605,12 +636,15 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
               else
                 asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(vx[0]), "=f"(vx[1]) : "r"(va));
 #pragma unroll
-              for (int r = 0; r < NR; ++r) {
-                if (r >= rows) continue;
-                const float w = __shfl_sync(0xffffffffu, pr[r], kx2);
+              for (int i = 0; i < NM; ++i) {
+                const float4 w4 = *reinterpret_cast<const float4*>(sp + kx2 * NR + 4 * i);
+                const float w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                for (int j = 0; j < CPL; j += 2)
-                  fma2(acc[r][j], acc[r][j + 1], w, w, vx[j], vx[j + 1], acc[r][j], acc[r][j + 1]);
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                  for (int j = 0; j < CPL; j += 2)
+                    fma2(acc[4 * i + r][j], acc[4 * i + r][j + 1], w[r], w[r], vx[j], vx[j + 1],
+                         acc[4 * i + r][j], acc[4 * i + r][j + 1]);
               }
             }
           }
@@ -630,12 +664,10 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
       }
     } else {
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        if (r >= rows) continue;
-        float x = l[r];
+      for (int i = 0; i < NM; ++i) {
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0) sml[warp * MAXR + r] = make_float2(m[r], x);
+        for (int o = 1; o < 8; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+        if ((lane & 7) == 0) sml[warp * MAXR + 4 * i + (lane >> 3)] = make_float2(m[i], l[i]);
       }
     }
     __syncthreads();
@@ -692,7 +724,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
           if (r >= rows) continue;
           float M, L;
           joined(r, M, L);
-          const float a = m[r] > -INFINITY ? exp2f(m[r] - M) : 0.0f;
+          const float mr = sml[warp * MAXR + r].x; const float a = mr > -INFINITY ? exp2f(mr - M) : 0.0f;
 #pragma unroll
           for (int j = 0; j < CPL; ++j)
             join[(warp * C::MR + rr) * C::JS + lane * CPL + j] = acc[r][j] * a;
@@ -736,25 +768,15 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
       __syncthreads();
       if (*flag) {
         for (int r = warp; r < rows; r += WARPS) {
-          float M = -INFINITY;
-          for (int cc = cf + lane; cc <= cl; cc += 32)
-            M = fmaxf(M, __ldcg(&p.ml[(int64_t)part_of(cc) * p.rows + r]).x);
+          float M = -INFINITY, L = 0.0f, x[CPL] = {};
+          for (int cc0 = cf; cc0 <= cl; cc0 += PARTS) {  // PARTS parts requested together
+            float z[PARTS][CPL];
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-          float L = 0.0f, x[CPL] = {};
-          for (int cc0 = cf; cc0 <= cl; cc0 += 32) {
-            float a = 0.0f, lp = 0.0f;
-            if (cc0 + lane <= cl) {
-              const float2 y = __ldcg(&p.ml[(int64_t)part_of(cc0 + lane) * p.rows + r]);
-              a = y.x > -INFINITY ? exp2f(y.x - M) : 0.0f;
-              lp = y.y * a;
-            }
-            const int np = min(32, cl - cc0 + 1);
-            for (int i0 = 0; i0 < np; i0 += 16) {  // 16 parts requested together
-              float z[16][CPL];
+            for (int i = 0; i < PARTS; ++i) {
+              const int cc = cc0 + i;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int cc = min(cc0 + i0 + i, cl);  // (behind the last: weight 0)
+              for (int j = 0; j < CPL; ++j) z[i][j] = 0.0f;
+              if (cc <= cl) {
                 const float* y = p.part + ((int64_t)part_of(cc) * p.rows + r) * D + lane * CPL;
                 if constexpr (CPL == 4) {
                   const float4 zz = __ldcg(reinterpret_cast<const float4*>(y));
@@ -764,13 +786,28 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
                   z[i][0] = zz.x; z[i][1] = zz.y;
                 }
               }
+            }
+            float2 y = make_float2(-INFINITY, 0.0f);  // of part cc0 + lane
+            if (lane < PARTS && cc0 + lane <= cl)
+              y = __ldcg(&p.ml[(int64_t)part_of(cc0 + lane) * p.rows + r]);
+            float mn = y.x;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float w = __shfl_sync(0xffffffffu, a, i0 + i);
-                L += __shfl_sync(0xffffffffu, lp, i0 + i);
+            for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+            mn = fmaxf(mn, M);
+            const float base = mn == -INFINITY ? 0.0f : mn;  // (no token so far: every factor is 0)
+            const float f = exp2f(M - base), a = exp2f(y.x - base);
+            M = mn;
+            float lp = y.y * a;
 #pragma unroll
-                for (int j = 0; j < CPL; ++j) x[j] = fmaf(w, z[i][j], x[j]);
-              }
+            for (int o = 16; o > 0; o >>= 1) lp += __shfl_xor_sync(0xffffffffu, lp, o);
+            L = L * f + lp;
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) x[j] *= f;
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) {
+              const float w = __shfl_sync(0xffffffffu, a, i);
+#pragma unroll
+              for (int j = 0; j < CPL; ++j) x[j] = fmaf(w, z[i][j], x[j]);
             }
           }
           const float inv = L > 0.0f ? 1.0f / L : 0.0f;
