@@ -26,8 +26,8 @@
  *   - Calls are asynchronous on `stream` (a cudaStream_t passed as void*;
  *     NULL = the legacy default stream). Argument errors are returned before
  *     any kernel is launched. Kernel-side failures (a bounded device wait that
- *     ran out) are recorded in a per-device error word read by
- *     mgb_device_status().
+ *     ran out, a bad index in device memory) are recorded in a per-device error
+ *     word read by mgb_device_status().
  *   - Tensors are dense and row-major: activations [T, features] with token
  *     t = b*S + s (batch-major); weights [out, in] (y = x W^T + b).
  *   - dtype MGB_BF16: every tensor is bfloat16 except LayerNorm statistics,
@@ -495,7 +495,8 @@ mgb_status mgb_kv_append(const mgb_kv_append_desc* desc, const mgb_kv_cache* cac
  * several streams at once (they only read it), each ordered after the prepare;
  * *plan (host memory) only names the workspace, nothing is read back.
  * cu_seqlens is not read again. A sequence whose offsets decrease or leave
- * [0, tokens] is MGB_ERR_INDEX and counts as empty.
+ * [0, tokens], or that begins before the end of an earlier one, is
+ * MGB_ERR_INDEX and counts as empty.
  *
  * mgb_attention_packed_fwd: q [tokens, nq*d], k, v [tokens, nkv*d], row strides
  * ld_q, ld_kv (e.g. the columns of one fused qkv buffer), o [tokens, nq*d] (row
@@ -534,7 +535,7 @@ mgb_status mgb_attention_packed_fwd(const mgb_attention_packed_plan* plan, int32
  * mgb_attention_decode: q [n_seqs, nq*d] (row stride ld_q, e.g. the query
  * columns of a fused qkv row), o [n_seqs, nq*d] (row stride ld_o), lse [n_seqs,
  * nq] float32 or NULL. The cache's dtype is q's and o's; bf16 or float32,
- * head_dim 64 or 128, any group size nq / nkv. A length past max_pages *
+ * head_dim 64 or 128, any group size nq / nkv; o must not overlap q. A length past max_pages *
  * page_size and a page outside [0, n_pages) are MGB_ERR_INDEX. Sums and softmax
  * statistics are float32; in bf16 the weights are rounded to bf16 before
  * they multiply V. Results repeat bit for bit with the same lengths. The
@@ -675,7 +676,8 @@ mgb_status mgb_memcpy_async(void* dst, const void* src, size_t bytes, void* stre
 /* Synchronises `stream`, then returns and clears the current device's error
  * word (MGB_ERR_DEVICE_TIMEOUT if a bounded device wait ran out since the last
  * call; MGB_ERR_DEVICE_CHECK if a device-side check of the checking build
- * failed; else MGB_OK), or MGB_ERR_CUDA if the synchronisation failed. */
+ * failed; MGB_ERR_INDEX if an index in device memory was outside its range;
+ * else MGB_OK), or MGB_ERR_CUDA if the synchronisation failed. */
 mgb_status mgb_device_status(void* stream);
 
 /* Launches one block that waits on a device flag nothing ever sets, bounded

@@ -834,8 +834,7 @@ mgb_status launch(const Params& p, cudaStream_t st) {
   return launch_pdl(k, SMS * ctas_per_sm(D), NT, C::SMEM, st, p);
 }
 
-// The smallest form that holds the item's query heads: fewer products, and
-// (float32, unrolled over the heads) code that stays in the instruction cache.
+// The smallest form that holds the item's query heads: the fewest products.
 template <typename T, int D>
 mgb_status launch_rows(const Params& p, cudaStream_t st) {
   if constexpr (sizeof(T) == 4)
@@ -881,7 +880,8 @@ mgb_status mgb_attention_decode_prepare(int32_t n_seqs, int32_t n_q_heads, int32
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     LaunchScope scope(PROF_ATTN_DECODE, st);
     decode_prepare_kernel<<<1, 1024, 0, st>>>(
-        n_seqs, l.groups, l.ctas, unit_tokens(head_dim), item_cost(head_dim), seq_lens, reinterpret_cast<Header*>(b + l.header),
+        n_seqs, l.groups, l.ctas, unit_tokens(head_dim), item_cost(head_dim), seq_lens,
+        reinterpret_cast<Header*>(b + l.header),
         reinterpret_cast<Start*>(b + l.start), reinterpret_cast<uint32_t*>(b + l.counter),
         reinterpret_cast<int32_t*>(b + l.len), reinterpret_cast<int64_t*>(b + l.prefix), err);
     if (cudaGetLastError() != cudaSuccess) return MGB_ERR_CUDA;
@@ -907,6 +907,7 @@ mgb_status mgb_attention_decode(const mgb_attention_decode_plan* plan, const mgb
     return MGB_ERR_MISALIGNED;
   const Layout l = make_layout(n, nq, nkv, d);
   if (plan->ws_bytes < l.total) return MGB_ERR_WORKSPACE_TOO_SMALL;
+  if (o != nullptr && o == q) return MGB_ERR_INVALID_ARG;  // the CTAs of a split item read q late
   s = check_arch();
   if (s != MGB_OK) return s;
   if (n == 0) return MGB_OK;

@@ -253,9 +253,12 @@ mgb_status launch(const AppendParams& p, bool inter, int most, cudaStream_t st) 
 
 template <typename T>
 mgb_status launch_t(const AppendParams& p, bool inter, cudaStream_t st) {
-  // Few tokens: as many threads as units, one each (one token 3.3 us; 3.8 with
-  // 128 threads). Many: small blocks with three units per thread (8192 tokens of
-  // 384 units 25.3 us, 5.0 TB/s; 31.8 with blocks of 384 threads).
+  // Few tokens: as many threads as units, one each (one token 3.1 us; 0.5 us more
+  // with 128 threads). Many: small blocks with three units per thread (4699
+  // tokens of 384 units, 127 MB, 23.9 us, 5.3 TB/s; 6 us more with blocks of 384
+  // threads). There the chain cu, length, page of each token is the bound: DRAM
+  // is 39 % busy, 33 % of the warps fit. Groups that take runs of tokens and
+  // find their places together need 27 us: too few of them hide the rest.
   return p.tokens <= 4 * device_sm_count() ? launch<T, 1>(p, inter, 512, st)
                                            : launch<T, 3>(p, inter, 128, st);
 }

@@ -39,24 +39,21 @@ Layout make_layout(int n, int tokens) {
   return l;
 }
 
-// Row range of sequence s; an offset outside its range (decreasing, below 0, past
-// the tokens) is an error and makes the sequence empty.
-__device__ __forceinline__ int2 range_of(const int32_t* cu, int s, int tokens, int* err) {
+// Row range of sequence s, (0, 0) and false if an offset is outside its range
+// (decreasing, below 0, past the tokens).
+__device__ __forceinline__ bool range_of(const int32_t* cu, int s, int tokens, int2& r) {
   const int a = cu[s], b = cu[s + 1];
-  if (a < 0 || b < a || b > tokens) {
-    record_error(err, kErrIndex);
-    return make_int2(0, 0);
-  }
-  return make_int2(a, b - a);
+  const bool ok = a >= 0 && b >= a && b <= tokens;
+  r = ok ? make_int2(a, b - a) : make_int2(0, 0);
+  return ok;
 }
 
 // Block x builds the list of R = 256 >> x query rows per entry.
 __global__ void __launch_bounds__(NTH) packed_prepare_kernel(int n, int tokens, int causal,
                                                              const int32_t* cu, PackedHeader* hdr,
                                                              int32_t* prefix, int4* list256,
-                                                             int4* list128, int64_t max256,
-                                                             int64_t max128, int* err) {
-  __shared__ int warp_sum[32];
+                                                             int4* list128, int* err) {
+  __shared__ int warp_sum[32], warp_max[32];
   __shared__ int carry_s, top_s;
   __shared__ int bin[BINS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -64,7 +61,6 @@ __global__ void __launch_bounds__(NTH) packed_prepare_kernel(int n, int tokens, 
   const int R = blockIdx.x == 0 ? 256 : 128;
   int32_t* pre = prefix + (int64_t)blockIdx.x * (n + 1);
   int4* list = blockIdx.x == 0 ? list256 : list128;
-  const int64_t room = blockIdx.x == 0 ? max256 : max128;
   // inclusive sum over the block; returns the total in every thread
   auto scan = [&](int v, int& incl) {
     int x = v;
@@ -91,23 +87,51 @@ __global__ void __launch_bounds__(NTH) packed_prepare_kernel(int n, int tokens, 
     __syncthreads();
     return total;
   };
+  // the maximum of `before` and of v in the threads before this one
+  auto max_before = [&](int v, int before) {
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = max(x, y);
+    }
+    if (lane == 31) warp_max[warp] = x;
+    x = __shfl_up_sync(0xffffffffu, x, 1);
+    int m = lane > 0 ? max(x, before) : before;
+    __syncthreads();  // (warp_max is written again only behind scan()'s barriers)
+    for (int w = 0; w < warp; ++w) m = max(m, warp_max[w]);
+    return m;
+  };
   bin[tid] = 0;
   if (tid == 0) top_s = 0;
   __syncthreads();
-  int total = 0, longest = 0;
+  int total = 0, longest = 0, reached = 0;
+  bool bad = false;
   for (int base = 0; base < n; base += NTH) {
     const int s = base + tid;
     int v = 0, incl;
-    if (s < n) {
-      const int len = range_of(cu, s, tokens, err).y;
-      longest = max(longest, len);
-      v = (len + R - 1) / R;
+    int2 r = make_int2(0, 0);
+    const bool ok = s >= n || range_of(cu, s, tokens, r);
+    // Behind a bad sequence another may begin before the end of an earlier one and
+    // share its rows: empty too, so that the lists and the work stay within those
+    // of `tokens` rows.
+    const bool bad_here = __syncthreads_or(!ok);
+    bool take = true;
+    if (bad || bad_here) {
+      if (!bad && base > 0) reached = cu[base];  // (no offset before it was larger)
+      bad = true;
+      take = r.x >= max_before(r.x + r.y, reached);
+      for (int w = 0; w < 32; ++w) reached = max(reached, warp_max[w]);
+    }
+    if (!ok || (!take && r.y > 0)) record_error(err, kErrIndex);
+    if (take) {
+      longest = max(longest, r.y);
+      v = (r.y + R - 1) / R;
     }
     const int sum = scan(v, incl);
     if (s < n) pre[s] = total + incl - v;
     total += sum;
   }
-  if (total > room) total = (int)room;  // overlapping ranges (decreasing offsets between them)
   if (tid == 0) pre[n] = total;
   atomicMax(&top_s, longest);
   __syncthreads();
@@ -122,7 +146,8 @@ __global__ void __launch_bounds__(NTH) packed_prepare_kernel(int n, int tokens, 
       if (pre[mid] <= e) lo = mid;
       else hi = mid - 1;
     }
-    const int2 r = range_of(cu, lo, tokens, nullptr);
+    int2 r;
+    range_of(cu, lo, tokens, r);
     const int q0 = (e - pre[lo]) * R;
     w = make_int4(r.x, r.y, q0, 0);
     const int seen = causal ? min(r.y, q0 + R) : r.y;
@@ -180,7 +205,7 @@ mgb_status mgb_attention_packed_prepare(int32_t n_seqs, int32_t tokens, int32_t 
     packed_prepare_kernel<<<2, NTH, 0, st>>>(
         n_seqs, tokens, causal, cu_seqlens, reinterpret_cast<PackedHeader*>(b + l.header),
         reinterpret_cast<int32_t*>(b + l.prefix), reinterpret_cast<int4*>(b + l.list256),
-        reinterpret_cast<int4*>(b + l.list128), l.max256, l.max128, err);
+        reinterpret_cast<int4*>(b + l.list128), err);
     if (cudaGetLastError() != cudaSuccess) return MGB_ERR_CUDA;
   }
   *plan = mgb_attention_packed_plan{n_seqs, tokens, causal, ws, ws_bytes};
@@ -208,6 +233,7 @@ mgb_status mgb_attention_packed_fwd(const mgb_attention_packed_plan* plan, int32
   if (plan->ws_bytes < l.total) return MGB_ERR_WORKSPACE_TOO_SMALL;
   // item numbers (entries x heads, up to four per entry) are 32-bit
   if (4 * l.max128 * n_q_heads >= (int64_t)1 << 30) return MGB_ERR_UNSUPPORTED;
+  if (o != nullptr && (o == q || o == k || o == v)) return MGB_ERR_INVALID_ARG;
   const mgb_status s = check_arch();
   if (s != MGB_OK) return s;
   if (plan->n_seqs == 0 || plan->tokens == 0) return MGB_OK;

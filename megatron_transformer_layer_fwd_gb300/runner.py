@@ -102,6 +102,13 @@ class ServingBatch:
                  cu_seqlens: torch.Tensor | None = None, tokens: int | None = None, stream=None):
         self.block_table, self.seq_lens, self.cu_seqlens = block_table, seq_lens, cu_seqlens
         n, dev = seq_lens.numel(), seq_lens.device
+        for t in (seq_lens, cu_seqlens):
+            if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()):
+                raise ValueError("seq_lens and cu_seqlens must be contiguous int32 vectors")
+        if block_table.dim() != 2 or block_table.shape[0] != n or (
+                cu_seqlens is not None and (cu_seqlens.numel() != n + 1 or tokens is None)):
+            raise ValueError("a batch of n sequences has n block-table rows and, packed, n + 1 row "
+                             "offsets and a number of tokens")
         self.tokens = n if cu_seqlens is None else tokens
         if cu_seqlens is None:
             self.ws = torch.empty(mgb.mgb_attention_decode_ws_bytes(
@@ -126,6 +133,12 @@ class ServingLayer:
         self.rope, self.rope_interleaved = rope, rope_interleaved
         self.dtype = torch_dtype(shape.dtype)
         self.mgb_dtype = mgb.MGB_BF16 if shape.dtype == "bf16" else mgb.MGB_F32
+        if k_pool.dtype != self.dtype or tuple(k_pool.shape[2:]) != (shape.n_kv_heads, shape.head_dim):
+            raise ValueError("the pools must be [n_pages, page_size, n_kv_heads, head_dim] of the "
+                             "layer's dtype")
+        if rope is not None and (rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[2] != 2
+                                 or not rope.is_contiguous()):
+            raise ValueError("rope must be [positions, rot_dim / 2, 2] float32, contiguous")
         self.w = {k: (to_device(arrays[k], self.dtype, k_pool.device) if arrays.get(k) is not None
                       else None) for k in WEIGHT_KEYS}
 
@@ -150,6 +163,8 @@ class ServingLayer:
         keys and values enter the cache. Rows of no sequence come out as the
         layer of a zero attention output."""
         s, w, d = self.shape, self.w, self.shape.head_dim
+        if tuple(x.shape) != (batch.tokens, s.hidden) or x.dtype != self.dtype or not x.is_contiguous():
+            raise ValueError("x must be [batch.tokens, hidden] of the layer's dtype, contiguous")
         T, nq, nkv = x.shape[0], self.shape.n_q_heads, self.shape.n_kv_heads
         pre = s.norm_pos == "pre"
         width = (nq + 2 * nkv) * d
