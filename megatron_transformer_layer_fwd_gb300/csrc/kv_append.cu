@@ -26,7 +26,9 @@ namespace mgb {
 
 namespace {
 
-constexpr int MAX_GROUPS = 8;  // tokens per block
+constexpr int MAX_GROUPS = 8;       // tokens per block
+constexpr int FEW_THREADS = 512;    // of a block at most, with few tokens
+constexpr int MANY_THREADS = 128;   // .. with many
 
 struct AppendParams {
   int tokens, n_seqs, nq, nkv, rot, rope_len;
@@ -115,7 +117,8 @@ __device__ __forceinline__ void rotate(uint4& w0, uint4& w1,
 }
 
 template <typename T, int UB, bool INTER>
-__global__ void kv_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(UB == 1 ? FEW_THREADS : MANY_THREADS, UB == 1 ? 1 : 8)
+    kv_append_kernel(const AppendParams p) {
   constexpr int VN = Vec<T>::VN;
   __shared__ int s_pos[MAX_GROUPS];       // -1: nothing to do for the token
   __shared__ int64_t s_slot[MAX_GROUPS];  // element offset in the pools, head 0
@@ -253,14 +256,15 @@ mgb_status launch(const AppendParams& p, bool inter, int most, cudaStream_t st) 
 
 template <typename T>
 mgb_status launch_t(const AppendParams& p, bool inter, cudaStream_t st) {
-  // Few tokens: as many threads as units, one each (one token 3.1 us; 0.5 us more
-  // with 128 threads). Many: small blocks with three units per thread (4699
-  // tokens of 384 units, 127 MB, 23.9 us, 5.3 TB/s; 6 us more with blocks of 384
-  // threads). There the chain cu, length, page of each token is the bound: DRAM
-  // is 39 % busy, 33 % of the warps fit. Groups that take runs of tokens and
-  // find their places together need 27 us: too few of them hide the rest.
-  return p.tokens <= 4 * device_sm_count() ? launch<T, 1>(p, inter, 512, st)
-                                           : launch<T, 3>(p, inter, 128, st);
+  // Few tokens: as many threads as units, one each (one token 3.0 us; 0.5 us more
+  // with 128 threads). Many: small blocks with three units per thread, eight per
+  // SM (4699 tokens of 384 units, 127 MB, 23.2 us, 5.5 TB/s; 24.8 with six, 24 and
+  // more with blocks of 192 threads and two units, 30 with 384 and one). There the
+  // chain cu, length, page of each token is the bound, not DRAM. Groups that
+  // take runs of tokens and find their places together need 27 us: too few of
+  // them are left to hide the rest.
+  return p.tokens <= 4 * device_sm_count() ? launch<T, 1>(p, inter, FEW_THREADS, st)
+                                           : launch<T, 3>(p, inter, MANY_THREADS, st);
 }
 
 }  // namespace
