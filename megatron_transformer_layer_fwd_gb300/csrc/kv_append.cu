@@ -260,7 +260,7 @@ mgb_status launch_t(const AppendParams& p, bool inter, cudaStream_t st) {
   // with 128 threads). Many: small blocks with three units per thread, eight per
   // SM (4699 tokens of 384 units, 127 MB, 23.2 us, 5.5 TB/s; 24.8 with six, 24 and
   // more with blocks of 192 threads and two units, 30 with 384 and one). There the
-  // chain cu, length, page of each token is the bound, not DRAM. Groups that
+  // chain cu, length, page of each token is the bound, not DRAM (41 % busy). Groups that
   // take runs of tokens and find their places together need 27 us: too few of
   // them are left to hide the rest.
   return p.tokens <= 4 * device_sm_count() ? launch<T, 1>(p, inter, FEW_THREADS, st)
