@@ -6,6 +6,8 @@ libmgb.so through `mgb`.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -92,6 +94,17 @@ def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda
     return torch.stack((torch.cos(a), torch.sin(a)), dim=-1).to(device, torch.float32).contiguous()
 
 
+def _on(stream, device: torch.device):
+    """Context with `stream` (None: the current one; a torch stream or a raw
+    handle) as torch's current stream: what is allocated and filled inside is
+    ordered with the kernels, and its memory goes back to that stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 class ServingBatch:
     """What all layers share in one step of running sequences: the lengths, the
     block table and the attention plan. Without `cu_seqlens` the step has one
@@ -110,16 +123,16 @@ class ServingBatch:
             raise ValueError("a batch of n sequences has n block-table rows and, packed, n + 1 row "
                              "offsets and a number of tokens")
         self.tokens = n if cu_seqlens is None else tokens
-        if cu_seqlens is None:
-            self.ws = torch.empty(mgb.mgb_attention_decode_ws_bytes(
-                n, shape.n_q_heads, shape.n_kv_heads, shape.head_dim), dtype=torch.uint8, device=dev)
-            self.plan = mgb.mgb_attention_decode_prepare(
-                n, shape.n_q_heads, shape.n_kv_heads, shape.head_dim, seq_lens, self.ws, stream)
-        else:
-            self.ws = torch.empty(mgb.mgb_attention_packed_ws_bytes(n, tokens), dtype=torch.uint8,
-                                  device=dev)
-            self.plan = mgb.mgb_attention_packed_prepare(n, tokens, shape.causal, cu_seqlens, self.ws,
-                                                         stream)
+        with _on(stream, dev):
+            if cu_seqlens is None:
+                self.ws = torch.empty(mgb.mgb_attention_decode_ws_bytes(
+                    n, shape.n_q_heads, shape.n_kv_heads, shape.head_dim), dtype=torch.uint8, device=dev)
+                self.plan = mgb.mgb_attention_decode_prepare(
+                    n, shape.n_q_heads, shape.n_kv_heads, shape.head_dim, seq_lens, self.ws)
+            else:
+                self.ws = torch.empty(mgb.mgb_attention_packed_ws_bytes(n, tokens), dtype=torch.uint8,
+                                      device=dev)
+                self.plan = mgb.mgb_attention_packed_prepare(n, tokens, shape.causal, cu_seqlens, self.ws)
 
 
 class ServingLayer:
@@ -142,35 +155,45 @@ class ServingLayer:
         self.w = {k: (to_device(arrays[k], self.dtype, k_pool.device) if arrays.get(k) is not None
                       else None) for k in WEIGHT_KEYS}
 
-    def _gemm(self, epilogue, a, w, bias, c, c2=None, resid=None, stream=None):
+    def _gemm(self, epilogue, a, w, bias, c, c2=None, resid=None):
         m, k, n = a.shape[0], a.shape[1], w.shape[0]
         d = mgb.GemmExDesc(
             g=mgb.GemmDesc(m=m, n=n, k=k, a_major=mgb.MGB_K_MAJOR, b_major=mgb.MGB_K_MAJOR, lda=k, ldb=k,
                            ldc=n, dtype=self.mgb_dtype, c_f32=0, accumulate=0, alpha=1.0),
             epilogue=epilogue, glu_block=self.shape.glu_block, ldc2=c2.shape[1] if c2 is not None else 0,
             ldr=n, ldaux=0)
-        mgb.mgb_gemm_ex(d, a, w, bias, c, c2=c2, resid=resid, stream=stream)
+        mgb.mgb_gemm_ex(d, a, w, bias, c, c2=c2, resid=resid)
         return c
 
-    def _norm(self, x, which, stream):
+    def _norm(self, x, which):
         y = torch.empty_like(x)
         mgb.mgb_layernorm_fwd(x.shape[0], x.shape[1], self.mgb_dtype, self.shape.ln_eps, x,
-                              self.w[f"ln{which}_g"], self.w[f"ln{which}_b"], y, None, None, stream)
+                              self.w[f"ln{which}_g"], self.w[f"ln{which}_b"], y, None, None)
         return y
 
     def step(self, x: torch.Tensor, batch: ServingBatch, stream=None) -> torch.Tensor:
         """The layer's output [tokens, hidden] for the batch's new rows x, whose
         keys and values enter the cache. Rows of no sequence come out as the
-        layer of a zero attention output."""
-        s, w, d = self.shape, self.w, self.shape.head_dim
+        layer of a zero attention output. With `stream` the whole step, its
+        temporaries included, runs on that stream, behind what the caller has
+        ordered it after; the output belongs to it."""
+        s = self.shape
         if tuple(x.shape) != (batch.tokens, s.hidden) or x.dtype != self.dtype or not x.is_contiguous():
             raise ValueError("x must be [batch.tokens, hidden] of the layer's dtype, contiguous")
+        with _on(stream, x.device):
+            if stream is not None:  # either may belong to another stream and be freed before the step is done
+                now = torch.cuda.current_stream(x.device)
+                x.record_stream(now)
+                batch.ws.record_stream(now)
+            return self._step(x, batch)
+
+    def _step(self, x: torch.Tensor, batch: ServingBatch) -> torch.Tensor:
+        s, w, d = self.shape, self.w, self.shape.head_dim
         T, nq, nkv = x.shape[0], self.shape.n_q_heads, self.shape.n_kv_heads
         pre = s.norm_pos == "pre"
         width = (nq + 2 * nkv) * d
         new = lambda cols: torch.empty((T, cols), dtype=self.dtype, device=x.device)
-        qkv = self._gemm(mgb.MGB_EPI_STORE, self._norm(x, 1, stream) if pre else x, w["w_qkv"],
-                         w["b_qkv"], new(width), stream=stream)
+        qkv = self._gemm(mgb.MGB_EPI_STORE, self._norm(x, 1) if pre else x, w["w_qkv"], w["b_qkv"], new(width))
         q, k, v = qkv, qkv[:, nq * d:], qkv[:, (nq + nkv) * d:]
         cache = mgb.kv_cache(self.k_pool, self.v_pool, batch.block_table)
         rot = 2 * self.rope.shape[1] if self.rope is not None else 0
@@ -178,19 +201,18 @@ class ServingLayer:
                                   self.rope.shape[0] if rot else 0)
         # queries and keys are rotated where they lie
         mgb.mgb_kv_append(desc, cache, batch.cu_seqlens, batch.seq_lens, self.rope, q, k, v, width, width,
-                          q, width, k, width, stream)
+                          q, width, k, width)
         o = torch.zeros((T, nq * d), dtype=self.dtype, device=x.device)
         if batch.cu_seqlens is None:
-            mgb.mgb_attention_decode(batch.plan, cache, q, width, o, nq * d, None, stream)
+            mgb.mgb_attention_decode(batch.plan, cache, q, width, o, nq * d, None)
         else:
             mgb.mgb_attention_packed_fwd(batch.plan, nq, nkv, d, self.mgb_dtype, q, k, v, width, width, o,
-                                         nq * d, None, stream)
-        h = self._gemm(mgb.MGB_EPI_BIAS_RESID, o, w["w_o"], w["b_o"], new(s.hidden), resid=x, stream=stream)
+                                         nq * d, None)
+        h = self._gemm(mgb.MGB_EPI_BIAS_RESID, o, w["w_o"], w["b_o"], new(s.hidden), resid=x)
         if not pre:
-            h = self._norm(h, 1, stream)
+            h = self._norm(h, 1)
         epi = mgb.MGB_EPI_BIAS_SWIGLU if s.act == "swiglu" else mgb.MGB_EPI_BIAS_GELU
         a = new(s.ffn)
-        self._gemm(epi, self._norm(h, 2, stream) if pre else h, w["w_1"], w["b_1"], new(w["w_1"].shape[0]),
-                   c2=a, stream=stream)
-        y = self._gemm(mgb.MGB_EPI_BIAS_RESID, a, w["w_2"], w["b_2"], new(s.hidden), resid=h, stream=stream)
-        return y if pre else self._norm(y, 2, stream)
+        self._gemm(epi, self._norm(h, 2) if pre else h, w["w_1"], w["b_1"], new(w["w_1"].shape[0]), c2=a)
+        y = self._gemm(mgb.MGB_EPI_BIAS_RESID, a, w["w_2"], w["b_2"], new(s.hidden), resid=h)
+        return y if pre else self._norm(y, 2)
