@@ -123,6 +123,8 @@ class ServingBatch:
             raise ValueError("a batch of n sequences has n block-table rows and, packed, n + 1 row "
                              "offsets and a number of tokens")
         self.tokens = n if cu_seqlens is None else tokens
+        self.heads = (shape.n_q_heads, shape.n_kv_heads, shape.head_dim)
+        self.causal = shape.causal
         with _on(stream, dev):
             if cu_seqlens is None:
                 self.ws = torch.empty(mgb.mgb_attention_decode_ws_bytes(
@@ -180,6 +182,11 @@ class ServingLayer:
         s = self.shape
         if tuple(x.shape) != (batch.tokens, s.hidden) or x.dtype != self.dtype or not x.is_contiguous():
             raise ValueError("x must be [batch.tokens, hidden] of the layer's dtype, contiguous")
+        # (a packed plan serves any heads, a decode plan those it was cut for)
+        if batch.cu_seqlens is None and batch.heads != (s.n_q_heads, s.n_kv_heads, s.head_dim):
+            raise ValueError("the batch was prepared for other heads than the layer's")
+        if batch.cu_seqlens is not None and bool(batch.causal) != bool(s.causal):
+            raise ValueError("the batch was prepared for a causal mask, or without one, unlike the layer")
         with _on(stream, x.device):
             if stream is not None:  # either may belong to another stream and be freed before the step is done
                 now = torch.cuda.current_stream(x.device)
