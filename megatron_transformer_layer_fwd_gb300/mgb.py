@@ -474,6 +474,8 @@ def kv_cache(k_pool, v_pool, block_table) -> KVCache:
     if block_table.dim() != 2 or block_table.dtype != torch.int32 or \
             (block_table.shape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError("block_table must be [n_seqs, max_pages] int32 with contiguous rows")
+    if k_pool.device != v_pool.device or k_pool.device != block_table.device:
+        raise ValueError("the pools and the block table must be on one device")
     dtypes = {torch.bfloat16: MGB_BF16, torch.float32: MGB_F32}
     if k_pool.dtype not in dtypes:
         raise ValueError("the pools must be bfloat16 or float32")

@@ -94,12 +94,16 @@ def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda
     return torch.stack((torch.cos(a), torch.sin(a)), dim=-1).to(device, torch.float32).contiguous()
 
 
+DEVICE = "cuda"  # where a batch's lengths, offsets and block table lie: kernels read them
+
+
 def _on(stream, device: torch.device):
     """Context with `stream` (None: the current one; a torch stream or a raw
     handle) as torch's current stream: what is allocated and filled inside is
-    ordered with the kernels, and its memory goes back to that stream."""
+    ordered with the kernels, and its memory goes back to that stream. The
+    tensors' device becomes the current one."""
     if stream is None:
-        return contextlib.nullcontext()
+        return torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)
@@ -122,6 +126,8 @@ class ServingBatch:
                 cu_seqlens is not None and (cu_seqlens.numel() != n + 1 or tokens is None)):
             raise ValueError("a batch of n sequences has n block-table rows and, packed, n + 1 row "
                              "offsets and a number of tokens")
+        if dev.type != DEVICE or any(t.device != dev for t in (block_table, cu_seqlens) if t is not None):
+            raise ValueError("seq_lens, cu_seqlens and the block table must be on one GPU device")
         self.tokens = n if cu_seqlens is None else tokens
         self.heads = (shape.n_q_heads, shape.n_kv_heads, shape.head_dim)
         self.causal = shape.causal
@@ -151,6 +157,8 @@ class ServingLayer:
         if k_pool.dtype != self.dtype or tuple(k_pool.shape[2:]) != (shape.n_kv_heads, shape.head_dim):
             raise ValueError("the pools must be [n_pages, page_size, n_kv_heads, head_dim] of the "
                              "layer's dtype")
+        if any(t is not None and t.device != k_pool.device for t in (v_pool, rope)):
+            raise ValueError("the pools and rope must be on one device")
         if rope is not None and (rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[2] != 2
                                  or not rope.is_contiguous()):
             raise ValueError("rope must be [positions, rot_dim / 2, 2] float32, contiguous")
@@ -182,6 +190,8 @@ class ServingLayer:
         s = self.shape
         if tuple(x.shape) != (batch.tokens, s.hidden) or x.dtype != self.dtype or not x.is_contiguous():
             raise ValueError("x must be [batch.tokens, hidden] of the layer's dtype, contiguous")
+        if any(t.device != x.device for t in (self.k_pool, batch.seq_lens)):
+            raise ValueError("x, the layer's pools and the batch must be on one device")
         # (a packed plan serves any heads, a decode plan those it was cut for)
         if batch.cu_seqlens is None and batch.heads != (s.n_q_heads, s.n_kv_heads, s.head_dim):
             raise ValueError("the batch was prepared for other heads than the layer's")

@@ -1,12 +1,12 @@
 """Serving calls whose parts do not belong together are turned down on the host
 before any launch: a batch prepared for other heads or another mask than the
-layer's (no GPU needed)."""
+layer's, tensors on different devices (no GPU needed)."""
 import dataclasses
 
 import pytest
 import torch
 
-from megatron_transformer_layer_fwd_gb300 import mgb
+from megatron_transformer_layer_fwd_gb300 import mgb, runner
 from megatron_transformer_layer_fwd_gb300.inputs import LayerShape, layer_inputs
 from megatron_transformer_layer_fwd_gb300.runner import ServingBatch, ServingLayer
 
@@ -26,9 +26,14 @@ def recorded(monkeypatch):
     for name in ("mgb_attention_decode_prepare", "mgb_attention_packed_prepare", "mgb_gemm_ex",
                  "mgb_layernorm_fwd", "mgb_kv_append", "mgb_attention_decode", "mgb_attention_packed_fwd"):
         monkeypatch.setattr(mgb, name, fake(name))
+    monkeypatch.setattr(runner, "DEVICE", "cpu")
     monkeypatch.setattr(mgb, "mgb_attention_decode_ws_bytes", lambda *a: 256)
     monkeypatch.setattr(mgb, "mgb_attention_packed_ws_bytes", lambda *a: 256)
     return calls
+
+
+def _ints(*a):
+    return torch.tensor(a, dtype=torch.int32)
 
 
 def _batch(shape, n, packed):
@@ -76,3 +81,45 @@ def test_a_batch_serves_layers_that_differ_elsewhere(recorded, packed):
         del recorded[:]
         _layer().step(_x(3), batch)
         assert recorded[-1] in ("mgb_gemm_ex", "mgb_layernorm_fwd") and len(recorded) >= 7
+
+
+META = torch.device("meta")   # a device that is not the others'
+
+
+@pytest.mark.parametrize("which", range(3))
+def test_cache_tensors_of_different_devices(which):
+    pools = [torch.zeros((4, 8, 2, 64), dtype=torch.bfloat16) for _ in range(2)]
+    a = pools + [torch.zeros((3, 2), dtype=torch.int32)]
+    a[which] = a[which].to(META)
+    with pytest.raises(ValueError, match="device"):
+        mgb.kv_cache(*a)
+
+
+@pytest.mark.parametrize("which", ["table", "lens", "cu"])
+def test_batch_tensors_of_different_devices(recorded, which):
+    a = dict(table=torch.zeros((3, 4), dtype=torch.int32), lens=_ints(1, 1, 1), cu=_ints(0, 1, 2, 3))
+    a[which] = a[which].to(META)
+    with pytest.raises(ValueError, match="device"):
+        ServingBatch(SHAPE, a["table"], a["lens"], a["cu"], 3)
+    assert recorded == []
+
+
+def test_layer_and_step_tensors_of_different_devices(recorded):
+    pool = torch.zeros((4, 8, 2, 64), dtype=torch.bfloat16)
+    for k, v, rope in [(pool, pool.to(META), None), (pool, pool, torch.zeros((9, 32, 2), device=META))]:
+        with pytest.raises(ValueError, match="device"):
+            ServingLayer(SHAPE, layer_inputs(SHAPE), k, v, rope)
+    layer, batch = _layer(), _batch(SHAPE, 3, False)
+    with pytest.raises(ValueError, match="device"):
+        layer.step(_x(3).to(META), batch)
+    batch.seq_lens = batch.seq_lens.to(META)
+    with pytest.raises(ValueError, match="device"):
+        layer.step(_x(3), batch)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_batch_on_the_host(recorded, monkeypatch, packed):
+    monkeypatch.setattr(runner, "DEVICE", "cuda")
+    with pytest.raises(ValueError, match="device"):
+        _batch(SHAPE, 3, packed)
+    assert recorded == []
