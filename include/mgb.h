@@ -468,8 +468,10 @@ typedef struct {
  * sequence belongs to none: their rows of q_out and k_out are left as they
  * were and nothing is cached. A position below 0, past the table's max_pages *
  * page_size or past rope_len, and a page outside [0, n_pages), are
- * MGB_ERR_INDEX; all of that row's stores are skipped. Two rows must not share
- * a slot. dtype (the cache's) bf16 or float32; head_dim <= 256 a multiple of
+ * MGB_ERR_INDEX; all of that row's stores are skipped. Offsets that do not
+ * begin with 0, decrease or leave [0, tokens] are MGB_ERR_INDEX too, and a row
+ * is not stored if by them it lies outside its sequence, or its sequence begins
+ * before the one in front. Two rows must not share a slot. dtype (the cache's) bf16 or float32; head_dim <= 256 a multiple of
  * 16 (bf16) or 8 (float32), rot_dim likewise and at most head_dim. */
 typedef struct {
   int32_t tokens, n_seqs, n_q_heads;

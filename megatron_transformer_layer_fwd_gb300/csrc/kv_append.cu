@@ -31,17 +31,19 @@ constexpr int FEW_THREADS = 512;    // of a block at most, with few tokens
 constexpr int MANY_THREADS = 128;   // .. with many
 
 struct AppendParams {
-  int tokens, n_seqs, nq, nkv, rot, rope_len;
+  int tokens, n_seqs, nq, nkv, rot;
   int units_head;              // units per head
   uint32_t m_head;             // 2^32 / units_head, rounded up; 0 for one unit
   int units;                   // per token: (nq + 2 nkv) heads (0 q heads without q_out)
-  int page_size, max_pages, n_pages, d;
+  int page_size, n_pages, d;
   const int32_t *cu, *lens, *table;
   int64_t ld_table, s_page, s_tok, s_head;
   const float* rope;
   const char *q, *k, *v;
   char *q_out, *k_out, *k_pool, *v_pool;
   int64_t ld_q, ld_kv, ld_qo, ld_ko;
+  int cap;                     // positions below this: the table's and the rotary table's
+  unsigned check_blocks;       // the last blocks, which check cu
   int* err;
 };
 
@@ -163,29 +165,46 @@ __global__ void __launch_bounds__(UB == 1 ? FEW_THREADS : MANY_THREADS, UB == 1 
   pdl_wait();  // everything the call reads may come from the kernel before
   load(threadIdx.x);
 
+  const unsigned back = gridDim.x - 1 - blockIdx.x;
+  if (back < p.check_blocks) {
+    // Every offset is checked once, by the grid's last threads (which start last and,
+    // in a call of one block, are not the warp that looks its token up): whatever
+    // sequence the search below finds in offsets that are not sorted, the call
+    // reports them.
+    const int nt = blockDim.x * blockDim.y;
+    for (int64_t i = (int64_t)back * nt + nt - 1 - (g * blockDim.x + threadIdx.x); i < p.n_seqs;
+         i += (int64_t)p.check_blocks * nt) {
+      const int c0 = p.cu[i], c1 = p.cu[i + 1];
+      if (c0 < 0 || c1 < c0 || c1 > p.tokens || (i == 0 && c0 != 0)) record_error(p.err, kErrIndex);
+    }
+  }
   if (threadIdx.x < 32 && t < p.tokens) {
-    int s = t, first = t, rows = 1;
+    int s = t, first = t, behind = t + 1;  // the sequence's rows first .. behind - 1
+    int before = 0;                        // offset of the sequence before
     if (p.cu != nullptr) {
       s = find_seq(p.cu, p.n_seqs, t);
       if (s < p.n_seqs) {
+        if (s > 0) before = p.cu[s - 1];
         first = p.cu[s];
-        rows = p.cu[s + 1] - first;
+        behind = p.cu[s + 1];
       }
     }
     int pos = -1;
     int64_t slot = 0;
     const int len = s < p.n_seqs ? p.lens[s] : 0;
     if (len != 0) {  // else padding, or behind the last sequence
-      const int64_t at = (int64_t)len - rows + ((int64_t)t - first);
-      bool ok = at >= 0 && at < (int64_t)p.max_pages * p.page_size && at < INT32_MAX &&
-                (p.rot == 0 || at < p.rope_len);
+      // (a row outside its sequence's, by bad offsets, would go over cached tokens or
+      // behind the sequence's length)
+      const bool in = first >= max(before, 0) && first <= t && t < behind && behind <= p.tokens;
+      const int at = in ? max(len, 0) - (behind - t) : -1;
+      bool ok = at >= 0 && at < p.cap;
       if (ok) {
-        const int pg = (int)at / p.page_size;
+        const int pg = at / p.page_size;
         const int page = p.table[s * p.ld_table + pg];
         ok = page >= 0 && page < p.n_pages;
-        slot = page * p.s_page + ((int)at - pg * p.page_size) * p.s_tok;
+        slot = page * p.s_page + (at - pg * p.page_size) * p.s_tok;
       }
-      if (ok) pos = (int)at;
+      if (ok) pos = at;
       else if (threadIdx.x == 0) record_error(p.err, kErrIndex);
     }
     if (threadIdx.x == 0) {
@@ -241,7 +260,7 @@ __global__ void __launch_bounds__(UB == 1 ? FEW_THREADS : MANY_THREADS, UB == 1 
 }
 
 template <typename T, int UB>
-mgb_status launch(const AppendParams& p, bool inter, int most, cudaStream_t st) {
+mgb_status launch(AppendParams p, bool inter, int most, cudaStream_t st) {
   // threads along a token's units (whole warps, up to `most`), and groups of
   // them until a block has about 128
   const int x = p.units >= most ? most : (p.units + 31) / 32 * 32;
@@ -249,6 +268,10 @@ mgb_status launch(const AppendParams& p, bool inter, int most, cudaStream_t st) 
   if (y > MAX_GROUPS) y = MAX_GROUPS;
   if (y > p.tokens) y = p.tokens;
   const int grid = (int)(((int64_t)p.tokens + y - 1) / y);
+  if (p.cu != nullptr) {
+    const int64_t all = ((int64_t)p.n_seqs + x * y - 1) / (x * y);
+    p.check_blocks = (unsigned)(all < grid ? all : grid);
+  }
   LaunchScope scope(PROF_KV_APPEND, st);
   return launch_pdl(inter ? kv_append_kernel<T, UB, true> : kv_append_kernel<T, UB, false>, grid,
                     dim3(x, y), 0, st, p);
@@ -258,7 +281,7 @@ template <typename T>
 mgb_status launch_t(const AppendParams& p, bool inter, cudaStream_t st) {
   // Few tokens: as many threads as units, one each (one token 3.0 us; 0.5 us more
   // with 128 threads). Many: small blocks with three units per thread, eight per
-  // SM (4699 tokens of 384 units, 127 MB, 23.2 us, 5.5 TB/s; 24.8 with six, 24 and
+  // SM (4699 tokens of 384 units, 127 MB, 23.7 us, 5.4 TB/s; 1.6 more with six, 24 and
   // more with blocks of 192 threads and two units, 30 with 384 and one). There the
   // chain cu, length, page of each token is the bound, not DRAM (41 % busy). Groups that
   // take runs of tokens and find their places together need 27 us: too few of
@@ -333,11 +356,14 @@ extern "C" mgb_status mgb_kv_append(const mgb_kv_append_desc* d, const mgb_kv_ca
   if (d->tokens == 0 || d->n_seqs == 0) return MGB_OK;
   AppendParams p{};
   p.tokens = d->tokens; p.n_seqs = d->n_seqs; p.nq = d->n_q_heads; p.nkv = c->n_kv_heads;
-  p.rot = d->rot_dim; p.rope_len = d->rope_len; p.d = c->head_dim;
+  p.rot = d->rot_dim; p.d = c->head_dim;
   p.units_head = c->head_dim / (2 * vn);
   p.m_head = p.units_head == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + p.units_head - 1) / p.units_head);
   p.units = ((q_out ? p.nq : 0) + 2 * p.nkv) * p.units_head;
-  p.page_size = c->page_size; p.max_pages = c->max_pages; p.n_pages = c->n_pages;
+  int64_t cap = (int64_t)c->max_pages * c->page_size;
+  if (d->rot_dim > 0 && cap > d->rope_len) cap = d->rope_len;
+  p.cap = (int)(cap < INT32_MAX ? cap : INT32_MAX);
+  p.page_size = c->page_size; p.n_pages = c->n_pages;
   p.cu = cu_seqlens; p.lens = seq_lens; p.table = c->block_table; p.ld_table = c->ld_table;
   p.s_page = c->stride_page; p.s_tok = c->stride_token; p.s_head = c->stride_head;
   p.rope = rope;
