@@ -280,13 +280,15 @@ mgb_status launch(AppendParams p, bool inter, int most, cudaStream_t st) {
 template <typename T>
 mgb_status launch_t(const AppendParams& p, bool inter, cudaStream_t st) {
   // Few tokens: as many threads as units, one each (one token 3.0 us; 0.5 us more
-  // with 128 threads). Many: small blocks with three units per thread, eight per
-  // SM (4699 tokens of 384 units, 127 MB, 23.7 us, 5.4 TB/s; 1.6 more with six, 24 and
-  // more with blocks of 192 threads and two units, 30 with 384 and one). There the
-  // chain cu, length, page of each token is the bound, not DRAM (41 % busy). Groups that
-  // take runs of tokens and find their places together need 27 us: too few of
-  // them are left to hide the rest.
-  return p.tokens <= 4 * device_sm_count() ? launch<T, 1>(p, inter, FEW_THREADS, st)
+  // with 128 threads), while all blocks are resident at once: one token per sequence,
+  // bf16 and 384 units, 304 tokens 3.7 us (the other form 4.0), 456 tokens 6.3 (4.3),
+  // 912 9.4 (5.4); float32 and 192 units 2.9 (3.2), 3.1 (3.4), 3.8 (3.9).
+  // Many: small blocks with three units per thread, eight per SM (4699 tokens of 384
+  // units, 127 MB, 23.7 us, 5.4 TB/s; 1.6 more with six, 24 and more with blocks of 192
+  // threads and two units, 30 with 384 and one). There the chain cu, length, page of
+  // each token is the bound, not DRAM (41 % busy). Groups that take runs of tokens and
+  // find their places together need 27 us: too few of them are left to hide the rest.
+  return p.tokens <= 2 * device_sm_count() ? launch<T, 1>(p, inter, FEW_THREADS, st)
                                            : launch<T, 3>(p, inter, MANY_THREADS, st);
 }
 
