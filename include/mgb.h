@@ -476,6 +476,9 @@ typedef struct {
 typedef struct {
   int32_t tokens, n_seqs, n_q_heads;
   int32_t rot_dim, interleaved, rope_len;
+  int32_t whole; /* 1: every sequence's rows are all of it, as packed attention over
+                    these rows takes them: a length that is neither 0 nor the number of
+                    rows is MGB_ERR_INDEX, and its rows are skipped */
 } mgb_kv_append_desc;
 
 mgb_status mgb_kv_append(const mgb_kv_append_desc* desc, const mgb_kv_cache* cache,
@@ -487,7 +490,9 @@ mgb_status mgb_kv_append(const mgb_kv_append_desc* desc, const mgb_kv_cache* cac
  * the other: sequence s owns rows cu_seqlens[s] .. cu_seqlens[s+1] - 1
  * (cu_seqlens [n_seqs + 1] int32, non-decreasing, from 0 to at most tokens).
  * Within each sequence, per query head h: softmax(Q_h K_g^T / sqrt(d)) V_g,
- * with causal key j visible to query i iff j <= i. Rows that belong to no
+ * with causal key j visible to query i iff j <= i. Keys and values are these rows
+ * alone: tokens that a cache holds of a sequence are not attended to (whole in
+ * mgb_kv_append_desc reports such a batch). Rows that belong to no
  * sequence are not read, and their rows of o and lse are left as they were.
  *
  * mgb_attention_packed_prepare derives the work list of a batch from the row

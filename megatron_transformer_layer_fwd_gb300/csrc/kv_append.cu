@@ -42,6 +42,7 @@ struct AppendParams {
   const char *q, *k, *v;
   char *q_out, *k_out, *k_pool, *v_pool;
   int64_t ld_q, ld_kv, ld_qo, ld_ko;
+  int whole;                   // lengths are the rows' numbers (or 0)
   int cap;                     // positions below this: the table's and the rotary table's
   unsigned check_blocks;       // the last blocks, which check cu
   int* err;
@@ -195,7 +196,8 @@ __global__ void __launch_bounds__(UB == 1 ? FEW_THREADS : MANY_THREADS, UB == 1 
     if (len != 0) {  // else padding, or behind the last sequence
       // (a row outside its sequence's, by bad offsets, would go over cached tokens or
       // behind the sequence's length)
-      const bool in = first >= max(before, 0) && first <= t && t < behind && behind <= p.tokens;
+      const bool in = first >= max(before, 0) && first <= t && t < behind && behind <= p.tokens &&
+                      (!p.whole || len == behind - first);
       const int at = in ? max(len, 0) - (behind - t) : -1;
       bool ok = at >= 0 && at < p.cap;
       if (ok) {
@@ -325,7 +327,7 @@ extern "C" mgb_status mgb_kv_append(const mgb_kv_append_desc* d, const mgb_kv_ca
                                     void* k_out, int64_t ld_ko, void* stream) {
   if (fault_injected()) return MGB_ERR_INVALID_ARG;
   if (d == nullptr || d->tokens < 0 || d->n_seqs < 0 || d->rot_dim < 0 || d->rope_len < 0 ||
-      (d->interleaved & ~1))
+      (d->interleaved & ~1) || (d->whole & ~1))
     return MGB_ERR_INVALID_ARG;
   mgb_status s = check_kv_cache(c, d->n_seqs);
   if (s != MGB_OK) return s;
@@ -358,7 +360,7 @@ extern "C" mgb_status mgb_kv_append(const mgb_kv_append_desc* d, const mgb_kv_ca
   if (d->tokens == 0 || d->n_seqs == 0) return MGB_OK;
   AppendParams p{};
   p.tokens = d->tokens; p.n_seqs = d->n_seqs; p.nq = d->n_q_heads; p.nkv = c->n_kv_heads;
-  p.rot = d->rot_dim; p.d = c->head_dim;
+  p.rot = d->rot_dim; p.whole = d->whole; p.d = c->head_dim;
   p.units_head = c->head_dim / (2 * vn);
   p.m_head = p.units_head == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + p.units_head - 1) / p.units_head);
   p.units = ((q_out ? p.nq : 0) + 2 * p.nkv) * p.units_head;

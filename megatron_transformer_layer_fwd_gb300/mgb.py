@@ -101,7 +101,7 @@ class KVCache(ctypes.Structure):
 
 class KVAppendDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
-        "tokens", "n_seqs", "n_q_heads", "rot_dim", "interleaved", "rope_len")]
+        "tokens", "n_seqs", "n_q_heads", "rot_dim", "interleaved", "rope_len", "whole")]
 
 
 class AttentionDecodePlan(ctypes.Structure):
@@ -490,8 +490,8 @@ def kv_cache(k_pool, v_pool, block_table) -> KVCache:
 
 
 def kv_append_desc(tokens: int, n_seqs: int, n_q_heads: int, rot_dim: int, interleaved: bool,
-                   rope_len: int) -> KVAppendDesc:
-    return KVAppendDesc(tokens, n_seqs, n_q_heads, rot_dim, int(interleaved), rope_len)
+                   rope_len: int, whole: bool = False) -> KVAppendDesc:
+    return KVAppendDesc(tokens, n_seqs, n_q_heads, rot_dim, int(interleaved), rope_len, int(whole))
 
 
 def mgb_kv_append(desc: KVAppendDesc, cache: KVCache, cu_seqlens, seq_lens, rope, q, k, v, ld_q,

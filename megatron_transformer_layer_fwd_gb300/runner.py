@@ -113,7 +113,12 @@ class ServingBatch:
     """What all layers share in one step of running sequences: the lengths, the
     block table and the attention plan. Without `cu_seqlens` the step has one
     new token per sequence (decode); with it, the rows of whole prompts packed
-    one behind the other (`tokens` rows, possibly more than they fill)."""
+    one behind the other (`tokens` rows, possibly more than they fill), whose
+    lengths are their numbers of rows, or 0 for padding: a prompt that continues
+    cached tokens is reported by mgb_device_status as MGB_ERR_INDEX and not
+    cached, since its rows would attend to each other alone. A prompt's rows see
+    each other as the shape's mask says; a decode step's row sees all of the
+    cache, with either mask."""
 
     def __init__(self, shape, block_table: torch.Tensor, seq_lens: torch.Tensor,
                  cu_seqlens: torch.Tensor | None = None, tokens: int | None = None, stream=None):
@@ -215,7 +220,7 @@ class ServingLayer:
         cache = mgb.kv_cache(self.k_pool, self.v_pool, batch.block_table)
         rot = 2 * self.rope.shape[1] if self.rope is not None else 0
         desc = mgb.kv_append_desc(T, batch.seq_lens.numel(), nq, rot, self.rope_interleaved,
-                                  self.rope.shape[0] if rot else 0)
+                                  self.rope.shape[0] if rot else 0, whole=batch.cu_seqlens is not None)
         # queries and keys are rotated where they lie
         mgb.mgb_kv_append(desc, cache, batch.cu_seqlens, batch.seq_lens, self.rope, q, k, v, width, width,
                           q, width, k, width)

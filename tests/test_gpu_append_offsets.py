@@ -98,3 +98,38 @@ def test_bad_offset_in_a_large_step(value):
     if value >= 0:
         # sequences on one side of the bad offset at least are served in full
         assert {(s, 1 + i) for s in good if s < 64 for i in range(2)} <= w
+
+
+@pytest.mark.parametrize("cu,lens,tokens,bad", [
+    ([0, 3, 6], [5, 3], 6, [0]),              # the first continues two cached tokens
+    ([0, 3, 6], [3, 2], 6, [1]),              # more rows than tokens
+    ([0, 3, 6, 8], [3, 0, 2], 9, []),         # a padding sequence, a row of none
+    ([0, 1, 1, 2], [1, 7, 4], 2, [2]),        # no rows: nothing to attend, not looked at
+    (None, [1, 2, 1], 3, [1]),
+])
+def test_whole_sequences(cu, lens, tokens, bad):
+    st, rows, slots = _append(cu, lens, tokens, whole=True)
+    assert st == (mgb.MGB_ERR_INDEX if bad else mgb.MGB_OK)
+    at = cu or list(range(tokens + 1))
+    good = [s for s in range(len(lens)) if s not in bad and lens[s] and at[s + 1] > at[s]]
+    assert slots == {(s, p) for s in good for p in range(lens[s])}
+    assert rows == [t for s in good for t in range(at[s], at[s + 1])]
+
+
+def test_a_prompt_batch_over_cached_tokens_is_reported():
+    """Packed attention sees the new rows alone: the runner's packed step of a sequence
+    that already has tokens in the cache must not pass for a right one."""
+    import numpy as np
+    from megatron_transformer_layer_fwd_gb300.inputs import LayerShape, layer_inputs
+    from megatron_transformer_layer_fwd_gb300.runner import ServingBatch, ServingLayer
+    shape = LayerShape(1, 1, 128, 4, 2, 64, 256, causal=True)
+    pools = torch.zeros((2, 8, 8, 2, 64), dtype=torch.bfloat16, device="cuda")
+    layer = ServingLayer(shape, layer_inputs(shape), pools[0], pools[1], rope_table(32, 64))
+    table, cu = ints(np.arange(8).reshape(2, 4)), ints([0, 5, 9])
+    x = torch.randn((9, 128), device="cuda").bfloat16()
+    layer.step(x, ServingBatch(shape, table, ints([5, 4]), cu, 9))
+    assert mgb.mgb_device_status() == mgb.MGB_OK
+    before = pools.clone()
+    layer.step(x, ServingBatch(shape, table, ints([5, 8]), cu, 9))
+    assert mgb.mgb_device_status() == mgb.MGB_ERR_INDEX
+    assert torch.equal(pools, before)      # the first stored what it had, the second nothing

@@ -2,6 +2,7 @@
 before any launch: a batch prepared for other heads or another mask than the
 layer's, tensors on different devices (no GPU needed)."""
 import dataclasses
+import os
 
 import pytest
 import torch
@@ -123,3 +124,17 @@ def test_a_batch_on_the_host(recorded, monkeypatch, packed):
     with pytest.raises(ValueError, match="device"):
         _batch(SHAPE, 3, packed)
     assert recorded == []
+
+
+def test_append_descriptor_of_whole_sequences():
+    import ctypes
+    from tests.test_serving_host import _cache, P
+    if not os.path.exists(mgb.LIB_PATH):
+        from megatron_transformer_layer_fwd_gb300 import build
+        build.build()
+    d = mgb.kv_append_desc(5, 3, 4, 64, False, 100)
+    assert d.whole == 0 and mgb.kv_append_desc(5, 3, 4, 64, False, 100, whole=True).whole == 1
+    for bad in (2, -1):
+        d.whole = bad
+        assert mgb.load().mgb_kv_append(ctypes.byref(d), ctypes.byref(_cache()), P, P, P, P, P, P, 256, 256, 2 * P,
+                                        256, 2 * P, 128, None) == mgb.MGB_ERR_INVALID_ARG
