@@ -542,8 +542,10 @@ mgb_status mgb_attention_packed_fwd(const mgb_attention_packed_plan* plan, int32
  * mgb_attention_decode: q [n_seqs, nq*d] (row stride ld_q, e.g. the query
  * columns of a fused qkv row), o [n_seqs, nq*d] (row stride ld_o), lse [n_seqs,
  * nq] float32 or NULL. The cache's dtype is q's and o's; bf16 or float32,
- * head_dim 64 or 128, any group size nq / nkv; o must not overlap q. A length past max_pages *
- * page_size and a page outside [0, n_pages) are MGB_ERR_INDEX. Sums and softmax
+ * head_dim 64 or 128, any group size nq / nkv; o must not overlap q. A length
+ * past max_pages * page_size is MGB_ERR_INDEX and counts as 0. A page outside
+ * [0, n_pages) is MGB_ERR_INDEX, and its tokens are left out of the softmax
+ * (where that leaves none, o is NaN and lse -inf). Sums and softmax
  * statistics are float32; in bf16 the weights are rounded to bf16 before
  * they multiply V. Results repeat bit for bit with the same lengths. The
  * calls of one plan share its workspace: each is ordered after the prepare

@@ -27,8 +27,8 @@
 // sums and output sums; the warps' sums are joined at the end of an item. Each
 // warp streams its tokens through a private ring in shared memory by 16-byte
 // asynchronous copies, so the main loop has no CTA-wide barrier, any page size
-// and any page layout works, and tokens past the length are never read (zero
-// fill). 2 (d = 64: 3) CTAs per SM keep 128 (96) KB in flight per SM.
+// and any page layout works, and tokens past the length or of a bad page are never
+// read (zero fill, weight 0). 2 (d = 64: 3) CTAs per SM keep 128 (96) KB in flight per SM.
 //   bf16: products on mma.sync m16n8k16, transposed: S^T = K Q^T with 16 tokens
 //   as the rows and the query heads as the columns, and O^T = V^T P^T with d as
 //   the rows. There is one query token per sequence, so an item has at most 16
@@ -211,7 +211,8 @@ struct Params {
   const void *k, *v;
   const int32_t* table;
   int64_t s_page, s_tok, s_head, ld_table;
-  int n_pages, page_size, max_pages;
+  int n_pages, page_size;
+  int cap;       // tokens a row of the table holds
   const void* q;
   int64_t ld_q;
   void* o;
@@ -270,9 +271,11 @@ struct Cursor {
     at = st.at; s = st.s; h = st.h; t = st.t; len = st.len; next_len = st.next_len;
     nt = tiles_of(len, TK);
   }
-  // to the next unit; the next sequence's length was requested one sequence ago
+  // to the next unit; the next sequence's length was requested one sequence ago. A
+  // length past the table counts as 0, and its units behind the first one looked
+  // at are passed over, however many they are
   __device__ void next(const Params& p) {
-    if (++t < nt) return;
+    if (len <= p.cap && ++t < nt) return;
     t = 0;
     at += cost_of(nt, item_cost(D));
     if (++h < p.groups) return;
@@ -291,6 +294,7 @@ struct Cfg {
   static constexpr int TK = unit_tokens(D);
   static constexpr int SK = 4096 / (D * ES);         // tokens per warp and stage: 4 KB of keys
   static constexpr int SUB = TK / (WARPS * SK);      // stages per unit
+  static constexpr uint32_t ALL = SK == 32 ? ~0u : (1u << SK) - 1u;  // a bit per token of a stage
   static constexpr int ROW = D * ES;                 // bytes of a token's vector
   static constexpr int CH = ROW / 16;                // 16-byte chunks of it
   static constexpr int KV = SK * ROW;                // bytes of a stage's keys (or values)
@@ -339,18 +343,19 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
   int ld_sub = 0, ld_n = 0;
   int pg = 0, slot = 0, hkv = 0;
   bool on = false, look = false;
+  // which tokens of the ST stages fetched last are to be seen, the oldest first
+  uint32_t seen[ST] = {};
   auto peek = [&]() {  // request the page of this lane's token of the next stage
     on = false;
     look = ld.before(end);
     if (!look) return;
     const int key = ld.t * TK + ld_sub * (WARPS * C::SK) + warp * C::SK + (lane % C::SK);
     hkv = ld.h / p.per_kv;
-    if (key < ld.len) {
+    on = key < ld.len && ld.len <= p.cap;
+    if (on) {
       const int i = key / p.page_size;
       slot = key - i * p.page_size;
-      on = i < p.max_pages;
-      if (on) pg = p.table[ld.s * p.ld_table + i];
-      else record_error(p.err, kErrIndex);
+      pg = p.table[ld.s * p.ld_table + i];
     }
     if (++ld_sub == C::SUB) {
       ld_sub = 0;
@@ -358,12 +363,16 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
     }
   };
   auto fetch = [&]() {  // copy the stage the last peek looked at, then peek
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) seen[i] = seen[i + 1];
+    seen[ST - 1] = 0;
     if (look) {
       bool ok = on && pg >= 0 && pg < p.n_pages;
       if (on && !ok) record_error(p.err, kErrIndex);
+      seen[ST - 1] = __ballot_sync(0xffffffffu, ok) & C::ALL;
       const int64_t off = ok ? pg * p.s_page + slot * p.s_tok + hkv * p.s_head : -1;
       const uint32_t dst = ring + (ld_n % ST) * 2 * C::KV;
-      if (__any_sync(0xffffffffu, ok)) {
+      if (seen[ST - 1] != 0) {
 #pragma unroll
         for (int i = 0; i < C::SK * C::CH / 32; ++i) {
           const int row = (i * 32 + lane) / C::CH, ch = (i * 32 + lane) % C::CH;
@@ -425,7 +434,9 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
 
   int n_use = 0;  // stages consumed
   while (cu.before(end)) {
-    const int s = cu.s, h = cu.h, len = cu.len, nt = cu.nt;
+    const int s = cu.s, h = cu.h, nt = cu.nt, t0 = cu.t;
+    const int len = cu.len <= p.cap ? cu.len : 0;
+    if (cu.len > p.cap && tid == 0) record_error(p.err, kErrIndex);
     const int64_t at = cu.at;
     const int rows = min(p.rows, p.G - (h % p.per_kv) * p.rows);
     uint32_t qa[BF ? NQ : 1];
@@ -471,9 +482,8 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
         fetch();
         const uint32_t sk = ring + (n_use % ST) * 2 * C::KV, sv = sk + C::KV;
         ++n_use;
-        const int key0 = cu.t * TK + sub * (WARPS * C::SK) + warp * C::SK;
-        const int left = len - key0;  // visible tokens of the slice
-        if (left <= 0) continue;
+        const uint32_t see = seen[0];  // the slice's visible tokens
+        if (see == 0) continue;
         if constexpr (BF) {
           // sc[mt][ht]: token 16 mt + lane / 4 (+ 8 in the upper two), heads 8 ht +
           // 2 (lane % 4) + {0, 1}
@@ -490,14 +500,15 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
               for (int ht = 0; ht < HT; ++ht)
                 mma_bf16(sc[mt][ht], a, qa[(kk * HT + ht) * 2], qa[(kk * HT + ht) * 2 + 1]);
             }
-          if (left < C::SK) {
+          if (see != C::ALL) {
+            const uint32_t sl = see >> (lane >> 2);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (16 * mt + (lane >> 2) + (e >> 1) * 8 >= left) sc[mt][ht][e] = -INFINITY;
+                  if (!((sl >> (16 * mt + (e >> 1) * 8)) & 1u)) sc[mt][ht][e] = -INFINITY;
           }
           bool up[NM], any = false;
           float mx[NM];
@@ -562,7 +573,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
           float* sp = join + warp * 8 * NR;  // [token][head] (join is free until the item's end)
 #pragma unroll
           for (int kt = 0; kt < C::SK / 8; ++kt) {  // eight tokens at a time
-            if (left <= 8 * kt) break;
+            if ((see >> (8 * kt)) == 0) break;
             float d0[NR] = {}, d1[NR] = {};
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -589,7 +600,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
               const float y0 = (hi ? x[2] : x[0]) + __shfl_xor_sync(0xffffffffu, hi ? x[0] : x[2], 16);
               const float y1 = (hi ? x[3] : x[1]) + __shfl_xor_sync(0xffffffffu, hi ? x[1] : x[3], 16);
               const float sc = (odd ? y1 : y0) + __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 8);
-              pr[i] = 8 * kt + key < left ? sc * p.sl2 : -INFINITY;
+              pr[i] = (see >> (8 * kt + key)) & 1u ? sc * p.sl2 : -INFINITY;
               mx[i] = pr[i];
             }
 #pragma unroll
@@ -654,6 +665,10 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
       more = cu.at == at && cu.before(end);
     }
 
+    if (len == 0 && t0 != 0) {
+      __syncthreads();  // (sq is free)
+      continue;  // the CTA with the first unit of a length past the table stores its zeros
+    }
     // ---------------- the item's units in this CTA are done: join the warps
     if constexpr (BF) {
 #pragma unroll
@@ -684,7 +699,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
     };
     // first and last CTA of the item
     const int64_t last = at + begin_of(nt - 1, nt);
-    const bool whole = at >= (int64_t)c * hd.chunk && last < end;
+    const bool whole = len == 0 || (at >= (int64_t)c * hd.chunk && last < end);
     const int cf = whole ? c : (int)(at / hd.chunk), cl = whole ? c : (int)(last / hd.chunk);
     // part 2 c: the CTA's range begins at or inside the item; 2 c + 1: before it
     auto part_of = [&](int cc) { return 2 * cc + ((int64_t)cc * hd.chunk < at ? 1 : 0); };
@@ -747,7 +762,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
         float M, L;
         joined(r, M, L);
         if (whole) {
-          const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+          const float inv = len > 0 ? 1.0f / L : 0.0f;  // (no token left: 0 / 0)
           store_o(r, col, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
           if (p.lse != nullptr && col == 0)
             p.lse[(int64_t)s * p.nq + head0 + r] = (M + log2f(L)) * LN2;
@@ -813,7 +828,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
               for (int j = 0; j < CPL; ++j) x[j] = fmaf(w, z[i][j], x[j]);
             }
           }
-          const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+          const float inv = 1.0f / L;
           T* o = static_cast<T*>(p.o) + s * p.ld_o + (int64_t)(head0 + r) * D + lane * CPL;
 #pragma unroll
           for (int j = 0; j < CPL; ++j) o[j] = from_f<T>(x[j] * inv);
@@ -927,7 +942,9 @@ mgb_status mgb_attention_decode(const mgb_attention_decode_plan* plan, const mgb
   p.k = c->k; p.v = c->v; p.table = c->block_table;
   p.s_page = c->stride_page; p.s_tok = c->stride_token; p.s_head = c->stride_head;
   p.ld_table = c->ld_table;
-  p.n_pages = c->n_pages; p.page_size = c->page_size; p.max_pages = c->max_pages;
+  p.n_pages = c->n_pages; p.page_size = c->page_size;
+  const int64_t cap = (int64_t)c->max_pages * c->page_size;
+  p.cap = cap < INT32_MAX ? (int)cap : INT32_MAX;
   p.q = q; p.ld_q = ld_q; p.o = o; p.ld_o = ld_o; p.lse = lse;
   p.sl2 = LOG2E / sqrtf((float)d);
   p.err = device_error_word();
