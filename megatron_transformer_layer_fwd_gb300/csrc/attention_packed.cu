@@ -602,14 +602,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (j == 0) m_ref = chunk_max(0, -INFINITY) * p.sl2;
         if (edge) form(std::true_type{});
         else form(std::false_type{});
-        // (NaN too; no reference: all first scores were -infinity)
-        if (__any_sync(0xffffffffu, !(sum <= SUM_LIMIT) || m_ref == -INFINITY)) {
+        // (NaN too; no reference: all first scores were -infinity.) Rows behind the end
+        // hold other sequences' queries and have no say; nor does a row move its
+        // reference because another one must, so that its bits are its own. The
+        // branch is the whole warp's, as the TMEM loads inside must be.
+        bool need = !(sum <= SUM_LIMIT) || m_ref == -INFINITY;
+        if (__any_sync(0xffffffffu, need) && __any_sync(0xffffffffu, need &= row < w.len)) {
           float mx = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 4; ++c) mx = chunk_max(c, mx);
           mx *= p.sl2;
           float alpha = 1.0f;
-          if (mx > m_ref) {
+          if (need && mx > m_ref) {
             alpha = exp2f(m_ref - mx);
             m_ref = mx;
             l *= alpha;
