@@ -510,7 +510,11 @@ mgb_status mgb_kv_append(const mgb_kv_append_desc* desc, const mgb_kv_cache* cac
  * stride ld_o; not overlapping the inputs), lse [nq, tokens] float32 or NULL.
  * dtype bf16 or float32, head_dim 64 or 128. Sums and softmax statistics are
  * float32; in bf16 the weights are rounded to bf16 before they multiply V.
- * Results repeat bit for bit. */
+ * Results repeat bit for bit. Where every visible score is -inf, o is NaN and
+ * lse -inf; a NaN score makes both NaN. Keys that a row does not see have no
+ * say, whatever they hold. A NaN or infinity in row j of v reaches every row
+ * that sees j and may reach earlier rows of the same sequence (0 times it), not
+ * another sequence. */
 typedef struct {
   int32_t n_seqs, tokens, causal;
   void* ws;
@@ -544,8 +548,9 @@ mgb_status mgb_attention_packed_fwd(const mgb_attention_packed_plan* plan, int32
  * nq] float32 or NULL. The cache's dtype is q's and o's; bf16 or float32,
  * head_dim 64 or 128, any group size nq / nkv; o must not overlap q. A length
  * past max_pages * page_size is MGB_ERR_INDEX and counts as 0. A page outside
- * [0, n_pages) is MGB_ERR_INDEX, and its tokens are left out of the softmax
- * (where that leaves none, o is NaN and lse -inf). Sums and softmax
+ * [0, n_pages) is MGB_ERR_INDEX, and its tokens are left out of the softmax.
+ * Where no token is left, or every score is -inf, o is NaN and lse -inf; a NaN
+ * score makes both NaN. Slots behind a length are not read. Sums and softmax
  * statistics are float32; in bf16 the weights are rounded to bf16 before
  * they multiply V. Results repeat bit for bit with the same lengths. The
  * calls of one plan share its workspace: each is ordered after the prepare

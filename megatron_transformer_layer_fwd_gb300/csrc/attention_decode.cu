@@ -693,8 +693,9 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
       L = 0.0f;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
+        // (no reference: no token or only scores of -infinity, 0, or NaN, which stays)
         const float2 x = sml[w * MAXR + r];
-        if (x.x > -INFINITY) L += x.y * exp2f(x.x - M);
+        L += x.x > -INFINITY ? x.y * exp2f(x.x - M) : x.y;
       }
     };
     // first and last CTA of the item

@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       ++ko;
       tc_fence_after();
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const float inv = 1.0f / l;  // (l = 0: every score is -infinity, 0 / 0)
       const bool row_ok = row < w.len;
       bf16* out = p.o + (int64_t)(w.a + row) * p.ld_o + w.h * D;
       if (p.wide) {

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(NT, Cfg<D, RPT>::BLOCKS) packed_f32_kernel(con
       for (int o = 1; o < 16; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
       const int row = RPT * ty + r;
       if (row >= rows) continue;
-      const float inv = l[r] > 0.0f ? 1.0f / l[r] : 0.0f;
+      const float inv = 1.0f / l[r];  // (l = 0: every score is -infinity, 0 / 0)
       float* o = p.o + (int64_t)(e.x + q0 + row) * p.ld_o + (int64_t)h * D;
 #pragma unroll
       for (int c = 0; c < OC; ++c)
