@@ -516,11 +516,18 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
           for (int i = 0; i < NM; ++i) {
             float x = -INFINITY;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              x = fmax3(x, sc[mt][i / 2][i & 1], sc[mt][i / 2][2 + (i & 1)]);
+            for (int mt = 0; mt < MT; ++mt) {
+              // scaled before the maximum and before it is subtracted: one rounding for
+              // both, so that the largest weight is 1 for scores of any size (a fused
+              // x sl2 - m is off by the product's rounding, powers of 2 past 2^24)
+              float &a = sc[mt][i / 2][i & 1], &b = sc[mt][i / 2][2 + (i & 1)];
+              a = __fmul_rn(a, p.sl2);
+              b = __fmul_rn(b, p.sl2);
+              x = fmax3(x, a, b);
+            }
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-            mx[i] = x * p.sl2;
+            mx[i] = x;
             up[i] = mx[i] > m[i] + TAU;
             any |= up[i];
           }
@@ -549,7 +556,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
             for (int mt = 0; mt < MT; ++mt) {
               float(&x)[4] = sc[mt][ht];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = ex2_ftz(fmaf(x[e], p.sl2, (e & 1) ? -r1 : -r0));
+              for (int e = 0; e < 4; ++e) x[e] = ex2_ftz(x[e] - ((e & 1) ? r1 : r0));
               l[2 * ht] += x[0] + x[2];
               l[2 * ht + 1] += x[1] + x[3];
               pb[mt][ht][0] = transpose8x8(pack_bf16x2(x[0], x[1]));
@@ -600,7 +607,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
               const float y0 = (hi ? x[2] : x[0]) + __shfl_xor_sync(0xffffffffu, hi ? x[0] : x[2], 16);
               const float y1 = (hi ? x[3] : x[1]) + __shfl_xor_sync(0xffffffffu, hi ? x[1] : x[3], 16);
               const float sc = (odd ? y1 : y0) + __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 8);
-              pr[i] = (see >> (8 * kt + key)) & 1u ? sc * p.sl2 : -INFINITY;
+              pr[i] = (see >> (8 * kt + key)) & 1u ? __fmul_rn(sc, p.sl2) : -INFINITY;
               mx[i] = pr[i];
             }
 #pragma unroll

@@ -66,6 +66,9 @@ constexpr int NTHREADS = 320;   // MMA warp, producer warp, 2 x 4 softmax warps
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float SUM_LIMIT = 8192.0f;  // of a row's weights in a tile
+// Reference (log2 units) up to which the fused scale-and-subtract is off by a factor of
+// at most 2, which all weights of a reference share, so that it cancels
+constexpr float REF_LIMIT = 16777216.0f;
 
 template <int D>
 struct Cfg2 {
@@ -547,7 +550,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           // per instruction) busy by itself: groups of four keys, the exponentials of
           // one between the sums and packing of the one before and the scaling
           // of the second next, scores of the next 16 keys on their way.
-          const float nref = m_ref == -INFINITY ? 0.0f : -m_ref;
+          // (past REF_LIMIT: below)
+          const float nref = fabsf(m_ref) <= REF_LIMIT ? -m_ref : 0.0f;
           float r0 = 0.0f, r1 = 0.0f, r2 = 0.0f, r3 = 0.0f;
           uint32_t q[2][16];
           float t[4][4];
@@ -599,19 +603,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // The first reference is the maximum of the first 32 keys (key 0 is
         // visible to every row): at most the row's, so the sum is at least 1, and
         // far below it only if the sum shows it.
-        if (j == 0) m_ref = chunk_max(0, -INFINITY) * p.sl2;
+        if (j == 0) m_ref = __fmul_rn(chunk_max(0, -INFINITY), p.sl2);
         if (edge) form(std::true_type{});
         else form(std::false_type{});
-        // (NaN too; no reference: all first scores were -infinity.) Rows behind the end
-        // hold other sequences' queries and have no say; nor does a row move its
-        // reference because another one must, so that its bits are its own. The
-        // branch is the whole warp's, as the TMEM loads inside must be.
-        bool need = !(sum <= SUM_LIMIT) || m_ref == -INFINITY;
+        // (NaN too; and a reference past REF_LIMIT, or none, as all first scores were
+        // -infinity, whose weights were not formed with it.) Rows behind the end hold
+        // other sequences' queries and have no say; nor does a row move its reference
+        // because another one must, so that its bits are its own. The branch is the
+        // whole warp's, as the TMEM loads inside must be.
+        bool need = !(sum <= SUM_LIMIT) || fabsf(m_ref) > REF_LIMIT;
         if (__any_sync(0xffffffffu, need) && __any_sync(0xffffffffu, need &= row < w.len)) {
           float mx = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 4; ++c) mx = chunk_max(c, mx);
-          mx *= p.sl2;
+          mx = __fmul_rn(mx, p.sl2);  // (rounded: not fused into what follows)
           float alpha = 1.0f;
           if (need && mx > m_ref) {
             alpha = exp2f(m_ref - mx);
@@ -635,6 +640,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               for (int e = 0; e < 32; ++e) ro[e] = __float_as_uint(__uint_as_float(ro[e]) * alpha);
               tmem_st32(t_o + c * 32, ro);
             }
+          }
+          const bool apart = fabsf(m_ref) > REF_LIMIT && m_ref > -INFINITY;
+          if (__any_sync(0xffffffffu, apart)) {
+            // The reference is subtracted from scores scaled and rounded as it was, so that
+            // equal scores leave exactly 0; the differences take the scores' place.
+            const float back = 1.0f / p.sl2;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t q[32];
+              tmem_ld32(t_s + c * 32, q);
+              tmem_ld_wait();
+              tmem_regs_ready(q);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (apart)
+                  q[e] = __float_as_uint((__fmul_rn(__uint_as_float(q[e]), p.sl2) - m_ref) * back);
+              tmem_st32(t_s + c * 32, q);
+            }
+            tmem_st_wait();
           }
           form(std::true_type{});  // (masks nothing inside)
         }

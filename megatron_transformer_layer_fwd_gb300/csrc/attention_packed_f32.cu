@@ -137,7 +137,8 @@ __global__ void __launch_bounds__(NT, Cfg<D, RPT>::BLOCKS) packed_f32_kernel(con
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
           const int key = k0 + tx + 16 * c;
-          s[r][c] = (s[r][c] + s2[r][c]) * p.sl2;
+          // (rounded before the maximum and the subtraction: the largest weight is 1)
+          s[r][c] = __fmul_rn(s[r][c] + s2[r][c], p.sl2);
           if (edge && (key >= len || (p.causal && key > q0 + RPT * ty + r))) s[r][c] = -INFINITY;
           mx = fmaxf(mx, s[r][c]);
         }
