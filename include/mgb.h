@@ -551,10 +551,10 @@ mgb_status mgb_attention_packed_fwd(const mgb_attention_packed_plan* plan, int32
  * [0, n_pages) is MGB_ERR_INDEX, and its tokens are left out of the softmax.
  * Where no token is left, or every score is -inf, o is NaN and lse -inf; a NaN
  * score makes both NaN. Slots behind a length are not read. Sums and softmax
- * statistics are float32; in bf16 the weights are rounded to bf16 before
- * they multiply V. Results repeat bit for bit with the same lengths. The
- * calls of one plan share its workspace: each is ordered after the prepare
- * and after the plan's previous call (same stream, or events). */
+ * statistics are float32; in bf16 the weights multiply V as the sum of two bf16
+ * parts, off by 2^-16 relative at most. Results repeat bit for bit with the same
+ * lengths. The calls of one plan share its workspace: each is ordered after the
+ * prepare and after the plan's previous call (same stream, or events). */
 typedef struct {
   int32_t n_seqs, n_q_heads, n_kv_heads, head_dim;
   void* ws;

@@ -545,9 +545,11 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
               }
             }
           }
-          // P as bf16 (the row sums take it unrounded): relative error 2^-8 at
-          // most per weight, below the output's own rounding after averaging
-          uint32_t pb[MT][HT][2];
+          // P in two bf16 parts, the second what the first leaves: a weight is off by
+          // 2^-16 relative at most. (Rounded to one part, 2^-8, the weights' errors shrink
+          // in the average over the tokens exactly as the result does, so they add as
+          // much again as the output's own rounding.)
+          uint32_t pb[MT][HT][2], pl[MT][HT][2];
 #pragma unroll
           for (int ht = 0; ht < HT; ++ht) {
             const float r0 = m[2 * ht] == -INFINITY ? 0.0f : m[2 * ht];
@@ -559,8 +561,13 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
               for (int e = 0; e < 4; ++e) x[e] = ex2_ftz(x[e] - ((e & 1) ? r1 : r0));
               l[2 * ht] += x[0] + x[2];
               l[2 * ht + 1] += x[1] + x[3];
-              pb[mt][ht][0] = transpose8x8(pack_bf16x2(x[0], x[1]));
-              pb[mt][ht][1] = transpose8x8(pack_bf16x2(x[2], x[3]));
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t hi = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                const float2 f = unpack_bf16x2(hi);
+                pb[mt][ht][i] = transpose8x8(hi);
+                pl[mt][ht][i] = transpose8x8(pack_bf16x2(x[2 * i] - f.x, x[2 * i + 1] - f.y));
+              }
             }
           }
 #pragma unroll
@@ -572,6 +579,9 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) decode_kernel(const Params
 #pragma unroll
               for (int ht = 0; ht < HT; ++ht)
                 mma_bf16(acc[nn * HT + ht], a, pb[mt][ht][0], pb[mt][ht][1]);
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht)
+                mma_bf16(acc[nn * HT + ht], a, pl[mt][ht][0], pl[mt][ht][1]);
             }
         } else {
           // no branch on `rows`: heads that do not exist have zero queries, and
