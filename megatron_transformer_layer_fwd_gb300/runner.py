@@ -111,7 +111,8 @@ def _on(stream, device: torch.device):
 
 class ServingBatch:
     """What all layers share in one step of running sequences: the lengths, the
-    block table and the attention plan. Without `cu_seqlens` the step has one
+    block table and the attention plan (made from the lengths as they are now: a
+    step with others takes a new batch, or a replay of a captured one). Without `cu_seqlens` the step has one
     new token per sequence (decode); with it, the rows of whole prompts packed
     one behind the other (`tokens` rows, possibly more than they fill), whose
     lengths are their numbers of rows, or 0 for padding: a prompt that continues
@@ -202,6 +203,8 @@ class ServingLayer:
             raise ValueError("the batch was prepared for other heads than the layer's")
         if batch.cu_seqlens is not None and bool(batch.causal) != bool(s.causal):
             raise ValueError("the batch was prepared for a causal mask, or without one, unlike the layer")
+        if batch.tokens == 0:
+            return torch.empty_like(x)
         with _on(stream, x.device):
             if stream is not None:  # either may belong to another stream and be freed before the step is done
                 now = torch.cuda.current_stream(x.device)
