@@ -509,7 +509,8 @@ mgb_status mgb_kv_append(const mgb_kv_append_desc* desc, const mgb_kv_cache* cac
  * ld_q, ld_kv (e.g. the columns of one fused qkv buffer), o [tokens, nq*d] (row
  * stride ld_o; not overlapping the inputs), lse [nq, tokens] float32 or NULL.
  * dtype bf16 or float32, head_dim 64 or 128. Sums and softmax statistics are
- * float32; in bf16 the weights are rounded to bf16 before they multiply V.
+ * float32; in bf16 the weights are rounded to bf16 before they multiply V, which
+ * adds about as much error as o's own rounding.
  * Results repeat bit for bit. Where every visible score is -inf, o is NaN and
  * lse -inf; a NaN score makes both NaN. Keys that a row does not see have no
  * say, whatever they hold. A NaN or infinity in row j of v reaches every row

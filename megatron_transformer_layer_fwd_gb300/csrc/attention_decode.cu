@@ -40,10 +40,10 @@
 //   that each lane keeps the softmax of a quarter of the heads.
 //
 // Measured: bf16, d = 128, 32 query and 8 KV heads: one sequence of 131001 cached
-// tokens 88 us, 6.1 TB/s; 64 sequences of 33 to 16000 tokens 107 us, 6.4 TB/s (a
+// tokens 88 us, 6.1 TB/s; 64 sequences of 33 to 16000 tokens 108 us, 6.3 TB/s (a
 // copy reaches 6.79). d = 64, 16 query and KV heads, 200 sequences of 20 to 1200
 // tokens: 44 us with the prepare kernel. float32, d = 128, 16 and 4 heads, 12
-// sequences to 5000 tokens: 14.2 us for 49 MB; the start of the loads (2 us), the
+// sequences to 5000 tokens: 13.6 us for 49 MB; the start of the loads (2 us), the
 // last CTAs' second item and the join (3 us) are as long as the copies.
 #include "common.cuh"
 #include "internal.h"
