@@ -488,7 +488,7 @@ mgb_status mgb_kv_append(const mgb_kv_append_desc* desc, const mgb_kv_cache* cac
 
 /* Attention over a batch of sequences of different lengths laid one behind
  * the other: sequence s owns rows cu_seqlens[s] .. cu_seqlens[s+1] - 1
- * (cu_seqlens [n_seqs + 1] int32, non-decreasing, from 0 to at most tokens).
+ * (cu_seqlens [n_seqs + 1] int32, non-decreasing, each in [0, tokens]).
  * Within each sequence, per query head h: softmax(Q_h K_g^T / sqrt(d)) V_g,
  * with causal key j visible to query i iff j <= i. Keys and values are these rows
  * alone: tokens that a cache holds of a sequence are not attended to (whole in
