@@ -572,6 +572,96 @@ mgb_status mgb_attention_decode(const mgb_attention_decode_plan* plan, const mgb
                                 const void* q, int64_t ld_q, void* o, int64_t ld_o, float* lse,
                                 void* stream);
 
+/* ---- several new tokens per sequence over the cache: drafted tokens ----
+ * A step that checks tokens it has guessed. Sequence s owns rows cu_seqlens[s]
+ * .. cu_seqlens[s+1] - 1 (from 0, non-decreasing, at most tokens), one per drafted
+ * token, at most MGB_TREE_MAX_TOKENS; seq_lens[s] is its length WITH them, so its
+ * i-th drafted token has slot ctx + i, ctx = seq_lens[s] - its rows. The drafted
+ * tokens form a tree: parents[row] is the parent's index in the sequence (below the
+ * token's own), or -1 for a child of the last cached token; several may be. A
+ * token's depth counts its ancestors in the draft, and its position is ctx +
+ * depth. parents NULL: each token's parent is the one before it (a chain; the next
+ * piece of a prompt is one).
+ *
+ * mgb_attention_tree_prepare derives into `ws` (16-byte aligned, caller-owned, at
+ * least mgb_attention_tree_ws_bytes) what the other calls of the step need: one
+ * prepare serves every layer's append, attention and accept with these lengths,
+ * heads and trees. *plan (host memory) only names the workspace, nothing is read
+ * back; cu_seqlens, seq_lens and parents are not read again. seq_lens[s] 0 is
+ * padding: its rows of every output are left as they were, as are rows behind the
+ * last sequence. From the first offset outside its range on, all sequences count as
+ * empty; a sequence with a length below 0, or with more rows than its length or
+ * than the limit, counts as empty too; a parent outside [-1, own index) counts as -1.
+ * All are MGB_ERR_INDEX.
+ *
+ * mgb_attention_tree: q [tokens, nq*d] (row stride ld_q), o [tokens, nq*d] (row stride
+ * ld_o), lse [tokens, nq] float32 or NULL. Per drafted token and query head:
+ * softmax(q K_g^T / sqrt(d)) V_g over the ctx cached tokens, the token's ancestors
+ * and itself, whose keys and values are in the cache. dtype (the cache's) bf16 or
+ * float32, head_dim 64 or 128, any group size; o must not overlap q. A length past
+ * max_pages * page_size (or 2^31 - 1024) is MGB_ERR_INDEX, and the sequence's rows are
+ * left as they were. A page outside [0, n_pages) is MGB_ERR_INDEX, and its tokens
+ * are left out of the softmax. Where no token is left, or every score is -inf, o is
+ * NaN and lse -inf; a NaN score makes both NaN. Slots behind a length are not read.
+ * Drafted tokens that a row does not see have no say by their keys; a NaN or
+ * infinity in the value of one may reach other drafted tokens of its sequence (0
+ * times it). Sums and softmax statistics are float32; in bf16 the weights multiply V
+ * as the sum of two bf16 parts, off by 2^-16 relative at most. Results repeat bit for
+ * bit. The attention calls of one plan share its workspace: each is ordered after the
+ * prepare and after the plan's previous one (same stream, or events). */
+#define MGB_TREE_MAX_TOKENS 256
+
+typedef struct {
+  int32_t n_seqs, tokens, n_q_heads, n_kv_heads, head_dim;
+  void* ws;
+  size_t ws_bytes;
+} mgb_attention_tree_plan;
+
+size_t mgb_attention_tree_ws_bytes(int32_t n_seqs, int32_t tokens, int32_t n_q_heads,
+                                   int32_t n_kv_heads, int32_t head_dim);
+mgb_status mgb_attention_tree_prepare(int32_t n_seqs, int32_t tokens, int32_t n_q_heads,
+                                      int32_t n_kv_heads, int32_t head_dim,
+                                      const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                      const int32_t* parents, void* ws, size_t ws_bytes,
+                                      mgb_attention_tree_plan* plan, void* stream);
+mgb_status mgb_attention_tree(const mgb_attention_tree_plan* plan, const mgb_kv_cache* cache,
+                              const void* q, int64_t ld_q, void* o, int64_t ld_o, float* lse,
+                              void* stream);
+
+/* mgb_kv_append for the drafted tokens of a plan: row by row the same rotation and
+ * stores, with slot ctx + i and the rotation of position ctx + depth. desc's tokens,
+ * n_seqs and n_q_heads (with q_out) are the plan's, whole is 0; the cache has the plan's
+ * heads. A slot past the table, a position past rope_len and a bad page are
+ * MGB_ERR_INDEX, and all of that row's stores are skipped. */
+mgb_status mgb_kv_append_tree(const mgb_attention_tree_plan* plan, const mgb_kv_append_desc* desc,
+                              const mgb_kv_cache* cache, const float* rope, const void* q,
+                              const void* k, const void* v, int64_t ld_q, int64_t ld_kv, void* q_out,
+                              int64_t ld_qo, void* k_out, int64_t ld_ko, void* stream);
+
+/* Keeps one path of each tree: accepted[s] is the index of its last token in the
+ * sequence's draft, or -1 for none. The path's keys and values move to slots ctx, ctx +
+ * 1, .. in order (a token at depth i to slot ctx + i, the position it was rotated by),
+ * and new_lens[s] (may be NULL, and may be the prepare's seq_lens) becomes ctx + the
+ * path's tokens; the slots behind are as undefined as before a draft. Sequences
+ * without drafted tokens keep their length (0 if it is below 0). One call per layer's
+ * cache; a second one on the same cache would move the moved slots again. An index
+ * outside [-1, rows) is MGB_ERR_INDEX and counts as -1; a length past the table and a
+ * bad page are MGB_ERR_INDEX, and what they would move stays. Pages that hold a
+ * sequence's drafted tokens are its own. */
+mgb_status mgb_kv_accept(const mgb_attention_tree_plan* plan, const mgb_kv_cache* cache,
+                         const int32_t* accepted, int32_t* new_lens, void* stream);
+
+/* Copies the first slots[i] slots (all heads, keys and values) of page src[i] to
+ * page dst[i], i < n_copies (int32, device; slots NULL: whole pages): a sequence that
+ * goes on in several ways shares its full pages and copies the last one. slots[i] 0
+ * copies nothing, src[i] == dst[i] changes nothing. A page outside [0, n_pages), or a
+ * number of slots outside [0, page_size], is MGB_ERR_INDEX, and that copy is skipped.
+ * Pages written by one call are different from each other and from those it reads,
+ * otherwise their contents are unspecified. The cache's block table is not used.
+ * head_dim a multiple of 8 (bf16) or 4 (float32). */
+mgb_status mgb_kv_copy_pages(const mgb_kv_cache* cache, int32_t n_copies, const int32_t* src,
+                             const int32_t* dst, const int32_t* slots, void* stream);
+
 /* Vocab-parallel embedding lookup [P2 section 3]: the table's rows [v0, v1)
  * are held as emb_shard [(v1 - v0), hidden] (row-major, the vocab shard of a
  * tensor-parallel rank; v0 = 0, v1 = vocab for the whole table). For each of

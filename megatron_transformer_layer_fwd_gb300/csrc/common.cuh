@@ -449,9 +449,9 @@ __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 template <typename K, typename... A>
-mgb_status launch_pdl(K kernel, int grid, dim3 threads, size_t smem, cudaStream_t st, const A&... args) {
+mgb_status launch_pdl(K kernel, dim3 grid, dim3 threads, size_t smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = threads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

@@ -322,6 +322,8 @@ enum ProfKind : int {
   PROF_GEMM_CE_DGRAD, PROF_GEMM_CE_WGRAD, PROF_SPLITK_REDUCE,
   // serving: the cache append, packed prompt attention, paged decode attention
   PROF_KV_APPEND, PROF_ATTN_PACKED, PROF_ATTN_DECODE,
+  // drafted tokens: attention with its plan and join, slots and pages moved
+  PROF_ATTN_TREE, PROF_KV_MOVE,
   // stages of the layer (CUDA events around groups of launches, not kernels):
   // attention sublayer forward (LN1, QKV, attention, output projection +
   // residual), MLP sublayer forward (LN2, fc1 + activation, fc2 + residual),

@@ -21,6 +21,7 @@
 // 32-way search over cu, then two dependent loads).
 #include "common.cuh"
 #include "internal.h"
+#include "tree.cuh"
 
 namespace mgb {
 
@@ -45,6 +46,10 @@ struct AppendParams {
   int whole;                   // lengths are the rows' numbers (or 0)
   int cap;                     // positions below this: the table's and the rotary table's
   unsigned check_blocks;       // the last blocks, which check cu
+  // drafted tokens: where the plan says that each one stands, and the rows it knows
+  const TreeToken* token;
+  const TreeHeader* hdr;
+  int rope_len;
   int* err;
 };
 
@@ -119,7 +124,8 @@ __device__ __forceinline__ void rotate(uint4& w0, uint4& w1,
   w1 = Vec<T>::pack(y);
 }
 
-template <typename T, int UB, bool INTER>
+// TREE: drafted tokens of a plan
+template <typename T, int UB, bool INTER, bool TREE>
 __global__ void __launch_bounds__(UB == 1 ? FEW_THREADS : MANY_THREADS, UB == 1 ? 1 : 8)
     kv_append_kernel(const AppendParams p) {
   constexpr int VN = Vec<T>::VN;
@@ -167,7 +173,7 @@ __global__ void __launch_bounds__(UB == 1 ? FEW_THREADS : MANY_THREADS, UB == 1 
   load(threadIdx.x);
 
   const unsigned back = gridDim.x - 1 - blockIdx.x;
-  if (back < p.check_blocks) {
+  if (!TREE && back < p.check_blocks) {
     // Every offset is checked once, by the grid's last threads (which start last and,
     // in a call of one block, are not the warp that looks its token up): whatever
     // sequence the search below finds in offsets that are not sorted, the call
@@ -179,7 +185,29 @@ __global__ void __launch_bounds__(UB == 1 ? FEW_THREADS : MANY_THREADS, UB == 1 
       if (c0 < 0 || c1 < c0 || c1 > p.tokens || (i == 0 && c0 != 0)) record_error(p.err, kErrIndex);
     }
   }
-  if (threadIdx.x < 32 && t < p.tokens) {
+  if constexpr (TREE) {
+    // the plan's offsets were checked; the rotation goes by the depth, the slot by the row
+    if (threadIdx.x == 0 && t < p.tokens) {
+      int pos = -1;
+      int64_t slot = 0;
+      if (t < p.hdr->rows) {
+        const int4 w = *reinterpret_cast<const int4*>(p.token + t);  // (s, slot, pos)
+        if (w.x >= 0) {
+          bool ok = w.y < p.cap && (p.rot == 0 || w.z < p.rope_len);
+          if (ok) {
+            const int pg = w.y / p.page_size;
+            const int page = p.table[w.x * p.ld_table + pg];
+            ok = page >= 0 && page < p.n_pages;
+            slot = page * p.s_page + (w.y - pg * p.page_size) * p.s_tok;
+          }
+          if (ok) pos = w.z;
+          else record_error(p.err, kErrIndex);
+        }
+      }
+      s_pos[g] = pos;
+      s_slot[g] = slot;
+    }
+  } else if (threadIdx.x < 32 && t < p.tokens) {
     int s = t, first = t, behind = t + 1;  // the sequence's rows first .. behind - 1
     int before = 0;                        // offset of the sequence before
     if (p.cu != nullptr) {
@@ -275,8 +303,11 @@ mgb_status launch(AppendParams p, bool inter, int most, cudaStream_t st) {
     p.check_blocks = (unsigned)(all < grid ? all : grid);
   }
   LaunchScope scope(PROF_KV_APPEND, st);
-  return launch_pdl(inter ? kv_append_kernel<T, UB, true> : kv_append_kernel<T, UB, false>, grid,
-                    dim3(x, y), 0, st, p);
+  if (p.token != nullptr)
+    return launch_pdl(inter ? kv_append_kernel<T, UB, true, true> : kv_append_kernel<T, UB, false, true>,
+                      grid, dim3(x, y), 0, st, p);
+  return launch_pdl(inter ? kv_append_kernel<T, UB, true, false> : kv_append_kernel<T, UB, false, false>,
+                    grid, dim3(x, y), 0, st, p);
 }
 
 template <typename T>
@@ -320,11 +351,13 @@ mgb_status check_kv_cache(const mgb_kv_cache* c, int n_seqs) {
 
 using namespace mgb;
 
-extern "C" mgb_status mgb_kv_append(const mgb_kv_append_desc* d, const mgb_kv_cache* c,
-                                    const int32_t* cu_seqlens, const int32_t* seq_lens,
-                                    const float* rope, const void* q, const void* k, const void* v,
-                                    int64_t ld_q, int64_t ld_kv, void* q_out, int64_t ld_qo,
-                                    void* k_out, int64_t ld_ko, void* stream) {
+namespace {
+
+// Rows whose place follows from cu_seqlens and seq_lens, or from a plan of drafted tokens.
+mgb_status append(const mgb_kv_append_desc* d, const mgb_kv_cache* c, const mgb_attention_tree_plan* plan,
+                  const int32_t* cu_seqlens, const int32_t* seq_lens, const float* rope, const void* q,
+                  const void* k, const void* v, int64_t ld_q, int64_t ld_kv, void* q_out, int64_t ld_qo,
+                  void* k_out, int64_t ld_ko, void* stream) {
   if (fault_injected()) return MGB_ERR_INVALID_ARG;
   if (d == nullptr || d->tokens < 0 || d->n_seqs < 0 || d->rot_dim < 0 || d->rope_len < 0 ||
       (d->interleaved & ~1) || (d->whole & ~1))
@@ -336,9 +369,19 @@ extern "C" mgb_status mgb_kv_append(const mgb_kv_append_desc* d, const mgb_kv_ca
     return MGB_ERR_UNSUPPORTED;
   if (d->rot_dim > c->head_dim || (d->rot_dim > 0 && (d->rope_len < 1 || rope == nullptr)))
     return MGB_ERR_INVALID_ARG;
-  if (cu_seqlens == nullptr && d->tokens != d->n_seqs) return MGB_ERR_INVALID_ARG;
+  if (plan != nullptr) {
+    s = check_tree_plan(plan);
+    if (s != MGB_OK) return s;
+    if (d->tokens != plan->tokens || d->n_seqs != plan->n_seqs || d->whole ||
+        c->n_kv_heads != plan->n_kv_heads || c->head_dim != plan->head_dim ||
+        (q_out != nullptr && d->n_q_heads != plan->n_q_heads))
+      return MGB_ERR_INVALID_ARG;
+  } else if (cu_seqlens == nullptr && d->tokens != d->n_seqs) {
+    return MGB_ERR_INVALID_ARG;
+  }
   if (q_out != nullptr && (d->n_q_heads < 1 || q == nullptr)) return MGB_ERR_INVALID_ARG;
-  if (d->tokens > 0 && (!k || !v || (d->n_seqs > 0 && !seq_lens))) return MGB_ERR_INVALID_ARG;
+  if (d->tokens > 0 && (!k || !v || (d->n_seqs > 0 && !seq_lens && plan == nullptr)))
+    return MGB_ERR_INVALID_ARG;
   const int64_t wq = (int64_t)d->n_q_heads * c->head_dim, wk = (int64_t)c->n_kv_heads * c->head_dim;
   // (units x units per head stays below 2^32, for the division by multiplication)
   if (wk >= ((int64_t)1 << 28) || (q_out != nullptr && wq >= ((int64_t)1 << 28)))
@@ -365,7 +408,7 @@ extern "C" mgb_status mgb_kv_append(const mgb_kv_append_desc* d, const mgb_kv_ca
   p.m_head = p.units_head == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + p.units_head - 1) / p.units_head);
   p.units = ((q_out ? p.nq : 0) + 2 * p.nkv) * p.units_head;
   int64_t cap = (int64_t)c->max_pages * c->page_size;
-  if (d->rot_dim > 0 && cap > d->rope_len) cap = d->rope_len;
+  if (plan == nullptr && d->rot_dim > 0 && cap > d->rope_len) cap = d->rope_len;
   p.cap = (int)(cap < INT32_MAX ? cap : INT32_MAX);
   p.page_size = c->page_size; p.n_pages = c->n_pages;
   p.cu = cu_seqlens; p.lens = seq_lens; p.table = c->block_table; p.ld_table = c->ld_table;
@@ -376,9 +419,37 @@ extern "C" mgb_status mgb_kv_append(const mgb_kv_append_desc* d, const mgb_kv_ca
   p.q_out = static_cast<char*>(q_out); p.k_out = static_cast<char*>(k_out);
   p.k_pool = static_cast<char*>(c->k); p.v_pool = static_cast<char*>(c->v);
   p.ld_q = ld_q; p.ld_kv = ld_kv; p.ld_qo = ld_qo; p.ld_ko = ld_ko;
+  p.rope_len = d->rope_len;
+  if (plan != nullptr) {
+    const TreeLayout l =
+        tree_layout(plan->n_seqs, plan->tokens, plan->n_q_heads, plan->n_kv_heads, plan->head_dim);
+    const char* b = static_cast<const char*>(plan->ws);
+    p.token = reinterpret_cast<const TreeToken*>(b + l.token);
+    p.hdr = reinterpret_cast<const TreeHeader*>(b + l.header);
+  }
   p.err = device_error_word();
   if (p.err == nullptr) return MGB_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return c->dtype == MGB_BF16 ? launch_t<bf16>(p, d->interleaved != 0, st)
                               : launch_t<float>(p, d->interleaved != 0, st);
+}
+
+}  // namespace
+
+extern "C" mgb_status mgb_kv_append(const mgb_kv_append_desc* d, const mgb_kv_cache* c,
+                                    const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                    const float* rope, const void* q, const void* k, const void* v,
+                                    int64_t ld_q, int64_t ld_kv, void* q_out, int64_t ld_qo,
+                                    void* k_out, int64_t ld_ko, void* stream) {
+  return append(d, c, nullptr, cu_seqlens, seq_lens, rope, q, k, v, ld_q, ld_kv, q_out, ld_qo, k_out, ld_ko,
+                stream);
+}
+
+extern "C" mgb_status mgb_kv_append_tree(const mgb_attention_tree_plan* plan,
+                                         const mgb_kv_append_desc* d, const mgb_kv_cache* c,
+                                         const float* rope, const void* q, const void* k, const void* v,
+                                         int64_t ld_q, int64_t ld_kv, void* q_out, int64_t ld_qo,
+                                         void* k_out, int64_t ld_ko, void* stream) {
+  if (plan == nullptr) return MGB_ERR_INVALID_ARG;
+  return append(d, c, plan, nullptr, nullptr, rope, q, k, v, ld_q, ld_kv, q_out, ld_qo, k_out, ld_ko, stream);
 }

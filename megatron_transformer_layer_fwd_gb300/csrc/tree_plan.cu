@@ -1,0 +1,427 @@
+// Drafted tokens over a paged cache: the plan of a step, the join of split
+// items, and the attention's entry points.
+//
+// The plan says what each drafted token sees and where it stands. Its mask is its own
+// bit and its parent's mask, found by doubling: with anc(i) the token 2^r steps
+// up, mask(i) |= mask(anc(i)), anc(i) = anc(anc(i)), at most eight rounds for 256
+// tokens; its depth adds up along the same steps.
+#include "tree.cuh"
+
+namespace mgb {
+
+namespace {
+
+constexpr float LN2 = 0.6931471805599453f;
+constexpr int NT = 256;
+
+// What a sequence's offsets and length say; `ok`: no offset up to it is bad.
+enum : int { SEQ_LIVE, SEQ_IDLE, SEQ_BAD };
+__device__ __forceinline__ int seq_kind(bool ok, int m, int len) {
+  if (!ok || len < 0) return SEQ_BAD;
+  if (m == 0 || len == 0) return SEQ_IDLE;  // no rows, or padding
+  return m <= TREE_MAX && m <= len ? SEQ_LIVE : SEQ_BAD;
+}
+
+struct PlanArgs {
+  int n, tokens, G, nkv;
+  const int32_t *cu, *lens, *parents;
+  TreeHeader* hdr;
+  TreeStart* start;
+  TreeSeq *seq, *live;
+  int64_t* prefix;
+  TreeToken* token;
+  uint32_t* mask;
+  int* err;
+};
+
+__device__ __forceinline__ bool pair_ok(const PlanArgs& a, int s, int c0, int c1) {
+  return c0 >= 0 && c1 >= c0 && c1 <= a.tokens && (s > 0 || c0 == 0);
+}
+
+// The last block: the live sequences in order, their costs summed up, the first
+// unit of every range. The others: block s, what the tokens of sequence s see.
+__global__ void __launch_bounds__(NT) tree_prepare_kernel(const PlanArgs a) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();  // the attention kernel may start up; it waits for this one's end
+  if ((int)blockIdx.x < a.n) {
+    __shared__ uint32_t m[TREE_MAX][TREE_WORDS + 1];
+    __shared__ int anc[TREE_MAX], dep[TREE_MAX];
+    const int s = blockIdx.x;
+    const int c0 = a.cu[s], c1 = a.cu[s + 1], len = a.lens[s];
+    bool good = pair_ok(a, s, c0, c1);
+    if (!good && tid == 0) record_error(a.err, kErrIndex);
+    if (c1 != c0)  // (a bad offset before it: the sequence counts as empty)
+      for (int i = tid; i < s; i += NT) good = good && pair_ok(a, i, a.cu[i], a.cu[i + 1]);
+    good = __syncthreads_and(good);
+    const int rows = c1 - c0;
+    const int kind = good ? seq_kind(true, rows, len) : SEQ_BAD;
+    if (tid == 0) {
+      if (good && kind == SEQ_BAD) record_error(a.err, kErrIndex);
+      *reinterpret_cast<int4*>(a.seq + s) =
+          make_int4(kind == SEQ_LIVE ? c0 : 0, kind == SEQ_LIVE ? rows : 0, max(len, 0), s);
+    }
+    if (!good) return;
+    if (kind != SEQ_LIVE) {
+      for (int i = tid; i < rows; i += NT)
+        *reinterpret_cast<int4*>(a.token + c0 + i) = make_int4(-1, 0, 0, 0);
+      return;
+    }
+    // NT >= TREE_MAX: a thread per token
+    const int i = tid;
+    if (i < rows) {
+      int up = i - 1;
+      if (a.parents != nullptr) {
+        up = a.parents[c0 + i];
+        if (up < -1 || up >= i) {  // counts as a child of the last cached token
+          record_error(a.err, kErrIndex);
+          up = -1;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < TREE_WORDS; ++w) m[i][w] = w == (i >> 5) ? 1u << (i & 31) : 0u;
+      anc[i] = up;
+      dep[i] = up >= 0 ? 1 : 0;
+    }
+    for (;;) {
+      const int x = i < rows ? anc[i] : -1;
+      if (!__syncthreads_or(x >= 0)) break;
+      uint32_t add[TREE_WORDS];
+      int xa = -1, xd = 0;
+      if (x >= 0) {
+#pragma unroll
+        for (int w = 0; w < TREE_WORDS; ++w) add[w] = m[x][w];
+        xa = anc[x];
+        xd = dep[x];
+      }
+      __syncthreads();
+      if (x >= 0) {
+#pragma unroll
+        for (int w = 0; w < TREE_WORDS; ++w) m[i][w] |= add[w];
+        anc[i] = xa;
+        dep[i] += xd;
+      }
+      __syncthreads();
+    }
+    if (i < rows) {
+      uint4* out = reinterpret_cast<uint4*>(a.mask + (int64_t)(c0 + i) * TREE_WORDS);
+      static_assert(TREE_WORDS == 8, "two stores per token");
+      out[0] = make_uint4(m[i][0], m[i][1], m[i][2], m[i][3]);
+      out[1] = make_uint4(m[i][4], m[i][5], m[i][6], m[i][7]);
+      *reinterpret_cast<int4*>(a.token + c0 + i) = make_int4(s, len - rows + i, len - rows + dep[i], 0);
+    }
+    return;
+  }
+
+  // ---------------- the ranges
+  __shared__ int64_t warp_cost[NT / 32];
+  __shared__ int warp_live[NT / 32];
+  int64_t cost = 0;
+  int live = 0, rows = 0;
+  bool good = true;
+  for (int base = 0; base < a.n; base += NT) {
+    const int s = base + tid;
+    int c0 = 0, c1 = 0, len = 0;
+    bool ok = true;
+    if (s < a.n) {
+      c0 = a.cu[s];
+      c1 = a.cu[s + 1];
+      len = a.lens[s];
+      ok = pair_ok(a, s, c0, c1);
+    }
+    // the first bad offset of this round
+    __shared__ int first_bad;
+    if (tid == 0) first_bad = INT32_MAX;
+    __syncthreads();
+    if (!ok) atomicMin(&first_bad, s);
+    __syncthreads();
+    const bool in = good && s < a.n && s < first_bad;
+    const bool is_live = in && seq_kind(true, c1 - c0, len) == SEQ_LIVE;
+    const int64_t v =
+        is_live ? tree_cost(tree_units(len)) * tree_blocks(c1 - c0, a.G) * a.nkv : 0;
+    int64_t x = v;
+    int y = is_live;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x1 = __shfl_up_sync(0xffffffffu, x, o);
+      const int y1 = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) x += x1, y += y1;
+    }
+    if (lane == 31) warp_cost[warp] = x, warp_live[warp] = y;
+    __syncthreads();
+    int64_t before = cost, all = cost;
+    int ybefore = live, yall = live;
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w < warp) before += warp_cost[w], ybefore += warp_live[w];
+      all += warp_cost[w];
+      yall += warp_live[w];
+    }
+    if (is_live) {
+      const int at = ybefore + y - 1;
+      *reinterpret_cast<int4*>(a.live + at) = make_int4(c0, c1 - c0, len, s);
+      a.prefix[at] = before + x - v;
+    }
+    cost = all;
+    live = yall;
+    if (good) {
+      const int last = min(min(first_bad, a.n), base + NT);  // sequences base .. last - 1 are good
+      if (last > base) rows = a.cu[last];
+      good = first_bad == INT32_MAX;
+    }
+    __syncthreads();
+  }
+  if (tid == 0) a.prefix[live] = cost;
+  __syncthreads();
+  int64_t chunk = (cost + TREE_RANGES - 1) / TREE_RANGES;
+  if (chunk < TREE_MIN_CHUNK) chunk = TREE_MIN_CHUNK;
+  if (tid == 0) *a.hdr = TreeHeader{cost, chunk, live, rows};
+  for (int c = tid; c <= TREE_RANGES; c += NT) {
+    const int64_t u = c * chunk;
+    TreeStart st{cost, live, 0, 0, 0};
+    if (u < cost) {
+      int lo = 0, hi = live - 1;  // the largest i with prefix[i] <= u
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (a.prefix[mid] <= u) lo = mid;
+        else hi = mid - 1;
+      }
+      const TreeSeq q = a.live[lo];
+      const int nt = tree_units(q.len), nb = tree_blocks(q.m, a.G);
+      const int64_t per = tree_cost(nt), r = u - a.prefix[lo];
+      const int64_t item = r / per, into = r - item * per, t = (into + TREE_UNIT - 1) / TREE_UNIT;
+      st.at = a.prefix[lo] + item * per;
+      st.i = lo;
+      st.h = (int)(item / nb);
+      st.b = (int)(item % nb);
+      if (into == 0 || (nt > TREE_WHOLE && t < nt)) {
+        st.t = (int)t;
+      } else {  // the item's last unit begins before: the next item
+        st.at += per;
+        if (++st.b == nb) {
+          st.b = 0;
+          if (++st.h == a.nkv) {
+            st.h = 0;
+            ++st.i;
+          }
+        }
+      }
+    }
+    a.start[c] = st;
+  }
+}
+
+// ---------------------------------------------------------------- join
+// Block (c, g): rows 8 g .. + 7 of the item that begins in CTA c's range and ends in
+// a later one, if there is one. A warp per row: the parts' maxima and sums by lanes,
+// then the weighted sum of their rows, four parts' loads under way at a time.
+constexpr int JOIN_ROWS = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * JOIN_ROWS) tree_join_kernel(const TreeParams p, int mult) {
+  constexpr int CPL = D / 32;
+  pdl_wait();
+  const int groups = (p.rows + JOIN_ROWS - 1) / JOIN_ROWS;
+  const int c = blockIdx.x / groups;
+  const int r = (blockIdx.x - c * groups) * JOIN_ROWS + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const TreeHeader hd = *p.hdr;
+  const TreeStart st = p.start[(c + 1) * mult];
+  const int64_t chunk = hd.chunk * mult;
+  if (st.i >= hd.live || st.t == 0 || st.at / chunk != c) return;
+  const TreeSeq q = p.live[st.i];
+  if (q.len > p.cap || r >= q.m * p.G - st.b * TREE_ROWS) return;
+  const int nt = tree_units(q.len);
+  const int cl = (int)((st.at + tree_begin(nt - 1, nt)) / chunk);
+  float M = -INFINITY, L = 0.0f, x[CPL] = {};
+  for (int c0 = c; c0 <= cl; c0 += 32) {
+    const int n = min(32, cl - c0 + 1);
+    float2 y = make_float2(-INFINITY, 0.0f);  // of part c0 + lane
+    if (lane < n) y = __ldcg(&p.ml[(int64_t)tree_part(c0 + lane, chunk, st.at) * p.rows + r]);
+    float mn = y.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mn = fmaxf(mn, M);
+    const float base = mn == -INFINITY ? 0.0f : mn;  // (no token so far: every factor is 0)
+    const float f = exp2f(M - base), w = exp2f(y.x - base);
+    M = mn;
+    // (a part without a reference has a row sum of 0, or NaN, which stays)
+    float lp = y.x > -INFINITY ? y.y * w : y.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) lp += __shfl_xor_sync(0xffffffffu, lp, o);
+    L = L * f + lp;
+#pragma unroll
+    for (int j = 0; j < CPL; ++j) x[j] *= f;
+    for (int i0 = 0; i0 < n; i0 += 4) {
+      float z[4][CPL];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) z[i][j] = 0.0f;
+        if (i0 + i < n) {
+          const float* y0 =
+              p.part + ((int64_t)tree_part(c0 + i0 + i, chunk, st.at) * p.rows + r) * D + lane * CPL;
+          if constexpr (CPL == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(y0));
+            z[i][0] = v.x; z[i][1] = v.y; z[i][2] = v.z; z[i][3] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(y0));
+            z[i][0] = v.x; z[i][1] = v.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i0 + i);
+        if (i0 + i < n)
+#pragma unroll
+          for (int j = 0; j < CPL; ++j) x[j] = fmaf(wi, z[i][j], x[j]);
+      }
+    }
+  }
+  const float inv = 1.0f / L;
+  const int rr = st.b * TREE_ROWS + r, tok = rr / p.G, head = st.h * p.G + rr - tok * p.G;
+  T* o = static_cast<T*>(p.o) + (q.row + tok) * p.ld_o + (int64_t)head * D + lane * CPL;
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (CPL == 4)
+      *reinterpret_cast<float4*>(o) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    else
+      *reinterpret_cast<float2*>(o) = make_float2(x[0] * inv, x[1] * inv);
+  } else {
+    if constexpr (CPL == 4)
+      *reinterpret_cast<uint2*>(o) =
+          make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(x[0] * inv, x[1] * inv);
+  }
+  if (p.lse != nullptr && lane == 0)
+    p.lse[(int64_t)(q.row + tok) * p.nq + head] = (M + log2f(L)) * LN2;
+}
+
+template <typename T>
+mgb_status join_t(const TreeParams& p, int d, int ctas, int mult, cudaStream_t st) {
+  const int groups = (p.rows + JOIN_ROWS - 1) / JOIN_ROWS;
+  return launch_pdl(d == 64 ? tree_join_kernel<T, 64> : tree_join_kernel<T, 128>, ctas * groups,
+                    dim3(32 * JOIN_ROWS), 0, st, p, mult);
+}
+
+mgb_status check_shape(int n, int tokens, int nq, int nkv, int d) {
+  if (n < 0 || tokens < 0 || nq < 1 || nkv < 1 || nq % nkv || nq > (1 << 20)) return MGB_ERR_INVALID_ARG;
+  return d == 64 || d == 128 ? MGB_OK : MGB_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+mgb_status tree_join(const TreeParams& p, int d, int dtype, int ctas, int mult, cudaStream_t st) {
+  return dtype == MGB_BF16 ? join_t<bf16>(p, d, ctas, mult, st) : join_t<float>(p, d, ctas, mult, st);
+}
+
+mgb_status check_tree_plan(const mgb_attention_tree_plan* plan) {
+  if (plan == nullptr || plan->ws == nullptr) return MGB_ERR_INVALID_ARG;
+  const mgb_status s =
+      check_shape(plan->n_seqs, plan->tokens, plan->n_q_heads, plan->n_kv_heads, plan->head_dim);
+  if (s != MGB_OK) return s;
+  if (!is_aligned16(plan->ws)) return MGB_ERR_MISALIGNED;
+  const TreeLayout l =
+      tree_layout(plan->n_seqs, plan->tokens, plan->n_q_heads, plan->n_kv_heads, plan->head_dim);
+  return plan->ws_bytes < l.total ? MGB_ERR_WORKSPACE_TOO_SMALL : MGB_OK;
+}
+
+}  // namespace mgb
+
+using namespace mgb;
+
+extern "C" {
+
+size_t mgb_attention_tree_ws_bytes(int32_t n_seqs, int32_t tokens, int32_t n_q_heads,
+                                   int32_t n_kv_heads, int32_t head_dim) {
+  if (check_shape(n_seqs, tokens, n_q_heads, n_kv_heads, head_dim) != MGB_OK) return 0;
+  return tree_layout(n_seqs, tokens, n_q_heads, n_kv_heads, head_dim).total;
+}
+
+mgb_status mgb_attention_tree_prepare(int32_t n_seqs, int32_t tokens, int32_t n_q_heads,
+                                      int32_t n_kv_heads, int32_t head_dim,
+                                      const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                      const int32_t* parents, void* ws, size_t ws_bytes,
+                                      mgb_attention_tree_plan* plan, void* stream) {
+  if (fault_injected() || plan == nullptr) return MGB_ERR_INVALID_ARG;
+  mgb_status s = check_shape(n_seqs, tokens, n_q_heads, n_kv_heads, head_dim);
+  if (s != MGB_OK) return s;
+  if (ws == nullptr || (n_seqs > 0 && (cu_seqlens == nullptr || seq_lens == nullptr)))
+    return MGB_ERR_INVALID_ARG;
+  if (!is_aligned16(ws) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(seq_lens) & 3u) || (reinterpret_cast<uintptr_t>(parents) & 3u))
+    return MGB_ERR_MISALIGNED;
+  const TreeLayout l = tree_layout(n_seqs, tokens, n_q_heads, n_kv_heads, head_dim);
+  if (ws_bytes < l.total) return MGB_ERR_WORKSPACE_TOO_SMALL;
+  s = check_arch();
+  if (s != MGB_OK) return s;
+  int* err = device_error_word();
+  if (err == nullptr) return MGB_ERR_CUDA;
+  if (n_seqs > 0) {
+    char* b = static_cast<char*>(ws);
+    PlanArgs a{};
+    a.n = n_seqs; a.tokens = tokens; a.G = n_q_heads / n_kv_heads; a.nkv = n_kv_heads;
+    a.cu = cu_seqlens; a.lens = seq_lens; a.parents = parents;
+    a.hdr = reinterpret_cast<TreeHeader*>(b + l.header);
+    a.start = reinterpret_cast<TreeStart*>(b + l.start);
+    a.seq = reinterpret_cast<TreeSeq*>(b + l.seq);
+    a.live = reinterpret_cast<TreeSeq*>(b + l.live);
+    a.prefix = reinterpret_cast<int64_t*>(b + l.prefix);
+    a.token = reinterpret_cast<TreeToken*>(b + l.token);
+    a.mask = reinterpret_cast<uint32_t*>(b + l.mask);
+    a.err = err;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    LaunchScope scope(PROF_ATTN_TREE, st);
+    tree_prepare_kernel<<<(unsigned)n_seqs + 1, NT, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return MGB_ERR_CUDA;
+  }
+  *plan = mgb_attention_tree_plan{n_seqs, tokens, n_q_heads, n_kv_heads, head_dim, ws, ws_bytes};
+  return MGB_OK;
+}
+
+mgb_status mgb_attention_tree(const mgb_attention_tree_plan* plan, const mgb_kv_cache* c,
+                              const void* q, int64_t ld_q, void* o, int64_t ld_o, float* lse,
+                              void* stream) {
+  if (fault_injected()) return MGB_ERR_INVALID_ARG;
+  mgb_status s = check_tree_plan(plan);
+  if (s != MGB_OK) return s;
+  const int n = plan->n_seqs, nq = plan->n_q_heads, nkv = plan->n_kv_heads, d = plan->head_dim;
+  s = check_kv_cache(c, n);
+  if (s != MGB_OK) return s;
+  if (c->n_kv_heads != nkv || c->head_dim != d || (plan->tokens > 0 && (!q || !o)))
+    return MGB_ERR_INVALID_ARG;
+  if (plan->tokens > 1 && (ld_q < (int64_t)nq * d || ld_o < (int64_t)nq * d)) return MGB_ERR_INVALID_ARG;
+  const int vn = c->dtype == MGB_BF16 ? 8 : 4;
+  if (!is_aligned16(q) || !is_aligned16(o) || ld_q % vn || ld_o % vn ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return MGB_ERR_MISALIGNED;
+  if (o != nullptr && o == q) return MGB_ERR_INVALID_ARG;  // the CTAs of a split item read q late
+  s = check_arch();
+  if (s != MGB_OK) return s;
+  if (n == 0 || plan->tokens == 0) return MGB_OK;
+  const TreeLayout l = tree_layout(n, plan->tokens, nq, nkv, d);
+  char* b = static_cast<char*>(plan->ws);
+  TreeParams p{};
+  p.nq = nq; p.nkv = nkv; p.G = nq / nkv;
+  p.hdr = reinterpret_cast<const TreeHeader*>(b + l.header);
+  p.start = reinterpret_cast<const TreeStart*>(b + l.start);
+  p.live = reinterpret_cast<const TreeSeq*>(b + l.live);
+  p.mask = reinterpret_cast<const uint32_t*>(b + l.mask);
+  p.ml = reinterpret_cast<float2*>(b + l.ml);
+  p.part = reinterpret_cast<float*>(b + l.part);
+  p.rows = l.rows;
+  p.k = c->k; p.v = c->v; p.table = c->block_table;
+  p.s_page = c->stride_page; p.s_tok = c->stride_token; p.s_head = c->stride_head;
+  p.ld_table = c->ld_table;
+  p.n_pages = c->n_pages; p.page_size = c->page_size;
+  const int64_t cap = (int64_t)c->max_pages * c->page_size;
+  p.cap = cap < TREE_LONGEST ? (int)cap : TREE_LONGEST;
+  p.q = q; p.ld_q = ld_q; p.o = o; p.ld_o = ld_o; p.lse = lse;
+  p.sl2 = 1.4426950408889634f / sqrtf((float)d);
+  p.err = device_error_word();
+  if (p.err == nullptr) return MGB_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  LaunchScope scope(PROF_ATTN_TREE, st, 2);
+  return c->dtype == MGB_BF16 ? attention_tree_bf16(p, d, st) : attention_tree_f32(p, d, st);
+}
+
+}  // extern "C"

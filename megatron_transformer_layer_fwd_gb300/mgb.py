@@ -39,6 +39,7 @@ CE_DEFAULT_TOKEN_BLOCK = 4096
 MGB_PRE_LN, MGB_POST_LN = 0, 1
 MGB_GELU_ERF, MGB_SWIGLU = 0, 1
 MGB_K_MAJOR, MGB_MN_MAJOR = 0, 1
+TREE_MAX_TOKENS = 256  # drafted tokens per sequence (MGB_TREE_MAX_TOKENS)
 MGB_RNG_DATA_PARALLEL, MGB_RNG_MODEL_PARALLEL, MGB_RNG_EXPERT_PARALLEL = 0, 1, 2
 (MGB_EPI_STORE, MGB_EPI_BIAS_GELU, MGB_EPI_BIAS_SWIGLU, MGB_EPI_BIAS_RESID, MGB_EPI_DGELU,
  MGB_EPI_DSWIGLU, MGB_EPI_F32) = range(7)
@@ -114,6 +115,12 @@ class AttentionPackedPlan(ctypes.Structure):
                 ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
 
 
+class AttentionTreePlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "tokens", "n_q_heads", "n_kv_heads",
+                                              "head_dim")] + [
+        ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+
+
 class GemmDesc(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("a_major", ctypes.c_int32), ("b_major", ctypes.c_int32),
@@ -181,6 +188,14 @@ def load() -> ctypes.CDLL:
                                              ctypes.POINTER(AttentionPackedPlan), P],
             "mgb_attention_packed_fwd": [ctypes.POINTER(AttentionPackedPlan), I32, I32, I32, I32, P, P,
                                          P, I64, I64, P, I64, P, P],
+            "mgb_attention_tree_prepare": [I32, I32, I32, I32, I32, P, P, P, P, SZ,
+                                           ctypes.POINTER(AttentionTreePlan), P],
+            "mgb_attention_tree": [ctypes.POINTER(AttentionTreePlan), ctypes.POINTER(KVCache), P, I64,
+                                   P, I64, P, P],
+            "mgb_kv_append_tree": [ctypes.POINTER(AttentionTreePlan), ctypes.POINTER(KVAppendDesc),
+                                   ctypes.POINTER(KVCache), P, P, P, P, I64, I64, P, I64, P, I64, P],
+            "mgb_kv_accept": [ctypes.POINTER(AttentionTreePlan), ctypes.POINTER(KVCache), P, P, P],
+            "mgb_kv_copy_pages": [ctypes.POINTER(KVCache), I32, P, P, P, P],
             "mgb_device_status": [P],
             "mgb_selftest_wait_timeout": [U64, P],
         }
@@ -206,6 +221,8 @@ def load() -> ctypes.CDLL:
         lib.mgb_attention_decode_ws_bytes.restype = SZ
         lib.mgb_attention_packed_ws_bytes.argtypes = [I32, I32]
         lib.mgb_attention_packed_ws_bytes.restype = SZ
+        lib.mgb_attention_tree_ws_bytes.argtypes = [I32, I32, I32, I32, I32]
+        lib.mgb_attention_tree_ws_bytes.restype = SZ
         lib.mgb_launch_count.argtypes = []
         lib.mgb_launch_count.restype = ctypes.c_uint64
         lib.mgb_profile_enable.argtypes = [I32]
@@ -545,6 +562,50 @@ def mgb_attention_packed_fwd(plan: AttentionPackedPlan, n_q_heads, n_kv_heads, h
     _check(load().mgb_attention_packed_fwd(ctypes.byref(plan), n_q_heads, n_kv_heads, head_dim, dtype,
                                            _ptr(q), _ptr(k), _ptr(v), ld_q, ld_kv, _ptr(o), ld_o,
                                            _ptr(lse), _stream(stream)), "mgb_attention_packed_fwd")
+
+
+def mgb_attention_tree_ws_bytes(n_seqs: int, tokens: int, n_q_heads: int, n_kv_heads: int,
+                                head_dim: int) -> int:
+    return load().mgb_attention_tree_ws_bytes(n_seqs, tokens, n_q_heads, n_kv_heads, head_dim)
+
+
+def mgb_attention_tree_prepare(n_seqs, tokens, n_q_heads, n_kv_heads, head_dim, cu_seqlens, seq_lens,
+                               parents, ws, stream=None) -> AttentionTreePlan:
+    """The plan (host struct, keeps `ws` alive) of a step with drafted tokens, for
+    mgb_kv_append_tree, mgb_attention_tree and mgb_kv_accept. parents None: chains."""
+    plan = AttentionTreePlan()
+    plan.tensors = (ws,)
+    _check(load().mgb_attention_tree_prepare(n_seqs, tokens, n_q_heads, n_kv_heads, head_dim,
+                                             _ptr(cu_seqlens), _ptr(seq_lens), _ptr(parents), _ptr(ws),
+                                             ws.numel() * ws.element_size(), ctypes.byref(plan),
+                                             _stream(stream)), "mgb_attention_tree_prepare")
+    return plan
+
+
+def mgb_attention_tree(plan: AttentionTreePlan, cache: KVCache, q, ld_q, o, ld_o, lse=None,
+                       stream=None) -> None:
+    _check(load().mgb_attention_tree(ctypes.byref(plan), ctypes.byref(cache), _ptr(q), ld_q, _ptr(o),
+                                     ld_o, _ptr(lse), _stream(stream)), "mgb_attention_tree")
+
+
+def mgb_kv_append_tree(plan: AttentionTreePlan, desc: KVAppendDesc, cache: KVCache, rope, q, k, v, ld_q,
+                       ld_kv, q_out, ld_qo, k_out, ld_ko, stream=None) -> None:
+    _check(load().mgb_kv_append_tree(ctypes.byref(plan), ctypes.byref(desc), ctypes.byref(cache),
+                                     _ptr(rope), _ptr(q), _ptr(k), _ptr(v), ld_q, ld_kv, _ptr(q_out),
+                                     ld_qo, _ptr(k_out), ld_ko, _stream(stream)), "mgb_kv_append_tree")
+
+
+def mgb_kv_accept(plan: AttentionTreePlan, cache: KVCache, accepted, new_lens=None, stream=None) -> None:
+    _check(load().mgb_kv_accept(ctypes.byref(plan), ctypes.byref(cache), _ptr(accepted), _ptr(new_lens),
+                                _stream(stream)), "mgb_kv_accept")
+
+
+def mgb_kv_copy_pages(cache: KVCache, src, dst, slots=None, stream=None) -> None:
+    """src, dst, slots: int32 vectors on the device, an entry per page copy."""
+    if dst.numel() != src.numel() or (slots is not None and slots.numel() != src.numel()):
+        raise ValueError("src, dst and slots must have one entry per copy")
+    _check(load().mgb_kv_copy_pages(ctypes.byref(cache), src.numel(), _ptr(src), _ptr(dst), _ptr(slots),
+                                    _stream(stream)), "mgb_kv_copy_pages")
 
 
 def mgb_memcpy_async(dst, src, nbytes: int, stream=None) -> None:
