@@ -2,33 +2,36 @@
 // (tcgen05): o = softmax(q K^T / sqrt(d)) V over the cached tokens that a drafted
 // token sees, all those before the draft, its ancestors in the tree and itself.
 //
-// An item's rows are the drafted tokens times the query heads of one KV head, in
-// two tiles A and B of 128 (B may be empty). Per 128 keys: S = Q K^T (TMEM), the
-// softmax threads (one per row) turn the scores into weights P in place, and O += P V
-// with P read from TMEM. Rows share all keys but the drafted ones, so K and V pass
-// once through shared memory for up to 256 rows: with few rows HBM is the bound, with
-// 256 the tensor core (3072 cycles per 128 keys) comes near it (2800 at 6.7 TB/s).
+// An item's rows are the drafted tokens times the query heads of one KV head. K and V
+// pass once through shared memory for up to 256 rows. Two streams A and B of 128 rows
+// take turns on the tensor core: with more than 128 rows they are the two halves of the
+// rows, each with all units of 128 keys; with fewer both are the same rows, A with the
+// even units, B with the odd ones, joined at the end. Per unit and stream: S = Q K^T
+// (TMEM), the softmax threads (one per row) turn the scores into weights P in place, and
+// O += P V with P read from TMEM. The MMA thread issues PV and the next S of one stream
+// while the other's softmax is at work.
 //
 // P multiplies V as the sum of two bf16 parts (off by 2^-16 relative at most): with one
 // part the weights' errors would add as much again as the output's own rounding. The
 // parts of 16 keys take the 16 columns that their scores had.
 //
-// K and V come through a ring of slots of 128 keys by 16-byte asynchronous copies of
-// four warps, a row per cached token, so any page size and layout works and tokens
-// behind the length or of a bad page are never read. The order is K_0, K_1, V_0, K_2,
-// V_1, ..: what the products need next.
+// K and V come through a ring of slots of 128 keys in the order in which the products need
+// them, K_0, K_1, V_0, K_2, V_1, .. Pages of a multiple of 8 slots are copied by the TMA
+// unit, a box of up to 128 slots of one page at a time; others row by row with 16-byte
+// asynchronous copies. Tokens behind the length or of a bad page are not read: zeros stand
+// in their place, and a bit per key says that no row sees them.
 #include "tree.cuh"
 
 namespace mgb {
 
-CUresult tmap_encode_bf16_2d(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer,
-                             int64_t ld, uint32_t box_inner, uint32_t box_outer);
+CUresult tmap_encode_bf16_nd(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
+                             const uint64_t* strides, const uint32_t* box);
 
 namespace {
 
-constexpr int TQ = 128;         // rows per tile (TMEM lanes)
+constexpr int TQ = 128;         // rows per stream (TMEM lanes)
 constexpr int TK = TREE_KEYS;   // keys per slot
-constexpr int NLOAD = 64;       // threads that copy K and V (without gather), or Q (with it)
+constexpr int NLOAD = 64;       // threads that copy K, V and Q, or with TMA Q
 constexpr int NTHREADS = 384;   // MMA warp, three loading warps, 2 x 4 softmax warps
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float TAU = 8.0f;     // the reference maximum moves in steps above this (log2 units)
@@ -39,47 +42,49 @@ constexpr float REF_LIMIT = 16777216.0f;
 template <int D>
 struct Cfg {
   static constexpr int NST = D == 64 ? 10 : 5;          // ring slots
-  static constexpr int KB = D / 64;                     // 64-wide d boxes
-  static constexpr int BOX = 128 * 128;                 // bytes of one [128][64] box
+  static constexpr int KB = D / 64;                     // 64-wide d blocks
   static constexpr int CH = D / 8;                      // 16-byte chunks of a row
-  static constexpr int Q_BYTES = TQ * D * 2;
-  static constexpr int KV_BYTES = TK * D * 2;
-  static constexpr int OFF_Q = 0;                       // [tile]
-  static constexpr int OFF_R = 2 * Q_BYTES;             // [slot]
-  static constexpr int OFF_SEE = OFF_R + NST * KV_BYTES;  // [NSEE][4]: a bit per key that may be seen
+  // A tile of 128 rows: groups of 8 rows, in a group the d blocks, in a block 8 rows of 128
+  // bytes in the 128-byte swizzle; so a TMA box of whole rows is a run of groups.
+  static constexpr int GROUP = KB * 1024;
+  static constexpr int TILE = 16 * GROUP;
+  static constexpr int OFF_Q = 0;                       // [half of the rows]
+  static constexpr int OFF_R = 2 * TILE;                // [slot]
+  static constexpr int OFF_SEE = OFF_R + NST * TILE;    // [NSEE][4]: a bit per key that may be seen
   static constexpr int NSEE = 16;
-  static constexpr int OFF_BAR = OFF_SEE + NSEE * 16;
+  static constexpr int OFF_ML = OFF_SEE + NSEE * 16;    // [128] maximum and row sum of stream B
+  static constexpr int OFF_BAR = OFF_ML + TQ * 8;
   static constexpr int SMEM = OFF_BAR + 512 + 1024;     // barriers, alignment slack
-  static constexpr int COL_S = 0;                       // two score buffers
+  static constexpr int COL_S = 0;                       // scores of A, of B
   static constexpr int COL_O = 2 * TK;                  // O_A, then O_B at + D
   static constexpr int TMEM_COLS = 512;
   static_assert(COL_O + 2 * D <= TMEM_COLS, "TMEM budget");
   static_assert(SMEM <= 232448, "shared memory budget");
-  // Barriers (8 bytes each). A waiter sees every phase of a barrier, or knows that at
-  // most one is outstanding (parity).
-  static constexpr int Q_FULL = 0;              // the item's queries copied     (every producer)
+  // Barriers (8 bytes each). A waiter sees every phase of a barrier, or knows that its
+  // phase is complete (parity).
+  static constexpr int Q_FULL = 0;              // the item's queries copied     (NLOAD threads)
   static constexpr int Q_EMPTY = 1;             // the item's last S done        (commit)
-  static constexpr int L_FULL = 2;              // [slot] copied                 (every producer)
+  static constexpr int L_FULL = 2;              // [slot] copied                 (tx, or NLOAD threads)
   static constexpr int L_EMPTY = L_FULL + NST;  // [slot] its products done      (commit)
-  static constexpr int S_FULL = L_EMPTY + NST;  // [tile][task & 1] scores       (commit)
-  static constexpr int P_FULL = S_FULL + 4;     // [tile][task & 1] weights      (4: one per warp)
-  static constexpr int PV_DONE = P_FULL + 4;    // [tile] a task's PV            (commit)
-  static constexpr int O_FULL = PV_DONE + 2;    // [tile] the item's last PV     (commit)
-  static constexpr int O_EMPTY = O_FULL + 2;    // [tile] O read out             (4: one per warp)
-  static constexpr int SEE = O_EMPTY + 2;       // [key tile % NSEE] bits there  (one per producer warp)
+  static constexpr int S_FULL = L_EMPTY + NST;  // [stream] scores, and the PV before  (commit)
+  static constexpr int O_FULL = S_FULL + 2;     // [stream] the item's last PV   (commit)
+  static constexpr int P_FULL = O_FULL + 2;     // [stream] weights              (4: one per warp)
+  static constexpr int O_EMPTY = P_FULL + 2;    // [stream] O read out           (4: one per warp)
+  static constexpr int ML = O_EMPTY + 2;        // B's maxima and sums are there (4: one per warp)
+  static constexpr int SEE = ML + 1;            // [unit % NSEE] bits are there  (one per loading warp)
   static constexpr int N_BAR = SEE + NSEE;
   static_assert(N_BAR * 8 <= 496, "barriers");
 };
 
-// A number for each of the tiles A (0) and B (1); selected, not indexed, so that it stays
+// A number for each of the streams A (0) and B (1); selected, not indexed, so that it stays
 // in registers.
-struct PerTile {
+struct PerStream {
   int a, b;
   __device__ int operator[](int x) const { return x ? b : a; }
   __device__ void inc(int x) { (x ? b : a) += 1; }
 };
 
-// The slot a key tile's K or V has in the item's order K_0, K_1, V_0, K_2, V_1, ..
+// The place of a unit's K or V in the item's order K_0, K_1, V_0, K_2, V_1, ..
 __device__ __forceinline__ int pos_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int pos_v(int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * n - 1; }
 
@@ -123,19 +128,20 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 
 // A warp copies 32 rows of D elements, lane r's at base + off (off < 0: zeros), to rows row0
-// .. of a [128][64]-box tile in the 128-byte swizzle.
+// .. of a tile.
 template <int D>
 __device__ __noinline__ void copy_rows(uint32_t dst, int row0, const bf16* base, int64_t off) {
   constexpr int CH = Cfg<D>::CH;
   const int lane = threadIdx.x & 31;
   const int ch = lane % CH, r0 = lane / CH;
   base += ch * 8;
-  dst += (ch >> 3) * Cfg<D>::BOX + row0 * 128;
+  dst += (row0 >> 3) * Cfg<D>::GROUP + (ch >> 3) * 1024;
 #pragma unroll 8
   for (int i = 0; i < CH; ++i) {
     const int r = i * (32 / CH) + r0;
     const int64_t ro = __shfl_sync(0xffffffffu, off, r);
-    cp_async16(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4), base + (ro >= 0 ? ro : 0), ro >= 0);
+    cp_async16(dst + (r >> 3) * Cfg<D>::GROUP + (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4),
+               base + (ro >= 0 ? ro : 0), ro >= 0);
   }
 }
 
@@ -146,63 +152,116 @@ __device__ __forceinline__ void copy_q(const TreeParams& p, const TreeSeg& w, ui
 #pragma unroll 1
   for (int g = first; g * 32 < w.rows; g += step) {
     const int r = g * 32 + lane, rr = w.b * TREE_ROWS + r, t = rr / p.G;
-    copy_rows<D>(sQ + (g >> 2) * Cfg<D>::Q_BYTES, (g & 3) * 32, static_cast<const bf16*>(p.q),
+    copy_rows<D>(sQ + (g >> 2) * Cfg<D>::TILE, (g & 3) * 32, static_cast<const bf16*>(p.q),
                  r < w.rows ? (w.q.row + t) * p.ld_q + (int64_t)(w.h * p.G + rr - t * p.G) * D : -1);
   }
 }
 
-// Scores of 32 keys -> weights 2^(s a + b) in two bf16 parts, per 16 keys the high parts of
-// the pairs in the first eight words, the low parts in the others; the sums take them
-// whole. The high part is the weight cut off, the low part what that leaves, rounded: off by
-// 2^-16 relative at most.
-__device__ __forceinline__ void weights(uint32_t (&s)[32], float a, float b, float (&sum)[4]) {
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    uint32_t hi[8], lo[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float x, y, u, v;
-      fma2(x, y, __uint_as_float(s[16 * g + 2 * e]), __uint_as_float(s[16 * g + 2 * e + 1]), a, a, b, b);
-      x = ex2_ftz(x);
-      y = ex2_ftz(y);
-      float* t = sum + 2 * (e & 1);
-      add2(t[0], t[1], t[0], t[1], x, y);
-      const uint32_t xu = __float_as_uint(x), yu = __float_as_uint(y);
-      hi[e] = __byte_perm(xu, yu, 0x7632);
-      add2(u, v, x, y, __uint_as_float((xu & 0xffff0000u) ^ 0x80000000u),
-           __uint_as_float((yu & 0xffff0000u) ^ 0x80000000u));
-      lo[e] = pack_bf16x2(u, v);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[16 * g + e] = hi[e], s[16 * g + 8 + e] = lo[e];
-  }
+// The steps of the weights in an order that the compiler keeps (volatile).
+__device__ __forceinline__ void v_fma2(float& r0, float& r1, uint32_t a0, uint32_t a1, float b, float c) {
+  asm volatile(
+      "{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n"
+      " mov.b64 c, {%5, %5};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r0), "=f"(r1)
+      : "r"(a0), "r"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void v_ex2(float& x) { asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(x)); }
+__device__ __forceinline__ void v_add2(float& r0, float& r1, float a0, float a1, float b0, float b1) {
+  asm volatile(
+      "{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r0), "=f"(r1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+// the upper halves of two words
+__device__ __forceinline__ uint32_t v_upper(float lo, float hi) {
+  uint32_t r;
+  asm volatile("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+// minus the value with its lower half cut off
+__device__ __forceinline__ float v_minus_upper(float x) {
+  float r;
+  asm volatile("lop3.b32 %0, %1, 0xffff0000, 0x80000000, 0x6A;" : "=f"(r) : "f"(x));  // (a & b) ^ c
+  return r;
+}
+__device__ __forceinline__ uint32_t v_pack(float lo, float hi) {
+  uint32_t r;
+  asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
-// Where the pools' vectors are as rows of a matrix: vector (page, slot, head) is row page
-// r_page + slot + head r_head, column head c_head. Copies take `box` rows (a power of two that
-// divides the page size, 8 to 128), which lie in one page.
-struct RowMap {
-  int r_page, r_head, c_head, rows, box, shift;  // box = 1 << shift
-};
-struct PoolMaps {
-  CUtensorMap k, v, k1, v1;  // boxes of `box` rows; of one row, for gather copies
-};
+// Scores of 64 keys -> weights 2^(s a + b) in two bf16 parts, per 16 keys the high parts of
+// the pairs in the first eight words, the low parts in the others; the sums take them
+// whole. The high part is the weight cut off, the low part what that leaves, rounded: off by
+// 2^-16 relative at most. Groups of four keys: the exponentials of one (4 cycles each) between
+// the sums and parts of the one before and the scaling of the second next.
+__device__ __forceinline__ void weights(uint32_t (&s)[2][32], float a, float b, float (&sum)[4]) {
+  float t[4][4];
+  auto scale = [&](int g) {
+    const uint32_t* z = s[g >> 3] + (g & 7) * 4;
+    v_fma2(t[g & 3][0], t[g & 3][1], z[0], z[1], a, b);
+    v_fma2(t[g & 3][2], t[g & 3][3], z[2], z[3], a, b);
+  };
+  scale(0);
+  scale(1);
+  uint32_t out[2][32];
+#pragma unroll
+  for (int g = 0; g <= 16; ++g) {
+    float* y = t[g & 3];
+    const float* u = t[(g + 3) & 3];  // group g - 1
+    uint32_t* o = g > 0 ? out[(g - 1) >> 3] + ((g - 1) & 4) * 4 + ((g - 1) & 3) * 2 : nullptr;
+    float n0, n1, n2, n3, r0, r1, r2, r3;
+    if (g < 16) v_ex2(y[0]);
+    if (g > 0) {
+      v_add2(sum[0], sum[1], sum[0], sum[1], u[0], u[1]);
+      n0 = v_minus_upper(u[0]);
+      n1 = v_minus_upper(u[1]);
+    }
+    if (g < 16) v_ex2(y[1]);
+    if (g > 0) {
+      v_add2(r0, r1, u[0], u[1], n0, n1);
+      o[0] = v_upper(u[0], u[1]);
+      n2 = v_minus_upper(u[2]);
+    }
+    if (g < 16) v_ex2(y[2]);
+    if (g > 0) {
+      v_add2(sum[2], sum[3], sum[2], sum[3], u[2], u[3]);
+      n3 = v_minus_upper(u[3]);
+      o[8] = v_pack(r0, r1);
+    }
+    if (g < 16) v_ex2(y[3]);
+    if (g > 0) {
+      v_add2(r2, r3, u[2], u[3], n2, n3);
+      o[1] = v_upper(u[2], u[3]);
+    }
+    if (g + 2 < 16) scale(g + 2);
+    if (g > 0) o[9] = v_pack(r2, r3);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 32; ++e) s[i][e] = out[i][e];
+}
 
-// Four rows of 64 columns from column x on, to 512 bytes of a 128-byte-swizzled tile; a row
-// outside the matrix gives zeros.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int32_t x, const int (&r)[4],
-                                            uint32_t bar) {
+// How the TMA unit finds a pool's vectors: an element of a head's vector, row of 8 slots, d
+// block, group of 8 slots, page.
+struct PoolMaps {
+  CUtensorMap k[3], v[3];  // boxes of `box` slots, of 8, of one (and one d block)
+  int shift;               // box = 1 << shift slots: 8 to 128, in one page
+};
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int x, int row, int kb, int group,
+                                            int page, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(row), "r"(kb), "r"(group), "r"(page), "r"(bar)
       : "memory");
 }
 
-// TMA: the pools are rows of a matrix, and the TMA unit copies
 template <int D, bool TMA>
 __global__ void __launch_bounds__(NTHREADS, 1)
-    tree_kernel(const __grid_constant__ PoolMaps tm, const RowMap rm, const TreeParams p) {
+    tree_kernel(const __grid_constant__ PoolMaps tm, const TreeParams p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -212,6 +271,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   constexpr int NST = C::NST;
   auto bar = [&](int which) { return sb + C::OFF_BAR + 8 * which; };
   volatile uint32_t* see = reinterpret_cast<uint32_t*>(smem + C::OFF_SEE);
+  volatile float* sml = reinterpret_cast<float*>(smem + C::OFF_ML);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 496);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 500);
 
@@ -229,8 +289,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int i = 0; i < C::N_BAR; ++i) {
       int n = 1;
       if (i == C::Q_FULL || (!TMA && i >= C::L_FULL && i < C::L_EMPTY)) n = NLOAD;
-      if ((i >= C::P_FULL && i < C::PV_DONE) || (i >= C::O_EMPTY && i < C::SEE)) n = 4;
-      if (i >= C::SEE) n = TMA ? 1 : NLOAD / 32;
+      if (i >= C::P_FULL && i <= C::ML) n = 4;
+      if (!TMA && i >= C::SEE) n = NLOAD / 32;
       mbar_init(bar(i), n);
     }
     fence_mbar_init();
@@ -248,13 +308,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (elect_one()) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(TQ, TK, 0, 0);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(TQ, D, 0, 1);
-      const uint64_t dq0 = smem_desc_sw128(sQ, 16, 1024);
-      const uint64_t dk0 = smem_desc_sw128(sR, 16, 1024);
-      const uint64_t dv0 = smem_desc_sw128(sR, C::BOX, 1024);
-      int nl = 0;          // slots of the items before
-      PerTile ns{0, 0};    // tasks of each tile whose S products are issued
-      PerTile np{0, 0};    // .. whose PV products are issued
-      PerTile no{0, 0};    // items of each tile so far
+      const uint64_t dq0 = smem_desc_sw128(sQ, 16, C::GROUP);
+      const uint64_t dk0 = smem_desc_sw128(sR, 16, C::GROUP);
+      const uint64_t dv0 = smem_desc_sw128(sR, 1024, C::GROUP);
+      int nl = 0;            // slots of the items before
+      PerStream np{0, 0};    // weights of each stream so far
+      PerStream no{0, 0};    // items of each stream so far
       bool good = true;
       for (int k = 0; good && sg.next(p, w); ++k) {
         const int nt = w.t1 - w.t0;
@@ -262,64 +321,60 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         auto ready = [&](int pos) {
           const int n = nl + pos;
           if (!wait_1(bar(C::L_FULL + n % NST), (n / NST) & 1, p.err, abort)) return false;
-          fence_proxy_async();  // the copies were ordinary writes, the tensor core reads
+          fence_proxy_async();  // what was copied by ordinary writes is read by the tensor core
           tc_fence_after();
           return true;
         };
         auto release = [&](int pos) { tc_commit(bar(C::L_EMPTY + (nl + pos) % NST)); };
         good = wait_1(bar(C::Q_FULL), k & 1, p.err, abort);
-        // Per unit: two tiles take turns, PV_A(j), S_A(j + 1), PV_B(j), S_B(j + 1), each in its
-        // score buffer; tile A alone has its scores one task ahead, S(j + 1), PV(j), in the
-        // two buffers by turns.
+        // A step: PV of the stream's unit before, S of its next one. Streams take turns;
+        // halves of the rows: A(0), B(0), A(1), ..; units: A(0), B(1), A(2), ..
+        const int steps = two ? 2 * nt + 2 : nt + 2;
 #pragma unroll 1
-        for (int j = -1; j < nt && good; ++j) {
-#pragma unroll 1
-          for (int i = 0; i < (two ? 4 : 2) && good; ++i) {
-            const int x = i >> 1;
-            const bool last = x == 1 || !two;
-            if (((i & 1) == 0) != two) {
-              if (j + 1 == nt) continue;
-              if (x == 0) good = ready(pos_k(j + 1));
-              if (!good) break;
-              const uint64_t da = dq0 + (uint64_t)((x * C::Q_BYTES) >> 4);
-              const uint64_t db = dk0 + (uint64_t)(((nl + pos_k(j + 1)) % NST * C::KV_BYTES) >> 4);
-              const uint32_t td = tmem + C::COL_S + (two ? x : (j + 1) & 1) * TK;
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * C::BOX + (kk & 3) * 32;
-                tc_mma_f16(td, da + (uint64_t)(off >> 4), db + (uint64_t)(off >> 4), idesc_s, kk > 0);
-              }
-              tc_commit(bar(C::S_FULL + 2 * x + (ns[x] & 1)));
-              ns.inc(x);
-              if (last) {
-                release(pos_k(j + 1));
-                if (j + 2 == nt) tc_commit(bar(C::Q_EMPTY));
-              }
-            } else {
-              if (j < 0) continue;
-              // O_X += P_X V_j, the K steps (16 keys) that hold keys of the sequence
-              good = (x == 1 || ready(pos_v(j, nt))) &&
-                     (j > 0 || no[x] == 0 || wait_1(bar(C::O_EMPTY + x), (no[x] - 1) & 1, p.err, abort)) &&
-                     wait_1(bar(C::P_FULL + 2 * x + (np[x] & 1)), (np[x] >> 1) & 1, p.err, abort);
-              if (!good) break;
-              np.inc(x);
-              tc_fence_after();
-              const int left = w.q.len - (w.t0 + j) * TK;
-              const int ks = left >= TK ? TK / 16 : (left + 15) / 16;
-              const uint64_t db = dv0 + (uint64_t)(((nl + pos_v(j, nt)) % NST * C::KV_BYTES) >> 4);
-              const uint32_t ta = tmem + C::COL_S + (two ? x : j & 1) * TK, to = tmem + C::COL_O + x * D;
+        for (int i = 0; i < steps && good; ++i) {
+          const int x = i & 1;
+          const int js = two ? i >> 1 : i, jv = two ? js - 1 : i - 2;
+          const bool first = x == 0 || !two, last = x == 1 || !two;  // use of a unit's K and V
+          if (jv >= 0) {
+            // O_X += P_X V_j, the K steps (16 keys) that hold keys of the sequence
+            const bool fresh = two ? jv == 0 : jv < 2;  // the stream's first unit of the item
+            good = (!first || ready(pos_v(jv, nt))) &&
+                   (!fresh || no[x] == 0 || wait_1(bar(C::O_EMPTY + x), (no[x] - 1) & 1, p.err, abort)) &&
+                   wait_1(bar(C::P_FULL + x), np[x] & 1, p.err, abort);
+            if (!good) break;
+            np.inc(x);
+            tc_fence_after();
+            const int left = w.q.len - (w.t0 + jv) * TK;
+            const int ks = left >= TK ? TK / 16 : (left + 15) / 16;
+            const uint64_t db = dv0 + (uint64_t)(((nl + pos_v(jv, nt)) % NST * C::TILE) >> 4);
+            const uint32_t ta = tmem + C::COL_S + x * TK, to = tmem + C::COL_O + x * D;
 #pragma unroll 4
-              for (int kk = 0; kk < ks; ++kk) {
-                const uint64_t dv = db + (uint64_t)((kk * 2048) >> 4);
-                tc_mma_f16_ts(to, ta + kk * 16, dv, idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-                tc_mma_f16_ts(to, ta + kk * 16 + 8, dv, idesc_pv, 1u);
-              }
-              tc_commit(bar(C::PV_DONE + x));
-              if (j == nt - 1) {
-                tc_commit(bar(C::O_FULL + x));
-                no.inc(x);
-              }
-              if (last) release(pos_v(j, nt));
+            for (int kk = 0; kk < ks; ++kk) {
+              const uint64_t dv = db + (uint64_t)((kk * 2 * C::GROUP) >> 4);
+              tc_mma_f16_ts(to, ta + kk * 16, dv, idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
+              tc_mma_f16_ts(to, ta + kk * 16 + 8, dv, idesc_pv, 1u);
+            }
+            if (last) release(pos_v(jv, nt));
+            if (two ? jv == nt - 1 : jv + 2 >= nt) {
+              tc_commit(bar(C::O_FULL + x));
+              no.inc(x);
+            }
+          }
+          if (js < nt) {
+            if (first) good = ready(pos_k(js));
+            if (!good) break;
+            const uint64_t da = dq0 + (uint64_t)((two ? x * C::TILE : 0) >> 4);
+            const uint64_t db = dk0 + (uint64_t)(((nl + pos_k(js)) % NST * C::TILE) >> 4);
+            const uint32_t td = tmem + C::COL_S + x * TK;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
+              tc_mma_f16(td, da + off, db + off, idesc_s, kk > 0);
+            }
+            tc_commit(bar(C::S_FULL + x));
+            if (last) {
+              release(pos_k(js));
+              if (js == nt - 1) tc_commit(bar(C::Q_EMPTY));
             }
           }
         }
@@ -330,17 +385,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     __syncwarp();
   } else if (TMA && warp == 1) {
     // ---------------- K and V: a lane finds the page of one box and asks for it
-    int nl = 0, nkey = 0;  // slots, key tiles so far
-    const int nbox = TK >> rm.shift;
+    int nl = 0, nkey = 0;  // slots, units so far
+    const int nbox = TK >> tm.shift;
     bool good = true;
     while (good && sg.next(p, w)) {
-      const int nt = w.t1 - w.t0, x = w.h * rm.c_head;
+      const int nt = w.t1 - w.t0, x = w.h * (int)p.s_head;
       const int32_t* table = p.table + (int64_t)w.q.s * p.ld_table;
-      // page of this lane's box of unit j, requested one unit ahead
+      // page and slot of this lane's box of unit j, requested one unit ahead
       int pg = 0, slot = 0;
       bool on = false;
       auto peek = [&](int j) {
-        const int key = (w.t0 + j) * TK + (lane << rm.shift);  // (lengths end well below 2^31)
+        const int key = (w.t0 + j) * TK + (lane << tm.shift);  // (lengths end well below 2^31)
         on = j < nt && lane < nbox && key < w.q.len;
         if (on) {
           const int e = key / p.page_size;
@@ -349,19 +404,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       };
       peek(0);
-      int now = rm.rows, before = rm.rows;  // first row of this lane's box of the newest unit, of the one before
+      // place of this lane's box of the newest unit, of the one before; page n_pages: zeros
+      int2 now = make_int2(p.n_pages, 0), before = now;
 #pragma unroll 1
       for (int pos = 0; pos < 2 * nt; ++pos) {
-        const bool is_v = pos == 2 * nt - 1 || (pos > 0 && (pos & 1) == 0);
+        const bool newest = pos == 2 * nt - 1;  // of V
+        const bool is_v = newest || (pos > 0 && (pos & 1) == 0);
         const int n = nl + pos, s = n % NST;
-        const int j = pos == 2 * nt - 1 ? nt - 1 : is_v ? (pos - 2) / 2 : (pos + 1) / 2;
+        const int j = newest ? nt - 1 : is_v ? (pos - 2) / 2 : (pos + 1) / 2;
         const int left = w.q.len - (w.t0 + j) * TK;  // keys of the sequence from here on
         uint32_t boxes = 0;
         if (!is_v) {
           const bool ok = on && pg >= 0 && pg < p.n_pages;
           if (on && !ok) record_error(p.err, kErrIndex);
           before = now;
-          now = ok ? pg * rm.r_page + slot + w.h * rm.r_head : rm.rows;  // (no row: zeros)
+          now = ok ? make_int2(pg, slot >> 3) : make_int2(p.n_pages, 0);
           boxes = __ballot_sync(0xffffffffu, ok);
           peek(j + 1);
         }
@@ -375,31 +432,33 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int key = 32 * i + lane;
-            const uint32_t bits = __ballot_sync(0xffffffffu, key < left && ((boxes >> (key >> rm.shift)) & 1u));
+            const uint32_t bits = __ballot_sync(0xffffffffu, key < left && ((boxes >> (key >> tm.shift)) & 1u));
             if (lane == 0) see[at * 4 + i] = bits;
           }
           if (lane == 0) mbar_arrive(bar(C::SEE + at));
         }
-        if (lane == 0) mbar_arrive_expect_tx(full, C::KV_BYTES);
+        if (lane == 0) mbar_arrive_expect_tx(full, C::TILE);
         __syncwarp();
-        const int row = !is_v || pos == 2 * nt - 1 ? now : before;
-        const uint32_t dst = sR + s * C::KV_BYTES;
-        // the box with the sequence's end: row by row, so that slots behind it are zeros
-        const int part = left < TK && (left & (rm.box - 1)) ? left >> rm.shift : nbox;
+        const int2 b = !is_v || newest ? now : before;
+        const CUtensorMap* maps = is_v ? tm.v : tm.k;
+        const uint32_t dst = sR + s * C::TILE;
+        // the box with the sequence's end: 8 slots at a time, the last of them one by one, so
+        // that those behind the end are zeros
+        const int part = left < TK && (left & ((1 << tm.shift) - 1)) ? left >> tm.shift : nbox;
         if (lane < nbox && lane != part)
-#pragma unroll
-          for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_2d(dst + kb * C::BOX + (lane << rm.shift) * 128, is_v ? &tm.v : &tm.k, x + kb * 64, row, full);
+          tma_load_5d(dst + ((lane << tm.shift) >> 3) * C::GROUP, &maps[0], x, 0, 0, b.y, b.x, full);
         if (part < nbox) {
-          const int first = __shfl_sync(0xffffffffu, row, part);
-          if ((4 * lane) >> rm.shift == part) {
-            int r[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              r[i] = first < rm.rows && 4 * lane + i < left ? first + 4 * lane + i - (part << rm.shift) : rm.rows;
-#pragma unroll
-            for (int kb = 0; kb < C::KB; ++kb)
-              tma_gather4(dst + kb * C::BOX + lane * 512, is_v ? &tm.v1 : &tm.k1, x + kb * 64, r, full);
+          const int pb = __shfl_sync(0xffffffffu, b.x, part), gb = __shfl_sync(0xffffffffu, b.y, part);
+          const int g0 = part << (tm.shift - 3);  // the box's first group of the tile
+          const int edge = left >> 3;             // the group with the end, if it is inside one
+          const int g = g0 + lane;
+          if (lane < (1 << (tm.shift - 3)) && !(g == edge && (left & 7)))
+            tma_load_5d(dst + g * C::GROUP, &maps[1], x, 0, 0, gb + lane, g < edge ? pb : p.n_pages, full);
+          if (left & 7) {
+            const int r = lane / C::KB, kb = lane % C::KB;
+            if (r < 8)
+              tma_load_5d(dst + edge * C::GROUP + kb * 1024 + r * 128, &maps[2], x, r, kb, gb + edge - g0,
+                          edge * 8 + r < left ? pb : p.n_pages, full);
           }
         }
       }
@@ -417,13 +476,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (!good) *abort = 1;
     cp_async_commit();
     cp_async_wait<0>();
-  } else if (!TMA && warp == 3) {
-    // (nothing to do)
   } else if (!TMA && warp < 1 + NLOAD / 32) {
-    // ---------------- producers: a lane finds one row's place, all copy it
+    // ---------------- Q, K and V row by row: a lane finds one row's place, all copy it
     const int pw = warp - 1;
     constexpr int NR = TQ / NLOAD;  // rows per lane: 32 (NR pw + i) + lane
-    int nl = 0, nkey = 0;  // slots, key tiles so far
+    int nl = 0, nkey = 0;  // slots, units so far
     bool good = true;
     for (int k = 0; good && sg.next(p, w); ++k) {
       const int nt = w.t1 - w.t0;
@@ -450,10 +507,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       copy_q<D>(p, w, sQ, pw, 2);
       cp_async_arrive(bar(C::Q_FULL));
-      int64_t now[NR], before[NR];  // this lane's places of the newest unit and the one before it
+      int64_t now[NR] = {}, before[NR] = {};  // this lane's places of the newest unit and the one before it
 #pragma unroll 1
       for (int pos = 0; pos < 2 * nt; ++pos) {
-        const bool is_v = pos == 2 * nt - 1 || (pos > 0 && (pos & 1) == 0);
+        const bool newest = pos == 2 * nt - 1;  // of V
+        const bool is_v = newest || (pos > 0 && (pos & 1) == 0);
         const int n = nl + pos, s = n % NST;
         uint32_t bits[NR];
         if (!is_v) {
@@ -479,11 +537,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_arrive(bar(C::SEE + at));
           }
         }
-        const bool newest = !is_v || pos == 2 * nt - 1;
 #pragma unroll
         for (int i = 0; i < NR; ++i)
-          copy_rows<D>(sR + s * C::KV_BYTES, (pw * NR + i) * 32,
-                       static_cast<const bf16*>(is_v ? p.v : p.k), newest ? now[i] : before[i]);
+          copy_rows<D>(sR + s * C::TILE, (pw * NR + i) * 32, static_cast<const bf16*>(is_v ? p.v : p.k),
+                       !is_v || newest ? now[i] : before[i]);
         cp_async_arrive(bar(C::L_FULL + s));
       }
       nl += 2 * nt;
@@ -491,34 +548,35 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (!good) *abort = 1;
     cp_async_commit();
     cp_async_wait<0>();
-  } else {
-    // ---------------- softmax: a thread per row; warps of tile A, then of tile B
+  } else if (warp >= 4) {
+    // ---------------- softmax: a thread per row; warps of stream A, then of stream B
     const int x = (warp - 4) >> 2;
     const int quarter = warp & 3;
-    const int r = quarter * 32 + lane;  // row of the tile
+    const int r = quarter * 32 + lane;  // row of the stream
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t t_o = tmem + C::COL_O + x * D + lane_base;
+    const uint32_t t_s = tmem + C::COL_S + x * TK + lane_base, t_o = tmem + C::COL_O + x * D + lane_base;
     bool good = true;
-    int nx = 0;    // tasks of this tile so far
-    int ko = 0;    // items of this tile so far
-    int nkey = 0;  // key tiles of the items before
+    int nx = 0;    // units of this stream so far
+    int ko = 0;    // items of this stream so far
+    int km = 0;    // items joined from both streams so far
+    int nkey = 0;  // units of the items before
     while (good && sg.next(p, w)) {
       const int nt = w.t1 - w.t0, key0 = nkey;
       nkey += nt;
       const bool two = w.rows > TQ;
-      if (x == 1 && !two) continue;
-      const int row = x * TQ + r;              // of the block
+      if (x == 1 && !two && nt < 2) continue;
+      const int row = (two ? x * TQ : 0) + r;  // of the block
       const bool live = row < w.rows;
-      const bool work = x * TQ + quarter * 32 < w.rows;  // the warp has a row
+      const bool work = row - lane < w.rows;   // the warp has a row
       const int rr = w.b * TREE_ROWS + (live ? row : 0);
       const int tok = rr / p.G, head = w.h * p.G + rr - tok * p.G;
       const uint32_t* mask = p.mask + (int64_t)(w.q.row + tok) * TREE_WORDS;
       const int ctx = w.q.len - w.q.m;         // tokens before the draft
       float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < nt; ++j, ++nx) {
+      const int j0 = two ? 0 : x;
+      for (int j = j0; j < nt; j += two ? 1 : 2, ++nx) {
         const int kv0 = (w.t0 + j) * TK;
-        const uint32_t t_s = tmem + C::COL_S + (two ? x : j & 1) * TK + lane_base;
-        if (!wait_w(bar(C::S_FULL + 2 * x + (nx & 1)), (nx >> 1) & 1, p.err, abort)) {
+        if (!wait_w(bar(C::S_FULL + x), nx & 1, p.err, abort)) {
           good = false;
           break;
         }
@@ -529,16 +587,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             good = false;
             break;
           }
-          // the keys of the tile that this row sees
+          // the keys of the unit that this row sees
           uint32_t vis[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) vis[i] = see[at * 4 + i];
-          const bool edge = kv0 + TK > ctx || (vis[0] & vis[1] & vis[2] & vis[3]) != ~0u;
-          if (kv0 + TK > ctx)
+          if (kv0 + TK > ctx || (vis[0] & vis[1] & vis[2] & vis[3]) != ~0u) {
+            // Few units have hidden keys: their scores are overwritten first.
+            if (kv0 + TK > ctx)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) vis[i] &= tree_window(mask, kv0 + 32 * i - ctx);
-          // Few tiles have hidden keys: their scores are overwritten first.
-          if (edge) {
+              for (int i = 0; i < 4; ++i) vis[i] &= tree_window(mask, kv0 + 32 * i - ctx);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t v = vis[i];
@@ -576,11 +633,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const float a = up ? exp2f(m - mx) : 1.0f;
             if (up) m = mx;
             l *= a;
-            if (j > 0) {
-              // (the scores were formed behind the PV before the last, and the task's own PV waits for
-              // its weights: at most one phase is outstanding)
-              if (!wait_w(bar(C::PV_DONE + x), (nx - 1) & 1, p.err, abort)) *abort = 1;
-              tc_fence_after();
+            if (j > j0) {  // (the PV before is complete: the scores were formed behind it)
 #pragma unroll 1
               for (int i = 0; i < D / 16; ++i) {
                 uint32_t o[16];
@@ -622,9 +675,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tmem_ld_wait();
             tmem_regs_ready(s[0]);
             tmem_regs_ready(s[1]);
-            weights(s[0], p.sl2, shift, sum);
+            weights(s, p.sl2, shift, sum);
             tmem_st32(t_s + i * 32, s[0]);
-            weights(s[1], p.sl2, shift, sum);
             tmem_st32(t_s + i * 32 + 32, s[1]);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -632,7 +684,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         tc_fence_before();
         __syncwarp();  // the warp's stores are done: one arrival for the warp
-        if (lane == 0) mbar_arrive(bar(C::P_FULL + 2 * x + (nx & 1)));
+        if (lane == 0) mbar_arrive(bar(C::P_FULL + x));
       }
       if (!good) break;
       // ---- the CTA's units of the item are done
@@ -641,34 +693,74 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         break;
       }
       tc_fence_after();
+      const bool join = !two && nt > 1;  // B's sums go to A
+      if (join && x == 1) {
+        sml[2 * r] = m;
+        sml[2 * r + 1] = l;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::ML));
+        continue;
+      }
+      float fa = 1.0f, fb = 0.0f;
+      if (join) {
+        if (!wait_w(bar(C::ML), km++ & 1, p.err, abort)) {
+          good = false;
+          break;
+        }
+        tc_fence_after();
+        const float mb = sml[2 * r], lb = sml[2 * r + 1], M = fmaxf(m, mb);
+        // (no reference: no key or only scores of -infinity, sum 0, or NaN, which stays)
+        fa = m > -INFINITY ? exp2f(m - M) : 1.0f;
+        fb = mb > -INFINITY ? exp2f(mb - M) : 1.0f;
+        l = l * fa + lb * fb;
+        m = M;
+      }
       if (work) {
         const bool whole = tree_begin(w.nt - 1, w.nt) + w.at < end && w.at >= c * chunk;
-        if (whole) {
-          const float inv = 1.0f / l;  // (no score: 0 / 0)
-          bf16* out = static_cast<bf16*>(p.o) + (w.q.row + tok) * p.ld_o + (int64_t)head * D;
-          store_tmem_row<D>(t_o, inv, live ? out : nullptr);
-          if (live && p.lse != nullptr)
-            p.lse[(int64_t)(w.q.row + tok) * p.nq + head] = (m + log2f(l)) * LN2;
-        } else {
-          const int64_t at = (int64_t)tree_part(c, chunk, w.at) * p.rows + row;
+        const float inv = whole ? 1.0f / l : 1.0f;  // (no score: 0 / 0)
+        fa *= inv;
+        fb *= inv;
+        bf16* out = static_cast<bf16*>(p.o) + (w.q.row + tok) * p.ld_o + (int64_t)head * D;
+        const int64_t at = (int64_t)tree_part(c, chunk, w.at) * p.rows + row;
+#pragma unroll 1
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t o[16], o2[16];
+          tmem_ld16(t_o + i * 16, o);
+          if (join) tmem_ld16(t_o + D + i * 16, o2);
+          tmem_ld_wait();
+          tmem_regs_ready(o);
+          tmem_regs_ready(o2);
+          float f[16];
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t o[32];
-            tmem_ld32(t_o + i * 32, o);
-            tmem_ld_wait();
-            tmem_regs_ready(o);
-            if (live)
-#pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<uint4*>(p.part + at * D + i * 32 + e) =
-                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 16; ++e) {
+            f[e] = __uint_as_float(o[e]) * fa;
+            if (join) f[e] = fmaf(__uint_as_float(o2[e]), fb, f[e]);
           }
-          if (live) p.ml[at] = make_float2(m, l);
+          if (live && whole) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              *reinterpret_cast<uint4*>(out + i * 16 + e) =
+                  make_uint4(pack_bf16x2(f[e], f[e + 1]), pack_bf16x2(f[e + 2], f[e + 3]),
+                             pack_bf16x2(f[e + 4], f[e + 5]), pack_bf16x2(f[e + 6], f[e + 7]));
+          } else if (live) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(p.part + at * D + i * 16 + e) =
+                  make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+          }
+          __syncwarp();  // (the loads are the whole warp's)
         }
+        if (live && whole && p.lse != nullptr)
+          p.lse[(int64_t)(w.q.row + tok) * p.nq + head] = (m + log2f(l)) * LN2;
+        if (live && !whole) p.ml[at] = make_float2(m, l);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::O_EMPTY + x));
+      if (lane == 0) {
+        mbar_arrive(bar(C::O_EMPTY + x));
+        if (join) mbar_arrive(bar(C::O_EMPTY + 1));
+      }
     }
     if (!good) *abort = 1;
   }
@@ -682,50 +774,44 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-// Whether the TMA unit can copy: pages of a multiple of 8 slots, and vectors one stride apart
-// over slots, pages and heads (or heads next to each other in a row).
-bool row_map(const TreeParams& p, int d, RowMap& m, int64_t& ld, int64_t& width) {
-  m.shift = __builtin_ctz((unsigned)p.page_size);
-  if (m.shift < 3) return false;
-  if (m.shift > 7) m.shift = 7;
-  m.box = 1 << m.shift;
-  ld = p.s_tok;
-  if (p.n_pages > 1 && p.s_page % ld) return false;
-  const int64_t across = (p.nkv - 1) * p.s_head + d;
-  const bool in_row = across <= ld;
-  if (!in_row && p.s_head % ld) return false;
-  width = in_row ? across : d;
-  const int64_t r_page = p.n_pages > 1 ? p.s_page / ld : 0, r_head = in_row ? 0 : p.s_head / ld;
-  const int64_t rows = (p.n_pages - 1) * r_page + p.page_size + (p.nkv - 1) * r_head;
-  if (rows >= (int64_t)1 << 31 || width >= (int64_t)1 << 31) return false;
-  m.r_page = (int)r_page; m.r_head = (int)r_head; m.c_head = in_row && p.nkv > 1 ? (int)p.s_head : 0;
-  m.rows = (int)rows;
-  return true;
+// Whether the TMA unit can copy: pages of a multiple of 8 slots (and sizes that its numbers hold).
+bool tma_ok(const TreeParams& p, int d) {
+  const int64_t most = (int64_t)1 << 31;
+  return p.page_size % 8 == 0 && (p.nkv - 1) * p.s_head + d < most && p.s_page < most * 128 &&
+         8 * p.s_tok < most * 128;
+}
+
+mgb_status encode_pool(CUtensorMap (&tm)[3], const void* pool, const TreeParams& p, int d, int shift) {
+  const uint64_t es = 2;
+  const uint64_t dims[5] = {(uint64_t)((p.nkv - 1) * p.s_head + 64), 8, (uint64_t)(d / 64),
+                            (uint64_t)(p.page_size / 8), (uint64_t)p.n_pages};
+  const uint64_t strides[4] = {(uint64_t)p.s_tok * es, 64 * es, 8 * (uint64_t)p.s_tok * es,
+                               (uint64_t)(p.n_pages > 1 ? p.s_page : 8) * es};
+  const uint32_t kb = (uint32_t)(d / 64);
+  const uint32_t box[3][5] = {{64, 8, kb, 1u << (shift - 3), 1}, {64, 8, kb, 1, 1}, {64, 1, 1, 1, 1}};
+  for (int i = 0; i < 3; ++i)
+    if (tmap_encode_bf16_nd(&tm[i], pool, 5, dims, strides, box[i]) != CUDA_SUCCESS) return MGB_ERR_CUDA;
+  return MGB_OK;
 }
 
 template <int D, bool TMA>
-mgb_status launch_k(const TreeParams& p, const PoolMaps& tm, const RowMap& rm, cudaStream_t st) {
+mgb_status launch_k(const TreeParams& p, const PoolMaps& tm, cudaStream_t st) {
   using C = Cfg<D>;
   auto k = tree_kernel<D, TMA>;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return MGB_ERR_CUDA;
-  const mgb_status s = launch_pdl(k, TREE_RANGES / 2, NTHREADS, C::SMEM, st, tm, rm, p);
+  const mgb_status s = launch_pdl(k, TREE_RANGES / 2, NTHREADS, C::SMEM, st, tm, p);
   return s != MGB_OK ? s : tree_join(p, D, MGB_BF16, TREE_RANGES / 2, 2, st);
 }
 
 template <int D>
 mgb_status launch_d(const TreeParams& p, cudaStream_t st) {
   PoolMaps tm{};
-  RowMap rm{};
-  int64_t ld, w;
-  if (!row_map(p, D, rm, ld, w)) return launch_k<D, false>(p, tm, rm, st);
-  const uint64_t n = (uint64_t)rm.rows;
-  if (tmap_encode_bf16_2d(&tm.k, p.k, w, n, ld, 64, rm.box) != CUDA_SUCCESS ||
-      tmap_encode_bf16_2d(&tm.v, p.v, w, n, ld, 64, rm.box) != CUDA_SUCCESS ||
-      tmap_encode_bf16_2d(&tm.k1, p.k, w, n, ld, 64, 1) != CUDA_SUCCESS ||
-      tmap_encode_bf16_2d(&tm.v1, p.v, w, n, ld, 64, 1) != CUDA_SUCCESS)
+  if (!tma_ok(p, D)) return launch_k<D, false>(p, tm, st);
+  while (tm.shift < 7 && p.page_size % (2 << tm.shift) == 0) ++tm.shift;
+  if (encode_pool(tm.k, p.k, p, D, tm.shift) != MGB_OK || encode_pool(tm.v, p.v, p, D, tm.shift) != MGB_OK)
     return MGB_ERR_CUDA;
-  return launch_k<D, true>(p, tm, rm, st);
+  return launch_k<D, true>(p, tm, st);
 }
 
 }  // namespace
