@@ -68,7 +68,8 @@ struct Cfg {
   static constexpr int L_EMPTY = L_FULL + NST;  // [slot] its products done      (commit)
   static constexpr int S_FULL = L_EMPTY + NST;  // [stream] scores, and the PV before  (commit)
   static constexpr int O_FULL = S_FULL + 2;     // [stream] the item's last PV   (commit)
-  static constexpr int P_FULL = O_FULL + 2;     // [stream] weights              (4: one per warp)
+  static constexpr int P_HALF = O_FULL + 2;     // [stream] weights of 64 keys   (4: one per warp)
+  static constexpr int P_FULL = P_HALF + 2;     // [stream] of all               (4: one per warp)
   static constexpr int O_EMPTY = P_FULL + 2;    // [stream] O read out           (4: one per warp)
   static constexpr int ML = O_EMPTY + 2;        // B's maxima and sums are there (4: one per warp)
   static constexpr int SEE = ML + 1;            // [unit % NSEE] bits are there  (one per loading warp)
@@ -194,49 +195,51 @@ __device__ __forceinline__ uint32_t v_pack(float lo, float hi) {
 // Scores of 64 keys -> weights 2^(s a + b) in two bf16 parts, per 16 keys the high parts of
 // the pairs in the first eight words, the low parts in the others; the sums take them
 // whole. The high part is the weight cut off, the low part what that leaves, rounded: off by
-// 2^-16 relative at most. Groups of four keys: the exponentials of one (4 cycles each) between
-// the sums and parts of the one before and the scaling of the second next.
+// 2^-16 relative at most. Groups of four keys: the exponentials of one between the sums and
+// parts of the second before (whose exponentials are done by then) and the scaling of the
+// second next.
 __device__ __forceinline__ void weights(uint32_t (&s)[2][32], float a, float b, float (&sum)[4]) {
-  float t[4][4];
+  float t[8][4];
   auto scale = [&](int g) {
     const uint32_t* z = s[g >> 3] + (g & 7) * 4;
-    v_fma2(t[g & 3][0], t[g & 3][1], z[0], z[1], a, b);
-    v_fma2(t[g & 3][2], t[g & 3][3], z[2], z[3], a, b);
+    v_fma2(t[g & 7][0], t[g & 7][1], z[0], z[1], a, b);
+    v_fma2(t[g & 7][2], t[g & 7][3], z[2], z[3], a, b);
   };
   scale(0);
   scale(1);
   uint32_t out[2][32];
 #pragma unroll
-  for (int g = 0; g <= 16; ++g) {
-    float* y = t[g & 3];
-    const float* u = t[(g + 3) & 3];  // group g - 1
-    uint32_t* o = g > 0 ? out[(g - 1) >> 3] + ((g - 1) & 4) * 4 + ((g - 1) & 3) * 2 : nullptr;
+  for (int g = 0; g < 16 + 2; ++g) {
+    float* y = t[g & 7];
+    const int h = g - 2;
+    const float* u = t[h & 7];
+    uint32_t* o = h >= 0 ? out[h >> 3] + (h & 4) * 4 + (h & 3) * 2 : nullptr;
     float n0, n1, n2, n3, r0, r1, r2, r3;
     if (g < 16) v_ex2(y[0]);
-    if (g > 0) {
+    if (h >= 0) {
       v_add2(sum[0], sum[1], sum[0], sum[1], u[0], u[1]);
       n0 = v_minus_upper(u[0]);
       n1 = v_minus_upper(u[1]);
     }
     if (g < 16) v_ex2(y[1]);
-    if (g > 0) {
-      v_add2(r0, r1, u[0], u[1], n0, n1);
-      o[0] = v_upper(u[0], u[1]);
+    if (h >= 0) {
       n2 = v_minus_upper(u[2]);
+      n3 = v_minus_upper(u[3]);
+      v_add2(r0, r1, u[0], u[1], n0, n1);
     }
     if (g < 16) v_ex2(y[2]);
-    if (g > 0) {
+    if (h >= 0) {
       v_add2(sum[2], sum[3], sum[2], sum[3], u[2], u[3]);
-      n3 = v_minus_upper(u[3]);
-      o[8] = v_pack(r0, r1);
+      v_add2(r2, r3, u[2], u[3], n2, n3);
+      o[0] = v_upper(u[0], u[1]);
     }
     if (g < 16) v_ex2(y[3]);
-    if (g > 0) {
-      v_add2(r2, r3, u[2], u[3], n2, n3);
-      o[1] = v_upper(u[2], u[3]);
-    }
     if (g + 2 < 16) scale(g + 2);
-    if (g > 0) o[9] = v_pack(r2, r3);
+    if (h >= 0) {
+      o[1] = v_upper(u[2], u[3]);
+      o[8] = v_pack(r0, r1);
+      o[9] = v_pack(r2, r3);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -289,7 +292,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int i = 0; i < C::N_BAR; ++i) {
       int n = 1;
       if (i == C::Q_FULL || (!TMA && i >= C::L_FULL && i < C::L_EMPTY)) n = NLOAD;
-      if (i >= C::P_FULL && i <= C::ML) n = 4;
+      if (i >= C::P_HALF && i <= C::ML) n = 4;
       if (!TMA && i >= C::SEE) n = NLOAD / 32;
       mbar_init(bar(i), n);
     }
@@ -340,20 +343,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const bool fresh = two ? jv == 0 : jv < 2;  // the stream's first unit of the item
             good = (!first || ready(pos_v(jv, nt))) &&
                    (!fresh || no[x] == 0 || wait_1(bar(C::O_EMPTY + x), (no[x] - 1) & 1, p.err, abort)) &&
-                   wait_1(bar(C::P_FULL + x), np[x] & 1, p.err, abort);
+                   wait_1(bar(C::P_HALF + x), np[x] & 1, p.err, abort);
             if (!good) break;
-            np.inc(x);
             tc_fence_after();
             const int left = w.q.len - (w.t0 + jv) * TK;
             const int ks = left >= TK ? TK / 16 : (left + 15) / 16;
             const uint64_t db = dv0 + (uint64_t)(((nl + pos_v(jv, nt)) % NST * C::TILE) >> 4);
             const uint32_t ta = tmem + C::COL_S + x * TK, to = tmem + C::COL_O + x * D;
+            // (the first half's products run while the other half's weights are formed)
+#pragma unroll 1
+            for (int k0 = 0; k0 < TK / 16; k0 += TK / 32) {
+              if (k0 > 0) {
+                good = wait_1(bar(C::P_FULL + x), np[x] & 1, p.err, abort);
+                if (!good) break;
+                tc_fence_after();
+              }
 #pragma unroll 4
-            for (int kk = 0; kk < ks; ++kk) {
-              const uint64_t dv = db + (uint64_t)((kk * 2 * C::GROUP) >> 4);
-              tc_mma_f16_ts(to, ta + kk * 16, dv, idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
-              tc_mma_f16_ts(to, ta + kk * 16 + 8, dv, idesc_pv, 1u);
+              for (int kk = k0; kk < min(ks, k0 + TK / 32); ++kk) {
+                const uint64_t dv = db + (uint64_t)((kk * 2 * C::GROUP) >> 4);
+                tc_mma_f16_ts(to, ta + kk * 16, dv, idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
+                tc_mma_f16_ts(to, ta + kk * 16 + 8, dv, idesc_pv, 1u);
+              }
             }
+            if (!good) break;
+            np.inc(x);
             if (last) release(pos_v(jv, nt));
             if (two ? jv == nt - 1 : jv + 2 >= nt) {
               tc_commit(bar(C::O_FULL + x));
@@ -678,13 +691,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             weights(s, p.sl2, shift, sum);
             tmem_st32(t_s + i * 32, s[0]);
             tmem_st32(t_s + i * 32 + 32, s[1]);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();  // the warp's stores are done: one arrival for the warp
+            if (lane == 0) mbar_arrive(bar((i == 0 ? C::P_HALF : C::P_FULL) + x));
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_st_wait();
+        } else if (lane == 0) {
+          mbar_arrive(bar(C::P_HALF + x));
+          mbar_arrive(bar(C::P_FULL + x));
         }
-        tc_fence_before();
-        __syncwarp();  // the warp's stores are done: one arrival for the warp
-        if (lane == 0) mbar_arrive(bar(C::P_FULL + x));
+        __syncwarp();
       }
       if (!good) break;
       // ---- the CTA's units of the item are done
