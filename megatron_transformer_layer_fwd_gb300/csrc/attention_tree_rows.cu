@@ -1,0 +1,44 @@
+// Attention of small drafts over a paged cache: items of up to 16 rows (drafted tokens times the
+// query heads of a KV head) for the kernel of the decode step, in bf16 on mma.sync, in float32 on
+// the CUDA cores. Its many small CTAs and warps with rings of their own stream through the
+// caches of many short sequences without waiting for one another, where the 128 rows of a
+// tcgen05 tile would stand empty.
+#include "paged_rows.cuh"
+
+namespace mgb {
+
+namespace {
+
+template <typename T, int D, int NR>
+mgb_status launch(const Params& p, cudaStream_t st) {
+  using C = Cfg<T, D, NR>;
+  auto k = paged_rows_kernel<T, D, NR, true>;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return MGB_ERR_CUDA;
+  return launch_pdl(k, SMS * ctas_per_sm(D), NT, C::SMEM, st, p);
+}
+
+template <typename T, int D>
+mgb_status launch_rows(const Params& p, cudaStream_t st) {
+  if constexpr (sizeof(T) == 4)
+    if (p.rows <= 4) return launch<T, D, 4>(p, st);
+  return p.rows <= 8 ? launch<T, D, 8>(p, st) : launch<T, D, 16>(p, st);
+}
+
+}  // namespace
+
+mgb_status attention_tree_rows(const TreeParams& t, int d, int dtype, cudaStream_t st) {
+  Params p{};
+  p.nkv = t.nkv; p.rows = t.rows; p.G = t.G; p.nq = t.nq;
+  p.thdr = t.hdr; p.tstart = t.start; p.live = t.live; p.mask = t.mask;
+  p.counter = t.counter; p.ml = t.ml; p.part = t.part;
+  p.k = t.k; p.v = t.v; p.table = t.table;
+  p.s_page = t.s_page; p.s_tok = t.s_tok; p.s_head = t.s_head; p.ld_table = t.ld_table;
+  p.n_pages = t.n_pages; p.page_size = t.page_size; p.cap = t.cap;
+  p.q = t.q; p.ld_q = t.ld_q; p.o = t.o; p.ld_o = t.ld_o; p.lse = t.lse;
+  p.sl2 = t.sl2; p.err = t.err;
+  if (dtype == MGB_BF16) return d == 64 ? launch_rows<bf16, 64>(p, st) : launch_rows<bf16, 128>(p, st);
+  return d == 64 ? launch_rows<float, 64>(p, st) : launch_rows<float, 128>(p, st);
+}
+
+}  // namespace mgb

@@ -1,16 +1,18 @@
 // Shared by the kernels for drafted tokens: the plan's workspace, and how the
 // attention's work is cut into ranges.
 //
-// Unit: 128 (UNIT_KEYS) consecutive cached tokens of an item. Item: all units of
-// one (sequence, KV head, block of at most 256 rows), a row being a drafted token and
-// one of the KV head's query heads (row r of a sequence: token r / G, head r % G).
-// Items stand one behind the other on a cost axis, sequence by sequence, head by
-// head, block by block: an item with n units takes n UNIT + ITEM, its unit t
-// beginning at t UNIT (all units of an item of at most WHOLE begin at its start:
-// splitting it would cost more than it evens out). CTA c takes the units that begin in
-// [c chunk, (c + 1) chunk). An item that lies in one CTA's range is finished
-// there; the parts of one that does not (unnormalised sums, maximum, row sum)
-// are joined in CTA order by a second kernel.
+// Unit: consecutive cached tokens of an item. Item: all units of one (sequence, KV head,
+// block of rows), a row being a drafted token and one of the KV head's query heads (row r of a
+// sequence: token r / G, head r % G). Items stand one behind the other on a cost axis,
+// sequence by sequence, head by head, block by block: an item with n units takes n unit
+// costs and a fixed one, its unit t beginning at t unit costs (all units of a short item begin
+// at its start: splitting it would cost more than it evens out). CTA c takes the units that
+// begin in [c chunk, (c + 1) chunk). An item that lies in one CTA's range is finished there;
+// the parts of one that does not (unnormalised sums, maximum, row sum) are joined in CTA order.
+//
+// Two ways to cut (TreeCut): for sequences with few rows on average, items of up to 16 rows
+// for the kernel of the decode step (paged_rows.cuh); else items of up to 256 rows for the
+// tcgen05 kernel and the float32 one.
 #pragma once
 
 #include "common.cuh"
@@ -20,6 +22,7 @@ namespace mgb {
 
 constexpr int TREE_MAX = MGB_TREE_MAX_TOKENS;
 constexpr int TREE_WORDS = TREE_MAX / 32;  // of a token's mask: bit j, the sequence's drafted token j is seen
+// the cut for many rows
 constexpr int TREE_ROWS = 256;             // rows of an item at most
 constexpr int TREE_KEYS = 128;             // keys of a unit
 constexpr int TREE_LONGEST = INT32_MAX - 1024;  // cached tokens (so that keys behind the last one stay below 2^31)
@@ -51,29 +54,20 @@ struct TreeToken {
 };
 
 struct TreeLayout {
-  size_t header, start, seq, live, prefix, token, mask, ml, part, total;
+  size_t header, start, seq, live, prefix, token, mask, counter, ml, part, total;
   int rows;  // of a part
 };
 
-inline TreeLayout tree_layout(int n, int tokens, int nq, int nkv, int d) {
-  TreeLayout l;
-  size_t o = 0;
-  auto take = [&](size_t b) { const size_t at = o; o += (b + 255) & ~(size_t)255; return at; };
-  const size_t live = n < tokens ? n : tokens;
-  const int64_t most = (int64_t)tokens * (nq / nkv);
-  l.rows = most < TREE_ROWS ? (int)((most + 31) / 32 * 32) : TREE_ROWS;
-  l.header = take(sizeof(TreeHeader));
-  l.start = take(sizeof(TreeStart) * (TREE_RANGES + 1));
-  l.seq = take(sizeof(TreeSeq) * (size_t)n);
-  l.live = take(sizeof(TreeSeq) * live);
-  l.prefix = take(8 * (live + 1));
-  l.token = take(sizeof(TreeToken) * (size_t)tokens);
-  l.mask = take(4 * TREE_WORDS * (size_t)tokens);
-  l.ml = take(8 * (size_t)2 * TREE_RANGES * l.rows);
-  l.part = take(4 * (size_t)2 * TREE_RANGES * l.rows * d);
-  l.total = o;
-  return l;
-}
+// How the work is cut, by the sizes that the host knows.
+struct TreeCut {
+  int narrow;
+  int keys, rows;        // of a unit; of an item at most
+  int unit, item;        // costs of a unit and of an item
+  int whole;             // units of an item that is never split
+  int min_chunk, ranges;
+};
+TreeCut tree_cut(int n, int tokens, int nq, int nkv, int d);
+TreeLayout tree_layout(int n, int tokens, int nq, int nkv, int d);
 
 __host__ __device__ inline int tree_units(int len) { return (int)(((int64_t)len + TREE_KEYS - 1) / TREE_KEYS); }
 __host__ __device__ inline int tree_blocks(int m, int G) {
@@ -91,6 +85,7 @@ struct TreeParams {
   const TreeStart* start;
   const TreeSeq* live;
   const uint32_t* mask;
+  uint32_t* counter;  // (few rows: a split item's arrivals)
   float2* ml;   // [2 CTAs][rows] (maximum in log2 units, row sum) of a part
   float* part;  // [2 CTAs][rows][d]
   int rows;
@@ -190,6 +185,7 @@ __device__ __forceinline__ uint32_t tree_window(const uint32_t* mask, int first)
 mgb_status check_tree_plan(const mgb_attention_tree_plan* plan);
 // Joins the parts of split items (bf16 or float32 output).
 mgb_status tree_join(const TreeParams& p, int d, int dtype, int ctas, int mult, cudaStream_t st);
+mgb_status attention_tree_rows(const TreeParams& p, int d, int dtype, cudaStream_t st);
 mgb_status attention_tree_bf16(const TreeParams& p, int d, cudaStream_t st);
 mgb_status attention_tree_f32(const TreeParams& p, int d, cudaStream_t st);
 

@@ -5,14 +5,13 @@
 // bit and its parent's mask, found by doubling: with anc(i) the token 2^r steps
 // up, mask(i) |= mask(anc(i)), anc(i) = anc(anc(i)), at most eight rounds for 256
 // tokens; its depth adds up along the same steps.
-#include "tree.cuh"
+#include "paged_rows.cuh"
 
 namespace mgb {
 
 namespace {
 
-constexpr float LN2 = 0.6931471805599453f;
-constexpr int NT = 256;
+constexpr int PT = 256;  // threads of the prepare kernel
 
 // What a sequence's offsets and length say; `ok`: no offset up to it is bad.
 enum : int { SEQ_LIVE, SEQ_IDLE, SEQ_BAD };
@@ -24,6 +23,7 @@ __device__ __forceinline__ int seq_kind(bool ok, int m, int len) {
 
 struct PlanArgs {
   int n, tokens, G, nkv;
+  TreeCut cut;
   const int32_t *cu, *lens, *parents;
   TreeHeader* hdr;
   TreeStart* start;
@@ -31,7 +31,11 @@ struct PlanArgs {
   int64_t* prefix;
   TreeToken* token;
   uint32_t* mask;
+  uint32_t* counter;
   int* err;
+  __device__ int units(int len) const { return (int)(((int64_t)len + cut.keys - 1) / cut.keys); }
+  __device__ int blocks(int m) const { return (int)(((int64_t)m * G + cut.rows - 1) / cut.rows); }
+  __device__ int64_t cost(int units) const { return (int64_t)units * cut.unit + cut.item; }
 };
 
 __device__ __forceinline__ bool pair_ok(const PlanArgs& a, int s, int c0, int c1) {
@@ -40,7 +44,7 @@ __device__ __forceinline__ bool pair_ok(const PlanArgs& a, int s, int c0, int c1
 
 // The last block: the live sequences in order, their costs summed up, the first
 // unit of every range. The others: block s, what the tokens of sequence s see.
-__global__ void __launch_bounds__(NT) tree_prepare_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(PT) tree_prepare_kernel(const PlanArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();  // the attention kernel may start up; it waits for this one's end
   if ((int)blockIdx.x < a.n) {
@@ -51,7 +55,7 @@ __global__ void __launch_bounds__(NT) tree_prepare_kernel(const PlanArgs a) {
     bool good = pair_ok(a, s, c0, c1);
     if (!good && tid == 0) record_error(a.err, kErrIndex);
     if (c1 != c0)  // (a bad offset before it: the sequence counts as empty)
-      for (int i = tid; i < s; i += NT) good = good && pair_ok(a, i, a.cu[i], a.cu[i + 1]);
+      for (int i = tid; i < s; i += PT) good = good && pair_ok(a, i, a.cu[i], a.cu[i + 1]);
     good = __syncthreads_and(good);
     const int rows = c1 - c0;
     const int kind = good ? seq_kind(true, rows, len) : SEQ_BAD;
@@ -62,11 +66,11 @@ __global__ void __launch_bounds__(NT) tree_prepare_kernel(const PlanArgs a) {
     }
     if (!good) return;
     if (kind != SEQ_LIVE) {
-      for (int i = tid; i < rows; i += NT)
+      for (int i = tid; i < rows; i += PT)
         *reinterpret_cast<int4*>(a.token + c0 + i) = make_int4(-1, 0, 0, 0);
       return;
     }
-    // NT >= TREE_MAX: a thread per token
+    // PT >= TREE_MAX: a thread per token
     const int i = tid;
     if (i < rows) {
       int up = i - 1;
@@ -113,12 +117,12 @@ __global__ void __launch_bounds__(NT) tree_prepare_kernel(const PlanArgs a) {
   }
 
   // ---------------- the ranges
-  __shared__ int64_t warp_cost[NT / 32];
-  __shared__ int warp_live[NT / 32];
+  __shared__ int64_t warp_cost[PT / 32];
+  __shared__ int warp_live[PT / 32];
   int64_t cost = 0;
   int live = 0, rows = 0;
   bool good = true;
-  for (int base = 0; base < a.n; base += NT) {
+  for (int base = 0; base < a.n; base += PT) {
     const int s = base + tid;
     int c0 = 0, c1 = 0, len = 0;
     bool ok = true;
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(NT) tree_prepare_kernel(const PlanArgs a) {
     const bool in = good && s < a.n && s < first_bad;
     const bool is_live = in && seq_kind(true, c1 - c0, len) == SEQ_LIVE;
     const int64_t v =
-        is_live ? tree_cost(tree_units(len)) * tree_blocks(c1 - c0, a.G) * a.nkv : 0;
+        is_live ? a.cost(a.units(len)) * a.blocks(c1 - c0) * a.nkv : 0;
     int64_t x = v;
     int y = is_live;
 #pragma unroll
@@ -150,7 +154,7 @@ __global__ void __launch_bounds__(NT) tree_prepare_kernel(const PlanArgs a) {
     __syncthreads();
     int64_t before = cost, all = cost;
     int ybefore = live, yall = live;
-    for (int w = 0; w < NT / 32; ++w) {
+    for (int w = 0; w < PT / 32; ++w) {
       if (w < warp) before += warp_cost[w], ybefore += warp_live[w];
       all += warp_cost[w];
       yall += warp_live[w];
@@ -163,7 +167,7 @@ __global__ void __launch_bounds__(NT) tree_prepare_kernel(const PlanArgs a) {
     cost = all;
     live = yall;
     if (good) {
-      const int last = min(min(first_bad, a.n), base + NT);  // sequences base .. last - 1 are good
+      const int last = min(min(first_bad, a.n), base + PT);  // sequences base .. last - 1 are good
       if (last > base) rows = a.cu[last];
       good = first_bad == INT32_MAX;
     }
@@ -171,10 +175,12 @@ __global__ void __launch_bounds__(NT) tree_prepare_kernel(const PlanArgs a) {
   }
   if (tid == 0) a.prefix[live] = cost;
   __syncthreads();
-  int64_t chunk = (cost + TREE_RANGES - 1) / TREE_RANGES;
-  if (chunk < TREE_MIN_CHUNK) chunk = TREE_MIN_CHUNK;
+  const int ranges = a.cut.ranges, unit = a.cut.unit;
+  int64_t chunk = (cost + ranges - 1) / ranges;
+  if (chunk < a.cut.min_chunk) chunk = a.cut.min_chunk;
+  for (int c = tid; c < ranges; c += PT) a.counter[c] = 0;
   if (tid == 0) *a.hdr = TreeHeader{cost, chunk, live, rows};
-  for (int c = tid; c <= TREE_RANGES; c += NT) {
+  for (int c = tid; c <= ranges; c += PT) {
     const int64_t u = c * chunk;
     TreeStart st{cost, live, 0, 0, 0};
     if (u < cost) {
@@ -185,14 +191,14 @@ __global__ void __launch_bounds__(NT) tree_prepare_kernel(const PlanArgs a) {
         else hi = mid - 1;
       }
       const TreeSeq q = a.live[lo];
-      const int nt = tree_units(q.len), nb = tree_blocks(q.m, a.G);
-      const int64_t per = tree_cost(nt), r = u - a.prefix[lo];
-      const int64_t item = r / per, into = r - item * per, t = (into + TREE_UNIT - 1) / TREE_UNIT;
+      const int nt = a.units(q.len), nb = a.blocks(q.m);
+      const int64_t per = a.cost(nt), r = u - a.prefix[lo];
+      const int64_t item = r / per, into = r - item * per, t = (into + unit - 1) / unit;
       st.at = a.prefix[lo] + item * per;
       st.i = lo;
       st.h = (int)(item / nb);
       st.b = (int)(item % nb);
-      if (into == 0 || (nt > TREE_WHOLE && t < nt)) {
+      if (into == 0 || (nt > a.cut.whole && t < nt)) {
         st.t = (int)t;
       } else {  // the item's last unit begins before: the next item
         st.at += per;
@@ -310,6 +316,39 @@ mgb_status check_shape(int n, int tokens, int nq, int nkv, int d) {
 
 }  // namespace
 
+// Few rows per sequence: the decode step's kernel, which streams through the caches of many short
+// items at a time but reads a sequence again for every 16 rows.
+constexpr int FEW_ROWS = 16;
+
+TreeCut tree_cut(int n, int tokens, int nq, int nkv, int d) {
+  const int64_t rows = (int64_t)tokens * (nq / nkv);
+  if (rows <= (int64_t)FEW_ROWS * n)
+    return TreeCut{1, unit_tokens(d), MAXR, UNIT, item_cost(d), WHOLE, MIN_CHUNK, SMS * ctas_per_sm(d)};
+  return TreeCut{0, TREE_KEYS, TREE_ROWS, TREE_UNIT, TREE_ITEM, TREE_WHOLE, TREE_MIN_CHUNK, TREE_RANGES};
+}
+
+TreeLayout tree_layout(int n, int tokens, int nq, int nkv, int d) {
+  TreeLayout l;
+  size_t o = 0;
+  auto take = [&](size_t b) { const size_t at = o; o += (b + 255) & ~(size_t)255; return at; };
+  const TreeCut cut = tree_cut(n, tokens, nq, nkv, d);
+  const size_t live = n < tokens ? n : tokens;
+  const int64_t most = (int64_t)tokens * (nq / nkv);
+  l.rows = most < cut.rows ? (int)((most + 7) / 8 * 8) : cut.rows;
+  l.header = take(sizeof(TreeHeader));
+  l.start = take(sizeof(TreeStart) * (cut.ranges + 1));
+  l.seq = take(sizeof(TreeSeq) * (size_t)n);
+  l.live = take(sizeof(TreeSeq) * live);
+  l.prefix = take(8 * (live + 1));
+  l.token = take(sizeof(TreeToken) * (size_t)tokens);
+  l.mask = take(4 * TREE_WORDS * (size_t)tokens);
+  l.counter = take(4 * (size_t)cut.ranges);
+  l.ml = take(8 * (size_t)2 * cut.ranges * l.rows);
+  l.part = take(4 * (size_t)2 * cut.ranges * l.rows * d);
+  l.total = o;
+  return l;
+}
+
 mgb_status tree_join(const TreeParams& p, int d, int dtype, int ctas, int mult, cudaStream_t st) {
   return dtype == MGB_BF16 ? join_t<bf16>(p, d, ctas, mult, st) : join_t<float>(p, d, ctas, mult, st);
 }
@@ -360,6 +399,8 @@ mgb_status mgb_attention_tree_prepare(int32_t n_seqs, int32_t tokens, int32_t n_
     char* b = static_cast<char*>(ws);
     PlanArgs a{};
     a.n = n_seqs; a.tokens = tokens; a.G = n_q_heads / n_kv_heads; a.nkv = n_kv_heads;
+    a.cut = tree_cut(n_seqs, tokens, n_q_heads, n_kv_heads, head_dim);
+    a.counter = reinterpret_cast<uint32_t*>(b + l.counter);
     a.cu = cu_seqlens; a.lens = seq_lens; a.parents = parents;
     a.hdr = reinterpret_cast<TreeHeader*>(b + l.header);
     a.start = reinterpret_cast<TreeStart*>(b + l.start);
@@ -371,7 +412,7 @@ mgb_status mgb_attention_tree_prepare(int32_t n_seqs, int32_t tokens, int32_t n_
     a.err = err;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     LaunchScope scope(PROF_ATTN_TREE, st);
-    tree_prepare_kernel<<<(unsigned)n_seqs + 1, NT, 0, st>>>(a);
+    tree_prepare_kernel<<<(unsigned)n_seqs + 1, PT, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return MGB_ERR_CUDA;
   }
   *plan = mgb_attention_tree_plan{n_seqs, tokens, n_q_heads, n_kv_heads, head_dim, ws, ws_bytes};
@@ -408,6 +449,7 @@ mgb_status mgb_attention_tree(const mgb_attention_tree_plan* plan, const mgb_kv_
   p.mask = reinterpret_cast<const uint32_t*>(b + l.mask);
   p.ml = reinterpret_cast<float2*>(b + l.ml);
   p.part = reinterpret_cast<float*>(b + l.part);
+  p.counter = reinterpret_cast<uint32_t*>(b + l.counter);
   p.rows = l.rows;
   p.k = c->k; p.v = c->v; p.table = c->block_table;
   p.s_page = c->stride_page; p.s_tok = c->stride_token; p.s_head = c->stride_head;
@@ -416,11 +458,13 @@ mgb_status mgb_attention_tree(const mgb_attention_tree_plan* plan, const mgb_kv_
   const int64_t cap = (int64_t)c->max_pages * c->page_size;
   p.cap = cap < TREE_LONGEST ? (int)cap : TREE_LONGEST;
   p.q = q; p.ld_q = ld_q; p.o = o; p.ld_o = ld_o; p.lse = lse;
-  p.sl2 = 1.4426950408889634f / sqrtf((float)d);
+  p.sl2 = LOG2E / sqrtf((float)d);
   p.err = device_error_word();
   if (p.err == nullptr) return MGB_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  LaunchScope scope(PROF_ATTN_TREE, st, 2);
+  const bool narrow = tree_cut(n, plan->tokens, nq, nkv, d).narrow;
+  LaunchScope scope(PROF_ATTN_TREE, st, narrow ? 1 : 2);
+  if (narrow) return attention_tree_rows(p, d, c->dtype, st);
   return c->dtype == MGB_BF16 ? attention_tree_bf16(p, d, st) : attention_tree_f32(p, d, st);
 }
 

@@ -78,10 +78,31 @@ def test_lengths_at_the_borders(dtype, d, page, head_major):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page,head_major", [(16, False), (1, False), (24, True), (100, False), (256, True)])
+@pytest.mark.parametrize("nq,nkv", [(2, 2), (3, 1)])
+def test_few_rows_at_the_borders(dtype, d, page, head_major, nq, nkv):
+    """At most 16 rows per sequence on average (and some with more): the other kernel."""
+    sizes = [2, 1, 3, 1, 4, 8, 5, 1, 3, 20, 1, 6, 1, 5, 2, 7]
+    seqs = _mixed(np.random.default_rng(32), BORDERS, sizes, roots=2)
+    assert sum(sizes) * nq // nkv <= 16 * len(sizes)
+    _run(31, dtype, nq, nkv, d, page, seqs, head_major, tail=3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("seqs", [[(5000, 4)], [(9000, 3), (40, 7), (2100, 1)], [(20000, 1), (7, 1)]])
+def test_few_rows_split_over_ctas(dtype, seqs):
+    rng = np.random.default_rng(33)
+    for d in (64, 128):
+        _run(34, dtype, 4, 1, d, 64, [(x, random_tree(rng, m)) for x, m in seqs])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("nq,nkv", [(1, 1), (3, 3), (7, 1), (16, 2), (17, 1), (40, 2), (71, 1)])
 def test_group_sizes(dtype, nq, nkv):
-    """Rows are tokens times heads of a group: blocks of 256 end inside a token."""
+    """Rows are tokens times heads of a group: blocks of rows end inside a token."""
     _run(12, dtype, nq, nkv, 128, 16, _mixed(np.random.default_rng(3), [70, 0, 300], [9, 40, 2]))
+    _run(12, dtype, nq, nkv, 64, 16, _mixed(np.random.default_rng(3), [70, 0, 300], [1, 2, 1]))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
