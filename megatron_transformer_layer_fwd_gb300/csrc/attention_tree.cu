@@ -30,7 +30,7 @@ CUresult tmap_encode_bf16_nd(CUtensorMap* tm, const void* base, int rank, const 
 namespace {
 
 constexpr int TQ = 128;         // rows per stream (TMEM lanes)
-constexpr int TK = TREE_KEYS;   // keys per slot
+constexpr int TK = CutTc::KEYS;   // keys per slot
 constexpr int NLOAD = 64;       // threads that copy K, V and Q, or with TMA Q
 constexpr int NTHREADS = 384;   // MMA warp, three loading warps, 2 x 4 softmax warps
 constexpr float LN2 = 0.6931471805599453f;
@@ -152,7 +152,7 @@ __device__ __forceinline__ void copy_q(const TreeParams& p, const TreeSeg& w, ui
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int g = first; g * 32 < w.rows; g += step) {
-    const int r = g * 32 + lane, rr = w.b * TREE_ROWS + r, t = rr / p.G;
+    const int r = g * 32 + lane, rr = w.b * CutTc::ROWS + r, t = rr / p.G;
     copy_rows<D>(sQ + (g >> 2) * Cfg<D>::TILE, (g & 3) * 32, static_cast<const bf16*>(p.q),
                  r < w.rows ? (w.q.row + t) * p.ld_q + (int64_t)(w.h * p.G + rr - t * p.G) * D : -1);
   }
@@ -282,11 +282,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   pdl_wait();     // everything the call reads may come from the kernel before
   pdl_trigger();  // the join may start up; it waits for this kernel's end
   const int c = blockIdx.x;
-  const TreeHeader hd = *p.hdr;
-  const TreeStart st = p.start[2 * c];
-  const int64_t chunk = 2 * hd.chunk, end = min((c + 1) * chunk, hd.cost);
-  TreeSegs sg;
-  if (!sg.begin(p, hd, st, end) || st.at + (int64_t)st.t * TREE_UNIT >= end) return;
+  TreeSegs<CutTc> sg;
+  if (!sg.begin(p, c)) return;
 
   if (tid == 0) {
     for (int i = 0; i < C::N_BAR; ++i) {
@@ -581,7 +578,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int row = (two ? x * TQ : 0) + r;  // of the block
       const bool live = row < w.rows;
       const bool work = row - lane < w.rows;   // the warp has a row
-      const int rr = w.b * TREE_ROWS + (live ? row : 0);
+      const int rr = w.b * CutTc::ROWS + (live ? row : 0);
       const int tok = rr / p.G, head = w.h * p.G + rr - tok * p.G;
       const uint32_t* mask = p.mask + (int64_t)(w.q.row + tok) * TREE_WORDS;
       const int ctx = w.q.len - w.q.m;         // tokens before the draft
@@ -734,12 +731,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         m = M;
       }
       if (work) {
-        const bool whole = tree_begin(w.nt - 1, w.nt) + w.at < end && w.at >= c * chunk;
+        const bool whole = sg.whole(w);
         const float inv = whole ? 1.0f / l : 1.0f;  // (no score: 0 / 0)
         fa *= inv;
         fb *= inv;
         bf16* out = static_cast<bf16*>(p.o) + (w.q.row + tok) * p.ld_o + (int64_t)head * D;
-        const int64_t at = (int64_t)tree_part(c, chunk, w.at) * p.rows + row;
+        const int64_t at = (int64_t)tree_part(c, sg.begin_at, w.at) * p.rows + row;
 #pragma unroll 1
         for (int i = 0; i < D / 16; ++i) {
           uint32_t o[16], o2[16];
@@ -817,8 +814,8 @@ mgb_status launch_k(const TreeParams& p, const PoolMaps& tm, cudaStream_t st) {
   auto k = tree_kernel<D, TMA>;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return MGB_ERR_CUDA;
-  const mgb_status s = launch_pdl(k, TREE_RANGES / 2, NTHREADS, C::SMEM, st, tm, p);
-  return s != MGB_OK ? s : tree_join(p, D, MGB_BF16, TREE_RANGES / 2, 2, st);
+  const mgb_status s = launch_pdl(k, CutTc::RANGES, NTHREADS, C::SMEM, st, tm, p);
+  return s != MGB_OK ? s : tree_join<bf16, D, CutTc>(p, st);
 }
 
 template <int D>

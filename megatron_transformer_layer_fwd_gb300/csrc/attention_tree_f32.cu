@@ -28,12 +28,12 @@ struct Cfg {
   static constexpr int OFF_AT = OFF_P + BM * PS;  // [2][BN] int64: places of the tile's tokens
   static constexpr int SMEM = OFF_AT * 4 + 2 * BN * 8;
   static_assert((SMEM + 1024) * 2 <= 228 * 1024, "two blocks per SM");
-  static_assert(OFF_AT % 2 == 0 && TREE_KEYS % BN == 0, "layout");
+  static_assert(OFF_AT % 2 == 0 && BN == CutF32<D>::KEYS && BM == CutF32<D>::ROWS, "layout");
 };
 
-// Rows row0 .. of the segment's block, RPT per thread.
+// The rows of a segment, RPT per thread.
 template <int D, int RPT>
-__device__ __forceinline__ void run_rows(const TreeParams& p, const TreeSeg& w, int row0, bool whole,
+__device__ __forceinline__ void run_rows(const TreeParams& p, const TreeSeg& w, bool whole,
                                          int part, float* sh) {
   using C = Cfg<D>;
   constexpr int RS = C::RS, PS = C::PS, BN = C::BN, BM = 8 * RPT;
@@ -42,9 +42,9 @@ __device__ __forceinline__ void run_rows(const TreeParams& p, const TreeSeg& w, 
   int64_t* sat = reinterpret_cast<int64_t*>(sh + C::OFF_AT);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const uint32_t bq = smem_u32(sq), bk = smem_u32(sk), bv = smem_u32(sv);
-  const int rows = min(BM, w.rows - row0), first = w.b * TREE_ROWS + row0;
+  const int rows = w.rows, first = w.b * CutF32<D>::ROWS;
   const int len = w.q.len, ctx = len - w.q.m;
-  const int k_first = w.t0 * TREE_KEYS, k_end = min(len, w.t1 * TREE_KEYS);
+  const int k_first = w.t0 * BN, k_end = min(len, w.t1 * BN);
   const int nt = (k_end - k_first + BN - 1) / BN;
   const int32_t* table = p.table + (int64_t)w.q.s * p.ld_table;
   // the place of this thread's token (tid < BN) of tile j, or -1
@@ -187,7 +187,7 @@ __device__ __forceinline__ void run_rows(const TreeParams& p, const TreeSeg& w, 
       if (tx == 0 && p.lse != nullptr)
         p.lse[(int64_t)(w.q.row + t) * p.nq + head] = (m[r] + log2f(l[r])) * LN2;
     } else {
-      const int64_t pr = (int64_t)part * p.rows + row0 + row;
+      const int64_t pr = (int64_t)part * p.rows + row;
       out = p.part + pr * D;
       if (tx == 0) p.ml[pr] = make_float2(m[r], l[r]);
     }
@@ -204,20 +204,16 @@ __global__ void __launch_bounds__(NT, 2) tree_f32_kernel(const TreeParams p) {
   extern __shared__ __align__(16) float sh[];
   pdl_wait();     // everything the call reads may come from the kernel before
   pdl_trigger();  // the join may start up; it waits for this kernel's end
-  const int c = blockIdx.x;
-  const TreeHeader hd = *p.hdr;
-  const int64_t end = min((c + 1) * hd.chunk, hd.cost);
-  TreeSegs sg;
-  if (!sg.begin(p, hd, p.start[c], end)) return;
+  TreeSegs<CutF32<D>> sg;
+  if (!sg.begin(p, blockIdx.x)) return;
   TreeSeg w;
   while (sg.next(p, w)) {
-    const bool whole = tree_begin(w.nt - 1, w.nt) + w.at < end && w.at >= c * hd.chunk;
-    const int part = tree_part(c, hd.chunk, w.at);
+    const bool whole = sg.whole(w);
+    const int part = tree_part(blockIdx.x, sg.begin_at, w.at);
     // the smallest form that holds the rows
-    if (w.rows <= 16) run_rows<D, 2>(p, w, 0, whole, part, sh);
-    else if (w.rows <= 32) run_rows<D, 4>(p, w, 0, whole, part, sh);
-    else
-      for (int r = 0; r < w.rows; r += 64) run_rows<D, 8>(p, w, r, whole, part, sh);
+    if (w.rows <= 16) run_rows<D, 2>(p, w, whole, part, sh);
+    else if (w.rows <= 32) run_rows<D, 4>(p, w, whole, part, sh);
+    else run_rows<D, 8>(p, w, whole, part, sh);
   }
   cp_async_wait<0>();
 }
@@ -228,8 +224,8 @@ mgb_status launch_d(const TreeParams& p, cudaStream_t st) {
   auto k = tree_f32_kernel<D>;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return MGB_ERR_CUDA;
-  const mgb_status s = launch_pdl(k, TREE_RANGES, NT, C::SMEM, st, p);
-  return s != MGB_OK ? s : tree_join(p, D, MGB_F32, TREE_RANGES, 1, st);
+  const mgb_status s = launch_pdl(k, CutF32<D>::RANGES, NT, C::SMEM, st, p);
+  return s != MGB_OK ? s : tree_join<float, D, CutF32<D>>(p, st);
 }
 
 }  // namespace

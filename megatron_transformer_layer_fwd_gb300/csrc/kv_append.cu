@@ -425,7 +425,7 @@ mgb_status append(const mgb_kv_append_desc* d, const mgb_kv_cache* c, const mgb_
         tree_layout(plan->n_seqs, plan->tokens, plan->n_q_heads, plan->n_kv_heads, plan->head_dim);
     const char* b = static_cast<const char*>(plan->ws);
     p.token = reinterpret_cast<const TreeToken*>(b + l.token);
-    p.hdr = reinterpret_cast<const TreeHeader*>(b + l.header);
+    p.hdr = reinterpret_cast<const TreeHeader*>(b + l.table[0].header);
   }
   p.err = device_error_word();
   if (p.err == nullptr) return MGB_ERR_CUDA;

@@ -10,9 +10,9 @@
 // begin in [c chunk, (c + 1) chunk). An item that lies in one CTA's range is finished there;
 // the parts of one that does not (unnormalised sums, maximum, row sum) are joined in CTA order.
 //
-// Two ways to cut (TreeCut): for sequences with few rows on average, items of up to 16 rows
-// for the kernel of the decode step (paged_rows.cuh); else items of up to 256 rows for the
-// tcgen05 kernel and the float32 one.
+// Ways to cut (TreeCut): for sequences with few rows on average, items of up to 16 rows for
+// the kernel of the decode step (paged_rows.cuh); else items of up to 256 rows for the tcgen05
+// kernel, and a second table with items of up to 64 rows for the float32 kernel.
 #pragma once
 
 #include "common.cuh"
@@ -22,15 +22,24 @@ namespace mgb {
 
 constexpr int TREE_MAX = MGB_TREE_MAX_TOKENS;
 constexpr int TREE_WORDS = TREE_MAX / 32;  // of a token's mask: bit j, the sequence's drafted token j is seen
-// the cut for many rows
-constexpr int TREE_ROWS = 256;             // rows of an item at most
-constexpr int TREE_KEYS = 128;             // keys of a unit
 constexpr int TREE_LONGEST = INT32_MAX - 1024;  // cached tokens (so that keys behind the last one stay below 2^31)
-constexpr int TREE_RANGES = 304;           // two per SM of a GB300 (the bf16 kernel takes two at a time)
-constexpr int TREE_UNIT = 4;               // cost of a unit
-constexpr int TREE_ITEM = 4;               // fixed cost of an item
-constexpr int TREE_WHOLE = 2;              // units of an item that is never split
-constexpr int TREE_MIN_CHUNK = TREE_UNIT;  // of a range: none between two others is empty
+
+// The cuts for many rows: keys of a unit, rows of an item, units of an item that is never split,
+// its fixed cost, CTAs, and the cost of a unit by the item's rows. A range costs at least one
+// unit, so that none between two others is empty.
+struct CutTc {
+  static constexpr int KEYS = 128, ROWS = 256, WHOLE = 2, ITEM = 4, RANGES = 152;
+  static constexpr int R1 = 128, R2 = 128, C1 = 4, C2 = 4, C3 = 7;  // (2612 and 4550 cycles at head dim 128)
+};
+template <int D>
+struct CutF32 {
+  static constexpr int KEYS = D == 64 ? 64 : 32, ROWS = 64, WHOLE = 2, ITEM = 4, RANGES = 304;
+  static constexpr int R1 = 16, R2 = 32, C1 = 2, C2 = 3, C3 = 5;
+};
+template <typename Cut>
+__host__ __device__ constexpr int unit_cost(int rows) {
+  return rows <= Cut::R1 ? Cut::C1 : rows <= Cut::R2 ? Cut::C2 : Cut::C3;
+}
 
 struct TreeHeader {
   int64_t cost, chunk;  // of all items; of a range
@@ -53,31 +62,24 @@ struct TreeToken {
   int32_t s, slot, pos, pad;
 };
 
-struct TreeLayout {
-  size_t header, start, seq, live, prefix, token, mask, counter, ml, part, total;
+struct TreeTable {
+  size_t header, start, live, prefix;
   int rows;  // of a part
+};
+struct TreeLayout {
+  size_t seq, token, mask, counter, ml, part, total;
+  TreeTable table[2];  // (the second: float32, many rows)
 };
 
 // How the work is cut, by the sizes that the host knows.
 struct TreeCut {
   int narrow;
-  int keys, rows;        // of a unit; of an item at most
-  int unit, item;        // costs of a unit and of an item
-  int whole;             // units of an item that is never split
-  int min_chunk, ranges;
+  int keys, rows;              // of a unit; of an item at most
+  int r1, r2, c1, c2, c3;      // cost of a unit: c1 up to r1 rows, c2 up to r2, c3
+  int item, whole, min_chunk, ranges;
 };
-TreeCut tree_cut(int n, int tokens, int nq, int nkv, int d);
+TreeCut tree_cut(int n, int tokens, int nq, int nkv, int d, int table);
 TreeLayout tree_layout(int n, int tokens, int nq, int nkv, int d);
-
-__host__ __device__ inline int tree_units(int len) { return (int)(((int64_t)len + TREE_KEYS - 1) / TREE_KEYS); }
-__host__ __device__ inline int tree_blocks(int m, int G) {
-  return (int)(((int64_t)m * G + TREE_ROWS - 1) / TREE_ROWS);
-}
-__host__ __device__ inline int64_t tree_cost(int units) { return (int64_t)units * TREE_UNIT + TREE_ITEM; }
-// where unit t of an item with n units begins on its part of the cost axis
-__host__ __device__ inline int64_t tree_begin(int t, int n) {
-  return n > TREE_WHOLE ? (int64_t)t * TREE_UNIT : 0;
-}
 
 struct TreeParams {
   int nq, nkv, G;
@@ -103,6 +105,16 @@ struct TreeParams {
   int* err;
 };
 
+template <typename Cut>
+__host__ __device__ inline int tree_units(int len) {
+  return (int)(((int64_t)len + Cut::KEYS - 1) / Cut::KEYS);
+}
+// where unit t of an item with n units begins on its part of the cost axis
+template <typename Cut>
+__host__ __device__ inline int64_t tree_begin(int t, int n, int rows) {
+  return n > Cut::WHOLE ? (int64_t)t * unit_cost<Cut>(rows) : 0;
+}
+
 // The units of one item that a CTA takes.
 struct TreeSeg {
   TreeSeq q;      // the sequence
@@ -114,8 +126,9 @@ struct TreeSeg {
 
 // A CTA's segments in order, the same for every role. The next sequence is
 // requested one sequence ahead.
+template <typename Cut>
 struct TreeSegs {
-  int64_t at, end;
+  int64_t at, begin_at, end;
   int i, h, b, t, n;
   TreeSeq cur, nxt;
   __device__ void fetch(const TreeParams& p) {
@@ -124,11 +137,14 @@ struct TreeSegs {
       nxt = TreeSeq{x.x, x.y, x.z, x.w};
     }
   }
-  // the units from st on that begin before range_end; false: none
-  __device__ bool begin(const TreeParams& p, const TreeHeader& hd, const TreeStart& st, int64_t range_end) {
+  // CTA c's units; false: none
+  __device__ bool begin(const TreeParams& p, int c) {
+    const TreeHeader hd = *p.hdr;
+    const TreeStart st = p.start[c];
     at = st.at; i = st.i; h = st.h; b = st.b; t = st.t;
     n = hd.live;
-    end = range_end;
+    begin_at = c * hd.chunk;
+    end = min(begin_at + hd.chunk, hd.cost);
     if (i >= n) return false;
     const int4 x = *reinterpret_cast<const int4*>(p.live + i);
     cur = TreeSeq{x.x, x.y, x.z, x.w};
@@ -139,18 +155,18 @@ struct TreeSegs {
   __device__ bool next(const TreeParams& p, TreeSeg& w) {
     for (;;) {
       if (i >= n) return false;
-      const int nt = tree_units(cur.len);
-      if (at + tree_begin(t, nt) >= end) return false;
-      const int nb = tree_blocks(cur.m, p.G);
+      const int nt = tree_units<Cut>(cur.len), left_rows = cur.m * p.G - b * Cut::ROWS;
+      const int rows = min(Cut::ROWS, left_rows), unit = unit_cost<Cut>(rows);
+      if (at + tree_begin<Cut>(t, nt, rows) >= end) return false;
       w.q = cur;
-      w.h = h; w.b = b; w.at = at; w.nt = nt; w.t0 = t;
-      w.rows = min(TREE_ROWS, cur.m * p.G - b * TREE_ROWS);
-      const int64_t left = (end - at + TREE_UNIT - 1) / TREE_UNIT;
-      w.t1 = nt > TREE_WHOLE && left < nt ? (int)left : nt;
+      w.h = h; w.b = b; w.at = at; w.nt = nt; w.t0 = t; w.rows = rows;
+      const int64_t left = (end - at + unit - 1) / unit;
+      w.t1 = nt > Cut::WHOLE && left < nt ? (int)left : nt;
       const bool skip = cur.len > p.cap;
       t = 0;
-      at += tree_cost(nt);
-      if (++b == nb) {
+      at += (int64_t)nt * unit + Cut::ITEM;
+      ++b;
+      if (left_rows <= Cut::ROWS) {
         b = 0;
         if (++h == p.nkv) {
           h = 0;
@@ -163,12 +179,16 @@ struct TreeSegs {
       if (threadIdx.x % 32 == 0) record_error(p.err, kErrIndex);
     }
   }
+  // whether all units of a segment's item are this CTA's
+  __device__ bool whole(const TreeSeg& w) const {
+    return w.at >= begin_at && w.at + tree_begin<Cut>(w.nt - 1, w.nt, w.rows) < end;
+  }
 };
 
-// The part of the workspace with CTA cc's share of the item at `at`: 2 cc when the
-// CTA's range begins at or inside the item, 2 cc + 1 when before it.
-__device__ __forceinline__ int tree_part(int cc, int64_t chunk, int64_t at) {
-  return 2 * cc + (cc * chunk < at ? 1 : 0);
+// The part of the workspace with the share of the item at `at` of CTA cc, whose range begins at
+// `begin`: 2 cc when that is at or inside the item, 2 cc + 1 when before it.
+__device__ __forceinline__ int tree_part(int cc, int64_t begin, int64_t at) {
+  return 2 * cc + (begin < at ? 1 : 0);
 }
 
 // The 32 mask bits of drafted tokens first .. first + 31 (those before 0 are cached
@@ -183,8 +203,9 @@ __device__ __forceinline__ uint32_t tree_window(const uint32_t* mask, int first)
 }
 
 mgb_status check_tree_plan(const mgb_attention_tree_plan* plan);
-// Joins the parts of split items (bf16 or float32 output).
-mgb_status tree_join(const TreeParams& p, int d, int dtype, int ctas, int mult, cudaStream_t st);
+// Joins the parts of split items (in tree_plan.cu, for the cuts above).
+template <typename T, int D, typename Cut>
+mgb_status tree_join(const TreeParams& p, cudaStream_t st);
 mgb_status attention_tree_rows(const TreeParams& p, int d, int dtype, cudaStream_t st);
 mgb_status attention_tree_bf16(const TreeParams& p, int d, cudaStream_t st);
 mgb_status attention_tree_f32(const TreeParams& p, int d, cudaStream_t st);

@@ -22,29 +22,46 @@ __device__ __forceinline__ int seq_kind(bool ok, int m, int len) {
 }
 
 struct PlanArgs {
-  int n, tokens, G, nkv;
-  TreeCut cut;
+  int n, tokens, G, nkv, tables;
   const int32_t *cu, *lens, *parents;
-  TreeHeader* hdr;
-  TreeStart* start;
-  TreeSeq *seq, *live;
-  int64_t* prefix;
+  TreeSeq* seq;
   TreeToken* token;
   uint32_t* mask;
   uint32_t* counter;
   int* err;
-  __device__ int units(int len) const { return (int)(((int64_t)len + cut.keys - 1) / cut.keys); }
-  __device__ int blocks(int m) const { return (int)(((int64_t)m * G + cut.rows - 1) / cut.rows); }
-  __device__ int64_t cost(int units) const { return (int64_t)units * cut.unit + cut.item; }
+  // per table
+  TreeCut cut[2];
+  TreeHeader* hdr[2];
+  TreeStart* start[2];
+  TreeSeq* live[2];
+  int64_t* prefix[2];
+};
+
+__device__ __forceinline__ int unit_of(const TreeCut& c, int rows) {
+  return rows <= c.r1 ? c.c1 : rows <= c.r2 ? c.c2 : c.c3;
+}
+// A sequence's items for one KV head: blocks of cut.rows rows, the last one smaller.
+struct SeqCost {
+  int units, blocks, unit_full, unit_last;
+  int64_t full, last;  // cost of an item of either kind
+  __device__ SeqCost(const TreeCut& c, int len, int64_t rows) {
+    units = (int)(((int64_t)len + c.keys - 1) / c.keys);
+    blocks = (int)((rows + c.rows - 1) / c.rows);
+    unit_full = unit_of(c, c.rows);
+    unit_last = unit_of(c, (int)(rows - (int64_t)(blocks - 1) * c.rows));
+    full = (int64_t)units * unit_full + c.item;
+    last = (int64_t)units * unit_last + c.item;
+  }
+  __device__ int64_t head() const { return (blocks - 1) * full + last; }
 };
 
 __device__ __forceinline__ bool pair_ok(const PlanArgs& a, int s, int c0, int c1) {
   return c0 >= 0 && c1 >= c0 && c1 <= a.tokens && (s > 0 || c0 == 0);
 }
 
-// The last block: the live sequences in order, their costs summed up, the first
-// unit of every range. The others: block s, what the tokens of sequence s see.
-__global__ void __launch_bounds__(PT) tree_prepare_kernel(const PlanArgs a) {
+// The blocks behind the sequences' (one per table): the live sequences in order, their costs
+// summed up, the first unit of every range. Block s: what the tokens of sequence s see.
+__global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant__ PlanArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();  // the attention kernel may start up; it waits for this one's end
   if ((int)blockIdx.x < a.n) {
@@ -116,7 +133,11 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const PlanArgs a) {
     return;
   }
 
-  // ---------------- the ranges
+  // ---------------- a table's ranges
+  const int tab = blockIdx.x - a.n;
+  const TreeCut cut = a.cut[tab];
+  TreeSeq* const live_out = a.live[tab];
+  int64_t* const prefix = a.prefix[tab];
   __shared__ int64_t warp_cost[PT / 32];
   __shared__ int warp_live[PT / 32];
   int64_t cost = 0;
@@ -141,7 +162,7 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const PlanArgs a) {
     const bool in = good && s < a.n && s < first_bad;
     const bool is_live = in && seq_kind(true, c1 - c0, len) == SEQ_LIVE;
     const int64_t v =
-        is_live ? a.cost(a.units(len)) * a.blocks(c1 - c0) * a.nkv : 0;
+        is_live ? SeqCost(cut, len, (int64_t)(c1 - c0) * a.G).head() * a.nkv : 0;
     int64_t x = v;
     int y = is_live;
 #pragma unroll
@@ -161,8 +182,8 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const PlanArgs a) {
     }
     if (is_live) {
       const int at = ybefore + y - 1;
-      *reinterpret_cast<int4*>(a.live + at) = make_int4(c0, c1 - c0, len, s);
-      a.prefix[at] = before + x - v;
+      *reinterpret_cast<int4*>(live_out + at) = make_int4(c0, c1 - c0, len, s);
+      prefix[at] = before + x - v;
     }
     cost = all;
     live = yall;
@@ -173,36 +194,39 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const PlanArgs a) {
     }
     __syncthreads();
   }
-  if (tid == 0) a.prefix[live] = cost;
+  if (tid == 0) prefix[live] = cost;
   __syncthreads();
-  const int ranges = a.cut.ranges, unit = a.cut.unit;
-  int64_t chunk = (cost + ranges - 1) / ranges;
-  if (chunk < a.cut.min_chunk) chunk = a.cut.min_chunk;
-  for (int c = tid; c < ranges; c += PT) a.counter[c] = 0;
-  if (tid == 0) *a.hdr = TreeHeader{cost, chunk, live, rows};
-  for (int c = tid; c <= ranges; c += PT) {
+  int64_t chunk = (cost + cut.ranges - 1) / cut.ranges;
+  if (chunk < cut.min_chunk) chunk = cut.min_chunk;
+  if (tid == 0) *a.hdr[tab] = TreeHeader{cost, chunk, live, rows};
+  for (int c = tid; c <= cut.ranges; c += PT) {
+    if (tab == 0 && c < cut.ranges) a.counter[c] = 0;
     const int64_t u = c * chunk;
     TreeStart st{cost, live, 0, 0, 0};
     if (u < cost) {
       int lo = 0, hi = live - 1;  // the largest i with prefix[i] <= u
       while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (a.prefix[mid] <= u) lo = mid;
+        if (prefix[mid] <= u) lo = mid;
         else hi = mid - 1;
       }
-      const TreeSeq q = a.live[lo];
-      const int nt = a.units(q.len), nb = a.blocks(q.m);
-      const int64_t per = a.cost(nt), r = u - a.prefix[lo];
-      const int64_t item = r / per, into = r - item * per, t = (into + unit - 1) / unit;
-      st.at = a.prefix[lo] + item * per;
+      const TreeSeq q = live_out[lo];
+      const SeqCost k(cut, q.len, (int64_t)q.m * a.G);
+      int64_t r = u - prefix[lo];
+      st.h = (int)(r / k.head());
+      r -= st.h * k.head();
+      st.b = (int)min(r / k.full, (int64_t)k.blocks - 1);
+      const int64_t into = r - st.b * k.full;
+      const bool last = st.b == k.blocks - 1;
+      const int unit = last ? k.unit_last : k.unit_full;
+      const int64_t t = (into + unit - 1) / unit;
+      st.at = u - into;
       st.i = lo;
-      st.h = (int)(item / nb);
-      st.b = (int)(item % nb);
-      if (into == 0 || (nt > a.cut.whole && t < nt)) {
+      if (into == 0 || (k.units > cut.whole && t < k.units)) {
         st.t = (int)t;
       } else {  // the item's last unit begins before: the next item
-        st.at += per;
-        if (++st.b == nb) {
+        st.at += last ? k.last : k.full;
+        if (++st.b == k.blocks) {
           st.b = 0;
           if (++st.h == a.nkv) {
             st.h = 0;
@@ -211,7 +235,7 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const PlanArgs a) {
         }
       }
     }
-    a.start[c] = st;
+    a.start[tab][c] = st;
   }
 }
 
@@ -221,8 +245,8 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const PlanArgs a) {
 // then the weighted sum of their rows, four parts' loads under way at a time.
 constexpr int JOIN_ROWS = 8;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * JOIN_ROWS) tree_join_kernel(const TreeParams p, int mult) {
+template <typename T, int D, typename Cut>
+__global__ void __launch_bounds__(32 * JOIN_ROWS) tree_join_kernel(const TreeParams p) {
   constexpr int CPL = D / 32;
   pdl_wait();
   const int groups = (p.rows + JOIN_ROWS - 1) / JOIN_ROWS;
@@ -230,18 +254,19 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) tree_join_kernel(const TreePar
   const int r = (blockIdx.x - c * groups) * JOIN_ROWS + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const TreeHeader hd = *p.hdr;
-  const TreeStart st = p.start[(c + 1) * mult];
-  const int64_t chunk = hd.chunk * mult;
+  const TreeStart st = p.start[c + 1];
+  const int64_t chunk = hd.chunk;
   if (st.i >= hd.live || st.t == 0 || st.at / chunk != c) return;
   const TreeSeq q = p.live[st.i];
-  if (q.len > p.cap || r >= q.m * p.G - st.b * TREE_ROWS) return;
-  const int nt = tree_units(q.len);
-  const int cl = (int)((st.at + tree_begin(nt - 1, nt)) / chunk);
+  const int rows = min(Cut::ROWS, q.m * p.G - st.b * Cut::ROWS);
+  if (q.len > p.cap || r >= rows) return;
+  const int nt = tree_units<Cut>(q.len);
+  const int cl = (int)((st.at + tree_begin<Cut>(nt - 1, nt, rows)) / chunk);
   float M = -INFINITY, L = 0.0f, x[CPL] = {};
   for (int c0 = c; c0 <= cl; c0 += 32) {
     const int n = min(32, cl - c0 + 1);
     float2 y = make_float2(-INFINITY, 0.0f);  // of part c0 + lane
-    if (lane < n) y = __ldcg(&p.ml[(int64_t)tree_part(c0 + lane, chunk, st.at) * p.rows + r]);
+    if (lane < n) y = __ldcg(&p.ml[(int64_t)tree_part(c0 + lane, (c0 + lane) * chunk, st.at) * p.rows + r]);
     float mn = y.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
@@ -264,7 +289,7 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) tree_join_kernel(const TreePar
         for (int j = 0; j < CPL; ++j) z[i][j] = 0.0f;
         if (i0 + i < n) {
           const float* y0 =
-              p.part + ((int64_t)tree_part(c0 + i0 + i, chunk, st.at) * p.rows + r) * D + lane * CPL;
+              p.part + ((int64_t)tree_part(c0 + i0 + i, (c0 + i0 + i) * chunk, st.at) * p.rows + r) * D + lane * CPL;
           if constexpr (CPL == 4) {
             const float4 v = __ldcg(reinterpret_cast<const float4*>(y0));
             z[i][0] = v.x; z[i][1] = v.y; z[i][2] = v.z; z[i][3] = v.w;
@@ -284,7 +309,7 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) tree_join_kernel(const TreePar
     }
   }
   const float inv = 1.0f / L;
-  const int rr = st.b * TREE_ROWS + r, tok = rr / p.G, head = st.h * p.G + rr - tok * p.G;
+  const int rr = st.b * Cut::ROWS + r, tok = rr / p.G, head = st.h * p.G + rr - tok * p.G;
   T* o = static_cast<T*>(p.o) + (q.row + tok) * p.ld_o + (int64_t)head * D + lane * CPL;
   if constexpr (sizeof(T) == 4) {
     if constexpr (CPL == 4)
@@ -302,13 +327,6 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) tree_join_kernel(const TreePar
     p.lse[(int64_t)(q.row + tok) * p.nq + head] = (M + log2f(L)) * LN2;
 }
 
-template <typename T>
-mgb_status join_t(const TreeParams& p, int d, int ctas, int mult, cudaStream_t st) {
-  const int groups = (p.rows + JOIN_ROWS - 1) / JOIN_ROWS;
-  return launch_pdl(d == 64 ? tree_join_kernel<T, 64> : tree_join_kernel<T, 128>, ctas * groups,
-                    dim3(32 * JOIN_ROWS), 0, st, p, mult);
-}
-
 mgb_status check_shape(int n, int tokens, int nq, int nkv, int d) {
   if (n < 0 || tokens < 0 || nq < 1 || nkv < 1 || nq % nkv || nq > (1 << 20)) return MGB_ERR_INVALID_ARG;
   return d == 64 || d == 128 ? MGB_OK : MGB_ERR_UNSUPPORTED;
@@ -320,38 +338,61 @@ mgb_status check_shape(int n, int tokens, int nq, int nkv, int d) {
 // items at a time but reads a sequence again for every 16 rows.
 constexpr int FEW_ROWS = 16;
 
-TreeCut tree_cut(int n, int tokens, int nq, int nkv, int d) {
+template <typename Cut>
+TreeCut cut_of() {
+  return TreeCut{0, Cut::KEYS, Cut::ROWS, Cut::R1, Cut::R2, Cut::C1, Cut::C2, Cut::C3, Cut::ITEM, Cut::WHOLE,
+                 Cut::C3, Cut::RANGES};
+}
+
+TreeCut tree_cut(int n, int tokens, int nq, int nkv, int d, int table) {
   const int64_t rows = (int64_t)tokens * (nq / nkv);
   if (rows <= (int64_t)FEW_ROWS * n)
-    return TreeCut{1, unit_tokens(d), MAXR, UNIT, item_cost(d), WHOLE, MIN_CHUNK, SMS * ctas_per_sm(d)};
-  return TreeCut{0, TREE_KEYS, TREE_ROWS, TREE_UNIT, TREE_ITEM, TREE_WHOLE, TREE_MIN_CHUNK, TREE_RANGES};
+    return TreeCut{1, unit_tokens(d), MAXR, MAXR, MAXR, UNIT, UNIT, UNIT, item_cost(d), WHOLE, MIN_CHUNK,
+                   SMS * ctas_per_sm(d)};
+  if (table == 0) return cut_of<CutTc>();
+  return d == 64 ? cut_of<CutF32<64>>() : cut_of<CutF32<128>>();
 }
 
 TreeLayout tree_layout(int n, int tokens, int nq, int nkv, int d) {
   TreeLayout l;
   size_t o = 0;
   auto take = [&](size_t b) { const size_t at = o; o += (b + 255) & ~(size_t)255; return at; };
-  const TreeCut cut = tree_cut(n, tokens, nq, nkv, d);
   const size_t live = n < tokens ? n : tokens;
   const int64_t most = (int64_t)tokens * (nq / nkv);
-  l.rows = most < cut.rows ? (int)((most + 7) / 8 * 8) : cut.rows;
-  l.header = take(sizeof(TreeHeader));
-  l.start = take(sizeof(TreeStart) * (cut.ranges + 1));
+  size_t parts = 0;
+  for (int i = 0; i < 2; ++i) {
+    const TreeCut cut = tree_cut(n, tokens, nq, nkv, d, i);
+    if (i == 1 && cut.narrow) {
+      l.table[1] = l.table[0];
+      continue;
+    }
+    TreeTable& t = l.table[i];
+    t.header = take(sizeof(TreeHeader));
+    t.start = take(sizeof(TreeStart) * (cut.ranges + 1));
+    t.live = take(sizeof(TreeSeq) * live);
+    t.prefix = take(8 * (live + 1));
+    t.rows = most < cut.rows ? (int)((most + 7) / 8 * 8) : cut.rows;
+    if ((size_t)2 * cut.ranges * t.rows > parts) parts = (size_t)2 * cut.ranges * t.rows;
+    if (i == 0) l.counter = take(4 * (size_t)cut.ranges);
+  }
   l.seq = take(sizeof(TreeSeq) * (size_t)n);
-  l.live = take(sizeof(TreeSeq) * live);
-  l.prefix = take(8 * (live + 1));
   l.token = take(sizeof(TreeToken) * (size_t)tokens);
   l.mask = take(4 * TREE_WORDS * (size_t)tokens);
-  l.counter = take(4 * (size_t)cut.ranges);
-  l.ml = take(8 * (size_t)2 * cut.ranges * l.rows);
-  l.part = take(4 * (size_t)2 * cut.ranges * l.rows * d);
+  l.ml = take(8 * parts);
+  l.part = take(4 * parts * d);
   l.total = o;
   return l;
 }
 
-mgb_status tree_join(const TreeParams& p, int d, int dtype, int ctas, int mult, cudaStream_t st) {
-  return dtype == MGB_BF16 ? join_t<bf16>(p, d, ctas, mult, st) : join_t<float>(p, d, ctas, mult, st);
+template <typename T, int D, typename Cut>
+mgb_status tree_join(const TreeParams& p, cudaStream_t st) {
+  const int groups = (p.rows + JOIN_ROWS - 1) / JOIN_ROWS;
+  return launch_pdl(tree_join_kernel<T, D, Cut>, Cut::RANGES * groups, dim3(32 * JOIN_ROWS), 0, st, p);
 }
+template mgb_status tree_join<bf16, 64, CutTc>(const TreeParams&, cudaStream_t);
+template mgb_status tree_join<bf16, 128, CutTc>(const TreeParams&, cudaStream_t);
+template mgb_status tree_join<float, 64, CutF32<64>>(const TreeParams&, cudaStream_t);
+template mgb_status tree_join<float, 128, CutF32<128>>(const TreeParams&, cudaStream_t);
 
 mgb_status check_tree_plan(const mgb_attention_tree_plan* plan) {
   if (plan == nullptr || plan->ws == nullptr) return MGB_ERR_INVALID_ARG;
@@ -399,20 +440,23 @@ mgb_status mgb_attention_tree_prepare(int32_t n_seqs, int32_t tokens, int32_t n_
     char* b = static_cast<char*>(ws);
     PlanArgs a{};
     a.n = n_seqs; a.tokens = tokens; a.G = n_q_heads / n_kv_heads; a.nkv = n_kv_heads;
-    a.cut = tree_cut(n_seqs, tokens, n_q_heads, n_kv_heads, head_dim);
-    a.counter = reinterpret_cast<uint32_t*>(b + l.counter);
     a.cu = cu_seqlens; a.lens = seq_lens; a.parents = parents;
-    a.hdr = reinterpret_cast<TreeHeader*>(b + l.header);
-    a.start = reinterpret_cast<TreeStart*>(b + l.start);
     a.seq = reinterpret_cast<TreeSeq*>(b + l.seq);
-    a.live = reinterpret_cast<TreeSeq*>(b + l.live);
-    a.prefix = reinterpret_cast<int64_t*>(b + l.prefix);
     a.token = reinterpret_cast<TreeToken*>(b + l.token);
     a.mask = reinterpret_cast<uint32_t*>(b + l.mask);
+    a.counter = reinterpret_cast<uint32_t*>(b + l.counter);
+    for (int i = 0; i < 2; ++i) {
+      a.cut[i] = tree_cut(n_seqs, tokens, n_q_heads, n_kv_heads, head_dim, i);
+      a.hdr[i] = reinterpret_cast<TreeHeader*>(b + l.table[i].header);
+      a.start[i] = reinterpret_cast<TreeStart*>(b + l.table[i].start);
+      a.live[i] = reinterpret_cast<TreeSeq*>(b + l.table[i].live);
+      a.prefix[i] = reinterpret_cast<int64_t*>(b + l.table[i].prefix);
+    }
+    a.tables = a.cut[0].narrow ? 1 : 2;
     a.err = err;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     LaunchScope scope(PROF_ATTN_TREE, st);
-    tree_prepare_kernel<<<(unsigned)n_seqs + 1, PT, 0, st>>>(a);
+    tree_prepare_kernel<<<(unsigned)n_seqs + a.tables, PT, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return MGB_ERR_CUDA;
   }
   *plan = mgb_attention_tree_plan{n_seqs, tokens, n_q_heads, n_kv_heads, head_dim, ws, ws_bytes};
@@ -443,14 +487,16 @@ mgb_status mgb_attention_tree(const mgb_attention_tree_plan* plan, const mgb_kv_
   char* b = static_cast<char*>(plan->ws);
   TreeParams p{};
   p.nq = nq; p.nkv = nkv; p.G = nq / nkv;
-  p.hdr = reinterpret_cast<const TreeHeader*>(b + l.header);
-  p.start = reinterpret_cast<const TreeStart*>(b + l.start);
-  p.live = reinterpret_cast<const TreeSeq*>(b + l.live);
+  const bool narrow = tree_cut(n, plan->tokens, nq, nkv, d, 0).narrow;
+  const TreeTable& t = l.table[c->dtype == MGB_F32 ? 1 : 0];
+  p.hdr = reinterpret_cast<const TreeHeader*>(b + t.header);
+  p.start = reinterpret_cast<const TreeStart*>(b + t.start);
+  p.live = reinterpret_cast<const TreeSeq*>(b + t.live);
   p.mask = reinterpret_cast<const uint32_t*>(b + l.mask);
   p.ml = reinterpret_cast<float2*>(b + l.ml);
   p.part = reinterpret_cast<float*>(b + l.part);
   p.counter = reinterpret_cast<uint32_t*>(b + l.counter);
-  p.rows = l.rows;
+  p.rows = t.rows;
   p.k = c->k; p.v = c->v; p.table = c->block_table;
   p.s_page = c->stride_page; p.s_tok = c->stride_token; p.s_head = c->stride_head;
   p.ld_table = c->ld_table;
@@ -462,7 +508,6 @@ mgb_status mgb_attention_tree(const mgb_attention_tree_plan* plan, const mgb_kv_
   p.err = device_error_word();
   if (p.err == nullptr) return MGB_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool narrow = tree_cut(n, plan->tokens, nq, nkv, d).narrow;
   LaunchScope scope(PROF_ATTN_TREE, st, narrow ? 1 : 2);
   if (narrow) return attention_tree_rows(p, d, c->dtype, st);
   return c->dtype == MGB_BF16 ? attention_tree_bf16(p, d, st) : attention_tree_f32(p, d, st);
