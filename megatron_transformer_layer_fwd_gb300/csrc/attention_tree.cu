@@ -48,7 +48,7 @@ struct Cfg {
   // bytes in the 128-byte swizzle; so a TMA box of whole rows is a run of groups.
   static constexpr int GROUP = KB * 1024;
   static constexpr int TILE = 16 * GROUP;
-  static constexpr int OFF_Q = 0;                       // [half of the rows]
+  static constexpr int OFF_Q = 0;                       // [tile] 128 rows: an item's halves, or items in turn
   static constexpr int OFF_R = 2 * TILE;                // [slot]
   static constexpr int OFF_SEE = OFF_R + NST * TILE;    // [NSEE][4]: a bit per key that may be seen
   static constexpr int NSEE = 16;
@@ -62,9 +62,9 @@ struct Cfg {
   static_assert(SMEM <= 232448, "shared memory budget");
   // Barriers (8 bytes each). A waiter sees every phase of a barrier, or knows that its
   // phase is complete (parity).
-  static constexpr int Q_FULL = 0;              // the item's queries copied     (NLOAD threads)
-  static constexpr int Q_EMPTY = 1;             // the item's last S done        (commit)
-  static constexpr int L_FULL = 2;              // [slot] copied                 (tx, or NLOAD threads)
+  static constexpr int Q_FULL = 0;              // [tile] 128 rows of queries copied  (NLOAD threads)
+  static constexpr int Q_EMPTY = 2;             // [tile] the item's last S done (commit)
+  static constexpr int L_FULL = 4;              // [slot] copied                 (tx, or NLOAD threads)
   static constexpr int L_EMPTY = L_FULL + NST;  // [slot] its products done      (commit)
   static constexpr int S_FULL = L_EMPTY + NST;  // [stream] scores, and the PV before  (commit)
   static constexpr int O_FULL = S_FULL + 2;     // [stream] the item's last PV   (commit)
@@ -146,16 +146,25 @@ __device__ __noinline__ void copy_rows(uint32_t dst, int row0, const bf16* base,
   }
 }
 
-// Queries of the item's rows, groups first, first + step, .. of 32 of them.
+// A loading warp's groups of 32 of the item's queries, into the next one or two tiles (nq so far).
 template <int D>
-__device__ __forceinline__ void copy_q(const TreeParams& p, const TreeSeg& w, uint32_t sQ, int first, int step) {
+__device__ __forceinline__ bool copy_q(const TreeParams& p, const TreeSeg& w, uint32_t sb, int first, int& nq,
+                                       volatile int* abort) {
+  using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int g = first; g * 32 < w.rows; g += step) {
-    const int r = g * 32 + lane, rr = w.b * CutTc::ROWS + r, t = rr / p.G;
-    copy_rows<D>(sQ + (g >> 2) * Cfg<D>::TILE, (g & 3) * 32, static_cast<const bf16*>(p.q),
-                 r < w.rows ? (w.q.row + t) * p.ld_q + (int64_t)(w.h * p.G + rr - t * p.G) * D : -1);
+  for (int x = 0; x * TQ < w.rows; ++x, ++nq) {
+    const int tile = nq & 1;
+    if (nq >= 2 && !wait_w(sb + C::OFF_BAR + 8 * (C::Q_EMPTY + tile), ((nq >> 1) - 1) & 1, p.err, abort)) return false;
+#pragma unroll 1
+    for (int g = 4 * x + first; g < 4 * x + 4 && g * 32 < w.rows; g += 2) {
+      const int r = g * 32 + lane, rr = w.b * CutTc::ROWS + r, t = rr / p.G;
+      copy_rows<D>(sb + C::OFF_Q + tile * C::TILE, (g & 3) * 32, static_cast<const bf16*>(p.q),
+                   r < w.rows ? (w.q.row + t) * p.ld_q + (int64_t)(w.h * p.G + rr - t * p.G) * D : -1);
+    }
+    cp_async_arrive(sb + C::OFF_BAR + 8 * (C::Q_FULL + tile));
   }
+  return true;
 }
 
 // The steps of the weights in an order that the compiler keeps (volatile).
@@ -288,7 +297,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < C::N_BAR; ++i) {
       int n = 1;
-      if (i == C::Q_FULL || (!TMA && i >= C::L_FULL && i < C::L_EMPTY)) n = NLOAD;
+      if (i < C::Q_EMPTY || (!TMA && i >= C::L_FULL && i < C::L_EMPTY)) n = NLOAD;
       if (i >= C::P_HALF && i <= C::ML) n = 4;
       if (!TMA && i >= C::SEE) n = NLOAD / 32;
       mbar_init(bar(i), n);
@@ -315,7 +324,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       PerStream np{0, 0};    // weights of each stream so far
       PerStream no{0, 0};    // items of each stream so far
       bool good = true;
-      for (int k = 0; good && sg.next(p, w); ++k) {
+      int nq = 0;            // query tiles of the items before
+      while (good && sg.next(p, w)) {
         const int nt = w.t1 - w.t0;
         const bool two = w.rows > TQ;
         auto ready = [&](int pos) {
@@ -326,7 +336,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           return true;
         };
         auto release = [&](int pos) { tc_commit(bar(C::L_EMPTY + (nl + pos) % NST)); };
-        good = wait_1(bar(C::Q_FULL), k & 1, p.err, abort);
+        for (int i = 0; i < (two ? 2 : 1) && good; ++i)
+          good = wait_1(bar(C::Q_FULL + ((nq + i) & 1)), ((nq + i) >> 1) & 1, p.err, abort);
         // A step: PV of the stream's unit before, S of its next one. Streams take turns;
         // halves of the rows: A(0), B(0), A(1), ..; units: A(0), B(1), A(2), ..
         const int steps = two ? 2 * nt + 2 : nt + 2;
@@ -373,7 +384,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (js < nt) {
             if (first) good = ready(pos_k(js));
             if (!good) break;
-            const uint64_t da = dq0 + (uint64_t)((two ? x * C::TILE : 0) >> 4);
+            const uint64_t da = dq0 + (uint64_t)((((nq + (two ? x : 0)) & 1) * C::TILE) >> 4);
             const uint64_t db = dk0 + (uint64_t)(((nl + pos_k(js)) % NST * C::TILE) >> 4);
             const uint32_t td = tmem + C::COL_S + x * TK;
 #pragma unroll
@@ -384,11 +395,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc_commit(bar(C::S_FULL + x));
             if (last) {
               release(pos_k(js));
-              if (js == nt - 1) tc_commit(bar(C::Q_EMPTY));
+              if (js == nt - 1) {
+                tc_commit(bar(C::Q_EMPTY + (nq & 1)));
+                if (two) tc_commit(bar(C::Q_EMPTY + ((nq + 1) & 1)));
+              }
             }
           }
         }
         nl += 2 * nt;
+        nq += two ? 2 : 1;
       }
       if (!good) *abort = 1;
     }
@@ -478,11 +493,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   } else if (TMA && warp < 4) {
     // ---------------- Q: groups of 32 rows in turn
     bool good = true;
-    for (int k = 0; good && sg.next(p, w); ++k) {
-      if (k >= 1) good = wait_w(bar(C::Q_EMPTY), (k - 1) & 1, p.err, abort);
-      if (good) copy_q<D>(p, w, sQ, warp - 2, 2);
-      cp_async_arrive(bar(C::Q_FULL));
-    }
+    int nq = 0;  // tiles so far
+    while (good && sg.next(p, w)) good = copy_q<D>(p, w, sb, warp - 2, nq, abort);
     if (!good) *abort = 1;
     cp_async_commit();
     cp_async_wait<0>();
@@ -490,9 +502,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // ---------------- Q, K and V row by row: a lane finds one row's place, all copy it
     const int pw = warp - 1;
     constexpr int NR = TQ / NLOAD;  // rows per lane: 32 (NR pw + i) + lane
-    int nl = 0, nkey = 0;  // slots, units so far
+    int nl = 0, nkey = 0, nq = 0;  // slots, units, query tiles so far
     bool good = true;
-    for (int k = 0; good && sg.next(p, w); ++k) {
+    while (good && sg.next(p, w)) {
       const int nt = w.t1 - w.t0;
       const int64_t table = (int64_t)w.q.s * p.ld_table;
       // pages of this lane's tokens of unit j, requested one unit ahead
@@ -511,12 +523,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       };
       peek(0);
-      if (k >= 1 && !wait_w(bar(C::Q_EMPTY), (k - 1) & 1, p.err, abort)) {
-        good = false;
-        break;
-      }
-      copy_q<D>(p, w, sQ, pw, 2);
-      cp_async_arrive(bar(C::Q_FULL));
+      good = copy_q<D>(p, w, sb, pw, nq, abort);
+      if (!good) break;
       int64_t now[NR] = {}, before[NR] = {};  // this lane's places of the newest unit and the one before it
 #pragma unroll 1
       for (int pos = 0; pos < 2 * nt; ++pos) {

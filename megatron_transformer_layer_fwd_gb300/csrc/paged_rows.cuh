@@ -116,10 +116,10 @@ struct Cursor {
   }
   __device__ void init(const Params& p, const TreeStart& st, int live) {
     at = st.at; s = st.i; t = st.t; n = live;
-    q = p.live[s];
+    q = st.q;
+    nq = st.next;
     take(p);
     h = st.h * per + st.b;
-    request(p);
   }
   __device__ void take(const Params& p) {
     len = q.len;

@@ -52,10 +52,18 @@ struct TreeSeq {
   int32_t row, m, len, s;
 };
 // Where a range begins: unit t of item (live sequence i, KV head h, block b), the
-// item at `at` on the cost axis.
+// item at `at` on the cost axis. The sequence and the next one are beside it, which saves the
+// kernels a dependent read.
 struct TreeStart {
   int64_t at;
   int32_t i, h, b, t;
+  TreeSeq q, next;
+};
+// The split item that begins in a CTA's range: `parts` of them (0: none), the first in the
+// workspace at `first`, those of the CTAs behind at 2 CTA.
+struct TreeSplit {
+  int32_t parts, first, row, len;  // the sequence's first row, its length
+  int32_t r0, rows, h, pad;        // the block's first row, its rows, the KV head
 };
 // What a drafted token is to the cache: its sequence (-1: none), slot and depth position.
 struct TreeToken {
@@ -63,7 +71,7 @@ struct TreeToken {
 };
 
 struct TreeTable {
-  size_t header, start, live, prefix;
+  size_t header, start, split, live, prefix;
   int rows;  // of a part
 };
 struct TreeLayout {
@@ -85,6 +93,7 @@ struct TreeParams {
   int nq, nkv, G;
   const TreeHeader* hdr;
   const TreeStart* start;
+  const TreeSplit* split;
   const TreeSeq* live;
   const uint32_t* mask;
   uint32_t* counter;  // (few rows: a split item's arrivals)
@@ -145,11 +154,9 @@ struct TreeSegs {
     n = hd.live;
     begin_at = c * hd.chunk;
     end = min(begin_at + hd.chunk, hd.cost);
-    if (i >= n) return false;
-    const int4 x = *reinterpret_cast<const int4*>(p.live + i);
-    cur = TreeSeq{x.x, x.y, x.z, x.w};
-    fetch(p);
-    return true;
+    cur = st.q;
+    nxt = st.next;
+    return i < n;
   }
   // false: no more. Sequences longer than the table are passed over.
   __device__ bool next(const TreeParams& p, TreeSeg& w) {

@@ -33,6 +33,7 @@ struct PlanArgs {
   TreeCut cut[2];
   TreeHeader* hdr[2];
   TreeStart* start[2];
+  TreeSplit* split[2];
   TreeSeq* live[2];
   int64_t* prefix[2];
 };
@@ -202,7 +203,8 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
   for (int c = tid; c <= cut.ranges; c += PT) {
     if (tab == 0 && c < cut.ranges) a.counter[c] = 0;
     const int64_t u = c * chunk;
-    TreeStart st{cost, live, 0, 0, 0};
+    TreeStart st{cost, live, 0, 0, 0, {}, {}};
+    TreeSplit sp{};
     if (u < cost) {
       int lo = 0, hi = live - 1;  // the largest i with prefix[i] <= u
       while (lo < hi) {
@@ -224,6 +226,16 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
       st.i = lo;
       if (into == 0 || (k.units > cut.whole && t < k.units)) {
         st.t = (int)t;
+        if (t > 0 && st.at >= u - chunk) {  // begun in the range before
+          const int64_t end = st.at + (int64_t)(k.units - 1) * unit;
+          sp.parts = (int)(end / chunk) - c + 2;
+          sp.first = 2 * (c - 1) + (u - chunk < st.at ? 1 : 0);
+          sp.row = q.row;
+          sp.len = q.len;
+          sp.r0 = st.b * cut.rows;
+          sp.rows = (int)min((int64_t)cut.rows, (int64_t)q.m * a.G - sp.r0);
+          sp.h = st.h;
+        }
       } else {  // the item's last unit begins before: the next item
         st.at += last ? k.last : k.full;
         if (++st.b == k.blocks) {
@@ -235,15 +247,18 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
         }
       }
     }
+    if (st.i < live) st.q = live_out[st.i];
+    if (st.i + 1 < live) st.next = live_out[st.i + 1];
     a.start[tab][c] = st;
+    if (c > 0) a.split[tab][c - 1] = sp;
   }
 }
 
 // ---------------------------------------------------------------- join
-// Block (c, g): rows 8 g .. + 7 of the item that begins in CTA c's range and ends in
-// a later one, if there is one. A warp per row: the parts' maxima and sums by lanes,
-// then the weighted sum of their rows, four parts' loads under way at a time.
-constexpr int JOIN_ROWS = 8;
+// Block (c, g): rows 8 g .. + 7 of the split item that begins in CTA c's range, if there
+// is one. A warp per row: the parts' maxima and sums by lanes, then the weighted sum of their
+// rows, JOIN_PARTS parts' loads under way at a time.
+constexpr int JOIN_ROWS = 8, JOIN_PARTS = 8;
 
 template <typename T, int D, typename Cut>
 __global__ void __launch_bounds__(32 * JOIN_ROWS) tree_join_kernel(const TreeParams p) {
@@ -253,20 +268,33 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) tree_join_kernel(const TreePar
   const int c = blockIdx.x / groups;
   const int r = (blockIdx.x - c * groups) * JOIN_ROWS + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const TreeHeader hd = *p.hdr;
-  const TreeStart st = p.start[c + 1];
-  const int64_t chunk = hd.chunk;
-  if (st.i >= hd.live || st.t == 0 || st.at / chunk != c) return;
-  const TreeSeq q = p.live[st.i];
-  const int rows = min(Cut::ROWS, q.m * p.G - st.b * Cut::ROWS);
-  if (q.len > p.cap || r >= rows) return;
-  const int nt = tree_units<Cut>(q.len);
-  const int cl = (int)((st.at + tree_begin<Cut>(nt - 1, nt, rows)) / chunk);
+  const TreeSplit sp = p.split[c];
+  if (r >= sp.rows || sp.len > p.cap) return;  // (no item: no rows)
+  auto part = [&](int i) { return (int64_t)(i == 0 ? sp.first : 2 * (c + i)) * p.rows + r; };
   float M = -INFINITY, L = 0.0f, x[CPL] = {};
-  for (int c0 = c; c0 <= cl; c0 += 32) {
-    const int n = min(32, cl - c0 + 1);
+  for (int c0 = 0; c0 < sp.parts; c0 += 32) {
+    const int n = min(32, sp.parts - c0);
+    float z[JOIN_PARTS][CPL];
+    auto request = [&](int i0) {
+#pragma unroll
+      for (int i = 0; i < JOIN_PARTS; ++i) {
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) z[i][j] = 0.0f;
+        if (i0 + i < n) {
+          const float* y0 = p.part + part(c0 + i0 + i) * D + lane * CPL;
+          if constexpr (CPL == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(y0));
+            z[i][0] = v.x; z[i][1] = v.y; z[i][2] = v.z; z[i][3] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(y0));
+            z[i][0] = v.x; z[i][1] = v.y;
+          }
+        }
+      }
+    };
     float2 y = make_float2(-INFINITY, 0.0f);  // of part c0 + lane
-    if (lane < n) y = __ldcg(&p.ml[(int64_t)tree_part(c0 + lane, (c0 + lane) * chunk, st.at) * p.rows + r]);
+    if (lane < n) y = __ldcg(&p.ml[part(c0 + lane)]);
+    request(0);
     float mn = y.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
@@ -281,26 +309,10 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) tree_join_kernel(const TreePar
     L = L * f + lp;
 #pragma unroll
     for (int j = 0; j < CPL; ++j) x[j] *= f;
-    for (int i0 = 0; i0 < n; i0 += 4) {
-      float z[4][CPL];
+    for (int i0 = 0; i0 < n; i0 += JOIN_PARTS) {
+      if (i0 > 0) request(i0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) z[i][j] = 0.0f;
-        if (i0 + i < n) {
-          const float* y0 =
-              p.part + ((int64_t)tree_part(c0 + i0 + i, (c0 + i0 + i) * chunk, st.at) * p.rows + r) * D + lane * CPL;
-          if constexpr (CPL == 4) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(y0));
-            z[i][0] = v.x; z[i][1] = v.y; z[i][2] = v.z; z[i][3] = v.w;
-          } else {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(y0));
-            z[i][0] = v.x; z[i][1] = v.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < JOIN_PARTS; ++i) {
         const float wi = __shfl_sync(0xffffffffu, w, i0 + i);
         if (i0 + i < n)
 #pragma unroll
@@ -309,8 +321,8 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) tree_join_kernel(const TreePar
     }
   }
   const float inv = 1.0f / L;
-  const int rr = st.b * Cut::ROWS + r, tok = rr / p.G, head = st.h * p.G + rr - tok * p.G;
-  T* o = static_cast<T*>(p.o) + (q.row + tok) * p.ld_o + (int64_t)head * D + lane * CPL;
+  const int rr = sp.r0 + r, tok = rr / p.G, head = sp.h * p.G + rr - tok * p.G;
+  T* o = static_cast<T*>(p.o) + (sp.row + tok) * p.ld_o + (int64_t)head * D + lane * CPL;
   if constexpr (sizeof(T) == 4) {
     if constexpr (CPL == 4)
       *reinterpret_cast<float4*>(o) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
@@ -324,7 +336,7 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) tree_join_kernel(const TreePar
       *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(x[0] * inv, x[1] * inv);
   }
   if (p.lse != nullptr && lane == 0)
-    p.lse[(int64_t)(q.row + tok) * p.nq + head] = (M + log2f(L)) * LN2;
+    p.lse[(int64_t)(sp.row + tok) * p.nq + head] = (M + log2f(L)) * LN2;
 }
 
 mgb_status check_shape(int n, int tokens, int nq, int nkv, int d) {
@@ -369,6 +381,7 @@ TreeLayout tree_layout(int n, int tokens, int nq, int nkv, int d) {
     TreeTable& t = l.table[i];
     t.header = take(sizeof(TreeHeader));
     t.start = take(sizeof(TreeStart) * (cut.ranges + 1));
+    t.split = take(sizeof(TreeSplit) * cut.ranges);
     t.live = take(sizeof(TreeSeq) * live);
     t.prefix = take(8 * (live + 1));
     t.rows = most < cut.rows ? (int)((most + 7) / 8 * 8) : cut.rows;
@@ -449,6 +462,7 @@ mgb_status mgb_attention_tree_prepare(int32_t n_seqs, int32_t tokens, int32_t n_
       a.cut[i] = tree_cut(n_seqs, tokens, n_q_heads, n_kv_heads, head_dim, i);
       a.hdr[i] = reinterpret_cast<TreeHeader*>(b + l.table[i].header);
       a.start[i] = reinterpret_cast<TreeStart*>(b + l.table[i].start);
+      a.split[i] = reinterpret_cast<TreeSplit*>(b + l.table[i].split);
       a.live[i] = reinterpret_cast<TreeSeq*>(b + l.table[i].live);
       a.prefix[i] = reinterpret_cast<int64_t*>(b + l.table[i].prefix);
     }
@@ -491,6 +505,7 @@ mgb_status mgb_attention_tree(const mgb_attention_tree_plan* plan, const mgb_kv_
   const TreeTable& t = l.table[c->dtype == MGB_F32 ? 1 : 0];
   p.hdr = reinterpret_cast<const TreeHeader*>(b + t.header);
   p.start = reinterpret_cast<const TreeStart*>(b + t.start);
+  p.split = reinterpret_cast<const TreeSplit*>(b + t.split);
   p.live = reinterpret_cast<const TreeSeq*>(b + t.live);
   p.mask = reinterpret_cast<const uint32_t*>(b + l.mask);
   p.ml = reinterpret_cast<float2*>(b + l.ml);
