@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         fa *= inv;
         fb *= inv;
         bf16* out = static_cast<bf16*>(p.o) + (w.q.row + tok) * p.ld_o + (int64_t)head * D;
-        const int64_t at = (int64_t)tree_part(c, sg.begin_at, w.at) * p.rows + row;
+        const int part = tree_part(c, sg.begin_at, w.at);
 #pragma unroll 1
         for (int i = 0; i < D / 16; ++i) {
           uint32_t o[16], o2[16];
@@ -768,14 +768,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           } else if (live) {
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(p.part + at * D + i * 16 + e) =
-                  make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+              *tree_part_at(p, part, D, (i * 16 + e) / 4, row) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
           }
           __syncwarp();  // (the loads are the whole warp's)
         }
         if (live && whole && p.lse != nullptr)
           p.lse[(int64_t)(w.q.row + tok) * p.nq + head] = (m + log2f(l)) * LN2;
-        if (live && !whole) p.ml[at] = make_float2(m, l);
+        if (live && !whole) p.ml[(int64_t)part * p.rows + row] = make_float2(m, l);
       }
       tc_fence_before();
       __syncwarp();
@@ -823,7 +822,7 @@ mgb_status launch_k(const TreeParams& p, const PoolMaps& tm, cudaStream_t st) {
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return MGB_ERR_CUDA;
   const mgb_status s = launch_pdl(k, CutTc::RANGES, NTHREADS, C::SMEM, st, tm, p);
-  return s != MGB_OK ? s : tree_join<bf16, D, CutTc>(p, st);
+  return s != MGB_OK ? s : tree_join<bf16, D>(p, st);
 }
 
 template <int D>

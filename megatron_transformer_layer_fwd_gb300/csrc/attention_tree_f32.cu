@@ -178,24 +178,24 @@ __device__ __forceinline__ void run_rows(const TreeParams& p, const TreeSeg& w, 
     for (int o = 1; o < 16; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
     const int row = RPT * ty + r;
     if (row >= rows) continue;
-    float* out;
-    float inv = 1.0f;
     if (whole) {
       const int t = (first + row) / p.G, head = w.h * p.G + first + row - t * p.G;
-      inv = 1.0f / l[r];  // (l = 0: no score, 0 / 0)
-      out = static_cast<float*>(p.o) + (w.q.row + t) * p.ld_o + (int64_t)head * D;
+      const float inv = 1.0f / l[r];  // (l = 0: no score, 0 / 0)
+      float* out = static_cast<float*>(p.o) + (w.q.row + t) * p.ld_o + (int64_t)head * D;
       if (tx == 0 && p.lse != nullptr)
         p.lse[(int64_t)(w.q.row + t) * p.nq + head] = (m[r] + log2f(l[r])) * LN2;
-    } else {
-      const int64_t pr = (int64_t)part * p.rows + row;
-      out = p.part + pr * D;
-      if (tx == 0) p.ml[pr] = make_float2(m[r], l[r]);
-    }
 #pragma unroll
-    for (int c = 0; c < OC; ++c)
-      *reinterpret_cast<float4*>(out + 4 * tx + 64 * c) =
-          make_float4(acc[r][4 * c] * inv, acc[r][4 * c + 1] * inv, acc[r][4 * c + 2] * inv,
-                      acc[r][4 * c + 3] * inv);
+      for (int c = 0; c < OC; ++c)
+        *reinterpret_cast<float4*>(out + 4 * tx + 64 * c) =
+            make_float4(acc[r][4 * c] * inv, acc[r][4 * c + 1] * inv, acc[r][4 * c + 2] * inv,
+                        acc[r][4 * c + 3] * inv);
+    } else {
+      if (tx == 0) p.ml[(int64_t)part * p.rows + row] = make_float2(m[r], l[r]);
+#pragma unroll
+      for (int c = 0; c < OC; ++c)
+        *tree_part_at(p, part, D, tx + 16 * c, row) =
+            make_float4(acc[r][4 * c], acc[r][4 * c + 1], acc[r][4 * c + 2], acc[r][4 * c + 3]);
+    }
   }
 }
 
@@ -225,7 +225,7 @@ mgb_status launch_d(const TreeParams& p, cudaStream_t st) {
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return MGB_ERR_CUDA;
   const mgb_status s = launch_pdl(k, CutF32<D>::RANGES, NT, C::SMEM, st, p);
-  return s != MGB_OK ? s : tree_join<float, D, CutF32<D>>(p, st);
+  return s != MGB_OK ? s : tree_join<float, D>(p, st);
 }
 
 }  // namespace

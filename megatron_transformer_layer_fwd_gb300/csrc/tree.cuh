@@ -45,6 +45,7 @@ struct TreeHeader {
   int64_t cost, chunk;  // of all items; of a range
   int32_t live;         // sequences with items
   int32_t rows;         // rows behind this one belong to no sequence
+  int32_t splits, pad;  // items in the parts of several CTAs
 };
 // A sequence's rows of q and o begin at row `row`, `m` of them; `len` cached tokens
 // with the drafted ones; `s` its row of the block table.
@@ -59,11 +60,11 @@ struct TreeStart {
   int32_t i, h, b, t;
   TreeSeq q, next;
 };
-// The split item that begins in a CTA's range: `parts` of them (0: none), the first in the
-// workspace at `first`, those of the CTAs behind at 2 CTA.
+// An item in the parts of several CTAs, c the first of them: its part in the workspace at
+// `first`, those of the others at 2 CTA.
 struct TreeSplit {
-  int32_t parts, first, row, len;  // the sequence's first row, its length
-  int32_t r0, rows, h, pad;        // the block's first row, its rows, the KV head
+  int32_t c, parts, first, row;  // row: the sequence's first one
+  int32_t r0, rows, h, len;      // the block's first row, its rows, the KV head, the sequence's length
 };
 // What a drafted token is to the cache: its sequence (-1: none), slot and depth position.
 struct TreeToken {
@@ -98,7 +99,7 @@ struct TreeParams {
   const uint32_t* mask;
   uint32_t* counter;  // (few rows: a split item's arrivals)
   float2* ml;   // [2 CTAs][rows] (maximum in log2 units, row sum) of a part
-  float* part;  // [2 CTAs][rows][d]
+  float* part;  // [2 CTAs][d / 4][rows][4] (few rows: [2 CTAs][rows][d])
   int rows;
   const void *k, *v;
   const int32_t* table;
@@ -198,6 +199,12 @@ __device__ __forceinline__ int tree_part(int cc, int64_t begin, int64_t at) {
   return 2 * cc + (begin < at ? 1 : 0);
 }
 
+// Place of columns 4 c .. of a row of a part: rows lie next to each other, as the threads that
+// write and read them do.
+__device__ __forceinline__ float4* tree_part_at(const TreeParams& p, int part, int d, int c, int row) {
+  return reinterpret_cast<float4*>(p.part) + ((int64_t)part * (d / 4) + c) * p.rows + row;
+}
+
 // The 32 mask bits of drafted tokens first .. first + 31 (those before 0 are cached
 // tokens, seen by all; those behind the mask are none).
 __device__ __forceinline__ uint32_t tree_window(const uint32_t* mask, int first) {
@@ -210,8 +217,8 @@ __device__ __forceinline__ uint32_t tree_window(const uint32_t* mask, int first)
 }
 
 mgb_status check_tree_plan(const mgb_attention_tree_plan* plan);
-// Joins the parts of split items (in tree_plan.cu, for the cuts above).
-template <typename T, int D, typename Cut>
+// Joins the parts of split items (in tree_plan.cu).
+template <typename T, int D>
 mgb_status tree_join(const TreeParams& p, cudaStream_t st);
 mgb_status attention_tree_rows(const TreeParams& p, int d, int dtype, cudaStream_t st);
 mgb_status attention_tree_bf16(const TreeParams& p, int d, cudaStream_t st);

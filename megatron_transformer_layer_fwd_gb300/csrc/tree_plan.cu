@@ -195,16 +195,16 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
     }
     __syncthreads();
   }
-  if (tid == 0) prefix[live] = cost;
+  __shared__ int splits;
+  if (tid == 0) prefix[live] = cost, splits = 0;
   __syncthreads();
   int64_t chunk = (cost + cut.ranges - 1) / cut.ranges;
   if (chunk < cut.min_chunk) chunk = cut.min_chunk;
-  if (tid == 0) *a.hdr[tab] = TreeHeader{cost, chunk, live, rows};
+  if (tid == 0) a.hdr[tab]->cost = cost, a.hdr[tab]->chunk = chunk, a.hdr[tab]->live = live, a.hdr[tab]->rows = rows;
   for (int c = tid; c <= cut.ranges; c += PT) {
     if (tab == 0 && c < cut.ranges) a.counter[c] = 0;
     const int64_t u = c * chunk;
     TreeStart st{cost, live, 0, 0, 0, {}, {}};
-    TreeSplit sp{};
     if (u < cost) {
       int lo = 0, hi = live - 1;  // the largest i with prefix[i] <= u
       while (lo < hi) {
@@ -228,13 +228,16 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
         st.t = (int)t;
         if (t > 0 && st.at >= u - chunk) {  // begun in the range before
           const int64_t end = st.at + (int64_t)(k.units - 1) * unit;
+          TreeSplit sp;
+          sp.c = c - 1;
           sp.parts = (int)(end / chunk) - c + 2;
           sp.first = 2 * (c - 1) + (u - chunk < st.at ? 1 : 0);
           sp.row = q.row;
-          sp.len = q.len;
           sp.r0 = st.b * cut.rows;
           sp.rows = (int)min((int64_t)cut.rows, (int64_t)q.m * a.G - sp.r0);
           sp.h = st.h;
+          sp.len = q.len;
+          a.split[tab][atomicAdd(&splits, 1)] = sp;  // (their order changes no result)
         }
       } else {  // the item's last unit begins before: the next item
         st.at += last ? k.last : k.full;
@@ -250,93 +253,100 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
     if (st.i < live) st.q = live_out[st.i];
     if (st.i + 1 < live) st.next = live_out[st.i + 1];
     a.start[tab][c] = st;
-    if (c > 0) a.split[tab][c - 1] = sp;
   }
+  __syncthreads();
+  if (tid == 0) a.hdr[tab]->splits = splits;
 }
 
 // ---------------------------------------------------------------- join
-// Block (c, g): rows 8 g .. + 7 of the split item that begins in CTA c's range, if there
-// is one. A warp per row: the parts' maxima and sums by lanes, then the weighted sum of their
-// rows, JOIN_PARTS parts' loads under way at a time.
-constexpr int JOIN_ROWS = 8, JOIN_PARTS = 8;
+// A warp takes 32 rows of a split item, a lane each, and some of their columns. 16 loads are
+// under way at a time: of 16 parts for 4 columns, or, where there are few parts, of 4 parts for
+// 16 columns.
+constexpr int JOIN_WARPS = 8, JOIN_BLOCKS = 2;  // warps per block, blocks per SM
+constexpr int JOIN_FEW = 4;
 
-template <typename T, int D, typename Cut>
-__global__ void __launch_bounds__(32 * JOIN_ROWS) tree_join_kernel(const TreeParams p) {
-  constexpr int CPL = D / 32;
-  pdl_wait();
-  const int groups = (p.rows + JOIN_ROWS - 1) / JOIN_ROWS;
-  const int c = blockIdx.x / groups;
-  const int r = (blockIdx.x - c * groups) * JOIN_ROWS + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const TreeSplit sp = p.split[c];
-  if (r >= sp.rows || sp.len > p.cap) return;  // (no item: no rows)
-  auto part = [&](int i) { return (int64_t)(i == 0 ? sp.first : 2 * (c + i)) * p.rows + r; };
-  float M = -INFINITY, L = 0.0f, x[CPL] = {};
-  for (int c0 = 0; c0 < sp.parts; c0 += 32) {
-    const int n = min(32, sp.parts - c0);
-    float z[JOIN_PARTS][CPL];
-    auto request = [&](int i0) {
+template <typename T, int D, int NP, int NC>
+__device__ __forceinline__ void join_rows(const TreeParams& p, const TreeSplit& sp, int r, int c0) {
+  auto part = [&](int i) { return i == 0 ? sp.first : 2 * (sp.c + i); };
+  const int row = min(r, sp.rows - 1);  // (lanes without a row: the last one's, not stored)
+  float M = -INFINITY, L = 0.0f, x[NC][4] = {};
+  for (int i0 = 0; i0 < sp.parts; i0 += NP) {
+    float2 y[NP];
+    float4 z[NP][NC];
 #pragma unroll
-      for (int i = 0; i < JOIN_PARTS; ++i) {
+    for (int i = 0; i < NP; ++i) {
+      y[i] = make_float2(-INFINITY, 0.0f);
+      if (i0 + i < sp.parts) {
+        y[i] = __ldcg(&p.ml[(int64_t)part(i0 + i) * p.rows + row]);
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) z[i][j] = 0.0f;
-        if (i0 + i < n) {
-          const float* y0 = p.part + part(c0 + i0 + i) * D + lane * CPL;
-          if constexpr (CPL == 4) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(y0));
-            z[i][0] = v.x; z[i][1] = v.y; z[i][2] = v.z; z[i][3] = v.w;
-          } else {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(y0));
-            z[i][0] = v.x; z[i][1] = v.y;
-          }
-        }
+        for (int c = 0; c < NC; ++c) z[i][c] = __ldcg(tree_part_at(p, part(i0 + i), D, c0 + c, row));
+      } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) z[i][c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
-    };
-    float2 y = make_float2(-INFINITY, 0.0f);  // of part c0 + lane
-    if (lane < n) y = __ldcg(&p.ml[part(c0 + lane)]);
-    request(0);
-    float mn = y.x;
+    }
+    float mn = M;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mn = fmaxf(mn, M);
+    for (int i = 0; i < NP; ++i) mn = fmaxf(mn, y[i].x);
     const float base = mn == -INFINITY ? 0.0f : mn;  // (no token so far: every factor is 0)
-    const float f = exp2f(M - base), w = exp2f(y.x - base);
+    const float f = exp2f(M - base);
     M = mn;
-    // (a part without a reference has a row sum of 0, or NaN, which stays)
-    float lp = y.x > -INFINITY ? y.y * w : y.y;
+    L *= f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lp += __shfl_xor_sync(0xffffffffu, lp, o);
-    L = L * f + lp;
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int j = 0; j < CPL; ++j) x[j] *= f;
-    for (int i0 = 0; i0 < n; i0 += JOIN_PARTS) {
-      if (i0 > 0) request(i0);
+      for (int j = 0; j < 4; ++j) x[c][j] *= f;
 #pragma unroll
-      for (int i = 0; i < JOIN_PARTS; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i0 + i);
-        if (i0 + i < n)
+    for (int i = 0; i < NP; ++i) {
+      const float w = exp2f(y[i].x - base);
+      // (a part without a reference has a row sum of 0, or NaN, which stays)
+      L += y[i].x > -INFINITY ? y[i].y * w : y[i].y;
 #pragma unroll
-          for (int j = 0; j < CPL; ++j) x[j] = fmaf(wi, z[i][j], x[j]);
+      for (int c = 0; c < NC; ++c) {
+        x[c][0] = fmaf(w, z[i][c].x, x[c][0]);
+        x[c][1] = fmaf(w, z[i][c].y, x[c][1]);
+        x[c][2] = fmaf(w, z[i][c].z, x[c][2]);
+        x[c][3] = fmaf(w, z[i][c].w, x[c][3]);
       }
     }
   }
+  if (r >= sp.rows) return;
   const float inv = 1.0f / L;
   const int rr = sp.r0 + r, tok = rr / p.G, head = sp.h * p.G + rr - tok * p.G;
-  T* o = static_cast<T*>(p.o) + (sp.row + tok) * p.ld_o + (int64_t)head * D + lane * CPL;
-  if constexpr (sizeof(T) == 4) {
-    if constexpr (CPL == 4)
-      *reinterpret_cast<float4*>(o) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+  T* o = static_cast<T*>(p.o) + (sp.row + tok) * p.ld_o + (int64_t)head * D + c0 * 4;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    float* v = x[c];
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4*>(o + 4 * c) = make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
     else
-      *reinterpret_cast<float2*>(o) = make_float2(x[0] * inv, x[1] * inv);
-  } else {
-    if constexpr (CPL == 4)
-      *reinterpret_cast<uint2*>(o) =
-          make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(x[0] * inv, x[1] * inv);
+      *reinterpret_cast<uint2*>(o + 4 * c) =
+          make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv));
   }
-  if (p.lse != nullptr && lane == 0)
+  if (p.lse != nullptr && c0 == 0)
     p.lse[(int64_t)(sp.row + tok) * p.nq + head] = (M + log2f(L)) * LN2;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * JOIN_WARPS, JOIN_BLOCKS) tree_join_kernel(const TreeParams p) {
+  // The plan is read before the attention kernel ends: that kernel let this one start only
+  // when what came before it, the plan among it, was complete.
+  const int groups = (p.rows + 31) / 32, per = groups * (D / 4), tasks = p.hdr->splits * per;
+  int t = blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+  TreeSplit sp{};
+  if (t < tasks) sp = p.split[t / per];
+  pdl_wait();
+  pdl_trigger();
+  while (t < tasks) {
+    const int u = t % per, g = u % groups, c = u / groups;
+    if (g * 32 < sp.rows && sp.len <= p.cap) {
+      const int r = g * 32 + (threadIdx.x & 31);
+      if (sp.parts > JOIN_FEW) join_rows<T, D, 16, 1>(p, sp, r, c);
+      else if (c < D / 16) join_rows<T, D, JOIN_FEW, 4>(p, sp, r, 4 * c);
+    }
+    t += gridDim.x * JOIN_WARPS;
+    if (t < tasks) sp = p.split[t / per];
+  }
 }
 
 mgb_status check_shape(int n, int tokens, int nq, int nkv, int d) {
@@ -397,15 +407,14 @@ TreeLayout tree_layout(int n, int tokens, int nq, int nkv, int d) {
   return l;
 }
 
-template <typename T, int D, typename Cut>
+template <typename T, int D>
 mgb_status tree_join(const TreeParams& p, cudaStream_t st) {
-  const int groups = (p.rows + JOIN_ROWS - 1) / JOIN_ROWS;
-  return launch_pdl(tree_join_kernel<T, D, Cut>, Cut::RANGES * groups, dim3(32 * JOIN_ROWS), 0, st, p);
+  return launch_pdl(tree_join_kernel<T, D>, device_sm_count() * JOIN_BLOCKS, dim3(32 * JOIN_WARPS), 0, st, p);
 }
-template mgb_status tree_join<bf16, 64, CutTc>(const TreeParams&, cudaStream_t);
-template mgb_status tree_join<bf16, 128, CutTc>(const TreeParams&, cudaStream_t);
-template mgb_status tree_join<float, 64, CutF32<64>>(const TreeParams&, cudaStream_t);
-template mgb_status tree_join<float, 128, CutF32<128>>(const TreeParams&, cudaStream_t);
+template mgb_status tree_join<bf16, 64>(const TreeParams&, cudaStream_t);
+template mgb_status tree_join<bf16, 128>(const TreeParams&, cudaStream_t);
+template mgb_status tree_join<float, 64>(const TreeParams&, cudaStream_t);
+template mgb_status tree_join<float, 128>(const TreeParams&, cudaStream_t);
 
 mgb_status check_tree_plan(const mgb_attention_tree_plan* plan) {
   if (plan == nullptr || plan->ws == nullptr) return MGB_ERR_INVALID_ARG;
