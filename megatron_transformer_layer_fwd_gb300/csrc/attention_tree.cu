@@ -822,7 +822,7 @@ mgb_status launch_k(const TreeParams& p, const PoolMaps& tm, cudaStream_t st) {
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return MGB_ERR_CUDA;
   const mgb_status s = launch_pdl(k, CutTc::RANGES, NTHREADS, C::SMEM, st, tm, p);
-  return s != MGB_OK ? s : tree_join<bf16, D>(p, st);
+  return s != MGB_OK ? s : tree_join<bf16, D>(p, CutTc::RANGES, st);
 }
 
 template <int D>

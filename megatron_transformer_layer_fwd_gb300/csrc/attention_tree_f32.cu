@@ -225,7 +225,7 @@ mgb_status launch_d(const TreeParams& p, cudaStream_t st) {
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return MGB_ERR_CUDA;
   const mgb_status s = launch_pdl(k, CutF32<D>::RANGES, NT, C::SMEM, st, p);
-  return s != MGB_OK ? s : tree_join<float, D>(p, st);
+  return s != MGB_OK ? s : tree_join<float, D>(p, CutF32<D>::RANGES, st);
 }
 
 }  // namespace

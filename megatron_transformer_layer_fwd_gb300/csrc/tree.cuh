@@ -41,11 +41,12 @@ __host__ __device__ constexpr int unit_cost(int rows) {
   return rows <= Cut::R1 ? Cut::C1 : rows <= Cut::R2 ? Cut::C2 : Cut::C3;
 }
 
+constexpr int TREE_FEW = 4;
 struct TreeHeader {
   int64_t cost, chunk;  // of all items; of a range
   int32_t live;         // sequences with items
   int32_t rows;         // rows behind this one belong to no sequence
-  int32_t splits, pad;  // items in the parts of several CTAs
+  int32_t few, many;    // items in up to TREE_FEW parts, in more: from the front and from the back of the list
 };
 // A sequence's rows of q and o begin at row `row`, `m` of them; `len` cached tokens
 // with the drafted ones; `s` its row of the block table.
@@ -219,7 +220,7 @@ __device__ __forceinline__ uint32_t tree_window(const uint32_t* mask, int first)
 mgb_status check_tree_plan(const mgb_attention_tree_plan* plan);
 // Joins the parts of split items (in tree_plan.cu).
 template <typename T, int D>
-mgb_status tree_join(const TreeParams& p, cudaStream_t st);
+mgb_status tree_join(const TreeParams& p, int ranges, cudaStream_t st);
 mgb_status attention_tree_rows(const TreeParams& p, int d, int dtype, cudaStream_t st);
 mgb_status attention_tree_bf16(const TreeParams& p, int d, cudaStream_t st);
 mgb_status attention_tree_f32(const TreeParams& p, int d, cudaStream_t st);

@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
     }
     __syncthreads();
   }
-  __shared__ int splits;
-  if (tid == 0) prefix[live] = cost, splits = 0;
+  __shared__ int few, many;
+  if (tid == 0) prefix[live] = cost, few = 0, many = 0;
   __syncthreads();
   int64_t chunk = (cost + cut.ranges - 1) / cut.ranges;
   if (chunk < cut.min_chunk) chunk = cut.min_chunk;
@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
           sp.rows = (int)min((int64_t)cut.rows, (int64_t)q.m * a.G - sp.r0);
           sp.h = st.h;
           sp.len = q.len;
-          a.split[tab][atomicAdd(&splits, 1)] = sp;  // (their order changes no result)
+          // (their order changes no result)
+          a.split[tab][sp.parts <= TREE_FEW ? atomicAdd(&few, 1) : cut.ranges - 1 - atomicAdd(&many, 1)] = sp;
         }
       } else {  // the item's last unit begins before: the next item
         st.at += last ? k.last : k.full;
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
     a.start[tab][c] = st;
   }
   __syncthreads();
-  if (tid == 0) a.hdr[tab]->splits = splits;
+  if (tid == 0) a.hdr[tab]->few = few, a.hdr[tab]->many = many;
 }
 
 // ---------------------------------------------------------------- join
@@ -263,7 +264,6 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
 // under way at a time: of 16 parts for 4 columns, or, where there are few parts, of 4 parts for
 // 16 columns.
 constexpr int JOIN_WARPS = 8, JOIN_BLOCKS = 2;  // warps per block, blocks per SM
-constexpr int JOIN_FEW = 4;
 
 template <typename T, int D, int NP, int NC>
 __device__ __forceinline__ void join_rows(const TreeParams& p, const TreeSplit& sp, int r, int c0) {
@@ -328,24 +328,31 @@ __device__ __forceinline__ void join_rows(const TreeParams& p, const TreeSplit& 
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * JOIN_WARPS, JOIN_BLOCKS) tree_join_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(32 * JOIN_WARPS, JOIN_BLOCKS) tree_join_kernel(const TreeParams p, int ranges) {
   // The plan is read before the attention kernel ends: that kernel let this one start only
   // when what came before it, the plan among it, was complete.
-  const int groups = (p.rows + 31) / 32, per = groups * (D / 4), tasks = p.hdr->splits * per;
-  int t = blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+  const int groups = (p.rows + 31) / 32, step = gridDim.x * JOIN_WARPS;
+  const int first = blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+  const int few = p.hdr->few * groups * (D / 16), all = few + p.hdr->many * groups * (D / 4);
+  // task t: a split item, 32 of its rows, 16 or 4 columns
+  auto item = [&](int t) {
+    const int i = t < few ? t / (groups * (D / 16)) : ranges - 1 - (t - few) / (groups * (D / 4));
+    return p.split[i];
+  };
+  int t = first;
   TreeSplit sp{};
-  if (t < tasks) sp = p.split[t / per];
+  if (t < all) sp = item(t);
   pdl_wait();
   pdl_trigger();
-  while (t < tasks) {
-    const int u = t % per, g = u % groups, c = u / groups;
+  while (t < all) {
+    const int u = (t < few ? t : t - few) / groups, g = (t < few ? t : t - few) - u * groups;
+    const int r = g * 32 + (threadIdx.x & 31);
     if (g * 32 < sp.rows && sp.len <= p.cap) {
-      const int r = g * 32 + (threadIdx.x & 31);
-      if (sp.parts > JOIN_FEW) join_rows<T, D, 16, 1>(p, sp, r, c);
-      else if (c < D / 16) join_rows<T, D, JOIN_FEW, 4>(p, sp, r, 4 * c);
+      if (t < few) join_rows<T, D, TREE_FEW, 4>(p, sp, r, u % (D / 16) * 4);
+      else join_rows<T, D, 16, 1>(p, sp, r, u % (D / 4));
     }
-    t += gridDim.x * JOIN_WARPS;
-    if (t < tasks) sp = p.split[t / per];
+    t += step;
+    if (t < all) sp = item(t);
   }
 }
 
@@ -408,13 +415,14 @@ TreeLayout tree_layout(int n, int tokens, int nq, int nkv, int d) {
 }
 
 template <typename T, int D>
-mgb_status tree_join(const TreeParams& p, cudaStream_t st) {
-  return launch_pdl(tree_join_kernel<T, D>, device_sm_count() * JOIN_BLOCKS, dim3(32 * JOIN_WARPS), 0, st, p);
+mgb_status tree_join(const TreeParams& p, int ranges, cudaStream_t st) {
+  const int blocks = device_sm_count() * JOIN_BLOCKS;
+  return launch_pdl(tree_join_kernel<T, D>, blocks, dim3(32 * JOIN_WARPS), 0, st, p, ranges);
 }
-template mgb_status tree_join<bf16, 64>(const TreeParams&, cudaStream_t);
-template mgb_status tree_join<bf16, 128>(const TreeParams&, cudaStream_t);
-template mgb_status tree_join<float, 64>(const TreeParams&, cudaStream_t);
-template mgb_status tree_join<float, 128>(const TreeParams&, cudaStream_t);
+template mgb_status tree_join<bf16, 64>(const TreeParams&, int, cudaStream_t);
+template mgb_status tree_join<bf16, 128>(const TreeParams&, int, cudaStream_t);
+template mgb_status tree_join<float, 64>(const TreeParams&, int, cudaStream_t);
+template mgb_status tree_join<float, 128>(const TreeParams&, int, cudaStream_t);
 
 mgb_status check_tree_plan(const mgb_attention_tree_plan* plan) {
   if (plan == nullptr || plan->ws == nullptr) return MGB_ERR_INVALID_ARG;
