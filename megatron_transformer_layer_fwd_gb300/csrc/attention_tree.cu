@@ -183,30 +183,28 @@ __device__ __forceinline__ void v_add2(float& r0, float& r1, float a0, float a1,
       : "=f"(r0), "=f"(r1)
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
-// the upper halves of two words
-__device__ __forceinline__ uint32_t v_upper(float lo, float hi) {
-  uint32_t r;
-  asm volatile("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-// minus the value with its lower half cut off
-__device__ __forceinline__ float v_minus_upper(float x) {
-  float r;
-  asm volatile("lop3.b32 %0, %1, 0xffff0000, 0x80000000, 0x6A;" : "=f"(r) : "f"(x));  // (a & b) ^ c
-  return r;
-}
 __device__ __forceinline__ uint32_t v_pack(float lo, float hi) {
   uint32_t r;
   asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// what a pair of bf16 leaves of the two numbers that it was rounded from (exact)
+__device__ __forceinline__ void v_rest(float& r0, float& r1, float x0, float x1, uint32_t pair) {
+  asm volatile(
+      "{\n .reg .b16 a, b, m;\n mov.b32 {a, b}, %4;\n mov.b16 m, 0xBF80;\n"
+      " fma.rn.f32.bf16 %0, a, m, %2;\n fma.rn.f32.bf16 %1, b, m, %3;\n}\n"
+      : "=f"(r0), "=f"(r1)
+      : "f"(x0), "f"(x1), "r"(pair));
+}
 
 // Scores of 64 keys -> weights 2^(s a + b) in two bf16 parts, per 16 keys the high parts of
 // the pairs in the first eight words, the low parts in the others; the sums take them
-// whole. The high part is the weight cut off, the low part what that leaves, rounded: off by
+// whole. The high part is the weight rounded, the low part what that leaves, rounded: off by
 // 2^-16 relative at most. Groups of four keys: the exponentials of one between the sums and
 // parts of the second before (whose exponentials are done by then) and the scaling of the
-// second next.
+// second next. (The exponential unit takes 4 cycles per instruction; conversions, masks and
+// permutes 2 like the paired products and sums, which they hold up; so what the high part leaves
+// comes from a mixed fused product of the FMA pipe, not from masks and a paired sum.)
 __device__ __forceinline__ void weights(uint32_t (&s)[2][32], float a, float b, float (&sum)[4]) {
   float t[8][4];
   auto scale = [&](int g) {
@@ -223,29 +221,23 @@ __device__ __forceinline__ void weights(uint32_t (&s)[2][32], float a, float b, 
     const int h = g - 2;
     const float* u = t[h & 7];
     uint32_t* o = h >= 0 ? out[h >> 3] + (h & 4) * 4 + (h & 3) * 2 : nullptr;
-    float n0, n1, n2, n3, r0, r1, r2, r3;
+    float r0, r1, r2, r3;
     if (g < 16) v_ex2(y[0]);
     if (h >= 0) {
+      o[0] = v_pack(u[0], u[1]);
       v_add2(sum[0], sum[1], sum[0], sum[1], u[0], u[1]);
-      n0 = v_minus_upper(u[0]);
-      n1 = v_minus_upper(u[1]);
     }
     if (g < 16) v_ex2(y[1]);
     if (h >= 0) {
-      n2 = v_minus_upper(u[2]);
-      n3 = v_minus_upper(u[3]);
-      v_add2(r0, r1, u[0], u[1], n0, n1);
+      o[1] = v_pack(u[2], u[3]);
+      v_add2(sum[2], sum[3], sum[2], sum[3], u[2], u[3]);
     }
     if (g < 16) v_ex2(y[2]);
-    if (h >= 0) {
-      v_add2(sum[2], sum[3], sum[2], sum[3], u[2], u[3]);
-      v_add2(r2, r3, u[2], u[3], n2, n3);
-      o[0] = v_upper(u[0], u[1]);
-    }
-    if (g < 16) v_ex2(y[3]);
+    if (h >= 0) v_rest(r0, r1, u[0], u[1], o[0]);
     if (g + 2 < 16) scale(g + 2);
+    if (g < 16) v_ex2(y[3]);
     if (h >= 0) {
-      o[1] = v_upper(u[2], u[3]);
+      v_rest(r2, r3, u[2], u[3], o[1]);
       o[8] = v_pack(r0, r1);
       o[9] = v_pack(r2, r3);
     }
