@@ -8,15 +8,17 @@
 // rows, each with all units of 128 keys; with fewer both are the same rows, A with the
 // even units, B with the odd ones, joined at the end. Per unit and stream: S = Q K^T
 // (TMEM), the softmax threads (one per row) turn the scores into weights P in place, and
-// O += P V with P read from TMEM. The MMA thread issues PV and the next S of one stream
-// while the other's softmax is at work.
+// O += P V with P read from TMEM. One thread issues PV and the next S of one stream while the
+// other's softmax is at work. (A thread per stream was slower, 156 us against 143 with 244 rows
+// over 131001 tokens: the streams' products mix, and their softmaxes fall together.)
 //
 // P multiplies V as the sum of two bf16 parts (off by 2^-16 relative at most): with one
 // part the weights' errors would add as much again as the output's own rounding. The
 // parts of 16 keys take the 16 columns that their scores had.
 //
 // K and V come through a ring of slots of 128 keys in the order in which the products need
-// them, K_0, K_1, V_0, K_2, V_1, .. Pages of a multiple of 8 slots are copied by the TMA
+// them: K_0, V_0, K_1, .., or, where the streams take the units in turn, K_0, K_1, V_0, K_2, V_1,
+// .. Pages of a multiple of 8 slots are copied by the TMA
 // unit, a box of up to 128 slots of one page at a time; others row by row with 16-byte
 // asynchronous copies. Tokens behind the length or of a bad page are not read: zeros stand
 // in their place, and a bit per key says that no row sees them.
@@ -31,8 +33,8 @@ namespace {
 
 constexpr int TQ = 128;         // rows per stream (TMEM lanes)
 constexpr int TK = CutTc::KEYS;   // keys per slot
-constexpr int NLOAD = 64;       // threads that copy K, V and Q, or with TMA Q
-constexpr int NTHREADS = 384;   // MMA warp, three loading warps, 2 x 4 softmax warps
+constexpr int NLOAD = 64;       // threads that copy K, V and Q without TMA
+constexpr int NTHREADS = 384;   // warp 0: products; 1 to 3: loads; 2 x 4: softmax
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float TAU = 8.0f;     // the reference maximum moves in steps above this (log2 units)
 // Reference (log2 units) up to which the fused scale-and-subtract is off by a factor of
@@ -48,6 +50,7 @@ struct Cfg {
   // bytes in the 128-byte swizzle; so a TMA box of whole rows is a run of groups.
   static constexpr int GROUP = KB * 1024;
   static constexpr int TILE = 16 * GROUP;
+  // (Q: the d blocks of all 128 rows one behind the other)
   static constexpr int OFF_Q = 0;                       // [tile] 128 rows: an item's halves, or items in turn
   static constexpr int OFF_R = 2 * TILE;                // [slot]
   static constexpr int OFF_SEE = OFF_R + NST * TILE;    // [NSEE][4]: a bit per key that may be seen
@@ -62,7 +65,7 @@ struct Cfg {
   static_assert(SMEM <= 232448, "shared memory budget");
   // Barriers (8 bytes each). A waiter sees every phase of a barrier, or knows that its
   // phase is complete (parity).
-  static constexpr int Q_FULL = 0;              // [tile] 128 rows of queries copied  (NLOAD threads)
+  static constexpr int Q_FULL = 0;              // [tile] 128 rows of queries    (tx, or the copying threads)
   static constexpr int Q_EMPTY = 2;             // [tile] the item's last S done (commit)
   static constexpr int L_FULL = 4;              // [slot] copied                 (tx, or NLOAD threads)
   static constexpr int L_EMPTY = L_FULL + NST;  // [slot] its products done      (commit)
@@ -84,10 +87,6 @@ struct PerStream {
   __device__ int operator[](int x) const { return x ? b : a; }
   __device__ void inc(int x) { (x ? b : a) += 1; }
 };
-
-// The place of a unit's K or V in the item's order K_0, K_1, V_0, K_2, V_1, ..
-__device__ __forceinline__ int pos_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
-__device__ __forceinline__ int pos_v(int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * n - 1; }
 
 // The hot loops of all roles share the instruction cache, which they outgrow easily (a
 // form with everything unrolled spent 60 % of its cycles waiting for instructions): what is
@@ -129,27 +128,28 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 
 // A warp copies 32 rows of D elements, lane r's at base + off (off < 0: zeros), to rows row0
-// .. of a tile.
+// .. of a tile whose groups of 8 rows and d blocks lie `group` and `block` bytes apart.
 template <int D>
-__device__ __noinline__ void copy_rows(uint32_t dst, int row0, const bf16* base, int64_t off) {
+__device__ __noinline__ void copy_rows(uint32_t dst, int row0, const bf16* base, int64_t off, int group, int block) {
   constexpr int CH = Cfg<D>::CH;
   const int lane = threadIdx.x & 31;
   const int ch = lane % CH, r0 = lane / CH;
   base += ch * 8;
-  dst += (row0 >> 3) * Cfg<D>::GROUP + (ch >> 3) * 1024;
+  dst += (row0 >> 3) * group + (ch >> 3) * block;
 #pragma unroll 8
   for (int i = 0; i < CH; ++i) {
     const int r = i * (32 / CH) + r0;
     const int64_t ro = __shfl_sync(0xffffffffu, off, r);
-    cp_async16(dst + (r >> 3) * Cfg<D>::GROUP + (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4),
+    cp_async16(dst + (r >> 3) * group + (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4),
                base + (ro >= 0 ? ro : 0), ro >= 0);
   }
 }
 
-// A loading warp's groups of 32 of the item's queries, into the next one or two tiles (nq so far).
+// A loading warp's groups of 32 of the item's queries (first, first + step, .. of four per
+// tile), into the next one or two tiles (nq so far).
 template <int D>
-__device__ __forceinline__ bool copy_q(const TreeParams& p, const TreeSeg& w, uint32_t sb, int first, int& nq,
-                                       volatile int* abort) {
+__device__ __forceinline__ bool copy_q(const TreeParams& p, const TreeSeg& w, uint32_t sb, int first, int step,
+                                       int& nq, volatile int* abort) {
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
@@ -157,10 +157,10 @@ __device__ __forceinline__ bool copy_q(const TreeParams& p, const TreeSeg& w, ui
     const int tile = nq & 1;
     if (nq >= 2 && !wait_w(sb + C::OFF_BAR + 8 * (C::Q_EMPTY + tile), ((nq >> 1) - 1) & 1, p.err, abort)) return false;
 #pragma unroll 1
-    for (int g = 4 * x + first; g < 4 * x + 4 && g * 32 < w.rows; g += 2) {
+    for (int g = 4 * x + first; g < 4 * x + 4 && g * 32 < w.rows; g += step) {
       const int r = g * 32 + lane, rr = w.b * CutTc::ROWS + r, t = rr / p.G;
       copy_rows<D>(sb + C::OFF_Q + tile * C::TILE, (g & 3) * 32, static_cast<const bf16*>(p.q),
-                   r < w.rows ? (w.q.row + t) * p.ld_q + (int64_t)(w.h * p.G + rr - t * p.G) * D : -1);
+                   r < w.rows ? (w.q.row + t) * p.ld_q + (int64_t)(w.h * p.G + rr - t * p.G) * D : -1, 1024, 16384);
     }
     cp_async_arrive(sb + C::OFF_BAR + 8 * (C::Q_FULL + tile));
   }
@@ -252,8 +252,18 @@ __device__ __forceinline__ void weights(uint32_t (&s)[2][32], float a, float b, 
 // block, group of 8 slots, page.
 struct PoolMaps {
   CUtensorMap k[3], v[3];  // boxes of `box` slots, of 8, of one (and one d block)
+  CUtensorMap q;           // an element of a head's vector, query head of a KV head, token, d block
   int shift;               // box = 1 << shift slots: 8 to 128, in one page
+  int q_tma;               // q is used: heads of a group divide 128
 };
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int head, int token, int kb,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(head), "r"(token), "r"(kb), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int x, int row, int kb, int group,
                                             int page, uint32_t bar) {
   asm volatile(
@@ -289,7 +299,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < C::N_BAR; ++i) {
       int n = 1;
-      if (i < C::Q_EMPTY || (!TMA && i >= C::L_FULL && i < C::L_EMPTY)) n = NLOAD;
+      if (i < C::Q_EMPTY) n = !TMA ? NLOAD : tm.q_tma ? 1 : 32;
+      else if (!TMA && i >= C::L_FULL && i < C::L_EMPTY) n = NLOAD;
       if (i >= C::P_HALF && i <= C::ML) n = 4;
       if (!TMA && i >= C::SEE) n = NLOAD / 32;
       mbar_init(bar(i), n);
@@ -305,97 +316,121 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   TreeSeg w;
 
   if (warp == 0) {
-    // ---------------- MMA issuer: one thread
+    // ---------------- products: one thread
     if (elect_one()) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(TQ, TK, 0, 0);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(TQ, D, 0, 1);
-      const uint64_t dq0 = smem_desc_sw128(sQ, 16, C::GROUP);
+      const uint64_t dq0 = smem_desc_sw128(sQ, 16, 1024);
       const uint64_t dk0 = smem_desc_sw128(sR, 16, C::GROUP);
       const uint64_t dv0 = smem_desc_sw128(sR, 1024, C::GROUP);
-      int nl = 0;            // slots of the items before
-      PerStream np{0, 0};    // weights of each stream so far
-      PerStream no{0, 0};    // items of each stream so far
-      bool good = true;
-      int nq = 0;            // query tiles of the items before
-      while (good && sg.next(p, w)) {
-        const int nt = w.t1 - w.t0;
-        const bool two = w.rows > TQ;
-        auto ready = [&](int pos) {
-          const int n = nl + pos;
-          if (!wait_1(bar(C::L_FULL + n % NST), (n / NST) & 1, p.err, abort)) return false;
-          fence_proxy_async();  // what was copied by ordinary writes is read by the tensor core
+      int slot = 0, phase = 0;  // of the next place in the ring
+      int nq = 0;               // query tiles of the items before
+      PerStream np{0, 0};       // weights of each stream so far
+      PerStream no{0, 0};       // items of each stream so far
+      // the next slot of the ring, once it is loaded
+      auto next_slot = [&](int& at) {
+        at = slot;
+        if (!wait_1(bar(C::L_FULL + at), phase, p.err, abort)) return false;
+        if (!TMA) fence_proxy_async();  // what was copied by ordinary writes is read by the tensor core
+        if (++slot == NST) slot = 0, phase ^= 1;
+        return true;
+      };
+      // S_X = Q_tile K^T, K in slot `at`
+      auto issue_s = [&](int x, int tile, int at) {
+        const uint64_t da = dq0 + (uint64_t)((tile * C::TILE) >> 4), db = dk0 + (uint64_t)((at * C::TILE) >> 4);
+        const uint32_t td = tmem + C::COL_S + x * TK;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_f16(td, da + (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                     db + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+        tc_commit(bar(C::S_FULL + x));
+      };
+      // O_X += P_X V, V in slot `at`; the K steps (16 keys) that hold keys of the sequence, of
+      // which `left` are left; fresh: the stream's first unit of the item, last: its last one
+      auto issue_pv = [&](int x, int at, int left, bool fresh, bool last) {
+        const int n = np[x];
+        if ((fresh && no[x] > 0 && !wait_1(bar(C::O_EMPTY + x), (no[x] - 1) & 1, p.err, abort)) ||
+            !wait_1(bar(C::P_HALF + x), n & 1, p.err, abort))
+          return false;
+        np.inc(x);
+        const int ks = left >= TK ? TK / 16 : (left + 15) / 16;
+        const uint64_t db = dv0 + (uint64_t)((at * C::TILE) >> 4);
+        const uint32_t ta = tmem + C::COL_S + x * TK, to = tmem + C::COL_O + x * D;
+        // (the first half's products run while the other half's weights are formed)
+#pragma unroll 1
+        for (int k0 = 0; k0 < TK / 16; k0 += TK / 32) {
+          if (k0 > 0 && !wait_1(bar(C::P_FULL + x), n & 1, p.err, abort)) return false;
           tc_fence_after();
-          return true;
-        };
-        auto release = [&](int pos) { tc_commit(bar(C::L_EMPTY + (nl + pos) % NST)); };
-        for (int i = 0; i < (two ? 2 : 1) && good; ++i)
-          good = wait_1(bar(C::Q_FULL + ((nq + i) & 1)), ((nq + i) >> 1) & 1, p.err, abort);
-        // A step: PV of the stream's unit before, S of its next one. Streams take turns;
-        // halves of the rows: A(0), B(0), A(1), ..; units: A(0), B(1), A(2), ..
-        const int steps = two ? 2 * nt + 2 : nt + 2;
-#pragma unroll 1
-        for (int i = 0; i < steps && good; ++i) {
-          const int x = i & 1;
-          const int js = two ? i >> 1 : i, jv = two ? js - 1 : i - 2;
-          const bool first = x == 0 || !two, last = x == 1 || !two;  // use of a unit's K and V
-          if (jv >= 0) {
-            // O_X += P_X V_j, the K steps (16 keys) that hold keys of the sequence
-            const bool fresh = two ? jv == 0 : jv < 2;  // the stream's first unit of the item
-            good = (!first || ready(pos_v(jv, nt))) &&
-                   (!fresh || no[x] == 0 || wait_1(bar(C::O_EMPTY + x), (no[x] - 1) & 1, p.err, abort)) &&
-                   wait_1(bar(C::P_HALF + x), np[x] & 1, p.err, abort);
-            if (!good) break;
-            tc_fence_after();
-            const int left = w.q.len - (w.t0 + jv) * TK;
-            const int ks = left >= TK ? TK / 16 : (left + 15) / 16;
-            const uint64_t db = dv0 + (uint64_t)(((nl + pos_v(jv, nt)) % NST * C::TILE) >> 4);
-            const uint32_t ta = tmem + C::COL_S + x * TK, to = tmem + C::COL_O + x * D;
-            // (the first half's products run while the other half's weights are formed)
-#pragma unroll 1
-            for (int k0 = 0; k0 < TK / 16; k0 += TK / 32) {
-              if (k0 > 0) {
-                good = wait_1(bar(C::P_FULL + x), np[x] & 1, p.err, abort);
-                if (!good) break;
-                tc_fence_after();
-              }
 #pragma unroll 4
-              for (int kk = k0; kk < min(ks, k0 + TK / 32); ++kk) {
-                const uint64_t dv = db + (uint64_t)((kk * 2 * C::GROUP) >> 4);
-                tc_mma_f16_ts(to, ta + kk * 16, dv, idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
-                tc_mma_f16_ts(to, ta + kk * 16 + 8, dv, idesc_pv, 1u);
-              }
-            }
+          for (int kk = k0; kk < min(ks, k0 + TK / 32); ++kk) {
+            const uint64_t dv = db + (uint64_t)((kk * 2 * C::GROUP) >> 4);
+            tc_mma_f16_ts(to, ta + kk * 16, dv, idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
+            tc_mma_f16_ts(to, ta + kk * 16 + 8, dv, idesc_pv, 1u);
+          }
+        }
+        if (last) {
+          tc_commit(bar(C::O_FULL + x));
+          no.inc(x);
+        }
+        return true;
+      };
+      auto free_slot = [&](int at) { tc_commit(bar(C::L_EMPTY + at)); };
+      bool good = true;
+      while (good && sg.next(p, w)) {
+        const int nt = w.t1 - w.t0, len = w.q.len - w.t0 * TK;
+        const bool two = w.rows > TQ;
+        const int ta = nq & 1, tb = two ? ta ^ 1 : ta;  // the streams' query tiles
+        for (int i = 0; i < (two ? 2 : 1) && good; ++i, ++nq)
+          good = wait_1(bar(C::Q_FULL + (nq & 1)), (nq >> 1) & 1, p.err, abort);
+        if (!TMA || !tm.q_tma) fence_proxy_async();
+        tc_fence_after();
+        int k, v;
+        if (two) {
+          // halves of the rows: PV_A(j), S_A(j + 1), PV_B(j), S_B(j + 1)
+          good = good && next_slot(k);
+          if (!good) break;
+          issue_s(0, ta, k);
+          issue_s(1, tb, k);
+          free_slot(k);
+          auto free_queries = [&]() {
+            tc_commit(bar(C::Q_EMPTY + ta));
+            tc_commit(bar(C::Q_EMPTY + tb));
+          };
+          if (nt == 1) free_queries();
+#pragma unroll 1
+          for (int j = 0; j < nt; ++j) {
+            const bool more = j + 1 < nt;
+            good = next_slot(v) && issue_pv(0, v, len - j * TK, j == 0, !more) && (!more || next_slot(k));
             if (!good) break;
-            np.inc(x);
-            if (last) release(pos_v(jv, nt));
-            if (two ? jv == nt - 1 : jv + 2 >= nt) {
-              tc_commit(bar(C::O_FULL + x));
-              no.inc(x);
+            if (more) issue_s(0, ta, k);
+            good = issue_pv(1, v, len - j * TK, j == 0, !more);
+            if (!good) break;
+            free_slot(v);
+            if (more) {
+              issue_s(1, tb, k);
+              free_slot(k);
+              if (j + 2 == nt) free_queries();
             }
           }
-          if (js < nt) {
-            if (first) good = ready(pos_k(js));
-            if (!good) break;
-            const uint64_t da = dq0 + (uint64_t)((((nq + (two ? x : 0)) & 1) * C::TILE) >> 4);
-            const uint64_t db = dk0 + (uint64_t)(((nl + pos_k(js)) % NST * C::TILE) >> 4);
-            const uint32_t td = tmem + C::COL_S + x * TK;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
-              tc_mma_f16(td, da + off, db + off, idesc_s, kk > 0);
+        } else {
+          // units in turn: S_A(0), S_B(1), PV_A(0), S_A(2), PV_B(1), S_B(3), ..
+#pragma unroll 1
+          for (int i = 0; i < nt + 2 && good; ++i) {
+            const int x = i & 1;
+            if (i >= 2) {
+              good = next_slot(v) && issue_pv(x, v, len - (i - 2) * TK, i < 4, i >= nt);
+              if (!good) break;
+              free_slot(v);
             }
-            tc_commit(bar(C::S_FULL + x));
-            if (last) {
-              release(pos_k(js));
-              if (js == nt - 1) {
-                tc_commit(bar(C::Q_EMPTY + (nq & 1)));
-                if (two) tc_commit(bar(C::Q_EMPTY + ((nq + 1) & 1)));
-              }
+            if (i < nt) {
+              good = next_slot(k);
+              if (!good) break;
+              issue_s(x, ta, k);
+              free_slot(k);
+              if (i == nt - 1) tc_commit(bar(C::Q_EMPTY + ta));
             }
           }
         }
-        nl += 2 * nt;
-        nq += two ? 2 : 1;
       }
       if (!good) *abort = 1;
     }
@@ -407,6 +442,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     bool good = true;
     while (good && sg.next(p, w)) {
       const int nt = w.t1 - w.t0, x = w.h * (int)p.s_head;
+      const bool two = w.rows > TQ;
       const int32_t* table = p.table + (int64_t)w.q.s * p.ld_table;
       // page and slot of this lane's box of unit j, requested one unit ahead
       int pg = 0, slot = 0;
@@ -425,10 +461,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       int2 now = make_int2(p.n_pages, 0), before = now;
 #pragma unroll 1
       for (int pos = 0; pos < 2 * nt; ++pos) {
-        const bool newest = pos == 2 * nt - 1;  // of V
-        const bool is_v = newest || (pos > 0 && (pos & 1) == 0);
+        const bool newest = two || pos == 2 * nt - 1;  // of V: of the newest unit
+        const bool is_v = two ? pos & 1 : newest || (pos > 0 && (pos & 1) == 0);
         const int n = nl + pos, s = n % NST;
-        const int j = newest ? nt - 1 : is_v ? (pos - 2) / 2 : (pos + 1) / 2;
+        const int j = newest ? pos / 2 : is_v ? (pos - 2) / 2 : (pos + 1) / 2;
         const int left = w.q.len - (w.t0 + j) * TK;  // keys of the sequence from here on
         uint32_t boxes = 0;
         if (!is_v) {
@@ -482,22 +518,39 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       nl += 2 * nt;
     }
     if (!good) *abort = 1;
-  } else if (TMA && warp < 4) {
-    // ---------------- Q: groups of 32 rows in turn
+  } else if (TMA && warp == 3) {
+    // ---------------- Q
     bool good = true;
     int nq = 0;  // tiles so far
-    while (good && sg.next(p, w)) good = copy_q<D>(p, w, sb, warp - 2, nq, abort);
+    while (good && sg.next(p, w)) {
+      if (!tm.q_tma) {
+        good = copy_q<D>(p, w, sb, 0, 1, nq, abort);
+        continue;
+      }
+      // (rows behind the item's last one: any queries)
+      for (int x = 0; x * TQ < w.rows && good; ++x, ++nq) {
+        const int tile = nq & 1;
+        good = nq < 2 || wait_w(bar(C::Q_EMPTY + tile), ((nq >> 1) - 1) & 1, p.err, abort);
+        if (good && lane == 0) {
+          mbar_arrive_expect_tx(bar(C::Q_FULL + tile), C::TILE);
+          tma_load_4d(sQ + tile * C::TILE, &tm.q, w.h * p.G * D, 0,
+                      w.q.row + (w.b * CutTc::ROWS + x * TQ) / p.G, 0, bar(C::Q_FULL + tile));
+        }
+        __syncwarp();
+      }
+    }
     if (!good) *abort = 1;
     cp_async_commit();
     cp_async_wait<0>();
-  } else if (!TMA && warp < 1 + NLOAD / 32) {
+  } else if (!TMA && warp < 4 && (warp & 1)) {
     // ---------------- Q, K and V row by row: a lane finds one row's place, all copy it
-    const int pw = warp - 1;
+    const int pw = warp >> 1;
     constexpr int NR = TQ / NLOAD;  // rows per lane: 32 (NR pw + i) + lane
     int nl = 0, nkey = 0, nq = 0;  // slots, units, query tiles so far
     bool good = true;
     while (good && sg.next(p, w)) {
       const int nt = w.t1 - w.t0;
+      const bool two = w.rows > TQ;
       const int64_t table = (int64_t)w.q.s * p.ld_table;
       // pages of this lane's tokens of unit j, requested one unit ahead
       int pg[NR], slot[NR];
@@ -515,13 +568,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       };
       peek(0);
-      good = copy_q<D>(p, w, sb, pw, nq, abort);
+      good = copy_q<D>(p, w, sb, pw, 2, nq, abort);
       if (!good) break;
       int64_t now[NR] = {}, before[NR] = {};  // this lane's places of the newest unit and the one before it
 #pragma unroll 1
       for (int pos = 0; pos < 2 * nt; ++pos) {
-        const bool newest = pos == 2 * nt - 1;  // of V
-        const bool is_v = newest || (pos > 0 && (pos & 1) == 0);
+        const bool newest = two || pos == 2 * nt - 1;  // of V: of the newest unit
+        const bool is_v = two ? pos & 1 : newest || (pos > 0 && (pos & 1) == 0);
         const int n = nl + pos, s = n % NST;
         uint32_t bits[NR];
         if (!is_v) {
@@ -533,7 +586,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             now[i] = ok ? pg[i] * p.s_page + slot[i] * p.s_tok + w.h * p.s_head : -1;
             bits[i] = __ballot_sync(0xffffffffu, ok);
           }
-          peek((pos + 1) / 2 + 1);
+          peek((two ? pos / 2 : (pos + 1) / 2) + 1);
         }
         if (n >= NST && !wait_w(bar(C::L_EMPTY + s), (n / NST - 1) & 1, p.err, abort)) {
           good = false;
@@ -550,7 +603,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
         for (int i = 0; i < NR; ++i)
           copy_rows<D>(sR + s * C::TILE, (pw * NR + i) * 32, static_cast<const bf16*>(is_v ? p.v : p.k),
-                       !is_v || newest ? now[i] : before[i]);
+                       !is_v || newest ? now[i] : before[i], C::GROUP, 1024);
         cp_async_arrive(bar(C::L_FULL + s));
       }
       nl += 2 * nt;
@@ -821,6 +874,14 @@ template <int D>
 mgb_status launch_d(const TreeParams& p, cudaStream_t st) {
   PoolMaps tm{};
   if (!tma_ok(p, D)) return launch_k<D, false>(p, tm, st);
+  // queries: the heads of a group next to each other, tokens ld_q apart; 128 rows are whole tokens
+  tm.q_tma = 128 % p.G == 0;
+  if (tm.q_tma) {
+    const uint64_t dims[4] = {(uint64_t)(p.nkv - 1) * p.G * D + 64, (uint64_t)p.G, (uint64_t)p.tokens, D / 64};
+    const uint64_t strides[3] = {2 * D, 2 * (uint64_t)(p.tokens > 1 ? p.ld_q : p.nq * D), 128};
+    const uint32_t box[4] = {64, (uint32_t)p.G, (uint32_t)(128 / p.G), D / 64};
+    if (tmap_encode_bf16_nd(&tm.q, p.q, 4, dims, strides, box) != CUDA_SUCCESS) return MGB_ERR_CUDA;
+  }
   while (tm.shift < 7 && p.page_size % (2 << tm.shift) == 0) ++tm.shift;
   if (encode_pool(tm.k, p.k, p, D, tm.shift) != MGB_OK || encode_pool(tm.v, p.v, p, D, tm.shift) != MGB_OK)
     return MGB_ERR_CUDA;

@@ -517,7 +517,7 @@ mgb_status mgb_attention_tree(const mgb_attention_tree_plan* plan, const mgb_kv_
   const TreeLayout l = tree_layout(n, plan->tokens, nq, nkv, d);
   char* b = static_cast<char*>(plan->ws);
   TreeParams p{};
-  p.nq = nq; p.nkv = nkv; p.G = nq / nkv;
+  p.nq = nq; p.nkv = nkv; p.G = nq / nkv; p.tokens = plan->tokens;
   const bool narrow = tree_cut(n, plan->tokens, nq, nkv, d, 0).narrow;
   const TreeTable& t = l.table[c->dtype == MGB_F32 ? 1 : 0];
   p.hdr = reinterpret_cast<const TreeHeader*>(b + t.header);

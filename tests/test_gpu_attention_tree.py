@@ -127,6 +127,17 @@ def test_more_sequences_than_ctas():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_items_of_one_unit_between_longer_ones(dtype, d):
+    """Some sequences of a single unit, some of many, with one block of rows and with two halves:
+    the streams that share the work go through items that one of them has no part in."""
+    rng = np.random.default_rng(35)
+    ctx = [int(x) for x in np.exp(rng.uniform(np.log(5), np.log(2500), 40))]
+    _run(36, dtype, 8, 2, d, 16, _mixed(rng, ctx, [int(m) for m in rng.integers(1, 50, 40)]), tail=2)
+    _run(37, dtype, 4, 2, d, 32, _mixed(rng, sorted(ctx), [20] * 40))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_chains_need_no_parents(dtype):
     _run(16, dtype, 4, 2, 128, 16, [(30, drafts.chain(256)), (None, drafts.chain(2)), (130, drafts.chain(1)),
                                     (0, drafts.chain(150))], parents=False)
