@@ -28,7 +28,7 @@ constexpr int TREE_LONGEST = INT32_MAX - 1024;  // cached tokens (so that keys b
 // its fixed cost, CTAs, and the cost of a unit by the item's rows. A range costs at least one
 // unit, so that none between two others is empty.
 struct CutTc {
-  static constexpr int KEYS = 128, ROWS = 256, WHOLE = 2, ITEM = 4, RANGES = 152;
+  static constexpr int KEYS = 128, ROWS = 256, WHOLE = 2, ITEM = 8, RANGES = 152;
   static constexpr int R1 = 128, R2 = 128, C1 = 4, C2 = 4, C3 = 7;  // (2612 and 4550 cycles at head dim 128)
 };
 template <int D>
@@ -73,12 +73,12 @@ struct TreeToken {
 };
 
 struct TreeTable {
-  size_t header, start, split, live, prefix;
+  size_t header, start, split, live, prefix, counter;
   int rows;  // of a part
 };
 struct TreeLayout {
-  size_t seq, token, mask, counter, ml, part, total;
-  TreeTable table[2];  // (the second: float32, many rows)
+  size_t seq, token, mask, ml, part, total;
+  TreeTable table[2];  // for bf16, for float32
 };
 
 // How the work is cut, by the sizes that the host knows.

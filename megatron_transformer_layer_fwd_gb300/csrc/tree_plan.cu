@@ -22,18 +22,18 @@ __device__ __forceinline__ int seq_kind(bool ok, int m, int len) {
 }
 
 struct PlanArgs {
-  int n, tokens, G, nkv, tables;
+  int n, tokens, G, nkv;
   const int32_t *cu, *lens, *parents;
   TreeSeq* seq;
   TreeToken* token;
   uint32_t* mask;
-  uint32_t* counter;
   int* err;
   // per table
   TreeCut cut[2];
   TreeHeader* hdr[2];
   TreeStart* start[2];
   TreeSplit* split[2];
+  uint32_t* counter[2];
   TreeSeq* live[2];
   int64_t* prefix[2];
 };
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
   if (chunk < cut.min_chunk) chunk = cut.min_chunk;
   if (tid == 0) a.hdr[tab]->cost = cost, a.hdr[tab]->chunk = chunk, a.hdr[tab]->live = live, a.hdr[tab]->rows = rows;
   for (int c = tid; c <= cut.ranges; c += PT) {
-    if (tab == 0 && c < cut.ranges) a.counter[c] = 0;
+    if (c < cut.ranges) a.counter[tab][c] = 0;
     const int64_t u = c * chunk;
     TreeStart st{cost, live, 0, 0, 0, {}, {}};
     if (u < cost) {
@@ -363,9 +363,13 @@ mgb_status check_shape(int n, int tokens, int nq, int nkv, int d) {
 
 }  // namespace
 
-// Few rows per sequence: the decode step's kernel, which streams through the caches of many short
-// items at a time but reads a sequence again for every 16 rows.
-constexpr int FEW_ROWS = 16;
+// Rows per sequence up to which, on average, the decode step's kernel is taken, which streams
+// through the caches of many short items at a time but reads a sequence again for every 16 rows.
+// bf16: 96 sequences, 16 heads of 64, 3 rows 53 us (by the tcgen05 kernel 90); 200 of 100 to
+// 600 tokens, 8 KV heads of 128, 16 rows 112 (86); 64 of 2000, 16 rows each 96 (98). float32, 4
+// heads of 128, 8 rows: 8 of 2000 32 us (the tiled kernel 34), 64 of 100 to 1000 52 (57); 16 rows
+// 38 (34), 59 (57); 32 rows 52 (43).
+constexpr int FEW_ROWS = 10;
 
 template <typename Cut>
 TreeCut cut_of() {
@@ -391,10 +395,6 @@ TreeLayout tree_layout(int n, int tokens, int nq, int nkv, int d) {
   size_t parts = 0;
   for (int i = 0; i < 2; ++i) {
     const TreeCut cut = tree_cut(n, tokens, nq, nkv, d, i);
-    if (i == 1 && cut.narrow) {
-      l.table[1] = l.table[0];
-      continue;
-    }
     TreeTable& t = l.table[i];
     t.header = take(sizeof(TreeHeader));
     t.start = take(sizeof(TreeStart) * (cut.ranges + 1));
@@ -403,7 +403,7 @@ TreeLayout tree_layout(int n, int tokens, int nq, int nkv, int d) {
     t.prefix = take(8 * (live + 1));
     t.rows = most < cut.rows ? (int)((most + 7) / 8 * 8) : cut.rows;
     if ((size_t)2 * cut.ranges * t.rows > parts) parts = (size_t)2 * cut.ranges * t.rows;
-    if (i == 0) l.counter = take(4 * (size_t)cut.ranges);
+    t.counter = take(4 * (size_t)cut.ranges);
   }
   l.seq = take(sizeof(TreeSeq) * (size_t)n);
   l.token = take(sizeof(TreeToken) * (size_t)tokens);
@@ -474,20 +474,19 @@ mgb_status mgb_attention_tree_prepare(int32_t n_seqs, int32_t tokens, int32_t n_
     a.seq = reinterpret_cast<TreeSeq*>(b + l.seq);
     a.token = reinterpret_cast<TreeToken*>(b + l.token);
     a.mask = reinterpret_cast<uint32_t*>(b + l.mask);
-    a.counter = reinterpret_cast<uint32_t*>(b + l.counter);
     for (int i = 0; i < 2; ++i) {
       a.cut[i] = tree_cut(n_seqs, tokens, n_q_heads, n_kv_heads, head_dim, i);
       a.hdr[i] = reinterpret_cast<TreeHeader*>(b + l.table[i].header);
       a.start[i] = reinterpret_cast<TreeStart*>(b + l.table[i].start);
       a.split[i] = reinterpret_cast<TreeSplit*>(b + l.table[i].split);
+      a.counter[i] = reinterpret_cast<uint32_t*>(b + l.table[i].counter);
       a.live[i] = reinterpret_cast<TreeSeq*>(b + l.table[i].live);
       a.prefix[i] = reinterpret_cast<int64_t*>(b + l.table[i].prefix);
     }
-    a.tables = a.cut[0].narrow ? 1 : 2;
     a.err = err;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     LaunchScope scope(PROF_ATTN_TREE, st);
-    tree_prepare_kernel<<<(unsigned)n_seqs + a.tables, PT, 0, st>>>(a);
+    tree_prepare_kernel<<<(unsigned)n_seqs + 2, PT, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return MGB_ERR_CUDA;
   }
   *plan = mgb_attention_tree_plan{n_seqs, tokens, n_q_heads, n_kv_heads, head_dim, ws, ws_bytes};
@@ -518,8 +517,9 @@ mgb_status mgb_attention_tree(const mgb_attention_tree_plan* plan, const mgb_kv_
   char* b = static_cast<char*>(plan->ws);
   TreeParams p{};
   p.nq = nq; p.nkv = nkv; p.G = nq / nkv; p.tokens = plan->tokens;
-  const bool narrow = tree_cut(n, plan->tokens, nq, nkv, d, 0).narrow;
-  const TreeTable& t = l.table[c->dtype == MGB_F32 ? 1 : 0];
+  const int table = c->dtype == MGB_F32 ? 1 : 0;
+  const bool narrow = tree_cut(n, plan->tokens, nq, nkv, d, table).narrow;
+  const TreeTable& t = l.table[table];
   p.hdr = reinterpret_cast<const TreeHeader*>(b + t.header);
   p.start = reinterpret_cast<const TreeStart*>(b + t.start);
   p.split = reinterpret_cast<const TreeSplit*>(b + t.split);
@@ -527,7 +527,7 @@ mgb_status mgb_attention_tree(const mgb_attention_tree_plan* plan, const mgb_kv_
   p.mask = reinterpret_cast<const uint32_t*>(b + l.mask);
   p.ml = reinterpret_cast<float2*>(b + l.ml);
   p.part = reinterpret_cast<float*>(b + l.part);
-  p.counter = reinterpret_cast<uint32_t*>(b + l.counter);
+  p.counter = reinterpret_cast<uint32_t*>(b + t.counter);
   p.rows = t.rows;
   p.k = c->k; p.v = c->v; p.table = c->block_table;
   p.s_page = c->stride_page; p.s_tok = c->stride_token; p.s_head = c->stride_head;

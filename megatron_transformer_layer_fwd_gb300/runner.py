@@ -119,26 +119,44 @@ class ServingBatch:
     cached tokens is reported by mgb_device_status as MGB_ERR_INDEX and not
     cached, since its rows would attend to each other alone. A prompt's rows see
     each other as the shape's mask says; a decode step's row sees all of the
-    cache, with either mask."""
+    cache, with either mask.
+
+    With `drafted` the step checks guessed tokens: the rows are each sequence's
+    drafted tokens, at most mgb.TREE_MAX_TOKENS, the lengths count them, and
+    `parents` [tokens] is each one's parent in its sequence (-1: the last cached
+    token), or None for chains (the next piece of a prompt is one). A row sees the
+    cached tokens, its ancestors and itself. ServingLayer.accept then keeps one path
+    of each tree."""
 
     def __init__(self, shape, block_table: torch.Tensor, seq_lens: torch.Tensor,
-                 cu_seqlens: torch.Tensor | None = None, tokens: int | None = None, stream=None):
+                 cu_seqlens: torch.Tensor | None = None, tokens: int | None = None, stream=None,
+                 drafted: bool = False, parents: torch.Tensor | None = None):
         self.block_table, self.seq_lens, self.cu_seqlens = block_table, seq_lens, cu_seqlens
+        self.drafted = drafted
         n, dev = seq_lens.numel(), seq_lens.device
-        for t in (seq_lens, cu_seqlens):
+        for t in (seq_lens, cu_seqlens, parents):
             if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()):
-                raise ValueError("seq_lens and cu_seqlens must be contiguous int32 vectors")
+                raise ValueError("seq_lens, cu_seqlens and parents must be contiguous int32 vectors")
+        if (drafted and cu_seqlens is None) or (parents is not None and (
+                not drafted or tokens is None or parents.numel() < tokens)):
+            raise ValueError("drafted tokens need row offsets, and parents are those of `tokens` drafted ones")
         if block_table.dim() != 2 or block_table.shape[0] != n or (
                 cu_seqlens is not None and (cu_seqlens.numel() != n + 1 or tokens is None)):
             raise ValueError("a batch of n sequences has n block-table rows and, packed, n + 1 row "
                              "offsets and a number of tokens")
-        if dev.type != DEVICE or any(t.device != dev for t in (block_table, cu_seqlens) if t is not None):
-            raise ValueError("seq_lens, cu_seqlens and the block table must be on one GPU device")
+        if dev.type != DEVICE or any(t.device != dev for t in (block_table, cu_seqlens, parents)
+                                     if t is not None):
+            raise ValueError("seq_lens, cu_seqlens, parents and the block table must be on one GPU device")
         self.tokens = n if cu_seqlens is None else tokens
         self.heads = (shape.n_q_heads, shape.n_kv_heads, shape.head_dim)
         self.causal = shape.causal
         with _on(stream, dev):
-            if cu_seqlens is None:
+            if drafted:
+                self.ws = torch.empty(mgb.mgb_attention_tree_ws_bytes(n, tokens, *self.heads), dtype=torch.uint8,
+                                      device=dev)
+                self.plan = mgb.mgb_attention_tree_prepare(n, tokens, *self.heads, cu_seqlens, seq_lens, parents,
+                                                           self.ws)
+            elif cu_seqlens is None:
                 self.ws = torch.empty(mgb.mgb_attention_decode_ws_bytes(
                     n, shape.n_q_heads, shape.n_kv_heads, shape.head_dim), dtype=torch.uint8, device=dev)
                 self.plan = mgb.mgb_attention_decode_prepare(
@@ -198,10 +216,11 @@ class ServingLayer:
             raise ValueError("x must be [batch.tokens, hidden] of the layer's dtype, contiguous")
         if any(t.device != x.device for t in (self.k_pool, batch.seq_lens)):
             raise ValueError("x, the layer's pools and the batch must be on one device")
-        # (a packed plan serves any heads, a decode plan those it was cut for)
-        if batch.cu_seqlens is None and batch.heads != (s.n_q_heads, s.n_kv_heads, s.head_dim):
+        # (a packed plan serves any heads, the others those they were cut for)
+        packed = batch.cu_seqlens is not None and not batch.drafted
+        if not packed and batch.heads != (s.n_q_heads, s.n_kv_heads, s.head_dim):
             raise ValueError("the batch was prepared for other heads than the layer's")
-        if batch.cu_seqlens is not None and bool(batch.causal) != bool(s.causal):
+        if packed and bool(batch.causal) != bool(s.causal):
             raise ValueError("the batch was prepared for a causal mask, or without one, unlike the layer")
         if batch.tokens == 0:
             return torch.empty_like(x)
@@ -211,6 +230,47 @@ class ServingLayer:
                 x.record_stream(now)
                 batch.ws.record_stream(now)
             return self._step(x, batch)
+
+    def accept(self, batch: ServingBatch, accepted: torch.Tensor, new_lens: torch.Tensor | None = None,
+               stream=None) -> None:
+        """Keeps, of each sequence's drafted tokens in this layer's cache, the path that ends
+        with token accepted[s] (-1: none), and writes the sequences' lengths with it into
+        new_lens (may be the batch's seq_lens). Once per layer and step."""
+        s, n, dev = self.shape, batch.seq_lens.numel(), self.k_pool.device
+        if not batch.drafted or batch.heads != (s.n_q_heads, s.n_kv_heads, s.head_dim):
+            raise ValueError("the batch must be one of drafted tokens, prepared for the layer's heads")
+        for t in (accepted, new_lens):
+            if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (n,) or not t.is_contiguous()):
+                raise ValueError("accepted and new_lens must be contiguous int32 vectors, one entry per sequence")
+        if any(t.device != dev for t in (accepted, new_lens, batch.seq_lens) if t is not None):
+            raise ValueError("accepted, new_lens, the layer's pools and the batch must be on one device")
+        with _on(stream, dev):
+            if stream is not None:
+                for t in (accepted, new_lens, batch.ws):
+                    if t is not None:
+                        t.record_stream(torch.cuda.current_stream(dev))
+            cache = mgb.kv_cache(self.k_pool, self.v_pool, batch.block_table)
+            mgb.mgb_kv_accept(batch.plan, cache, accepted, new_lens)
+
+    def copy_pages(self, src: torch.Tensor, dst: torch.Tensor, slots: torch.Tensor | None = None,
+                   stream=None) -> None:
+        """Copies the first slots[i] tokens (None: all) of this layer's page src[i] to page dst[i]: what a
+        sequence that goes on in several ways needs of its last page, the full ones being shared."""
+        dev = self.k_pool.device
+        if dev.type != DEVICE:
+            raise ValueError("the pools must be on a GPU device")
+        for t in (src, dst, slots):
+            if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != tuple(src.shape) or t.dim() != 1
+                                  or not t.is_contiguous() or t.device != dev):
+                raise ValueError("src, dst and slots must be contiguous int32 vectors on the pools' device, "
+                                 "one entry per copy")
+        with _on(stream, dev):
+            if stream is not None:
+                for t in (src, dst, slots):
+                    if t is not None:
+                        t.record_stream(torch.cuda.current_stream(dev))
+            # (the table is not used, but a cache has one)
+            mgb.mgb_kv_copy_pages(mgb.kv_cache(self.k_pool, self.v_pool, dst.view(-1, 1)), src, dst, slots)
 
     def _step(self, x: torch.Tensor, batch: ServingBatch) -> torch.Tensor:
         s, w, d = self.shape, self.w, self.shape.head_dim
@@ -223,12 +283,18 @@ class ServingLayer:
         cache = mgb.kv_cache(self.k_pool, self.v_pool, batch.block_table)
         rot = 2 * self.rope.shape[1] if self.rope is not None else 0
         desc = mgb.kv_append_desc(T, batch.seq_lens.numel(), nq, rot, self.rope_interleaved,
-                                  self.rope.shape[0] if rot else 0, whole=batch.cu_seqlens is not None)
+                                  self.rope.shape[0] if rot else 0,
+                                  whole=batch.cu_seqlens is not None and not batch.drafted)
         # queries and keys are rotated where they lie
-        mgb.mgb_kv_append(desc, cache, batch.cu_seqlens, batch.seq_lens, self.rope, q, k, v, width, width,
-                          q, width, k, width)
+        if batch.drafted:
+            mgb.mgb_kv_append_tree(batch.plan, desc, cache, self.rope, q, k, v, width, width, q, width, k, width)
+        else:
+            mgb.mgb_kv_append(desc, cache, batch.cu_seqlens, batch.seq_lens, self.rope, q, k, v, width, width,
+                              q, width, k, width)
         o = torch.zeros((T, nq * d), dtype=self.dtype, device=x.device)
-        if batch.cu_seqlens is None:
+        if batch.drafted:
+            mgb.mgb_attention_tree(batch.plan, cache, q, width, o, nq * d, None)
+        elif batch.cu_seqlens is None:
             mgb.mgb_attention_decode(batch.plan, cache, q, width, o, nq * d, None)
         else:
             mgb.mgb_attention_packed_fwd(batch.plan, nq, nkv, d, self.mgb_dtype, q, k, v, width, width, o,
