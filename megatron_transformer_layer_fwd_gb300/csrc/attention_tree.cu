@@ -290,30 +290,29 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 500);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();     // everything the call reads may come from the kernel before
-  pdl_trigger();  // the join may start up; it waits for this kernel's end
-  const int c = blockIdx.x;
-  TreeSegs<CutTc> sg;
-  if (!sg.begin(p, c)) return;
-
-  if (tid == 0) {
-    for (int i = 0; i < C::N_BAR; ++i) {
-      int n = 1;
-      if (i < C::Q_EMPTY) n = !TMA ? NLOAD : tm.q_tma ? 1 : 32;
-      else if (!TMA && i >= C::L_FULL && i < C::L_EMPTY) n = NLOAD;
-      if (i >= C::P_HALF && i <= C::ML) n = 4;
-      if (!TMA && i >= C::SEE) n = NLOAD / 32;
-      mbar_init(bar(i), n);
-    }
+  // (shared memory and TMEM while the kernel before may still run)
+  if (tid < C::N_BAR) {
+    int n = 1;
+    if (tid < C::Q_EMPTY) n = !TMA ? NLOAD : tm.q_tma ? 1 : 32;
+    else if (!TMA && tid >= C::L_FULL && tid < C::L_EMPTY) n = NLOAD;
+    if (tid >= C::P_HALF && tid <= C::ML) n = 4;
+    if (!TMA && tid >= C::SEE) n = NLOAD / 32;
+    mbar_init(bar(tid), n);
     fence_mbar_init();
-    *abort = 0;
   }
+  if (tid == 0) *abort = 0;
+  if (TMA && tid >= 64 && tid < 71) tma_prefetch_desc(tid < 67 ? &tm.k[tid - 64] : tid < 70 ? &tm.v[tid - 67] : &tm.q);
   if (warp == 0) tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();     // everything the call reads may come from the kernel before
+  pdl_trigger();  // the join may start up; it waits for this kernel's end
+  const int c = blockIdx.x;
   TreeSeg w;
+  TreeSegs<CutTc> sg;
+  sg.begin(p, c);  // (without work the roles find nothing)
 
   if (warp == 0) {
     // ---------------- products: one thread

@@ -46,9 +46,7 @@ struct AppendParams {
   int whole;                   // lengths are the rows' numbers (or 0)
   int cap;                     // positions below this: the table's and the rotary table's
   unsigned check_blocks;       // the last blocks, which check cu
-  // drafted tokens: where the plan says that each one stands, and the rows it knows
-  const TreeToken* token;
-  const TreeHeader* hdr;
+  const TreeToken* token;      // drafted tokens: where the plan says that each one stands
   int rope_len;
   int* err;
 };
@@ -190,19 +188,17 @@ __global__ void __launch_bounds__(UB == 1 ? FEW_THREADS : MANY_THREADS, UB == 1 
     if (threadIdx.x == 0 && t < p.tokens) {
       int pos = -1;
       int64_t slot = 0;
-      if (t < p.hdr->rows) {
-        const int4 w = *reinterpret_cast<const int4*>(p.token + t);  // (s, slot, pos)
-        if (w.x >= 0) {
-          bool ok = w.y < p.cap && (p.rot == 0 || w.z < p.rope_len);
-          if (ok) {
-            const int pg = w.y / p.page_size;
-            const int page = p.table[w.x * p.ld_table + pg];
-            ok = page >= 0 && page < p.n_pages;
-            slot = page * p.s_page + (w.y - pg * p.page_size) * p.s_tok;
-          }
-          if (ok) pos = w.z;
-          else record_error(p.err, kErrIndex);
+      const int4 w = *reinterpret_cast<const int4*>(p.token + t);  // (s, slot, pos)
+      if (w.x >= 0) {
+        bool ok = w.y < p.cap && (p.rot == 0 || w.z < p.rope_len);
+        if (ok) {
+          const int pg = w.y / p.page_size;
+          const int page = p.table[w.x * p.ld_table + pg];
+          ok = page >= 0 && page < p.n_pages;
+          slot = page * p.s_page + (w.y - pg * p.page_size) * p.s_tok;
         }
+        if (ok) pos = w.z;
+        else record_error(p.err, kErrIndex);
       }
       s_pos[g] = pos;
       s_slot[g] = slot;
@@ -425,7 +421,6 @@ mgb_status append(const mgb_kv_append_desc* d, const mgb_kv_cache* c, const mgb_
         tree_layout(plan->n_seqs, plan->tokens, plan->n_q_heads, plan->n_kv_heads, plan->head_dim);
     const char* b = static_cast<const char*>(plan->ws);
     p.token = reinterpret_cast<const TreeToken*>(b + l.token);
-    p.hdr = reinterpret_cast<const TreeHeader*>(b + l.table[0].header);
   }
   p.err = device_error_word();
   if (p.err == nullptr) return MGB_ERR_CUDA;

@@ -97,8 +97,10 @@ __global__ void __launch_bounds__(NT) kv_accept_kernel(const MoveParams p, const
 
 // ---------------------------------------------------------------- copy
 // A block takes COPY_VECS vectors of one page's keys or values at a time, COPY_PER per
-// thread, all requested before the first is stored.
-constexpr int CT = 256, COPY_PER = 8, COPY_VECS = CT * COPY_PER;
+// thread, all requested before the first is stored. 1000 pages of 256 KB (524 MB read and
+// written) 84 us, 6.2 TB/s, 0.93 of a plain copy; three pages 2.4 us. (256 threads and 8 vectors
+// 91 and 4.0, 8 blocks per SM 86, one vector 112 and 1.8.)
+constexpr int CT = 128, COPY_PER = 4, COPY_BLOCKS = 24, COPY_VECS = CT * COPY_PER;  // blocks per SM
 
 __global__ void __launch_bounds__(CT) kv_copy_kernel(const MoveParams p, int n, int parts, int slot_inner,
                                                      const int32_t* src, const int32_t* dst,
@@ -209,7 +211,7 @@ mgb_status mgb_kv_copy_pages(const mgb_kv_cache* c, int32_t n_copies, const int3
   if (n_copies == 0) return MGB_OK;
   p.err = device_error_word();
   if (p.err == nullptr) return MGB_ERR_CUDA;
-  const int64_t all = 2 * (int64_t)n_copies * parts, most = (int64_t)device_sm_count() * 8;
+  const int64_t all = 2 * (int64_t)n_copies * parts, most = (int64_t)device_sm_count() * COPY_BLOCKS;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   LaunchScope scope(PROF_KV_MOVE, st);
   return launch_pdl(kv_copy_kernel, (int)(all < most ? all : most), dim3(CT), 0, st, p, (int)n_copies,

@@ -44,8 +44,7 @@ __host__ __device__ constexpr int unit_cost(int rows) {
 constexpr int TREE_FEW = 4;
 struct TreeHeader {
   int64_t cost, chunk;  // of all items; of a range
-  int32_t live;         // sequences with items
-  int32_t rows;         // rows behind this one belong to no sequence
+  int32_t live, pad;    // sequences with items
   int32_t few, many;    // items in up to TREE_FEW parts, in more: from the front and from the back of the list
 };
 // A sequence's rows of q and o begin at row `row`, `m` of them; `len` cached tokens
@@ -148,7 +147,7 @@ struct TreeSegs {
       nxt = TreeSeq{x.x, x.y, x.z, x.w};
     }
   }
-  // CTA c's units; false: none
+  // CTA c's units; false: none (and next() says so too)
   __device__ bool begin(const TreeParams& p, int c) {
     const TreeHeader hd = *p.hdr;
     const TreeStart st = p.start[c];

@@ -38,6 +38,10 @@ struct PlanArgs {
   int64_t* prefix[2];
 };
 
+// a / b for a >= 0, b > 0: most are small, and a division of 64 bits takes some hundred instructions
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 __device__ __forceinline__ int unit_of(const TreeCut& c, int rows) {
   return rows <= c.r1 ? c.c1 : rows <= c.r2 ? c.c2 : c.c3;
 }
@@ -46,8 +50,8 @@ struct SeqCost {
   int units, blocks, unit_full, unit_last;
   int64_t full, last;  // cost of an item of either kind
   __device__ SeqCost(const TreeCut& c, int len, int64_t rows) {
-    units = (int)(((int64_t)len + c.keys - 1) / c.keys);
-    blocks = (int)((rows + c.rows - 1) / c.rows);
+    units = (int)quot((int64_t)len + c.keys - 1, c.keys);
+    blocks = (int)quot(rows + c.rows - 1, c.rows);
     unit_full = unit_of(c, c.rows);
     unit_last = unit_of(c, (int)(rows - (int64_t)(blocks - 1) * c.rows));
     full = (int64_t)units * unit_full + c.item;
@@ -138,7 +142,12 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
   const int tab = blockIdx.x - a.n;
   const TreeCut cut = a.cut[tab];
   TreeSeq* const live_out = a.live[tab];
-  int64_t* const prefix = a.prefix[tab];
+  // (read back below: from shared memory if they fit)
+  __shared__ TreeSeq live_s[PT];
+  __shared__ int64_t prefix_s[PT + 1];
+  const bool fits = a.n <= PT;
+  TreeSeq* const live_at = fits ? live_s : live_out;
+  int64_t* const prefix = fits ? prefix_s : a.prefix[tab];
   __shared__ int64_t warp_cost[PT / 32];
   __shared__ int warp_live[PT / 32];
   int64_t cost = 0;
@@ -184,6 +193,7 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
     if (is_live) {
       const int at = ybefore + y - 1;
       *reinterpret_cast<int4*>(live_out + at) = make_int4(c0, c1 - c0, len, s);
+      if (fits) live_s[at] = TreeSeq{c0, c1 - c0, len, s};
       prefix[at] = before + x - v;
     }
     cost = all;
@@ -198,9 +208,11 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
   __shared__ int few, many;
   if (tid == 0) prefix[live] = cost, few = 0, many = 0;
   __syncthreads();
-  int64_t chunk = (cost + cut.ranges - 1) / cut.ranges;
+  if (tab == 0)  // rows of no sequence
+    for (int t = rows + tid; t < a.tokens; t += PT) *reinterpret_cast<int4*>(a.token + t) = make_int4(-1, 0, 0, 0);
+  int64_t chunk = quot(cost + cut.ranges - 1, cut.ranges);
   if (chunk < cut.min_chunk) chunk = cut.min_chunk;
-  if (tid == 0) a.hdr[tab]->cost = cost, a.hdr[tab]->chunk = chunk, a.hdr[tab]->live = live, a.hdr[tab]->rows = rows;
+  if (tid == 0) a.hdr[tab]->cost = cost, a.hdr[tab]->chunk = chunk, a.hdr[tab]->live = live;
   for (int c = tid; c <= cut.ranges; c += PT) {
     if (c < cut.ranges) a.counter[tab][c] = 0;
     const int64_t u = c * chunk;
@@ -212,16 +224,16 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
         if (prefix[mid] <= u) lo = mid;
         else hi = mid - 1;
       }
-      const TreeSeq q = live_out[lo];
+      const TreeSeq q = live_at[lo];
       const SeqCost k(cut, q.len, (int64_t)q.m * a.G);
       int64_t r = u - prefix[lo];
-      st.h = (int)(r / k.head());
+      st.h = (int)quot(r, k.head());
       r -= st.h * k.head();
-      st.b = (int)min(r / k.full, (int64_t)k.blocks - 1);
+      st.b = (int)min(quot(r, k.full), (int64_t)k.blocks - 1);
       const int64_t into = r - st.b * k.full;
       const bool last = st.b == k.blocks - 1;
       const int unit = last ? k.unit_last : k.unit_full;
-      const int64_t t = (into + unit - 1) / unit;
+      const int64_t t = quot(into + unit - 1, unit);
       st.at = u - into;
       st.i = lo;
       if (into == 0 || (k.units > cut.whole && t < k.units)) {
@@ -230,7 +242,7 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
           const int64_t end = st.at + (int64_t)(k.units - 1) * unit;
           TreeSplit sp;
           sp.c = c - 1;
-          sp.parts = (int)(end / chunk) - c + 2;
+          sp.parts = (int)quot(end, chunk) - c + 2;
           sp.first = 2 * (c - 1) + (u - chunk < st.at ? 1 : 0);
           sp.row = q.row;
           sp.r0 = st.b * cut.rows;
@@ -251,8 +263,8 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
         }
       }
     }
-    if (st.i < live) st.q = live_out[st.i];
-    if (st.i + 1 < live) st.next = live_out[st.i + 1];
+    if (st.i < live) st.q = live_at[st.i];
+    if (st.i + 1 < live) st.next = live_at[st.i + 1];
     a.start[tab][c] = st;
   }
   __syncthreads();
@@ -370,6 +382,7 @@ mgb_status check_shape(int n, int tokens, int nq, int nkv, int d) {
 // heads of 128, 8 rows: 8 of 2000 32 us (the tiled kernel 34), 64 of 100 to 1000 52 (57); 16 rows
 // 38 (34), 59 (57); 32 rows 52 (43).
 constexpr int FEW_ROWS = 10;
+constexpr int EIGHT_ROWS = 5;  // .. and up to which its items have 8 rows, else 16
 
 template <typename Cut>
 TreeCut cut_of() {
@@ -380,7 +393,7 @@ TreeCut cut_of() {
 TreeCut tree_cut(int n, int tokens, int nq, int nkv, int d, int table) {
   const int64_t rows = (int64_t)tokens * (nq / nkv);
   if (rows <= (int64_t)FEW_ROWS * n)
-    return TreeCut{1, unit_tokens(d), MAXR, MAXR, MAXR, UNIT, UNIT, UNIT, item_cost(d), WHOLE, MIN_CHUNK,
+    return TreeCut{1, unit_tokens(d), rows <= (int64_t)EIGHT_ROWS * n ? 8 : MAXR, MAXR, MAXR, UNIT, UNIT, UNIT, item_cost(d), WHOLE, MIN_CHUNK,
                    SMS * ctas_per_sm(d)};
   if (table == 0) return cut_of<CutTc>();
   return d == 64 ? cut_of<CutF32<64>>() : cut_of<CutF32<128>>();
