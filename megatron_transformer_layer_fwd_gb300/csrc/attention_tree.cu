@@ -255,7 +255,11 @@ struct PoolMaps {
   CUtensorMap q;           // an element of a head's vector, query head of a KV head, token, d block
   int shift;               // box = 1 << shift slots: 8 to 128, in one page
   int q_tma;               // q is used: heads of a group divide 128
+  int split;               // V of long sequences comes by threads
 };
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int head, int token, int kb,
                                             uint32_t bar) {
   asm volatile(
@@ -272,6 +276,16 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int 
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(row), "r"(kb), "r"(group), "r"(page), "r"(bar)
       : "memory");
 }
+
+// Whether V comes by two warps, row by row, beside K by the TMA unit: the unit needs 100 to 150
+// cycles per box and 4 to 5 per row of 128 bytes, so with small boxes, and at head dim 64, it
+// alone is slower than the memory. One choice for a launch. Sequences that average 1000 tokens or
+// more (8 units of up to 128 rows) gain, 64 of 2000 tokens: head dim 64, pages of 8, 16, 32 and
+// 64, 231, 177, 152 and 140 us with V by TMA, 150, 131, 131 and 132 by threads; head dim 128 143,
+// 115, 103 and 98 and 105, 103, 103 and 103. Short ones wait longer for a V by threads (200
+// of 100 to 600 tokens, pages of 16, 78 us and 104), and with items of more than 128 rows the
+// tensor cores are the bound (64 of 2000 tokens, 256 rows, 156 us and 169).
+constexpr int SPLIT_COST = 8 * CutTc::C1 + CutTc::ITEM;
 
 template <int D, bool TMA>
 __global__ void __launch_bounds__(NTHREADS, 1)
@@ -294,7 +308,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (tid < C::N_BAR) {
     int n = 1;
     if (tid < C::Q_EMPTY) n = !TMA ? NLOAD : tm.q_tma ? 1 : 32;
-    else if (!TMA && tid >= C::L_FULL && tid < C::L_EMPTY) n = NLOAD;
+    else if ((!TMA || tm.split) && tid >= C::L_FULL && tid < C::L_EMPTY) n = NLOAD;
     if (tid >= C::P_HALF && tid <= C::ML) n = 4;
     if (!TMA && tid >= C::SEE) n = NLOAD / 32;
     mbar_init(bar(tid), n);
@@ -313,6 +327,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   TreeSeg w;
   TreeSegs<CutTc> sg;
   sg.begin(p, c);  // (without work the roles find nothing)
+  const bool split = TMA && tm.split && p.hdr->cost >= p.hdr->live * (int64_t)p.nkv * SPLIT_COST;
 
   if (warp == 0) {
     // ---------------- products: one thread
@@ -330,7 +345,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       auto next_slot = [&](int& at) {
         at = slot;
         if (!wait_1(bar(C::L_FULL + at), phase, p.err, abort)) return false;
-        if (!TMA) fence_proxy_async();  // what was copied by ordinary writes is read by the tensor core
+        if (!TMA || tm.split) fence_proxy_async();  // what was copied by ordinary writes is read by the tensor core
         if (++slot == NST) slot = 0, phase ^= 1;
         return true;
       };
@@ -462,6 +477,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int pos = 0; pos < 2 * nt; ++pos) {
         const bool newest = two || pos == 2 * nt - 1;  // of V: of the newest unit
         const bool is_v = two ? pos & 1 : newest || (pos > 0 && (pos & 1) == 0);
+        if (is_v && split) continue;
         const int n = nl + pos, s = n % NST;
         const int j = newest ? pos / 2 : is_v ? (pos - 2) / 2 : (pos + 1) / 2;
         const int left = w.q.len - (w.t0 + j) * TK;  // keys of the sequence from here on
@@ -489,7 +505,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           if (lane == 0) mbar_arrive(bar(C::SEE + at));
         }
-        if (lane == 0) mbar_arrive_expect_tx(full, C::TILE);
+        if (lane == 0) {
+          if (tm.split) mbar_arrive_n(full, NLOAD - 1);
+          mbar_arrive_expect_tx(full, C::TILE);
+        }
         __syncwarp();
         const int2 b = !is_v || newest ? now : before;
         const CUtensorMap* maps = is_v ? tm.v : tm.k;
@@ -517,17 +536,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       nl += 2 * nt;
     }
     if (!good) *abort = 1;
-  } else if (TMA && warp == 3) {
-    // ---------------- Q
+  } else if (TMA && warp < 4 && (warp == 3 || split)) {
+    // ---------------- Q, and V row by row
+    const int pw = warp - 2;
+    constexpr int NR = TQ / NLOAD;  // rows per lane: 32 (NR pw + i) + lane
     bool good = true;
-    int nq = 0;  // tiles so far
+    int nq = 0, nl = 0;  // query tiles, slots so far
     while (good && sg.next(p, w)) {
-      if (!tm.q_tma) {
-        good = copy_q<D>(p, w, sb, 0, 1, nq, abort);
-        continue;
-      }
+      if (warp == 3 && !tm.q_tma) good = copy_q<D>(p, w, sb, 0, 1, nq, abort);
       // (rows behind the item's last one: any queries)
-      for (int x = 0; x * TQ < w.rows && good; ++x, ++nq) {
+      for (int x = 0; warp == 3 && tm.q_tma && x * TQ < w.rows && good; ++x, ++nq) {
         const int tile = nq & 1;
         good = nq < 2 || wait_w(bar(C::Q_EMPTY + tile), ((nq >> 1) - 1) & 1, p.err, abort);
         if (good && lane == 0) {
@@ -537,6 +555,39 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         __syncwarp();
       }
+      if (!split) continue;
+      const int nt = w.t1 - w.t0, ahead = w.rows > TQ ? 1 : min(2, nt);
+      const int64_t table = (int64_t)w.q.s * p.ld_table;
+      // places of this lane's tokens of a unit, requested one unit ahead
+      int64_t off[NR];
+      auto find = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const int key = (w.t0 + j) * TK + (pw * NR + i) * 32 + lane;  // (lengths end well below 2^31)
+          off[i] = -1;
+          if (j < nt && key < w.q.len) {
+            const int e = key / p.page_size, page = p.table[table + e];  // (a bad one is reported with K)
+            if (page >= 0 && page < p.n_pages)
+              off[i] = page * p.s_page + (key - e * p.page_size) * p.s_tok + w.h * p.s_head;
+          }
+        }
+      };
+      find(0);
+#pragma unroll 1
+      for (int j = 0; j < nt && good; ++j) {
+        const int n = nl + (j < nt - ahead ? ahead + 2 * j : nt + j), s = n % NST;  // V_j's place
+        good = n < NST || wait_w(bar(C::L_EMPTY + s), (n / NST - 1) & 1, p.err, abort);
+        if (!good) break;
+        int64_t now[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) now[i] = off[i];
+        find(j + 1);
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+          copy_rows<D>(sR + s * C::TILE, (pw * NR + i) * 32, static_cast<const bf16*>(p.v), now[i], C::GROUP, 1024);
+        cp_async_arrive(bar(C::L_FULL + s));
+      }
+      nl += 2 * nt;
     }
     if (!good) *abort = 1;
     cp_async_commit();
@@ -882,6 +933,7 @@ mgb_status launch_d(const TreeParams& p, cudaStream_t st) {
     if (tmap_encode_bf16_nd(&tm.q, p.q, 4, dims, strides, box) != CUDA_SUCCESS) return MGB_ERR_CUDA;
   }
   while (tm.shift < 7 && p.page_size % (2 << tm.shift) == 0) ++tm.shift;
+  tm.split = tm.shift <= (D == 64 ? 6 : 4) && (int64_t)p.tokens * p.G <= (int64_t)p.n * TQ;
   if (encode_pool(tm.k, p.k, p, D, tm.shift) != MGB_OK || encode_pool(tm.v, p.v, p, D, tm.shift) != MGB_OK)
     return MGB_ERR_CUDA;
   return launch_k<D, true>(p, tm, st);

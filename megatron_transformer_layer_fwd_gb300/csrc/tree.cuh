@@ -91,7 +91,7 @@ TreeCut tree_cut(int n, int tokens, int nq, int nkv, int d, int table);
 TreeLayout tree_layout(int n, int tokens, int nq, int nkv, int d);
 
 struct TreeParams {
-  int nq, nkv, G, tokens;
+  int n, nq, nkv, G, tokens;
   const TreeHeader* hdr;
   const TreeStart* start;
   const TreeSplit* split;

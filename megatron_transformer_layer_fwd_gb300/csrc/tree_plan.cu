@@ -529,7 +529,7 @@ mgb_status mgb_attention_tree(const mgb_attention_tree_plan* plan, const mgb_kv_
   const TreeLayout l = tree_layout(n, plan->tokens, nq, nkv, d);
   char* b = static_cast<char*>(plan->ws);
   TreeParams p{};
-  p.nq = nq; p.nkv = nkv; p.G = nq / nkv; p.tokens = plan->tokens;
+  p.n = n; p.nq = nq; p.nkv = nkv; p.G = nq / nkv; p.tokens = plan->tokens;
   const int table = c->dtype == MGB_F32 ? 1 : 0;
   const bool narrow = tree_cut(n, plan->tokens, nq, nkv, d, table).narrow;
   const TreeTable& t = l.table[table];

@@ -137,6 +137,17 @@ def test_items_of_one_unit_between_longer_ones(dtype, d):
     _run(37, dtype, 4, 2, d, 32, _mixed(rng, sorted(ctx), [20] * 40))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page,head_major", [(8, False), (16, True), (24, False), (32, False), (64, True)])
+def test_long_sequences_over_small_pages(d, page, head_major):
+    """Batches that average more than 1000 tokens, short sequences and one with two halves of
+    rows among them; groups of 2 and of 3 heads."""
+    rng = np.random.default_rng(38)
+    seqs = _mixed(rng, [2500, 1517, 30, None, 900, 4001, 1150], [12, 40, 70, 3, 100, 5, 1], roots=2)
+    for nq, nkv in ((4, 2), (3, 1)):
+        _run(39, "bf16", nq, nkv, d, page, seqs, head_major, tail=2)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_chains_need_no_parents(dtype):
     _run(16, dtype, 4, 2, 128, 16, [(30, drafts.chain(256)), (None, drafts.chain(2)), (130, drafts.chain(1)),
@@ -211,6 +222,28 @@ def test_tokens_of_a_bad_page_are_left_out(dtype, entry):
     ref, ref_lse, a, m = drafts.tree_attention(q, c.k, c.v, np.where(c.table == entry, 0, c.table), b.cu, b.lens,
                                                b.trees)
     check_attention(o[on], lse[on], ref[on], ref_lse[on], a[on], m[on], np.full((3, 2), 64), 64, dtype)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_bad_pages_of_long_sequences_are_left_out(d):
+    gone = [0, 17, 99, 100, 140]
+
+    def spoil(b, c):
+        c.table[0][gone] = [-1, 10 ** 6, -1, -7, 2 ** 31 - 1]
+    o, lse, b, c, q = _bad([(1200, drafts.chain(9)), (1100, drafts.chain(12))], d=d, page=8, spoil=spoil)
+    n = 1209
+    keep = np.array([p for p in range(n) if p // 8 not in gone])
+    k, v = (x[c.table[0][keep // 8], keep % 8] for x in (c.k, c.v))
+    seen = keep[None, :] <= np.arange(1200, n)[:, None]
+    for h in range(2):
+        sc = np.where(seen, q[:9, h] @ k[:, 0].T / np.sqrt(d), -np.inf)
+        p = np.exp(sc - sc.max(1, keepdims=True))
+        p /= p.sum(1, keepdims=True)
+        assert (np.abs(o[:9, h] - p @ v[:, 0]) <= 2.0 ** -7 * (p @ np.abs(v[:, 0]))).all()
+    on = np.arange(9, 21)
+    table = np.where((c.table < 0) | (c.table >= len(c.k)), 0, c.table)
+    ref, ref_lse, a, m = drafts.tree_attention(q, c.k, c.v, table, b.cu, b.lens, b.trees)
+    check_attention(o[on], lse[on], ref[on], ref_lse[on], a[on], m[on], np.full((12, 2), 1112), d, "bf16")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
