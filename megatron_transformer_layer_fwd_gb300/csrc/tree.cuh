@@ -27,9 +27,13 @@ constexpr int TREE_LONGEST = INT32_MAX - 1024;  // cached tokens (so that keys b
 // The cuts for many rows: keys of a unit, rows of an item, units of an item that is never split,
 // its fixed cost, CTAs, and the cost of a unit by the item's rows. A range costs at least one
 // unit, so that none between two others is empty.
+// bf16: more than 64 rows keep the warps busy whose schedulers run the loaders too, which with pages
+// of 16 slots takes up to a fifth longer, with large pages nothing: 9 / 8 is between (32
+// sequences of 33 to 16000 tokens, 8 to 96 rows: with one cost for both 61 us at pages of 16 and
+// 54.7 at 64, with 9 / 8 57.4 and 55.0, with 10 / 8 57.2 and 55.4). Two halves: 4550 cycles at head dim 128, one 2612.
 struct CutTc {
-  static constexpr int KEYS = 128, ROWS = 256, WHOLE = 2, ITEM = 8, RANGES = 152;
-  static constexpr int R1 = 128, R2 = 128, C1 = 4, C2 = 4, C3 = 7;  // (2612 and 4550 cycles at head dim 128)
+  static constexpr int KEYS = 128, ROWS = 256, WHOLE = 2, ITEM = 16, RANGES = 152;
+  static constexpr int R1 = 64, R2 = 128, C1 = 8, C2 = 9, C3 = 14;
 };
 template <int D>
 struct CutF32 {
