@@ -19,6 +19,14 @@ __host__ __device__ constexpr int unit_tokens(int d) { return d == 64 ? 128 : 64
 // with 4 at D = 128, 59.7 with 8, 64 with 12; D = 64, to 1200 tokens, 45 with 2, 47 with 6
 __host__ __device__ constexpr int item_cost(int d) { return d == 64 ? 2 : 4; }
 constexpr int UNIT = 4;                // cost of a unit
+// .. of an item of drafted tokens. bf16, head dim 64, 16 heads, 96 sequences of 20 to 1200
+// tokens: 38.3 us with 2, 33.6 with 4, 31.9 with 8, 32.6 with 12; head dim 128 75, 65, 55.9 and
+// 56.4 with 4, 6, 10 and 16, and 32 query and 8 KV heads, 64 of 33 to 4000 69.6, 60.8, 54.1,
+// 52.4 and 54.4 with 4, 6, 10, 12 and 16. float32, whose products take longer: 47.6, 52.5 and 50.5
+// with 2, 4 and 6 (96 of 20 to 600, head dim 64), 71.4, 68.3, 69.3 and 72.2 with 2, 4, 6 and 8 (128).
+__host__ __device__ constexpr int tree_item_cost(int d, bool bf) {
+  return !bf ? item_cost(d) : d == 64 ? 8 : 12;
+}
 constexpr int PARTS = 16;              // of a split item, joined at a time (at most 32)
 constexpr int WHOLE = 4;               // units of an item that is never split
 constexpr int MIN_CHUNK = 2 * UNIT;    // of a CTA (at least UNIT: no CTA between two others is empty)
@@ -103,9 +111,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 }
 
 // Position in a CTA's range of units of TK tokens. TREE: of drafted tokens.
-template <int D, bool TREE>
+template <typename T, int D, bool TREE>
 struct Cursor {
-  static constexpr int TK = unit_tokens(D);
+  static constexpr int TK = unit_tokens(D), ITEM = TREE ? tree_item_cost(D, sizeof(T) == 2) : item_cost(D);
   int64_t at;  // the item on the cost axis
   int s, h, t, nt, len, next_len;
   TreeSeq q, nq;  // TREE: sequences s and s + 1 of the plan's
@@ -143,7 +151,7 @@ struct Cursor {
   __device__ void next(const Params& p) {
     if (len <= p.cap && ++t < nt) return;
     t = 0;
-    at += cost_of(nt, item_cost(D));
+    at += cost_of(nt, ITEM);
     if (++h < (TREE ? per * p.nkv : p.groups)) return;
     h = 0;
     ++s;
@@ -200,7 +208,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) paged_rows_kernel(const Pa
   const int c = blockIdx.x;
   pdl_wait();  // everything the call reads may come from the kernel before
   Header hd;
-  Cursor<D, TREE> ld, cu;
+  Cursor<T, D, TREE> ld, cu;
   int64_t end;
   if constexpr (TREE) {
     const TreeHeader th = *p.thdr;
@@ -280,7 +288,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) paged_rows_kernel(const Pa
 
   // ---------------- queries: the next item's are requested one item ahead
   // row r of the cursor's group: its offset in q (or, with the strides of o, in o), or -1
-  auto row_at = [&](const Cursor<D, TREE>& x, int r, int64_t ld_row) -> int64_t {
+  auto row_at = [&](const Cursor<T, D, TREE>& x, int r, int64_t ld_row) -> int64_t {
     const int per = x.per_kv(p), kv = x.h / per, first = (x.h - kv * per) * p.rows + r;
     if constexpr (TREE) {
       if (r >= p.rows || first >= x.q.m * p.G) return -1;
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) paged_rows_kernel(const Pa
   constexpr int HT = BF ? NR / 8 : 1;  // bf16: tiles of 8 query heads
   constexpr int NQ = BF ? D / 16 * 2 * HT : (NR * D / 4 + NT - 1) / NT * 4;
   uint32_t qn[NQ];
-  auto request_q = [&](const Cursor<D, TREE>& at) {
+  auto request_q = [&](const Cursor<T, D, TREE>& at) {
     const T* qs = static_cast<const T*>(p.q);
     if constexpr (BF) {
 #pragma unroll
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) paged_rows_kernel(const Pa
 
   int n_use = 0;  // stages consumed
   while (cu.before(end)) {
-    const Cursor<D, TREE> it = cu;  // the item
+    const Cursor<T, D, TREE> it = cu;  // the item
     const int nt = cu.nt, t0 = cu.t;
     const int len = cu.len <= p.cap ? cu.len : 0;
     if (cu.len > p.cap && tid == 0) record_error(p.err, kErrIndex);
@@ -344,7 +352,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(D)) paged_rows_kernel(const Pa
       __syncthreads();
     }
     {  // the next item's queries
-      Cursor<D, TREE> nx = cu;
+      Cursor<T, D, TREE> nx = cu;
       nx.t = nx.nt - 1;
       nx.next(p);
       if (nx.before(end) && (!TREE || nx.s < nx.n)) request_q(nx);

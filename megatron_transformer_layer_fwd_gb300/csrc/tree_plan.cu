@@ -377,12 +377,17 @@ mgb_status check_shape(int n, int tokens, int nq, int nkv, int d) {
 
 // Rows per sequence up to which, on average, the decode step's kernel is taken, which streams
 // through the caches of many short items at a time but reads a sequence again for every 16 rows.
-// bf16: 96 sequences, 16 heads of 64, 3 rows 53 us (by the tcgen05 kernel 90); 200 of 100 to
-// 600 tokens, 8 KV heads of 128, 16 rows 112 (86); 64 of 2000, 16 rows each 96 (98). float32, 4
-// heads of 128, 8 rows: 8 of 2000 32 us (the tiled kernel 34), 64 of 100 to 1000 52 (57); 16 rows
-// 38 (34), 59 (57); 32 rows 52 (43).
-constexpr int FEW_ROWS = 10;
-constexpr int EIGHT_ROWS = 5;  // .. and up to which its items have 8 rows, else 16
+// bf16, head dim 64, 16 heads: 64 sequences of 2000 tokens, 12 rows 93 us (by the tcgen05 kernel
+// 131), 16 rows 95 (131), 24 174 (131); 200 of 100 to 600 90 (138), 94 (140), 164 (141). Head dim 128,
+// 8 KV heads: 10 rows 93 (94) and 77 (80), 12 rows 92 (94) and 71 (79), but 4 to 20 rows, some of
+// them read twice, 109 (96) and 86 (81). float32, 4 heads of 128, 64 of 2000: 12 rows 166
+// (by the tiled kernel 213); 64 of 100 to 600 50 (46).
+constexpr int few_rows(int d, int table) { return table == 0 && d == 64 ? 16 : 10; }
+// .. and up to which its items have 8 rows, else 16. 8 rows each, 64 of 2000 and 200 of 100 to 600
+// tokens: bf16 86.4 and 57 us at head dim 64 (as 16 rows 89 and 71), 86.6 and 54 at 128 (87.5
+// and 61), float32 97 (162). 1 to 15 rows, some in two items: bf16, head dim 64, 117 and 64 (100
+// and 80).
+constexpr int EIGHT_ROWS = 8;
 
 template <typename Cut>
 TreeCut cut_of() {
@@ -392,9 +397,9 @@ TreeCut cut_of() {
 
 TreeCut tree_cut(int n, int tokens, int nq, int nkv, int d, int table) {
   const int64_t rows = (int64_t)tokens * (nq / nkv);
-  if (rows <= (int64_t)FEW_ROWS * n)
-    return TreeCut{1, unit_tokens(d), rows <= (int64_t)EIGHT_ROWS * n ? 8 : MAXR, MAXR, MAXR, UNIT, UNIT, UNIT, item_cost(d), WHOLE, MIN_CHUNK,
-                   SMS * ctas_per_sm(d)};
+  if (rows <= (int64_t)few_rows(d, table) * n)
+    return TreeCut{1, unit_tokens(d), rows <= (int64_t)EIGHT_ROWS * n ? 8 : MAXR, MAXR,
+                   MAXR, UNIT, UNIT, UNIT, tree_item_cost(d, table == 0), WHOLE, MIN_CHUNK, SMS * ctas_per_sm(d)};
   if (table == 0) return cut_of<CutTc>();
   return d == 64 ? cut_of<CutF32<64>>() : cut_of<CutF32<128>>();
 }
