@@ -31,8 +31,10 @@ constexpr int TREE_LONGEST = INT32_MAX - 1024;  // cached tokens (so that keys b
 // of 16 slots takes up to a fifth longer, with large pages nothing: 9 / 8 is between (32
 // sequences of 33 to 16000 tokens, 8 to 96 rows: with one cost for both 61 us at pages of 16 and
 // 54.7 at 64, with 9 / 8 57.4 and 55.0, with 10 / 8 57.2 and 55.4). Two halves: 4550 cycles at head dim 128, one 2612.
+// An item's fixed cost, 64 sequences of 33 to 4000 tokens, 240 rows: 127, 113, 97 and 96 us with 8,
+// 16, 24 and 32, 20 rows 76, 67.7, 68.2 and 70.7.
 struct CutTc {
-  static constexpr int KEYS = 128, ROWS = 256, WHOLE = 2, ITEM = 16, RANGES = 152;
+  static constexpr int KEYS = 128, ROWS = 256, WHOLE = 2, ITEM = 24, RANGES = 152;
   static constexpr int R1 = 64, R2 = 128, C1 = 8, C2 = 9, C3 = 14;
 };
 template <int D>
