@@ -22,12 +22,11 @@
 // unit, a box of up to 128 slots of one page at a time; others row by row with 16-byte
 // asynchronous copies. Tokens behind the length or of a bad page are not read: zeros stand
 // in their place, and a bit per key says that no row sees them.
+#include <cudaTypedefs.h>
+
 #include "tree.cuh"
 
 namespace mgb {
-
-CUresult tmap_encode_bf16_nd(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
-                             const uint64_t* strides, const uint32_t* box);
 
 namespace {
 
@@ -890,6 +889,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
+  }();
+  return fn;
+}
+
+// bf16 tensor map with 128-byte swizzle and zero fill; strides (bytes) of the dimensions behind
+// the first.
+bool encode_map(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box) {
+  const auto fn = encode_fn();
+  if (!fn) return false;
+  const uint32_t es[5] = {1, 1, 1, 1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Whether the TMA unit can copy: pages of a multiple of 8 slots (and sizes that its numbers hold).
 bool tma_ok(const TreeParams& p, int d) {
   const int64_t most = (int64_t)1 << 31;
@@ -906,7 +929,7 @@ mgb_status encode_pool(CUtensorMap (&tm)[3], const void* pool, const TreeParams&
   const uint32_t kb = (uint32_t)(d / 64);
   const uint32_t box[3][5] = {{64, 8, kb, 1u << (shift - 3), 1}, {64, 8, kb, 1, 1}, {64, 1, 1, 1, 1}};
   for (int i = 0; i < 3; ++i)
-    if (tmap_encode_bf16_nd(&tm[i], pool, 5, dims, strides, box[i]) != CUDA_SUCCESS) return MGB_ERR_CUDA;
+    if (!encode_map(&tm[i], pool, 5, dims, strides, box[i])) return MGB_ERR_CUDA;
   return MGB_OK;
 }
 
@@ -930,7 +953,7 @@ mgb_status launch_d(const TreeParams& p, cudaStream_t st) {
     const uint64_t dims[4] = {(uint64_t)(p.nkv - 1) * p.G * D + 64, (uint64_t)p.G, (uint64_t)p.tokens, D / 64};
     const uint64_t strides[3] = {2 * D, 2 * (uint64_t)(p.tokens > 1 ? p.ld_q : p.nq * D), 128};
     const uint32_t box[4] = {64, (uint32_t)p.G, (uint32_t)(128 / p.G), D / 64};
-    if (tmap_encode_bf16_nd(&tm.q, p.q, 4, dims, strides, box) != CUDA_SUCCESS) return MGB_ERR_CUDA;
+    if (!encode_map(&tm.q, p.q, 4, dims, strides, box)) return MGB_ERR_CUDA;
   }
   while (tm.shift < 7 && p.page_size % (2 << tm.shift) == 0) ++tm.shift;
   tm.split = tm.shift <= (D == 64 ? 6 : 4) && (int64_t)p.tokens * p.G <= (int64_t)p.n * TQ;

@@ -1428,25 +1428,6 @@ CUresult tmap_encode_f32_2d(CUtensorMap* tm, const void* base, uint64_t inner, u
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-// bf16 tensor map of any rank with 128-byte swizzle and zero fill; strides (bytes) of the
-// dimensions behind the first.
-CUresult tmap_encode_bf16_nd(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
-                             const uint64_t* strides, const uint32_t* box) {
-  auto fn = encode_fn();
-  if (!fn) return CUDA_ERROR_NOT_INITIALIZED;
-  cuuint64_t d[5], st[4];
-  cuuint32_t b[5], es[5];
-  for (int i = 0; i < rank; ++i) {
-    d[i] = dims[i];
-    b[i] = box[i];
-    es[i] = 1;
-    if (i > 0) st[i - 1] = strides[i - 1];
-  }
-  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-}
-
 // 2-D uint32 tensor map without swizzle (box rows of box_inner words).
 CUresult tmap_encode_u32_2d(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer,
                             int64_t ld, uint32_t box_inner, uint32_t box_outer) {
