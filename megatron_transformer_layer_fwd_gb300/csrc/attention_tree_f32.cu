@@ -7,6 +7,10 @@
 // the output, two FMAs per instruction. K of the next tile is copied while the softmax
 // and the second product run, V of this one while the scores are formed. Tokens of a
 // bad page and behind the length are zeros in shared memory (never read) and hidden.
+//
+// Bound: the 16-byte reads of Q, K, V and P from shared memory, one per 2 to 8 paired FMAs. 8 sequences to 3000 tokens, 16 query and 4 KV heads of
+// 128, 12 to 80 rows 29 us (HBM 5); 64 of 2000, 20 rows 281 us; one of 20000, 240 rows 301 us, 33
+// TFLOP/s. (K and V in two buffers each, one block per SM: no gain.)
 #include "tree.cuh"
 
 namespace mgb {

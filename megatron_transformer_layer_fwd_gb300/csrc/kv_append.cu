@@ -122,7 +122,8 @@ __device__ __forceinline__ void rotate(uint4& w0, uint4& w1,
   w1 = Vec<T>::pack(y);
 }
 
-// TREE: drafted tokens of a plan
+// TREE: drafted tokens of a plan, whose place is one read away (64 sequences of 4 to 61, 39 MB, 9.7
+// us; 7 tokens 2.0)
 template <typename T, int UB, bool INTER, bool TREE>
 __global__ void __launch_bounds__(UB == 1 ? FEW_THREADS : MANY_THREADS, UB == 1 ? 1 : 8)
     kv_append_kernel(const AppendParams p) {

