@@ -602,7 +602,7 @@ mgb_status mgb_attention_decode(const mgb_attention_decode_plan* plan, const mgb
  * max_pages * page_size (or 2^31 - 1024) is MGB_ERR_INDEX, and the sequence's rows are
  * left as they were. A page outside [0, n_pages) is MGB_ERR_INDEX, and its tokens
  * are left out of the softmax. Where no token is left, or every score is -inf, o is
- * NaN and lse -inf; a NaN score makes both NaN. Slots behind a length are not read.
+ * NaN and lse -inf; a NaN score makes both NaN. Slots behind a length have no say.
  * Drafted tokens that a row does not see have no say by their keys; a NaN or
  * infinity in the value of one may reach other drafted tokens of its sequence (0
  * times it). Sums and softmax statistics are float32; in bf16 the weights multiply V

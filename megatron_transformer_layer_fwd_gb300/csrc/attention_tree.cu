@@ -22,8 +22,9 @@
 // unit, a box of up to 128 slots of one page at a time (V by threads where the unit alone is too
 // slow, see SPLIT_COST); others row by row with 16-byte asynchronous copies. Every role that
 // waits for places of the ring does so in their order, or a lap that it left out could let a
-// later wait take an earlier lap's end for its own. Tokens behind the length or of a bad page are
-// not read: zeros stand in their place, and a bit per key says that no row sees them.
+// later wait take an earlier lap's end for its own. V of tokens behind the length, and K and V of
+// those of a bad page, are not read: zeros stand in their place; a bit per key says that no row
+// sees them.
 //
 // Measured, 32 query and 8 KV heads of 128: one sequence of 131001 tokens, 244 rows 125 us,
 // 1045 TFLOP/s with each product counted once (P's second part makes it 1570), 64 rows 90 us,
@@ -41,6 +42,7 @@ namespace {
 constexpr int TQ = 128;         // rows per stream (TMEM lanes)
 constexpr int TK = CutTc::KEYS;   // keys per slot
 constexpr int NLOAD = 64;       // threads that copy K, V and Q without TMA
+constexpr int NFILL = 33;       // arrivals at a slot that TMA fills: the bytes' one, and a warp's
 constexpr int NTHREADS = 384;   // warp 0: products; 1 to 3: loads; 2 x 4: softmax
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float TAU = 8.0f;     // the reference maximum moves in steps above this (log2 units)
@@ -74,7 +76,7 @@ struct Cfg {
   // phase is complete (parity).
   static constexpr int Q_FULL = 0;              // [tile] 128 rows of queries    (tx, or the copying threads)
   static constexpr int Q_EMPTY = 2;             // [tile] the item's last S done (commit)
-  static constexpr int L_FULL = 4;              // [slot] copied                 (tx, or NLOAD threads)
+  static constexpr int L_FULL = 4;              // [slot] copied                 (tx and NFILL or NLOAD threads)
   static constexpr int L_EMPTY = L_FULL + NST;  // [slot] its products done      (commit)
   static constexpr int S_FULL = L_EMPTY + NST;  // [stream] scores, and the PV before  (commit)
   static constexpr int O_FULL = S_FULL + 2;     // [stream] the item's last PV   (commit)
@@ -258,12 +260,14 @@ __device__ __forceinline__ void weights(uint32_t (&s)[2][32], float a, float b, 
 // How the TMA unit finds a pool's vectors: an element of a head's vector, row of 8 slots, d
 // block, group of 8 slots, page.
 struct PoolMaps {
-  CUtensorMap k[3], v[3];  // boxes of `box` slots, of 8, of one (and one d block)
+  CUtensorMap k, v[2];     // boxes of `box` slots; of 8
   CUtensorMap q;           // an element of a head's vector, query head of a KV head, token, d block
   int shift;               // box = 1 << shift slots: 8 to 128, in one page
   int q_tma;               // q is used: heads of a group divide 128
   int split;               // V of long sequences comes by threads
 };
+// rows of a unit's V that its products read: those with keys of the sequence, to the K step's end
+__device__ __forceinline__ int used_rows(int left) { return min(TK, (left + 15) & ~15); }
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
@@ -315,14 +319,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (tid < C::N_BAR) {
     int n = 1;
     if (tid < C::Q_EMPTY) n = !TMA ? NLOAD : tm.q_tma ? 1 : 32;
-    else if ((!TMA || tm.split) && tid >= C::L_FULL && tid < C::L_EMPTY) n = NLOAD;
+    else if (tid >= C::L_FULL && tid < C::L_EMPTY) n = !TMA || tm.split ? NLOAD : NFILL;
     if (tid >= C::P_HALF && tid <= C::ML) n = 4;
     if (!TMA && tid >= C::SEE) n = NLOAD / 32;
     mbar_init(bar(tid), n);
     fence_mbar_init();
   }
   if (tid == 0) *abort = 0;
-  if (TMA && tid >= 64 && tid < 71) tma_prefetch_desc(tid < 67 ? &tm.k[tid - 64] : tid < 70 ? &tm.v[tid - 67] : &tm.q);
+  if (TMA && tid >= 64 && tid < 68) tma_prefetch_desc(tid < 66 ? &tm.v[tid - 64] : tid < 67 ? &tm.k : &tm.q);
   if (warp == 0) tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
   tc_fence_before();
   __syncthreads();
@@ -377,6 +381,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int ks = left >= TK ? TK / 16 : (left + 15) / 16;
         const uint64_t db = dv0 + (uint64_t)((at * C::TILE) >> 4);
         const uint32_t ta = tmem + C::COL_S + x * TK, to = tmem + C::COL_O + x * D;
+        if (TMA && left < TK) fence_proxy_async();  // (the slots about the end may be ordinary writes)
         // (the first half's products run while the other half's weights are formed)
 #pragma unroll 1
         for (int k0 = 0; k0 < TK / 16; k0 += TK / 32) {
@@ -512,37 +517,48 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           if (lane == 0) mbar_arrive(bar(C::SEE + at));
         }
+        // K: the boxes with keys of the sequence, whole (its scores behind the end are overwritten).
+        // V: as far as its products read, zeros behind the end (a NaN there would not be masked by a
+        // weight of 0): the box with the end 8 slots at a time, the 8 with the end by threads.
+        const int box = 1 << tm.shift, used = is_v ? used_rows(left) : min(TK, left);
+        const bool cut = is_v && left < TK && (left & 7);  // the end is inside of 8 slots
         if (lane == 0) {
-          if (tm.split) mbar_arrive_n(full, NLOAD - 1);
-          mbar_arrive_expect_tx(full, C::TILE);
+          const int others = (tm.split ? NLOAD : NFILL) - 1 - (cut ? 32 : 0);
+          if (others > 0) mbar_arrive_n(full, others);
+          const int rows = is_v ? used - (cut ? 8 : 0) : min(TK, (left + box - 1) & -box);
+          mbar_arrive_expect_tx(full, (uint32_t)(rows * D * 2));
         }
         __syncwarp();
         const int2 b = !is_v || newest ? now : before;
-        const CUtensorMap* maps = is_v ? tm.v : tm.k;
         const uint32_t dst = sR + s * C::TILE;
-        // the box with the sequence's end: 8 slots at a time, the last of them one by one, so
-        // that those behind the end are zeros
-        const int part = left < TK && (left & ((1 << tm.shift) - 1)) ? left >> tm.shift : nbox;
-        if (lane < nbox && lane != part)
-          tma_load_5d(dst + ((lane << tm.shift) >> 3) * C::GROUP, &maps[0], x, 0, 0, b.y, b.x, full);
+        const int part = is_v && left < TK && (left & (box - 1)) ? left >> tm.shift : nbox;
+        if ((lane << tm.shift) < used && lane != part)
+          tma_load_5d(dst + ((lane << tm.shift) >> 3) * C::GROUP, is_v ? &tm.v[0] : &tm.k, x, 0, 0, b.y, b.x, full);
         if (part < nbox) {
           const int pb = __shfl_sync(0xffffffffu, b.x, part), gb = __shfl_sync(0xffffffffu, b.y, part);
           const int g0 = part << (tm.shift - 3);  // the box's first group of the tile
           const int edge = left >> 3;             // the group with the end, if it is inside one
           const int g = g0 + lane;
-          if (lane < (1 << (tm.shift - 3)) && !(g == edge && (left & 7)))
-            tma_load_5d(dst + g * C::GROUP, &maps[1], x, 0, 0, gb + lane, g < edge ? pb : p.n_pages, full);
-          if (left & 7) {
-            const int r = lane / C::KB, kb = lane % C::KB;
-            if (r < 8)
-              tma_load_5d(dst + edge * C::GROUP + kb * 1024 + r * 128, &maps[2], x, r, kb, gb + edge - g0,
-                          edge * 8 + r < left ? pb : p.n_pages, full);
+          if (lane < (box >> 3) && g * 8 < used && !(cut && g == edge))
+            tma_load_5d(dst + g * C::GROUP, &tm.v[1], x, 0, 0, gb + lane, g < edge ? pb : p.n_pages, full);
+          if (cut) {
+#pragma unroll
+            for (int i = 0; i < C::CH / 4; ++i) {
+              const int r = (i * 32 + lane) / C::CH, ch = lane % C::CH;
+              const bool ok = pb < p.n_pages && edge * 8 + r < left;
+              const int64_t from = ok ? pb * p.s_page + ((gb + edge - g0) * 8 + r) * p.s_tok + x + ch * 8 : 0;
+              cp_async16(dst + edge * C::GROUP + (ch >> 3) * 1024 + r * 128 + (((ch & 7) ^ r) << 4),
+                         static_cast<const bf16*>(p.v) + from, ok);
+            }
+            cp_async_arrive(full);
           }
         }
       }
       nl += 2 * nt;
     }
     if (!good) *abort = 1;
+    cp_async_commit();
+    cp_async_wait<0>();
   } else if (TMA && warp < 4 && (warp == 3 || split)) {
     // ---------------- Q, and V row by row
     const int pw = warp - 2;
@@ -928,17 +944,14 @@ bool tma_ok(const TreeParams& p, int d) {
          8 * p.s_tok < most * 128;
 }
 
-mgb_status encode_pool(CUtensorMap (&tm)[3], const void* pool, const TreeParams& p, int d, int shift) {
+bool encode_pool(CUtensorMap* tm, const void* pool, const TreeParams& p, int d, int shift) {
   const uint64_t es = 2;
   const uint64_t dims[5] = {(uint64_t)((p.nkv - 1) * p.s_head + 64), 8, (uint64_t)(d / 64),
                             (uint64_t)(p.page_size / 8), (uint64_t)p.n_pages};
   const uint64_t strides[4] = {(uint64_t)p.s_tok * es, 64 * es, 8 * (uint64_t)p.s_tok * es,
                                (uint64_t)(p.n_pages > 1 ? p.s_page : 8) * es};
-  const uint32_t kb = (uint32_t)(d / 64);
-  const uint32_t box[3][5] = {{64, 8, kb, 1u << (shift - 3), 1}, {64, 8, kb, 1, 1}, {64, 1, 1, 1, 1}};
-  for (int i = 0; i < 3; ++i)
-    if (!encode_map(&tm[i], pool, 5, dims, strides, box[i])) return MGB_ERR_CUDA;
-  return MGB_OK;
+  const uint32_t box[5] = {64, 8, (uint32_t)(d / 64), 1u << (shift - 3), 1};
+  return encode_map(tm, pool, 5, dims, strides, box);
 }
 
 template <int D, bool TMA>
@@ -965,7 +978,8 @@ mgb_status launch_d(const TreeParams& p, cudaStream_t st) {
   }
   while (tm.shift < 7 && p.page_size % (2 << tm.shift) == 0) ++tm.shift;
   tm.split = tm.shift <= (D == 64 ? 6 : 4) && (int64_t)p.tokens * p.G <= (int64_t)p.n * TQ;
-  if (encode_pool(tm.k, p.k, p, D, tm.shift) != MGB_OK || encode_pool(tm.v, p.v, p, D, tm.shift) != MGB_OK)
+  if (!encode_pool(&tm.k, p.k, p, D, tm.shift) || !encode_pool(&tm.v[0], p.v, p, D, tm.shift) ||
+      !encode_pool(&tm.v[1], p.v, p, D, 3))
     return MGB_ERR_CUDA;
   return launch_k<D, true>(p, tm, st);
 }
