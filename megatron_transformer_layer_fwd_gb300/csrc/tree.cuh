@@ -174,8 +174,8 @@ struct TreeSegs {
       if (at + tree_begin<Cut>(t, nt, rows) >= end) return false;
       w.q = cur;
       w.h = h; w.b = b; w.at = at; w.nt = nt; w.t0 = t; w.rows = rows;
-      const int64_t left = (end - at + unit - 1) / unit;
-      w.t1 = nt > Cut::WHOLE && left < nt ? (int)left : nt;
+      const int64_t room = end - at;  // (a division only where the range ends inside the item)
+      w.t1 = nt > Cut::WHOLE && room <= (int64_t)(nt - 1) * unit ? (int)((room + unit - 1) / unit) : nt;
       const bool skip = cur.len > p.cap;
       t = 0;
       at += (int64_t)nt * unit + Cut::ITEM;
