@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(PT) tree_prepare_kernel(const __grid_constant_
       len = a.lens[s];
       ok = pair_ok(a, s, c0, c1);
     }
-    // the first bad offset of this round
+    // the first bad offset among these
     __shared__ int first_bad;
     if (tid == 0) first_bad = INT32_MAX;
     __syncthreads();
