@@ -152,11 +152,13 @@ def test_plans_on_streams_of_their_own():
     assert mgb.mgb_device_status() == mgb.MGB_OK
 
 
-def test_one_plan_for_layers_of_two_types_and_in_two_graphs():
-    """Caches of both types under one plan, in two graphs that are replayed by turns."""
+@pytest.mark.parametrize("d,sizes", [(128, (20, 33, 5)), (64, (2, 3, 4)), (64, (20, 33, 5)), (128, (1, 2, 1))])
+def test_one_plan_for_layers_of_two_types_and_in_two_graphs(d, sizes):
+    """Caches of both types under one plan, in two graphs that are replayed by turns; with twelve
+    rows per sequence at head dim 64 the types go to different kernels."""
     rng = np.random.default_rng(64)
-    nq, nkv, d = 8, 2, 128
-    b = Batch([(2500, random_tree(rng, 20)), (17, random_tree(rng, 33)), (400, random_tree(rng, 5))])
+    nq, nkv = 8, 2
+    b = Batch([(x, random_tree(rng, m)) for x, m in zip((2500, 17, 400), sizes)])
     plan = b.plan(nq, nkv, d)
     layers = []
     for dtype in ("bf16", "f32", "bf16"):
