@@ -18,17 +18,17 @@
 //
 // K and V come through a ring of slots of 128 keys in the order in which the products need
 // them: K_0, V_0, K_1, .., or, where the streams take the units in turn, K_0, K_1, V_0, K_2, V_1,
-// .. Pages of a multiple of 8 slots are copied by the TMA
-// unit, a box of up to 128 slots of one page at a time (V by threads where the unit alone is too
-// slow, see SPLIT_COST); others row by row with 16-byte asynchronous copies. Every role that
+// .. Pages of a multiple of 8 slots are copied by the TMA unit, a box of up to 128 slots of one
+// page at a time (V by threads where the unit alone is too slow, see SPLIT_COST); others row by
+// row with 16-byte asynchronous copies. Every role that
 // waits for places of the ring does so in their order, or a lap that it left out could let a
 // later wait take an earlier lap's end for its own. V of tokens behind the length, and K and V of
 // those of a bad page, are not read: zeros stand in their place; a bit per key says that no row
 // sees them.
 //
-// Measured, 32 query and 8 KV heads of 128: one sequence of 131001 tokens, 244 rows 125 us,
-// 1045 TFLOP/s with each product counted once (P's second part makes it 1570), 64 rows 90 us,
-// 6.0 TB/s; 32 sequences of 33 to 16000 tokens, 8 to 96 rows 58 us, 4.5 TB/s; two of 7000 to
+// Measured, 32 query and 8 KV heads of 128: one sequence of 131001 tokens, 244 rows 125 to 130
+// us, 1010 to 1045 TFLOP/s with each product counted once (P's second part makes it half as much
+// again), 64 rows 90 to 94 us, 5.7 to 6.0 TB/s; 32 sequences of 33 to 16000 tokens, 8 to 96 rows 58 us, 4.5 TB/s; two of 7000 to
 // 9000 with 1024 rows each 69 us. Bound: with two halves of rows the tensor cores, 101 of the
 // 125 us at the rate of a large product (start and join 10); with one the HBM.
 #include <cudaTypedefs.h>
