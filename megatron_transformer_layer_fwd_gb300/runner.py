@@ -109,6 +109,14 @@ def _on(stream, device: torch.device):
     return torch.cuda.stream(stream)
 
 
+def _used_by(stream, *tensors):
+    """Work under way on `stream` uses the tensors (None: left out), which may belong to another
+    stream and be freed before it is done."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 class ServingBatch:
     """What all layers share in one step of running sequences: the lengths, the
     block table and the attention plan (made from the lengths as they are now: a
@@ -131,7 +139,8 @@ class ServingBatch:
     def __init__(self, shape, block_table: torch.Tensor, seq_lens: torch.Tensor,
                  cu_seqlens: torch.Tensor | None = None, tokens: int | None = None, stream=None,
                  drafted: bool = False, parents: torch.Tensor | None = None):
-        self.block_table, self.seq_lens, self.cu_seqlens = block_table, seq_lens, cu_seqlens
+        # (kept for the layers' calls and, parents too, for replays of a captured prepare)
+        self.block_table, self.seq_lens, self.cu_seqlens, self.parents = block_table, seq_lens, cu_seqlens, parents
         self.drafted = drafted
         n, dev = seq_lens.numel(), seq_lens.device
         for t in (seq_lens, cu_seqlens, parents):
@@ -151,6 +160,8 @@ class ServingBatch:
         self.heads = (shape.n_q_heads, shape.n_kv_heads, shape.head_dim)
         self.causal = shape.causal
         with _on(stream, dev):
+            if stream is not None:  # the plan is made from them there, whenever this batch is dropped
+                _used_by(torch.cuda.current_stream(dev), seq_lens, cu_seqlens, parents)
             if drafted:
                 self.ws = torch.empty(mgb.mgb_attention_tree_ws_bytes(n, tokens, *self.heads), dtype=torch.uint8,
                                       device=dev)

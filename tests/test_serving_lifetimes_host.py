@@ -1,0 +1,63 @@
+"""Which tensors a batch and a layer keep, and which they say are in use on a stream that is
+not the current one (no GPU needed: the library's calls and torch's streams are stood in for)."""
+import contextlib
+
+import pytest
+import torch
+
+from megatron_transformer_layer_fwd_gb300 import mgb, runner
+from megatron_transformer_layer_fwd_gb300.inputs import LayerShape
+from megatron_transformer_layer_fwd_gb300.runner import ServingBatch
+
+SHAPE = LayerShape(1, 1, 128, 4, 2, 64, 256, causal=True)
+OTHER = object()     # a stream
+
+
+@pytest.fixture
+def used(monkeypatch):
+    """The tensors that were recorded as used on OTHER, by address."""
+    seen = set()
+
+    def record(t, stream):
+        assert stream is OTHER
+        seen.add(t.data_ptr())
+    for name in ("mgb_attention_decode_prepare", "mgb_attention_packed_prepare", "mgb_attention_tree_prepare"):
+        monkeypatch.setattr(mgb, name, lambda *a, **k: object())
+    for name in ("decode", "packed", "tree"):
+        monkeypatch.setattr(mgb, f"mgb_attention_{name}_ws_bytes", lambda *a: 256)
+    monkeypatch.setattr(runner, "DEVICE", "cpu")
+    monkeypatch.setattr(runner, "_on", lambda stream, device: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: OTHER)
+    monkeypatch.setattr(torch.Tensor, "record_stream", record)
+    return seen
+
+
+def _ints(*a):
+    return torch.tensor(a, dtype=torch.int32)
+
+
+def _batch(kind, stream=None):
+    """A batch of two sequences and the tensors that its plan is made from."""
+    lens, cu, parents = _ints(5, 6), _ints(0, 2, 3), _ints(-1, 0, -1)
+    table = torch.zeros((2, 4), dtype=torch.int32)
+    kw = {"decode": {}, "packed": dict(cu_seqlens=cu, tokens=3),
+          "drafted": dict(cu_seqlens=cu, tokens=3, drafted=True, parents=parents),
+          "chains": dict(cu_seqlens=cu, tokens=3, drafted=True)}[kind]
+    made_from = [lens] + ([] if kind == "decode" else [cu]) + ([parents] if kind == "drafted" else [])
+    return ServingBatch(SHAPE, table, lens, stream=stream, **kw), made_from
+
+
+KINDS = ["decode", "packed", "drafted", "chains"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_plan_made_on_a_given_stream_holds_what_it_is_made_from(used, kind):
+    _, made_from = _batch(kind, OTHER)
+    assert {t.data_ptr() for t in made_from} <= used
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_batch_keeps_what_a_replayed_prepare_reads(used, kind):
+    b, made_from = _batch(kind)
+    held = [b.seq_lens, b.cu_seqlens, b.parents]
+    assert all(any(t is h for h in held) for t in made_from)
