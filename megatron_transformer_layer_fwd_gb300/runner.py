@@ -236,10 +236,9 @@ class ServingLayer:
         if batch.tokens == 0:
             return torch.empty_like(x)
         with _on(stream, x.device):
-            if stream is not None:  # either may belong to another stream and be freed before the step is done
-                now = torch.cuda.current_stream(x.device)
-                x.record_stream(now)
-                batch.ws.record_stream(now)
+            if stream is not None:
+                _used_by(torch.cuda.current_stream(x.device), x, batch.ws, batch.block_table, batch.seq_lens,
+                         batch.cu_seqlens)
             return self._step(x, batch)
 
     def accept(self, batch: ServingBatch, accepted: torch.Tensor, new_lens: torch.Tensor | None = None,
@@ -257,9 +256,7 @@ class ServingLayer:
             raise ValueError("accepted, new_lens, the layer's pools and the batch must be on one device")
         with _on(stream, dev):
             if stream is not None:
-                for t in (accepted, new_lens, batch.ws):
-                    if t is not None:
-                        t.record_stream(torch.cuda.current_stream(dev))
+                _used_by(torch.cuda.current_stream(dev), accepted, new_lens, batch.ws, batch.block_table)
             cache = mgb.kv_cache(self.k_pool, self.v_pool, batch.block_table)
             mgb.mgb_kv_accept(batch.plan, cache, accepted, new_lens)
 
@@ -277,9 +274,7 @@ class ServingLayer:
                                  "one entry per copy")
         with _on(stream, dev):
             if stream is not None:
-                for t in (src, dst, slots):
-                    if t is not None:
-                        t.record_stream(torch.cuda.current_stream(dev))
+                _used_by(torch.cuda.current_stream(dev), src, dst, slots)
             # (the table is not used, but a cache has one)
             mgb.mgb_kv_copy_pages(mgb.kv_cache(self.k_pool, self.v_pool, dst.view(-1, 1)), src, dst, slots)
 

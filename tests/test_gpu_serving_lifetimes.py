@@ -100,6 +100,58 @@ def test_a_batch_made_on_a_busy_stream_from_temporaries(kind, handle):
         assert torch.equal(got, want) and torch.equal(c.pools, pools)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_step_on_a_busy_stream_and_nothing_kept(kind, handle):
+    c = Case(kind)
+    want, pools = c.want()
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if handle else s
+    for _ in range(3):
+        c.reset()
+        torch.cuda.synchronize()
+        dropped = c.index()
+        x = c.x.clone()
+        _busy(s)
+        b = ServingBatch(SHAPE, **dropped, stream=stream)
+        got = c.layer.step(x, b, stream=stream)
+        del dropped, b, x
+        _poison()
+        torch.cuda.synchronize()
+        assert mgb.mgb_device_status() == mgb.MGB_OK
+        assert torch.equal(got, want) and torch.equal(c.pools, pools)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_an_accept_and_copies_on_a_busy_stream_and_nothing_kept(handle):
+    """The paths of the last tokens, then page 0 to page 3 and half of page 4 to page 7."""
+    c = Case("drafted")
+    c.want()
+    after, new, outs = c.pools.clone(), torch.zeros(3, dtype=torch.int32, device="cuda"), []
+    last = [m - 1 for m in NEW]
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if handle else s
+    for own in (False, True, True):
+        c.pools.copy_(after)
+        new.zero_()
+        torch.cuda.synchronize()
+        b = ServingBatch(SHAPE, **c.index())
+        a = [ints(last), ints([0, 4]), ints([3, 7]), ints([16, 8])]
+        if own:
+            _busy(s)
+        c.layer.accept(b, a[0], new, stream if own else None)
+        del b
+        c.layer.copy_pages(*a[1:], stream if own else None)
+        del a
+        if own:
+            _poison()
+        torch.cuda.synchronize()
+        assert mgb.mgb_device_status() == mgb.MGB_OK
+        outs.append((c.pools.clone(), new.tolist()))
+    assert all(torch.equal(p, outs[0][0]) and n == outs[0][1] for p, n in outs[1:])
+    assert outs[0][1][0] > 30 and not torch.equal(outs[0][0], after)
+
+
 def test_a_captured_batch_is_all_that_a_replay_needs():
     c = Case("drafted")
     want, pools = c.want()

@@ -6,8 +6,8 @@ import pytest
 import torch
 
 from megatron_transformer_layer_fwd_gb300 import mgb, runner
-from megatron_transformer_layer_fwd_gb300.inputs import LayerShape
-from megatron_transformer_layer_fwd_gb300.runner import ServingBatch
+from megatron_transformer_layer_fwd_gb300.inputs import LayerShape, layer_inputs
+from megatron_transformer_layer_fwd_gb300.runner import ServingBatch, ServingLayer
 
 SHAPE = LayerShape(1, 1, 128, 4, 2, 64, 256, causal=True)
 OTHER = object()     # a stream
@@ -21,7 +21,9 @@ def used(monkeypatch):
     def record(t, stream):
         assert stream is OTHER
         seen.add(t.data_ptr())
-    for name in ("mgb_attention_decode_prepare", "mgb_attention_packed_prepare", "mgb_attention_tree_prepare"):
+    for name in ("mgb_attention_decode_prepare", "mgb_attention_packed_prepare", "mgb_attention_tree_prepare",
+                 "mgb_gemm_ex", "mgb_layernorm_fwd", "mgb_kv_append", "mgb_kv_append_tree", "mgb_attention_decode",
+                 "mgb_attention_packed_fwd", "mgb_attention_tree", "mgb_kv_accept", "mgb_kv_copy_pages"):
         monkeypatch.setattr(mgb, name, lambda *a, **k: object())
     for name in ("decode", "packed", "tree"):
         monkeypatch.setattr(mgb, f"mgb_attention_{name}_ws_bytes", lambda *a: 256)
@@ -61,3 +63,31 @@ def test_a_batch_keeps_what_a_replayed_prepare_reads(used, kind):
     b, made_from = _batch(kind)
     held = [b.seq_lens, b.cu_seqlens, b.parents]
     assert all(any(t is h for h in held) for t in made_from)
+
+
+def _layer():
+    pool = torch.zeros((4, 8, 2, 64), dtype=torch.bfloat16)
+    return ServingLayer(SHAPE, layer_inputs(SHAPE), pool, torch.zeros_like(pool))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_step_on_a_given_stream_holds_the_batch(used, kind):
+    b, made_from = _batch(kind)
+    x = torch.zeros((b.tokens, 128), dtype=torch.bfloat16)
+    _layer().step(x, b, stream=OTHER)
+    read = [x, b.ws, b.block_table] + ([b.seq_lens, b.cu_seqlens] if kind == "packed" else [b.seq_lens])
+    assert {t.data_ptr() for t in read} <= used
+
+
+@pytest.mark.parametrize("kind", ["drafted", "chains"])
+def test_an_accept_on_a_given_stream_holds_the_batch(used, kind):
+    b, _ = _batch(kind)
+    accepted, new_lens = _ints(0, -1), _ints(0, 0)
+    _layer().accept(b, accepted, new_lens, stream=OTHER)
+    assert {t.data_ptr() for t in (accepted, new_lens, b.ws, b.block_table)} <= used
+
+
+def test_page_copies_on_a_given_stream_hold_their_lists(used):
+    lists = _ints(0, 1), _ints(2, 3), _ints(8, 4)
+    _layer().copy_pages(*lists, stream=OTHER)
+    assert {t.data_ptr() for t in lists} <= used
