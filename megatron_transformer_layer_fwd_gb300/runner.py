@@ -176,6 +176,15 @@ class ServingBatch:
                 self.ws = torch.empty(mgb.mgb_attention_packed_ws_bytes(n, tokens), dtype=torch.uint8,
                                       device=dev)
                 self.plan = mgb.mgb_attention_packed_prepare(n, tokens, shape.causal, cu_seqlens, self.ws)
+            self.apart = stream is not None
+
+    def hold(self, stream, *tensors):
+        """A layer's call uses the batch and `tensors` on the current stream, which `stream` was made if
+        it was given. The workspace belongs to the constructor's stream, which may be a third one."""
+        if stream is not None:
+            _used_by(torch.cuda.current_stream(self.seq_lens.device), self.ws, self.block_table, *tensors)
+        elif self.apart:
+            _used_by(torch.cuda.current_stream(self.seq_lens.device), self.ws)
 
 
 class ServingLayer:
@@ -236,9 +245,7 @@ class ServingLayer:
         if batch.tokens == 0:
             return torch.empty_like(x)
         with _on(stream, x.device):
-            if stream is not None:
-                _used_by(torch.cuda.current_stream(x.device), x, batch.ws, batch.block_table, batch.seq_lens,
-                         batch.cu_seqlens)
+            batch.hold(stream, x, batch.seq_lens, batch.cu_seqlens)
             return self._step(x, batch)
 
     def accept(self, batch: ServingBatch, accepted: torch.Tensor, new_lens: torch.Tensor | None = None,
@@ -255,8 +262,7 @@ class ServingLayer:
         if any(t.device != dev for t in (accepted, new_lens, batch.seq_lens) if t is not None):
             raise ValueError("accepted, new_lens, the layer's pools and the batch must be on one device")
         with _on(stream, dev):
-            if stream is not None:
-                _used_by(torch.cuda.current_stream(dev), accepted, new_lens, batch.ws, batch.block_table)
+            batch.hold(stream, accepted, new_lens)
             cache = mgb.kv_cache(self.k_pool, self.v_pool, batch.block_table)
             mgb.mgb_kv_accept(batch.plan, cache, accepted, new_lens)
 

@@ -122,6 +122,29 @@ def test_a_step_on_a_busy_stream_and_nothing_kept(kind, handle):
         assert torch.equal(got, want) and torch.equal(c.pools, pools)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_batch_of_one_stream_in_a_step_of_the_current_one(kind):
+    """The workspace goes back to the stream that it was made on, where other work takes it."""
+    c = Case(kind)
+    want, pools = c.want()
+    a, index = torch.cuda.Stream(), c.index()
+    for _ in range(3):
+        c.reset()
+        torch.cuda.synchronize()
+        b = ServingBatch(SHAPE, **index, stream=a)
+        torch.cuda.current_stream().wait_stream(a)
+        torch.cuda._sleep(DELAY)
+        got = c.layer.step(c.x, b)
+        size = b.ws.numel()
+        del b
+        with torch.cuda.stream(a):
+            junk = [torch.full((size,), 0xC3, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        torch.cuda.synchronize()
+        del junk
+        assert mgb.mgb_device_status() == mgb.MGB_OK
+        assert torch.equal(got, want) and torch.equal(c.pools, pools)
+
+
 @pytest.mark.parametrize("handle", [False, True])
 def test_an_accept_and_copies_on_a_busy_stream_and_nothing_kept(handle):
     """The paths of the last tokens, then page 0 to page 3 and half of page 4 to page 7."""

@@ -91,3 +91,23 @@ def test_page_copies_on_a_given_stream_hold_their_lists(used):
     lists = _ints(0, 1), _ints(2, 3), _ints(8, 4)
     _layer().copy_pages(*lists, stream=OTHER)
     assert {t.data_ptr() for t in lists} <= used
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_workspace_of_another_stream_is_held_by_a_step_on_the_current_one(used, kind):
+    b, _ = _batch(kind, OTHER)
+    used.clear()
+    layer = _layer()
+    layer.step(torch.zeros((b.tokens, 128), dtype=torch.bfloat16), b)
+    assert used == {b.ws.data_ptr()}
+    if kind in ("drafted", "chains"):
+        used.clear()
+        layer.accept(b, _ints(0, -1))
+        assert used == {b.ws.data_ptr()}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_nothing_is_recorded_on_one_stream(used, kind):
+    b, _ = _batch(kind)
+    _layer().step(torch.zeros((b.tokens, 128), dtype=torch.bfloat16), b)
+    assert not used
