@@ -641,13 +641,14 @@ mgb_status mgb_kv_append_tree(const mgb_attention_tree_plan* plan, const mgb_kv_
 /* Keeps one path of each tree: accepted[s] is the index of its last token in the
  * sequence's draft, or -1 for none. The path's keys and values move to slots ctx, ctx +
  * 1, .. in order (a token at depth i to slot ctx + i, the position it was rotated by),
- * and new_lens[s] (may be NULL, and may be the prepare's seq_lens) becomes ctx + the
- * path's tokens; the slots behind are as undefined as before a draft. Sequences
- * without drafted tokens keep their length (0 if it is below 0). One call per layer's
- * cache; a second one on the same cache would move the moved slots again. An index
- * outside [-1, rows) is MGB_ERR_INDEX and counts as -1; a length past the table and a
- * bad page are MGB_ERR_INDEX, and what they would move stays. Pages that hold a
- * sequence's drafted tokens are its own. */
+ * and new_lens[s] (may be NULL, and may be the prepare's seq_lens; not overlapping
+ * accepted) becomes ctx + the path's tokens; the slots behind are as undefined as before
+ * a draft. Sequences without drafted tokens keep their length (0 if it is below 0), and
+ * their index is not looked at. One call per layer's cache; a second one on the same
+ * cache would move the moved slots again. Otherwise an index outside [-1, rows) is
+ * MGB_ERR_INDEX and counts as -1; a length past the table and a bad page are
+ * MGB_ERR_INDEX, and what they would move stays (new_lens goes by the path alone). Pages
+ * that hold a sequence's drafted tokens are its own. */
 mgb_status mgb_kv_accept(const mgb_attention_tree_plan* plan, const mgb_kv_cache* cache,
                          const int32_t* accepted, int32_t* new_lens, void* stream);
 

@@ -174,7 +174,10 @@ mgb_status mgb_kv_accept(const mgb_attention_tree_plan* plan, const mgb_kv_cache
     return MGB_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(accepted) & 3u) || (reinterpret_cast<uintptr_t>(new_lens) & 3u))
     return MGB_ERR_MISALIGNED;
-  if (new_lens != nullptr && new_lens == accepted) return MGB_ERR_INVALID_ARG;
+  // (a block per sequence: one would write what another has yet to read)
+  const uintptr_t from = reinterpret_cast<uintptr_t>(accepted), to = reinterpret_cast<uintptr_t>(new_lens);
+  const uintptr_t size = sizeof(int32_t) * (uintptr_t)plan->n_seqs;
+  if (new_lens != nullptr && from < to + size && to < from + size) return MGB_ERR_INVALID_ARG;
   MoveParams p{};
   if (!move_params(c, p)) return MGB_ERR_UNSUPPORTED;
   const int64_t blocks = ((int64_t)2 * p.nkv * p.ch + NT - 1) / NT;
