@@ -19,11 +19,11 @@ mgb_status launch(const Params& p, cudaStream_t st) {
   return launch_pdl(k, SMS * ctas_per_sm(D), NT, C::SMEM, st, p);
 }
 
+// A part holds a multiple of TREE_ROW_STEP rows, up to MAXR: these are all forms that a plan asks for.
 template <typename T, int D>
 mgb_status launch_rows(const Params& p, cudaStream_t st) {
-  if constexpr (sizeof(T) == 4)
-    if (p.rows <= 4) return launch<T, D, 4>(p, st);
-  return p.rows <= 8 ? launch<T, D, 8>(p, st) : launch<T, D, 16>(p, st);
+  static_assert(TREE_ROW_STEP == 8 && MAXR == 2 * TREE_ROW_STEP, "a form for each number of rows");
+  return p.rows == TREE_ROW_STEP ? launch<T, D, TREE_ROW_STEP>(p, st) : launch<T, D, MAXR>(p, st);
 }
 
 }  // namespace

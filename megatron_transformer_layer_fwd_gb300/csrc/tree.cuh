@@ -48,6 +48,7 @@ __host__ __device__ constexpr int unit_cost(int rows) {
 }
 
 constexpr int TREE_FEW = 4;
+constexpr int TREE_ROW_STEP = 8;  // rows of a part in the workspace: a multiple of it
 struct TreeHeader {
   int64_t cost, chunk;  // of all items; of a range
   int32_t live, pad;    // sequences with items

@@ -388,7 +388,7 @@ constexpr int few_rows(int d, int table) { return table == 0 && d == 64 ? 16 : 1
 // tokens: bf16 86.4 and 57 us at head dim 64 (as 16 rows 89 and 71), 86.6 and 54 at 128 (87.5
 // and 61), float32 97 (162). 1 to 15 rows, some in two items: bf16, head dim 64, 117 and 64 (100
 // and 80).
-constexpr int EIGHT_ROWS = 8;
+constexpr int EIGHT_ROWS = TREE_ROW_STEP;
 
 template <typename Cut>
 TreeCut cut_of() {
@@ -399,7 +399,7 @@ TreeCut cut_of() {
 TreeCut tree_cut(int n, int tokens, int nq, int nkv, int d, int table) {
   const int64_t rows = (int64_t)tokens * (nq / nkv);
   if (rows <= (int64_t)few_rows(d, table) * n)
-    return TreeCut{1, unit_tokens(d), rows <= (int64_t)EIGHT_ROWS * n ? 8 : MAXR, MAXR,
+    return TreeCut{1, unit_tokens(d), rows <= (int64_t)EIGHT_ROWS * n ? EIGHT_ROWS : MAXR, MAXR,
                    MAXR, UNIT, UNIT, UNIT, tree_item_cost(d, table == 0), WHOLE, MIN_CHUNK, SMS * ctas_per_sm(d)};
   if (table == 0) return cut_of<CutTc>();
   return d == 64 ? cut_of<CutF32<64>>() : cut_of<CutF32<128>>();
@@ -420,7 +420,7 @@ TreeLayout tree_layout(int n, int tokens, int nq, int nkv, int d) {
     t.split = take(sizeof(TreeSplit) * cut.ranges);
     t.live = take(sizeof(TreeSeq) * live);
     t.prefix = take(8 * (live + 1));
-    t.rows = most < cut.rows ? (int)((most + 7) / 8 * 8) : cut.rows;
+    t.rows = most < cut.rows ? (int)((most + TREE_ROW_STEP - 1) / TREE_ROW_STEP * TREE_ROW_STEP) : cut.rows;
     if ((size_t)2 * cut.ranges * t.rows > parts) parts = (size_t)2 * cut.ranges * t.rows;
     t.counter = take(4 * (size_t)cut.ranges);
   }
