@@ -51,7 +51,7 @@ constexpr int TREE_FEW = 4;
 constexpr int TREE_ROW_STEP = 8;  // rows of a part in the workspace: a multiple of it
 struct TreeHeader {
   int64_t cost, chunk;  // of all items; of a range
-  int32_t live, pad;    // sequences with items
+  int32_t live, bad;    // sequences with items; (of many) the first one with an offset outside its range
   int32_t few, many;    // items in up to TREE_FEW parts, in more: from the front and from the back of the list
 };
 // A sequence's rows of q and o begin at row `row`, `m` of them; `len` cached tokens
