@@ -20,11 +20,13 @@
 // them: K_0, V_0, K_1, .., or, where the streams take the units in turn, K_0, K_1, V_0, K_2, V_1,
 // .. Pages of a multiple of 8 slots are copied by the TMA unit, a box of up to 128 slots of one
 // page at a time (V by threads where the unit alone is too slow, see SPLIT_COST); others row by
-// row with 16-byte asynchronous copies. Every role that
-// waits for places of the ring does so in their order, or a lap that it left out could let a
-// later wait take an earlier lap's end for its own. V of tokens behind the length, and K and V of
-// those of a bad page, are not read: zeros stand in their place; a bit per key says that no row
-// sees them.
+// row with 16-byte asynchronous copies. A wait for a
+// place n to be free tells its laps apart by a parity, so whoever waits has to know that the place's lap
+// before, n - 2 NST, is free. It does: one thread frees the places in their order, and of those that a
+// role waits for (all; where V has threads of its own, those of K or of V) each is at most RING_GAP
+// <= NST behind the one before, whose wait has shown everything up to n - RING_GAP - NST free. V of
+// tokens behind the length, and K and V of those of a bad page, are not read: zeros stand in their
+// place; a bit per key says that no row sees them.
 //
 // Measured, 32 query and 8 KV heads of 128: one sequence of 131001 tokens, 244 rows 125 to 130
 // us, 1010 to 1045 TFLOP/s with each product counted once (P's second part makes it half as much
@@ -53,6 +55,10 @@ constexpr float REF_LIMIT = 16777216.0f;
 template <int D>
 struct Cfg {
   static constexpr int NST = D == 64 ? 10 : 5;          // ring slots
+  // Two K, or two V, that follow each other in the ring are at most this many places apart: an item's
+  // last K, V, V and the next item's K; an item's last V and the next item's K, K, V.
+  static constexpr int RING_GAP = 3;
+  static_assert(RING_GAP <= NST, "a wait could take a lap long past for its own");
   static constexpr int KB = D / 64;                     // 64-wide d blocks
   static constexpr int CH = D / 8;                      // 16-byte chunks of a row
   // A tile of 128 rows: groups of 8 rows, in a group the d blocks, in a block 8 rows of 128
