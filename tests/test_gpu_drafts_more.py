@@ -1,14 +1,19 @@
 """GPU tests of the operators for drafted tokens beside those in test_gpu_kv_tree.py and
 test_gpu_tree_more.py: vectors next to each other, many sequences with a bad offset, the time
-that many sequences take."""
+that many sequences take, accepts and page copies in a captured graph, a drafted chain against
+single steps."""
 import numpy as np
 import pytest
 import torch
 
 from megatron_transformer_layer_fwd_gb300 import mgb
+from megatron_transformer_layer_fwd_gb300.inputs import LayerShape
+from megatron_transformer_layer_fwd_gb300.runner import ServingBatch
 from oracle import drafts
 from tests.drafts_util import Batch, random_tree
 from tests.serving_util import Cache, host, ints
+from tests.test_gpu_drafts_run import Net
+from tests.util import TOL, rel_l2
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +100,87 @@ def test_time_of_a_prepare_goes_with_the_sequences():
         times.append(min(best))
     assert mgb.mgb_device_status() == mgb.MGB_OK
     assert times[1] < 8 * times[0], times
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_accepts_and_copies_are_replayed_with_other_indices(dtype):
+    """Prepare, accept and page copies in one graph, whose offsets, trees, leaves, pages and numbers
+    of slots change between the replays; one replay's indices are bad."""
+    rng = np.random.default_rng(82)
+    n, T, page, nkv, d, copies = 4, 60, 16, 2, 64, 3
+    c = Cache(rng, [page * 6] * n, page, nkv, d, dtype, extra=4)
+    cu, lens, parents, accepted = (ints([0] * (n + 1)), ints([0] * n), ints([-1] * T), ints([-1] * n))
+    new, src, dst, slots = ints([-9] * n), ints([0] * copies), ints([0] * copies), ints([0] * copies)
+    ws = torch.empty(mgb.mgb_attention_tree_ws_bytes(n, T, 4, nkv, d), dtype=torch.uint8, device="cuda")
+
+    def step():
+        plan = mgb.mgb_attention_tree_prepare(n, T, 4, nkv, d, cu, lens, parents, ws)
+        mgb.mgb_kv_accept(plan, c.desc, accepted, new)
+        mgb.mgb_kv_copy_pages(c.desc, src, dst, slots)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()              # (nothing drafted, page 0 onto itself)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    pools = [c.k, c.v]
+    for replay in range(6):
+        sizes = [int(m) for m in rng.integers(1, 15, n)]
+        b = Batch([(None if m == 3 else int(rng.integers(0, 6 * page - m + 1)), random_tree(rng, m)) for m in sizes])
+        leaf = [int(rng.integers(-1, m)) for m in sizes]
+        order = rng.permutation(c.n_pages)
+        a, z, k = order[:copies], order[copies:2 * copies], rng.integers(0, page + 1, copies)
+        bad = replay == 3
+        cu.copy_(ints(b.cu)), lens.copy_(ints(b.lens)), parents.copy_(ints(b.parents + [-1] * (T - b.tokens)))
+        accepted.copy_(ints([leaf[0], leaf[1], leaf[2], 99 if bad else leaf[3]]))
+        src.copy_(ints(a)), dst.copy_(ints([z[0], z[1], c.n_pages if bad else z[2]])), slots.copy_(ints(k))
+        graph.replay()
+        assert mgb.mgb_device_status() == (mgb.MGB_ERR_INDEX if bad else mgb.MGB_OK)
+        if bad:
+            leaf[3], k[2] = -1, 0
+        pools, want = drafts.accept(pools, c.table, b.cu, b.lens, b.trees, leaf)
+        for x in pools:
+            for i, j, m in zip(a, z, k):
+                x[j, :m] = x[i, :m]
+        assert new.tolist() == want
+        for got, x in ((host(c.tk), pools[0]), (host(c.tv), pools[1])):
+            assert ((got == x) | (np.isnan(got) & np.isnan(x))).all()
+
+
+@pytest.mark.parametrize("shape", [LayerShape(1, 1, 256, 4, 2, 64, 512, act="swiglu", causal=True),
+                                   LayerShape(1, 1, 256, 8, 1, 128, 512, causal=True),
+                                   LayerShape(1, 1, 128, 4, 2, 64, 256, dtype="f32", causal=True)])
+@pytest.mark.parametrize("m", [1, 3, 17])
+def test_a_drafted_chain_gives_what_single_steps_give(shape, m):
+    """Two layers of each: a result is within 2 TOL of the float64 layers, so two are within 4 of each
+    other; the caches, which a step more may have left at the same distance, too."""
+    prompts, outs = [40, 1, 200], []
+    for chain in (True, False):
+        rng = np.random.default_rng(83)
+        n = len(prompts)
+        net = Net(shape, 64, False, n, 16)
+        for layer in net.layers:
+            layer.k_pool.zero_(), layer.v_pool.zero_()
+        table, cu = ints(net.table), np.cumsum([0] + prompts)
+        net.run(net.rows(rng, int(cu[-1])), ServingBatch(shape, table, ints(prompts), ints(cu), int(cu[-1])))
+        x = net.rows(rng, n * m).reshape(n, m, -1)
+        if chain:
+            lens = ints([p + m for p in prompts])
+            batch = ServingBatch(shape, table, lens, ints(np.arange(n + 1) * m), n * m, drafted=True)
+            y = host(net.run(x.reshape(n * m, -1), batch)).reshape(n, m, -1)
+            for layer in net.layers:
+                layer.accept(batch, ints([m - 1] * n), lens)
+            assert lens.tolist() == [p + m for p in prompts]
+        else:
+            y = np.stack([host(net.run(x[:, i].copy(), ServingBatch(shape, table, ints([p + i + 1 for p in prompts]))))
+                          for i in range(m)], axis=1)
+        assert mgb.mgb_device_status() == mgb.MGB_OK
+        outs.append((y, [host(t) for layer in net.layers for t in (layer.k_pool, layer.v_pool)]))
+    tol = 4 * TOL[shape.dtype][0]
+    for a, b in zip(outs[0][0].reshape(-1, shape.hidden), outs[1][0].reshape(-1, shape.hidden)):
+        assert rel_l2(a, b) < tol
+    for a, b in zip(outs[0][1], outs[1][1]):
+        assert rel_l2(a, b) < tol
