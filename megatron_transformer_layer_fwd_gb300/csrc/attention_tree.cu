@@ -28,8 +28,8 @@
 // tokens behind the length, and K and V of those of a bad page, are not read: zeros stand in their
 // place; a bit per key says that no row sees them.
 //
-// Measured, 32 query and 8 KV heads of 128: one sequence of 131001 tokens, 244 rows 125 to 130
-// us, 1010 to 1045 TFLOP/s with each product counted once (P's second part makes it half as much
+// Measured, 32 query and 8 KV heads of 128: one sequence of 131001 tokens, 244 rows 125 to 131
+// us, 1000 to 1045 TFLOP/s with each product counted once (P's second part makes it half as much
 // again), 64 rows 90 to 94 us, 5.7 to 6.0 TB/s; 32 sequences of 33 to 16000 tokens, 8 to 96 rows 58 us, 4.5 TB/s; two of 7000 to
 // 9000 with 1024 rows each 69 us. Bound: with two halves of rows the tensor cores, 101 of the
 // 125 us at the rate of a large product (start and join 10); with one the HBM.

@@ -111,7 +111,7 @@ def _on(stream, device: torch.device):
 
 def _used_by(stream, *tensors):
     """Work under way on `stream` uses the tensors (None: left out), which may belong to another
-    stream and be freed before it is done."""
+    stream and be freed before it is done. (A stream known by its handle has to outlive them.)"""
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
@@ -179,8 +179,8 @@ class ServingBatch:
             self.apart = stream is not None
 
     def hold(self, stream, *tensors):
-        """A layer's call uses the batch and `tensors` on the current stream, which `stream` was made if
-        it was given. The workspace belongs to the constructor's stream, which may be a third one."""
+        """A layer's call uses the batch and `tensors` on the current stream (`stream`, if one was given).
+        The workspace belongs to the constructor's stream, which may be another one in either case."""
         if stream is not None:
             _used_by(torch.cuda.current_stream(self.seq_lens.device), self.ws, self.block_table, *tensors)
         elif self.apart:
@@ -190,7 +190,8 @@ class ServingBatch:
 class ServingLayer:
     """One layer for running sequences: its weights and its paged key/value
     pools ([n_pages, page_size, n_kv_heads, head_dim]; every layer has its own,
-    the block table is shared). `rope`: the table of rope_table, or None."""
+    the block table is shared). `rope`: the table of rope_table, or None. The
+    layer has to outlive its steps."""
 
     def __init__(self, shape, arrays: dict, k_pool: torch.Tensor, v_pool: torch.Tensor,
                  rope: torch.Tensor | None = None, rope_interleaved: bool = False):
